@@ -18,11 +18,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtr.so")
 
 TR_OK, TR_E_INVAL, TR_E_UNSUPPORTED, TR_E_CUDA, TR_E_DEVICE, TR_E_TIMEOUT = range(6)
-TR_DEV_BAD_TOKEN, TR_DEV_CACHE_FULL, TR_DEV_BAD_LENGTH, TR_DEV_TIMEOUT = 1, 2, 4, 8
+TR_DEV_BAD_TOKEN, TR_DEV_CACHE_FULL, TR_DEV_BAD_LENGTH, TR_DEV_TIMEOUT, TR_DEV_BAD_PAGE = 1, 2, 4, 8, 16
 TR_I32, TR_I64 = 0, 1
 TR_F32, TR_BF16 = 0, 1
 TR_INIT_ZERO, TR_INIT_RANDOM, TR_INIT_INHERIT = 0, 1, 2
 TR_UPD_ALL, TR_UPD_ACCEPTED = 0, 1
+TR_KV_BF16, TR_KV_F16, TR_KV_E4M3 = 0, 1, 2
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -51,6 +52,15 @@ class tr_step_args(ctypes.Structure):
     ]
 
 
+class tr_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("K", _p), ("V", _p), ("type", _i), ("B", _i), ("Hkv", _i), ("d", _i), ("L", _p),
+        ("page_table", _p), ("max_pages", _i), ("page_size", _i), ("num_pages", _i), ("cap", _i),
+        ("block_stride", _i64), ("head_stride", _i64), ("row_stride", _i64),
+        ("k_scale", _p), ("v_scale", _p), ("scores", _p), ("scores_ld", _i64),
+    ]
+
+
 # name -> (restype, argtypes)
 _SIGS = {
     "tr_tree_create": (_i, [_p, _i, _i, ctypes.POINTER(_p)]),
@@ -73,6 +83,12 @@ _SIGS = {
     "tr_update": (_i, [_p, _i, _i, _i64, _i, _p, _p, _p, _i, _p, _p, _p]),
     "tr_kv_commit": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
     "tr_kv_commit_workspace_bytes": (_sz, [_i]),
+    "tr_decode_attn": (_i, [_p, ctypes.POINTER(tr_kv_cache), _i, _f, _p, _p, _i, _p, _sz, _p]),
+    "tr_decode_attn_workspace_bytes": (_sz, [ctypes.POINTER(tr_kv_cache), _i, _i]),
+    "tr_kv_append": (_i, [_p, _p, _i, _p, ctypes.POINTER(tr_kv_cache), _p, _sz, _p]),
+    "tr_kv_append_workspace_bytes": (_sz, [ctypes.POINTER(tr_kv_cache)]),
+    "tr_kv_evict": (_i, [ctypes.POINTER(tr_kv_cache), _i, _i, _p, _sz, _p]),
+    "tr_kv_evict_workspace_bytes": (_sz, [ctypes.POINTER(tr_kv_cache), _i]),
     "tr_step": (_i, [ctypes.POINTER(tr_step_args), _p]),
     "tr_step_workspace_bytes": (_sz, [ctypes.POINTER(tr_step_args)]),
     "tr_get_status": (_i, [ctypes.POINTER(ctypes.c_int32), _p]),
@@ -146,6 +162,12 @@ def _ftype(x):
 def _i32(t, name):
     if t is not None and t.dtype != torch.int32:
         raise ValueError("%s must be int32" % name)
+
+
+def _i31(n, name):
+    """ctypes would keep the low 32 bits of a larger number."""
+    if not 0 <= n < 1 << 31:
+        raise ValueError("%s must be in [0, 2**31)" % name)
 
 
 class Tree:
@@ -317,6 +339,145 @@ def tr_kv_commit(Kt, Vt, Kc, Vc, L, tree, path, acc_len, ws):
 
 def tr_kv_commit_workspace_bytes(B):
     return lib().tr_kv_commit_workspace_bytes(B)
+
+
+_KV_TYPES = {torch.bfloat16: TR_KV_BF16, torch.float16: TR_KV_F16, torch.float8_e4m3fn: TR_KV_E4M3}
+
+
+class KVCache:
+    """A batch's KV cache as tr_kv_append, tr_decode_attn and tr_kv_evict take it
+    (``tr_kv_cache``): a view of the caller's tensors, which it keeps alive.
+
+    K, V: dense [B, Hkv, cap, d], or with ``page_table`` [B, max_pages] (int32)
+    pages [num_pages, Hkv, page_size, d]; bfloat16, float16 or float8_e4m3fn.
+    Permuted and sliced views are taken as they are (the last axis contiguous,
+    K and V strided alike), so pages laid out [num_pages, page_size, Hkv, d]
+    are passed as ``x.transpose(1, 2)``.
+    L [B] int32: the rows each sequence holds.  k_scale, v_scale [Hkv] float32:
+    the scales of an 8-bit cache.  scores [B, Hkv, n] float32, n at least the
+    positions a sequence can hold: the attention weight gathered by each row."""
+
+    def __init__(self, K, V, L, page_table=None, scores=None, k_scale=None, v_scale=None):
+        if K.dtype not in _KV_TYPES or V.dtype != K.dtype:
+            raise ValueError("K and V must both be bfloat16, float16 or float8_e4m3fn")
+        if K.dim() != 4 or V.shape != K.shape:
+            raise ValueError("K and V must be 4-dimensional and of the same shape")
+        if K.numel() == 0:
+            raise ValueError("K and V must not be empty")
+        for t in (K, V):
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the CUDA device")
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError("K and V must be contiguous along the last axis")
+        if any(n > 1 and a != b for n, a, b in zip(K.shape, K.stride(), V.stride())):
+            raise ValueError("K and V must have the same strides")
+        blocks, Hkv, rows, d = K.shape
+        if L.dim() != 1:
+            raise ValueError("L must be [B]")
+        _i32(L, "L")
+        B = L.shape[0]
+        if page_table is None:
+            if blocks != B:
+                raise ValueError("a dense cache must be [B, Hkv, cap, d]")
+            self.cap = rows
+        else:
+            _i32(page_table, "page_table")
+            if page_table.dim() != 2 or page_table.shape[0] != B:
+                raise ValueError("page_table must be [B, max_pages]")
+            self.cap = page_table.shape[1] * rows
+        if (K.dtype == torch.float8_e4m3fn) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and it needs both")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (Hkv,)):
+                raise ValueError("%s must be float32 [Hkv]" % name)
+        if scores is not None and (scores.dtype != torch.float32 or scores.dim() != 3 or
+                                   scores.shape[:2] != (B, Hkv) or scores.shape[2] < self.cap):
+            raise ValueError("scores must be float32 [B, Hkv, n], n >= the positions a sequence can hold")
+        for t, name in ((V, "V"), (L, "L"), (page_table, "page_table"), (scores, "scores"), (k_scale, "k_scale"),
+                        (v_scale, "v_scale")):
+            if t is not None and t.device != K.device:
+                raise ValueError("%s must live on K's device" % name)
+        self.K, self.V, self.L, self.page_table, self.scores = K, V, L, page_table, scores
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.B, self.Hkv, self.d, self.dtype, self.device = B, Hkv, d, K.dtype, K.device
+        self.row_dtype = torch.float16 if K.dtype == torch.float16 else torch.bfloat16  # of queries and new rows
+        c = tr_kv_cache()
+        c.K, c.V = K.data_ptr(), V.data_ptr()
+        c.type, c.B, c.Hkv, c.d = _KV_TYPES[K.dtype], B, Hkv, d
+        c.L = _ptr(L)
+        c.page_table = _ptr(page_table)
+        if page_table is None:
+            c.cap = rows
+        else:
+            c.max_pages, c.page_size, c.num_pages = page_table.shape[1], rows, blocks
+        c.block_stride, c.head_stride, c.row_stride = K.stride()[:3]
+        c.k_scale, c.v_scale, c.scores = _ptr(k_scale), _ptr(v_scale), _ptr(scores)
+        c.scores_ld = scores.shape[2] if scores is not None else 0
+        self.struct = c
+        self._ref = ctypes.byref(c)
+
+    def _stream(self):
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError("the cache must live on the current CUDA device")
+        return _stream()
+
+    def _arg(self, t, name, dtype):
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s" % (name, dtype))
+        if t.device != self.device:
+            raise ValueError("%s must live on the cache's device" % name)
+        return _ptr(t)
+
+
+def tr_decode_attn_workspace_bytes(cache, Hq, accumulate=False):
+    return lib().tr_decode_attn_workspace_bytes(cache._ref, Hq, int(accumulate))
+
+
+def tr_decode_attn(Q, cache, O, scale, ws, lse=None, accumulate=False):
+    """Attention of one new token per sequence: Q [B, Hq, d] over the cache's first
+    L[b] rows into O [B, Hq, d] float32 (and lse [B, Hq] float32); ``accumulate``
+    adds each row's weights to cache.scores."""
+    if Q.dim() != 3 or Q.shape[0] != cache.B or Q.shape[2] != cache.d:
+        raise ValueError("Q must be [B, Hq, d]")
+    if O.shape != Q.shape:
+        raise ValueError("O must be [B, Hq, d]")
+    if lse is not None and lse.shape != Q.shape[:2]:
+        raise ValueError("lse must be [B, Hq]")
+    _check("tr_decode_attn", lib().tr_decode_attn(
+        cache._arg(Q, "Q", cache.row_dtype), cache._ref, Q.shape[1], scale, cache._arg(O, "O", torch.float32),
+        None if lse is None else cache._arg(lse, "lse", torch.float32), int(accumulate),
+        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream()))
+
+
+def tr_kv_append_workspace_bytes(cache):
+    return lib().tr_kv_append_workspace_bytes(cache._ref)
+
+
+def tr_kv_append(Kn, Vn, cache, ws, count=None):
+    """Appends the first count[b] (all T without ``count``) rows of Kn, Vn [B, T, Hkv, d]
+    to each sequence, converting them to the cache's type, and advances L."""
+    if Kn.dim() != 4 or Kn.shape[0] != cache.B or Kn.shape[2:] != (cache.Hkv, cache.d) or Vn.shape != Kn.shape:
+        raise ValueError("Kn and Vn must be [B, T, Hkv, d]")
+    if count is not None and tuple(count.shape) != (cache.B,):
+        raise ValueError("count must be [B]")
+    _check("tr_kv_append", lib().tr_kv_append(
+        cache._arg(Kn, "Kn", cache.row_dtype), cache._arg(Vn, "Vn", cache.row_dtype), Kn.shape[1],
+        None if count is None else cache._arg(count, "count", torch.int32), cache._ref,
+        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream()))
+
+
+def tr_kv_evict_workspace_bytes(cache, budget):
+    _i31(budget, "budget")
+    return lib().tr_kv_evict_workspace_bytes(cache._ref, budget)
+
+
+def tr_kv_evict(cache, budget, recent, ws):
+    """Cuts every sequence longer than ``budget`` down to it: the last ``recent`` rows
+    and the best-scored others stay, per KV head, moved up in their old order."""
+    _i31(budget, "budget")
+    _i31(recent, "recent")
+    _check("tr_kv_evict", lib().tr_kv_evict(cache._ref, budget, recent, cache._arg(ws, "ws", torch.uint8),
+                                            ws.numel(), cache._stream()))
 
 
 def make_step_args(tree, M, tree_tok, ids, vals, acc_len, path, committed, root, L, logits=None, H=None, Wt=None,

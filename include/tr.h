@@ -37,7 +37,8 @@
  *  - No exception crosses the ABI.  Calls keep no hidden state besides the
  *    status word and may run concurrently on different streams as long as
  *    they do not share output buffers or workspace.
- *  - Limits: tree nodes N <= 128, K <= 32, head dim d == 128.
+ *  - Limits: tree nodes N <= 128, K <= 32, head dim d == 128 (the single-token
+ *    calls on a tr_kv_cache also take d == 64).
  */
 #ifndef TR_H
 #define TR_H
@@ -65,6 +66,7 @@ typedef enum {
 #define TR_DEV_CACHE_FULL 0x2u /* a KV commit would pass the cache capacity */
 #define TR_DEV_BAD_LENGTH 0x4u /* a cache length L[b] outside [0, cap] */
 #define TR_DEV_TIMEOUT 0x8u    /* a bounded device wait gave up */
+#define TR_DEV_BAD_PAGE 0x10u  /* a page table entry in use outside [0, num_pages) */
 
 typedef enum { TR_I32 = 0, TR_I64 = 1 } tr_itype;  /* element type of M */
 typedef enum { TR_F32 = 0, TR_BF16 = 1 } tr_ftype; /* element type of logits */
@@ -308,6 +310,106 @@ int tr_kv_commit(const void *Kt, const void *Vt, void *Kc, void *Vc, int32_t *L,
                  int Hkv, int d, const struct tr_tree *tree, const int32_t *path,
                  const int32_t *acc_len, void *ws, size_t ws_bytes, tr_stream_t stream);
 size_t tr_kv_commit_workspace_bytes(int B);
+
+/* ------------------------------------------------------------------------ */
+/* Single-token decoding over a KV cache                                      */
+/* ------------------------------------------------------------------------ */
+
+/* Decoding without a draft (a step whose matrix has nothing to offer, the
+ * autoregressive decoding that the method is compared with) needs the
+ * attention of one new token; long-running sequences need their cache bounded.
+ * tr_kv_append, tr_decode_attn and tr_kv_evict do that on a cache that is
+ * either the dense [B, Hkv, cap, d] of tr_verify_attn and tr_kv_commit (the
+ * two can be mixed on one bf16 cache) or divided into pages. */
+
+/* Element type of the cached rows.  bf16 and fp16 caches take queries and new
+ * rows of their own type; an e4m3 cache (8-bit, no infinities) takes bf16 ones
+ * and holds K = k_scale[h] * e4m3, V = v_scale[h] * e4m3. */
+typedef enum { TR_KV_BF16 = 0, TR_KV_F16 = 1, TR_KV_E4M3 = 2 } tr_kvtype;
+
+/* A batch's KV cache.  Position p of sequence b, KV head h, starts at element
+ *   dense  (page_table == NULL)  b * block_stride + h * head_stride + p * row_stride
+ *   paged  page_table[b, p / page_size] * block_stride + h * head_stride
+ *          + (p % page_size) * row_stride
+ * of K and of V; the d elements of a row are contiguous.  Entries of the page
+ * table behind a sequence's last row are not read.  Rows at and behind L[b]
+ * are never read, so they may hold anything.  A page may be shared between
+ * sequences for reading; tr_kv_append and tr_kv_evict need the pages that they
+ * write (append: those that receive rows; evict: all of the sequence's) to
+ * belong to one sequence.
+ * K, V and all strides are 16-byte aligned, rows do not overlap, d is 64 or
+ * 128, page_size a power of two, B <= 1024 and B * Hkv * (positions a sequence
+ * can hold) < 2^31. */
+typedef struct tr_kv_cache {
+  void *K, *V;
+  tr_kvtype type;
+  int B, Hkv, d;
+  int32_t *L;                /* [B] (device) rows held by each sequence */
+  const int32_t *page_table; /* [B, max_pages] (device), or NULL: dense */
+  int max_pages;             /* paged: pages a sequence can hold */
+  int page_size;             /* paged: positions per page */
+  int num_pages;             /* paged: pages behind K and V */
+  int cap;                   /* dense: positions per sequence */
+  int64_t block_stride;      /* elements between sequences (dense) or pages */
+  int64_t head_stride;       /* elements between KV heads */
+  int64_t row_stride;        /* elements between positions */
+  const float *k_scale;      /* [Hkv] (device), e4m3 only (else NULL) */
+  const float *v_scale;
+  float *scores;             /* [B, Hkv, scores_ld] (device), or NULL: the attention weight
+                              * gathered by each row, scores[b, h, p] */
+  int64_t scores_ld;         /* >= positions a sequence can hold */
+} tr_kv_cache;
+
+/* Attention of one new token per sequence: with g = hq / (Hq / Hkv),
+ *   O[b, hq] = sum_p w_p V[b, g, p],  w = softmax_p(scale * Q[b, hq] . K[b, g, p]),
+ *   lse[b, hq] = ln sum_p exp(scale * Q[b, hq] . K[b, g, p])    over 0 <= p < L[b].
+ * The token's own row takes part once it has been appended (tr_kv_append
+ * first).  A sequence with L[b] == 0 gets O = 0 and lse = -inf.
+ *   Q   [B, Hq, d] bf16 (fp16 for an fp16 cache)
+ *   O   [B, Hq, d] fp32 output         lse [B, Hq] fp32 output, may be NULL
+ * accumulate != 0: also scores[b, g, p] += sum over the Hq / Hkv query heads of
+ * group g of w_p, for p < L[b]; the sums' order is fixed, so equal calls give
+ * equal bits.
+ * Hq a multiple of Hkv (any group size), scale positive and finite.  A length
+ * outside the cache sets TR_DEV_BAD_LENGTH and counts as 0; an entry of the
+ * page table outside [0, num_pages) sets TR_DEV_BAD_PAGE, is not followed, and
+ * leaves that sequence's results undefined.
+ * ws: tr_decode_attn_workspace_bytes bytes, 16-byte aligned; its contents do
+ * not matter and nothing is kept in it between calls. */
+int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, float scale, float *O, float *lse,
+                   int accumulate, void *ws, size_t ws_bytes, tr_stream_t stream);
+size_t tr_decode_attn_workspace_bytes(const tr_kv_cache *cache, int Hq, int accumulate);
+
+/* Appends rows: for i < n, with n = count[b] (T where count is NULL),
+ *   K[b, h, L[b] + i] = Kn[b, i, h], same for V,  then L[b] += n.
+ * An e4m3 cache gets e4m3(Kn / k_scale[h]) (IEEE division, round to nearest
+ * even, clamped to +-448; NaN stays NaN).  scores, if present, is set to 0 at
+ * the new rows.
+ *   Kn, Vn [B, T, Hkv, d] bf16 (fp16 for an fp16 cache)
+ *   count  [B] int32 (device), 0 <= count[b] <= T, or NULL
+ * A sequence whose L[b] or count[b] is out of range (TR_DEV_BAD_LENGTH), whose
+ * rows would not fit (TR_DEV_CACHE_FULL) or need a bad page (TR_DEV_BAD_PAGE)
+ * is left untouched.
+ * ws: tr_kv_append_workspace_bytes bytes, zeroed once before first use; every
+ * call leaves its counters at zero again. */
+int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t *count, const tr_kv_cache *cache, void *ws,
+                 size_t ws_bytes, tr_stream_t stream);
+size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache);
+
+/* Evicts rows by accumulated attention weight: every sequence with
+ * L[b] > budget keeps, for each KV head on its own, its last `recent` rows and,
+ * of the rows before them, the budget - recent with the largest scores (equal
+ * scores: the lower position stays; -0 equals +0; NaN ranks below -inf).  The
+ * kept rows of K, V and scores move to positions 0 .. budget-1 in their old
+ * order and L[b] becomes budget; what lies behind is left as it is.  Sequences
+ * within the budget are left alone.  cache->scores must be present.
+ *   1 <= budget, 0 <= recent <= budget
+ * A length outside the cache (TR_DEV_BAD_LENGTH) or a bad page in use
+ * (TR_DEV_BAD_PAGE) leaves that sequence untouched.
+ * ws: tr_kv_evict_workspace_bytes bytes, 16-byte aligned; its contents do not
+ * matter and nothing is kept in it between calls. */
+int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, void *ws, size_t ws_bytes, tr_stream_t stream);
+size_t tr_kv_evict_workspace_bytes(const tr_kv_cache *cache, int budget);
 
 /* ------------------------------------------------------------------------ */
 /* Fused step                                                                 */

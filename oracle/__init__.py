@@ -38,11 +38,12 @@ from .tr import (
     init_matrix, retrieve, tree_attention, topk, topk_rows, accept, update,
     kv_commit, lmhead_logits, mix64_stream, softmax_stats, target_probs, accept_sampled, draw_is_valid,
 )
+from .kv import decode_attention, e4m3_round, evict_keep
 from .loop import TRState, tr_loop, greedy_decode
 
 __all__ = [
     "TreePlan", "INIT_ZERO", "INIT_RANDOM", "INIT_INHERIT", "UPD_ALL", "UPD_ACCEPTED",
     "init_matrix", "retrieve", "tree_attention", "topk", "topk_rows", "accept", "update",
     "kv_commit", "lmhead_logits", "mix64_stream", "softmax_stats", "target_probs", "accept_sampled",
-    "draw_is_valid", "TRState", "tr_loop", "greedy_decode",
+    "draw_is_valid", "decode_attention", "e4m3_round", "evict_keep", "TRState", "tr_loop", "greedy_decode",
 ]
