@@ -1,4 +1,36 @@
 // Attention of one new token per sequence over a KV cache.
+//
+// For query head hq with KV head g, O = sum_p w_p V[g, p] with w the softmax of
+// scale * Q[hq] . K[g, p] over the cached rows p < L[b].  Every cached row is
+// needed once and used for the few query heads of its group, so the cache's
+// bytes bound the work (1 flop per byte for one head per group, 2 G in general).
+//
+// Split.  A pair is (sequence, KV head) with ceil(L / 16) tiles of 16 rows.  All
+// pairs' tiles are laid end to end and cut into equal ranges, one per WARP of
+// a one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
+// shared memory (cp.async) and meets no barrier on the way, whatever the mix of lengths.
+// Warps are numbered across CTAs first, so little work still spreads over
+// every SM.  A pair that lies inside one range is finished by its warp; the
+// others leave (m, l, O) partials, two slots per warp at most, that
+// finish_kernel joins in a fixed order.
+//
+// Tile.  S = Q K^T with m16n8k16 matrix instructions: the group's query heads
+// are the 16 rows (8 of them empty when the group has at most 8 heads), 16
+// cached rows are two columns blocks.  The contraction runs over d in an order of
+// its own: a lane's 16-byte piece of a row of K is used as the B fragments of
+// two (8-bit: four) instructions, and Q is loaded in the same order, so that K needs no
+// transposing load.  The accumulators of S are laid out as the A fragments of
+// P V.  V's B fragments pair two rows: a lane reads the same 16-byte piece of
+// four rows and interleaves them with byte permutes; the columns of O come
+// out in runs of 8 or 16 per lane.
+//
+// Precision.  The output is fp32, so P must not be rounded to the cache's type:
+// p is split exactly into three bf16 parts (8 + 8 + 8 bits), or into two fp16 parts
+// (22 bits, p scaled up to 2^15 so that small weights stay normal numbers), and
+// each part is multiplied with V.  With at most 8 heads the empty half of the
+// instruction's rows carries the second part at no extra cost.
+// An 8-bit row is widened to fp16 (exact); Q is scaled by a power of two per
+// head so that narrowing bf16 to fp16 is exact for all but negligible elements.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -9,118 +41,655 @@
 
 namespace {
 
+using sm100::ex2;
+using sm100::smem_u32;
+
+constexpr int kMaxB = 1024;
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;               // cached rows per tile
+constexpr int kRingBytes = 24 * 1024;   // per warp
+constexpr int kMinTiles = 2;            // tiles of a warp's range, at least
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;            // the running maximum follows once it is 2^8 behind
 
 struct DecodeArgs {
   const void *Q;
   float *O, *lse;
-  float *s;  // workspace: logits (log2 units) [B, Hq, ld]
+  float *part_o;     // [row tiles][warps][2][MT][d]
+  float2 *part_ml;   // [row tiles][warps][2][MT] (reference maximum, sum), log2 units
+  float *lse2;       // [B, Hq] log2 of the softmax denominator of pairs finished by one warp
+  float *s;          // [B, Hq, s_ld] logits, log2 units (accumulate)
+  int *plan;         // [0] tiles per warp, [1 + b] tiles of one head before sequence b
   long long s_ld;
   int Hq, G, accumulate;
   float scale_log2;
   unsigned *status;
 };
 
-template <int TYPE, int N>
-__device__ __forceinline__ void load_row(const char *p, float (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    if constexpr (TYPE == TR_KV_BF16) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + 2 * i));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    } else if constexpr (TYPE == TR_KV_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(p + 2 * i));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    } else {
-      const __half2 v = __half2(__nv_cvt_fp8x2_to_halfraw2(*reinterpret_cast<const unsigned short *>(p + i), __NV_E4M3));
-      const float2 f = __half22float2(v);
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    }
+template <int TYPE, int D>
+struct Shape {
+  static constexpr bool F8 = TYPE == TR_KV_E4M3;
+  static constexpr bool BF = TYPE == TR_KV_BF16;
+  static constexpr int ROW = D * (F8 ? 1 : 2);          // bytes
+  static constexpr int CPR = ROW / 16;                  // 16-byte pieces of a row
+  static constexpr int STAGE = 2 * kTile * ROW;         // K tile, V tile
+  static constexpr int STAGES = kRingBytes / STAGE;
+  static constexpr int VW = F8 && D == 128 ? 16 : 8;    // columns of a lane's piece of V
+  static constexpr int VS = D / (8 * VW);               // pieces of V per lane and row
+  static constexpr int NT = D / 8;                      // column blocks of O
+  static constexpr int QR = D / 8;                      // registers of one query row's fragments
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, bool bf) {
+  if (bf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t half2_of(uint32_t e4m3x2) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A place in the global order of tiles: tile kt of (b, h), whose nt tiles hold L rows.
+struct Cursor {
+  int b, h, kt, nt, L;
+};
+
+template <typename Prefix>
+__device__ __forceinline__ void seek(Cursor &u, const Prefix &tp, const int *Ls, int B, int Hkv, int t) {
+  // the last sequence whose first tile is at or before t (skips empty ones)
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)tp[mid] * Hkv <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  u.b = lo;
+  u.nt = tp[lo + 1] - tp[lo];
+  const int r = t - tp[lo] * Hkv;
+  u.h = r / u.nt;
+  u.kt = r - u.h * u.nt;
+  u.L = Ls[lo];
+}
+
+__device__ __forceinline__ void step(Cursor &u, const int *Ls, int B, int Hkv) {
+  if (++u.kt < u.nt) return;
+  u.kt = 0;
+  if (++u.h < Hkv) return;
+  u.h = 0;
+  while (++u.b < B && Ls[u.b] == 0) {
+  }
+  if (u.b < B) {
+    u.L = Ls[u.b];
+    u.nt = (u.L + kTile - 1) / kTile;
   }
 }
 
-// One CTA per (KV head, sequence), one query head after the other: each warp
-// takes every eighth key with a running maximum and sum, the warps' parts are
-// joined in shared memory.
-template <int TYPE, int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const KvDev c, const DecodeArgs a) {
-  constexpr int N = D / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int L = c.L[b];
-  if (L < 0 || L > c.cap) {
-    if (h == 0 && threadIdx.x == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
-    L = 0;
+// Swizzles of the 16-byte pieces of row r, so that the fragment reads below
+// meet no bank conflict (8-bit rows of 64 bytes: two-way ones on V).
+template <int CPR>
+__device__ __forceinline__ int swz_k(int r, int ch) {
+  return CPR >= 8 ? ch ^ ((r & 1) << 2) : ch;
+}
+template <int CPR>
+__device__ __forceinline__ int swz_v(int r, int ch) {
+  return CPR >= 8 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3);
+}
+
+template <int TYPE, int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const DecodeArgs a) {
+  using S = Shape<TYPE, D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  // lengths and, for one head, the tiles before each sequence
+  int mine[kMaxB / kThreads], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxB / kThreads; ++i) {
+    const int b = threadIdx.x * (kMaxB / kThreads) + i;
+    int L = b < c.B ? c.L[b] : 0;
+    if (L < 0 || L > c.cap) {
+      if (blockIdx.x == 0 && blockIdx.y == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
+      L = 0;
+    }
+    Ls[b] = L;
+    mine[i] = sum;
+    sum += (L + kTile - 1) / kTile;
   }
-  const float ks = TYPE == TR_KV_E4M3 ? __ldg(c.k_scale + h) : 1.f, vs = TYPE == TR_KV_E4M3 ? __ldg(c.v_scale + h) : 1.f;
-  constexpr int ESZ = TYPE == TR_KV_E4M3 ? 1 : 2;
-  constexpr int QT = TYPE == TR_KV_F16 ? TR_KV_F16 : TR_KV_BF16;
-  for (int g = 0; g < a.G; ++g) {
-    const long long row = (long long)b * a.Hq + h * a.G + g;
-    float q[N], o[N] = {}, m = -INFINITY, l = 0.f;
-    load_row<QT, N>((const char *)a.Q + (row * D + lane * N) * 2, q);
-    for (int p = warp; p < L; p += kWarps) {
-      const long long blk = kv_block(c, b, p);
-      if (blk < 0) {
-        if (lane == 0) tr_flag(a.status, TR_DEV_BAD_PAGE);
-        continue;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int before = incl - sum;
+  for (int w = 0; w < warp; ++w) before += wsum[w];
+#pragma unroll
+  for (int i = 0; i < kMaxB / kThreads; ++i) tp[threadIdx.x * (kMaxB / kThreads) + i] = before + mine[i];
+  if (threadIdx.x == kThreads - 1) tp[kMaxB] = before + sum;
+  __syncthreads();
+  const int T = tp[c.B] * c.Hkv, W = gridDim.x * kWarps;
+  const int per = max((T + W - 1) / W, kMinTiles);
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i <= c.B; i += kThreads) {
+      a.plan[1 + i] = tp[i];
+      if (i == 0) a.plan[0] = per;
+    }
+  // sequences without rows belong to no warp's range
+  if (blockIdx.y == 0)
+    for (int b = blockIdx.x; b < c.B; b += gridDim.x)
+      if (Ls[b] == 0)
+        for (int i = threadIdx.x; i < a.Hq * D; i += kThreads) {
+          a.O[(long long)b * a.Hq * D + i] = 0.f;
+          if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+        }
+
+  const int w = warp * gridDim.x + blockIdx.x;
+  const long long first = (long long)w * per;
+  if (first >= T) return;
+  const int t0 = (int)first, t1 = (int)min((long long)T, first + per);
+  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+  const int row0 = blockIdx.y * MT;  // first query head of this row tile inside its group
+
+  Cursor ld, cur;
+  seek(ld, tp, Ls, c.B, c.Hkv, t0);
+  cur = ld;
+  int t_ld = t0;
+
+  auto issue = [&](int stage) {
+    if (t_ld < t1) {
+      const uint32_t dk = ring + stage * S::STAGE, dv = dk + kTile * S::ROW;
+      const int p0 = ld.kt * kTile, ch = lane % S::CPR;
+      const long long head = (long long)ld.h * c.head_stride + ch * 16;
+      const bool whole = !c.page_table || c.page_log2 >= 4;  // the tile lies in one page
+      long long blk = kv_block(c, ld.b, p0);
+#pragma unroll
+      for (int i = 0; i < S::CPR / 2; ++i) {
+        const int r = lane / S::CPR + i * (32 / S::CPR), p = p0 + r;
+        bool valid = p < ld.L;
+        if (!whole && valid) blk = kv_block(c, ld.b, p);
+        if (blk < 0) {
+          if (valid) tr_flag(a.status, TR_DEV_BAD_PAGE);
+          valid = false;
+        }
+        const long long at = valid ? blk + head + kv_row(c, p) : 0;
+        copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
+        copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at, valid);
       }
-      const long long at = blk + (long long)h * c.head_stride + kv_row(c, p) + lane * N * ESZ;
-      float k[N], v[N], s = 0.f;
-      load_row<TYPE, N>(c.K + at, k);
-      load_row<TYPE, N>(c.V + at, v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s += q[i] * k[i];
-      for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(~0u, s, off);
-      s *= a.scale_log2 * ks;
-      if (a.accumulate && lane == 0) a.s[row * a.s_ld + p] = s;
-      const float mn = fmaxf(m, s);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-      l = l * f + w;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * f + w * v[i];
-      m = mn;
+      step(ld, Ls, c.B, c.Hkv);
+      ++t_ld;
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
+    copy_commit();
+  };
+  for (int i = 0; i < S::STAGES - 1; ++i) issue(i);
+
+  constexpr int R = MT / 8;                           // query rows of a lane: g, g + 8
+  constexpr float kOff = S::BF ? 0.f : 7.f;           // fp16 weights run up to 2^15
+  uint32_t q[R][S::QR];
+  float mul[R], m[R], l[R], o[S::NT][4];
+  int kt0 = 0;
+
+  for (int i = t0; i < t1; ++i) {
+    const int stage = (i - t0) % S::STAGES;
+    if (i == t0 || cur.kt == 0) {
+      // a new pair: its queries, empty sums
+      kt0 = cur.kt;
 #pragma unroll
-    for (int i = 0; i < N; ++i) so[warp][lane * N + i] = o[i];
-    __syncthreads();
-    float M = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < kWarps; ++w) sum += sm[w] == -INFINITY ? 0.f : sl[w] * exp2f(sm[w] - M);
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-      float x = 0.f;
-      for (int w = 0; w < kWarps; ++w) x += sm[w] == -INFINITY ? 0.f : so[w][d] * exp2f(sm[w] - M);
-      a.O[row * D + d] = sum > 0.f ? x / sum * vs : 0.f;
+      for (int r = 0; r < R; ++r) {
+        const int m_row = row0 + g + r * 8;
+        const bool valid = m_row < a.G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.Q) +
+                           ((long long)cur.b * a.Hq + (long long)cur.h * a.G + m_row) * (D / 8);
+        mul[r] = a.scale_log2;
+        if constexpr (S::F8) {
+          // a lane's pieces are 16 elements; narrowed to fp16 after scaling the head's largest to 2^14
+          float amax = 0.f;
+#pragma unroll
+          for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint4 x = valid ? __ldg(src + (4 * s + t) * 2 + j) : make_uint4(0, 0, 0, 0);
+              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                q[r][s * 8 + j * 4 + e] = y[e];
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(y[e] << 16)), fabsf(__uint_as_float(y[e] & 0xFFFF0000u))));
+              }
+            }
+          amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+          const int up = amax > 0.f ? 14 - ilogbf(amax) : 0;
+#pragma unroll
+          for (int e = 0; e < S::QR; ++e)
+            q[r][e] = pack_half2(scalbnf(__uint_as_float(q[r][e] << 16), up),
+                                 scalbnf(__uint_as_float(q[r][e] & 0xFFFF0000u), up));
+          mul[r] = scalbnf(a.scale_log2 * __ldg(c.k_scale + cur.h), -up);
+        } else {
+#pragma unroll
+          for (int s = 0; s < D / 32; ++s) {
+            const uint4 x = valid ? __ldg(src + 4 * s + t) : make_uint4(0, 0, 0, 0);
+            q[r][s * 4] = x.x;
+            q[r][s * 4 + 1] = x.y;
+            q[r][s * 4 + 2] = x.z;
+            q[r][s * 4 + 3] = x.w;
+          }
+        }
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     }
-    const float lse2 = sum > 0.f ? M + log2f(sum) : -INFINITY;
-    if (a.lse && threadIdx.x == 0) a.lse[row] = lse2 * kLn2;
-    if (a.accumulate)
-      for (int p = threadIdx.x; p < L; p += kWarps * 32)
-        if (kv_block(c, b, p) >= 0)
-          c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] += exp2f(a.s[row * a.s_ld + p] - lse2);
-    __syncthreads();
+
+    copy_wait<S::STAGES - 2>();
+    __syncwarp();
+    issue((i - t0 + S::STAGES - 1) % S::STAGES);  // the stage read in the previous turn
+    const uint32_t sk = ring + stage * S::STAGE, sv = sk + kTile * S::ROW;
+
+    // S = Q K^T: columns j * 8 + n are the tile's rows
+    float s[2][4] = {};
+#pragma unroll
+    for (int e = 0; e < S::CPR / 4; ++e)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = j * 8 + g;
+        const uint4 x = lds16(sk + r * S::ROW + swz_k<S::CPR>(r, e * 4 + t) * 16);
+        if constexpr (S::F8) {
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int at = e * 8 + f * 2;
+            mma(s[j], q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u,
+                half2_of(y[f] & 0xFFFFu), half2_of(y[f] >> 16), false);
+          }
+        } else {
+          const int at = e * 4;
+          mma(s[j], q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u, x.x, x.y, S::BF);
+          mma(s[j], q[0][at + 2], R > 1 ? q[R - 1][at + 2] : 0u, q[0][at + 3], R > 1 ? q[R - 1][at + 3] : 0u, x.z, x.w,
+              S::BF);
+        }
+      }
+
+    // logits in log2 units; rows behind the last get none
+    const int p0 = cur.kt * kTile, rows = cur.L - p0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) s[j][2 * r + e] = j * 8 + 2 * t + e < rows ? s[j][2 * r + e] * mul[r] : -INFINITY;
+      if (a.accumulate && row0 + g + r * 8 < a.G) {
+        float *dst = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + row0 + g + r * 8) * a.s_ld + p0 + 2 * t;
+        *reinterpret_cast<float2 *>(dst) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
+        *reinterpret_cast<float2 *>(dst + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+      }
+      float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+      const bool grow = mx > m[r] + (kOff + kLazy);
+      if (__any_sync(~0u, grow)) {
+        const float mn = grow ? mx - kOff : m[r];
+        const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f;
+#pragma unroll
+        for (int n = 0; n < S::NT; ++n) {
+          if constexpr (R == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] *= f;
+          } else {
+            o[n][2 * r] *= f;
+            o[n][2 * r + 1] *= f;
+          }
+        }
+      }
+      const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[j][2 * r + e] = ex2(s[j][2 * r + e] - base);
+          l[r] += s[j][2 * r + e];
+        }
+    }
+
+    // P in parts: pt[part][r][j] holds rows 2t, 2t + 1 of half j for query row g + 8 r
+    constexpr int kParts = S::BF ? 3 : 2;
+    uint32_t pt[kParts][R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = s[j][2 * r], y = s[j][2 * r + 1];
+        if constexpr (S::BF) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            pt[k][r][j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+            if (k < 2) {
+              x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+              y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+            }
+          }
+        } else {
+          pt[0][r][j] = pack_half2(x, y);
+          const __half2 h = *reinterpret_cast<const __half2 *>(&pt[0][r][j]);
+          pt[1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
+        }
+      }
+    auto pv = [&](float(&acc)[4], uint32_t b0, uint32_t b1) {
+      if constexpr (R == 1) {
+        mma(acc, pt[0][0][0], pt[1][0][0], pt[0][0][1], pt[1][0][1], b0, b1, S::BF);
+        if constexpr (S::BF) mma(acc, pt[kParts - 1][0][0], 0u, pt[kParts - 1][0][1], 0u, b0, b1, true);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+          mma(acc, pt[k][0][0], pt[k][R - 1][0], pt[k][0][1], pt[k][R - 1][1], b0, b1, S::BF);
+      }
+    };
+    // O += P V: column block n = VW * s + e holds columns (lane / 4 + 8 s) * VW + e
+#pragma unroll
+    for (int v = 0; v < S::VS; ++v) {
+      constexpr int NW = S::F8 ? S::VW / 4 : S::VW / 2;  // words of a piece
+      uint32_t x[4][NW];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 2 * t + (k & 1) + (k >> 1) * 8;
+        if constexpr (NW == 4) {
+          const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR>(r, g + 8 * v) * 16);
+          x[k][0] = y.x;
+          x[k][1] = y.y;
+          x[k][2] = y.z;
+          x[k][3] = y.w;
+        } else {
+          const uint2 y = lds8(sv + r * S::ROW + swz_v<S::CPR>(r, g >> 1) * 16 + (g & 1) * 8);
+          x[k][0] = y.x;
+          x[k][1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < NW; ++e) {
+        if constexpr (S::F8) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t sel = f ? 0x7362 : 0x5140;
+            const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
+            pv(o[v * S::VW + e * 4 + f * 2], half2_of(lo & 0xFFFFu), half2_of(hi & 0xFFFFu));
+            pv(o[v * S::VW + e * 4 + f * 2 + 1], half2_of(lo >> 16), half2_of(hi >> 16));
+          }
+        } else {
+          pv(o[v * S::VW + e * 2], __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
+          pv(o[v * S::VW + e * 2 + 1], __byte_perm(x[0][e], x[1][e], 0x7632), __byte_perm(x[2][e], x[3][e], 0x7632));
+        }
+      }
+    }
+
+    if (cur.kt == cur.nt - 1 || i == t1 - 1) {
+      // the range leaves this pair: the result, or a partial
+      const bool whole = kt0 == 0 && cur.kt == cur.nt - 1;
+      const long long slot = ((long long)blockIdx.y * W + w) * 2 + (kt0 > 0 ? 0 : 1);
+      const float vs = S::F8 ? __ldg(c.v_scale + cur.h) : 1.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        l[r] += __shfl_xor_sync(~0u, l[r], 1);
+        l[r] += __shfl_xor_sync(~0u, l[r], 2);
+        const int row = g + r * 8;
+        if (row0 + row >= a.G) continue;
+        const long long hq = (long long)cur.b * a.Hq + (long long)cur.h * a.G + row0 + row;
+        const float f = whole ? vs / l[r] : 1.f;
+        float *dst = whole ? a.O + hq * D : a.part_o + (slot * MT + row) * D;
+        if (t == 0) {
+          if (whole) {
+            const float x = m[r] + log2f(l[r]);
+            if (a.lse) a.lse[hq] = x * kLn2;
+            a.lse2[hq] = x;
+          } else {
+            a.part_ml[slot * MT + row] = make_float2(m[r], l[r]);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < S::VS; ++v)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < S::VW; e += 4) {
+              float y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float *z = o[v * S::VW + e + k];
+                y[k] = (R == 1 ? z[n] + z[n + 2] : z[2 * r + n]) * f;
+              }
+              *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+      }
+    }
+    step(cur, Ls, c.B, c.Hkv);
   }
+}
+
+// Which warps hold parts of pair (b, h): parts w0 .. w1, the first in slot 1
+// of its warp (the pair starts inside that range), the others in slot 0.
+struct Parts {
+  int w0, w1, L;
+};
+__device__ __forceinline__ Parts parts_of(const KvDev &c, const DecodeArgs &a, int b, int h) {
+  const int per = a.plan[0], p0 = a.plan[1 + b], nt = a.plan[2 + b] - p0;
+  Parts r;
+  r.L = nt;
+  const long long first = (long long)p0 * c.Hkv + (long long)h * nt;
+  r.w0 = (int)(first / per);
+  r.w1 = (int)((first + nt - 1) / per);
+  return r;
+}
+
+constexpr int kFinThreads = 128;
+constexpr int kFinWarps = kFinThreads / 32;
+constexpr int kScoreRows = 1024;  // rows of one CTA when weights are gathered
+
+// (maximum, sum) of the parts of query head m of a pair, the same in every thread.
+__device__ __forceinline__ float2 join_ml(const DecodeArgs &a, const Parts &u, long long W, int MT, int m,
+                                          float2 *sh) {
+  const long long base = (long long)(m / MT) * W;
+  const int row = m % MT, lane = threadIdx.x & 31;
+  auto at = [&](int w) { return a.part_ml[((base + w) * 2 + (w == u.w0)) * MT + row]; };
+  float M = -INFINITY, sum = 0.f;
+  for (int w = u.w0 + threadIdx.x; w <= u.w1; w += kFinThreads) M = fmaxf(M, at(w).x);
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+  if (lane == 0) sh[threadIdx.x >> 5].x = M;
+  __syncthreads();
+  for (int i = 0; i < kFinWarps; ++i) M = fmaxf(M, sh[i].x);
+  for (int w = u.w0 + threadIdx.x; w <= u.w1; w += kFinThreads) {
+    const float2 x = at(w);
+    sum += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (lane == 0) sh[threadIdx.x >> 5].y = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int i = 0; i < kFinWarps; ++i) sum += sh[i].y;
+  __syncthreads();
+  return make_float2(M, sum);
+}
+
+// Blocks [0, B * Hq): join the partials of one query head.  The blocks behind
+// them (accumulate): add the weights of kScoreRows rows of a pair to its scores.
+template <int D>
+__global__ void __launch_bounds__(kFinThreads) finish_kernel(const KvDev c, const DecodeArgs a, int W, int MT,
+                                                             int score_blocks) {
+  __shared__ float2 sh[kFinWarps];
+  __shared__ float4 acc[kFinWarps][D / 4];
+  const int joins = c.B * a.Hq, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x < joins) {
+    const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
+    const Parts u = parts_of(c, a, b, h);
+    if (u.L == 0 || u.w0 == u.w1) return;  // empty, or finished by one warp
+    const float2 ml = join_ml(a, u, W, MT, m, sh);
+    const long long base = (long long)(m / MT) * W;
+    const int row = m % MT;
+    constexpr int kPer = 128 / D;  // partials of a warp side by side (d = 64: two)
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = u.w0 + warp * kPer + lane / (D / 4); w <= u.w1; w += kFinWarps * kPer) {
+      const long long slot = ((base + w) * 2 + (w == u.w0)) * MT + row;
+      const float pm = a.part_ml[slot].x, f = pm == -INFINITY ? 0.f : ex2(pm - ml.x);
+      const float4 y = *reinterpret_cast<const float4 *>(a.part_o + slot * D + (lane % (D / 4)) * 4);
+      x.x += y.x * f;
+      x.y += y.y * f;
+      x.z += y.z * f;
+      x.w += y.w * f;
+    }
+    if constexpr (kPer == 2) {
+      x.x += __shfl_xor_sync(~0u, x.x, 16);
+      x.y += __shfl_xor_sync(~0u, x.y, 16);
+      x.z += __shfl_xor_sync(~0u, x.z, 16);
+      x.w += __shfl_xor_sync(~0u, x.w, 16);
+    }
+    if (lane < D / 4) acc[warp][lane] = x;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+      float4 y = acc[0][threadIdx.x];
+      for (int i = 1; i < kFinWarps; ++i) {
+        y.x += acc[i][threadIdx.x].x;
+        y.y += acc[i][threadIdx.x].y;
+        y.z += acc[i][threadIdx.x].z;
+        y.w += acc[i][threadIdx.x].w;
+      }
+      const float f = (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / ml.y;
+      *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
+          make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = (ml.x + log2f(ml.y)) * kLn2;
+    return;
+  }
+  const int k = blockIdx.x - joins, chunk = k % score_blocks, pair = k / score_blocks;
+  const int h = pair % c.Hkv, b = pair / c.Hkv;
+  int L = c.L[b];
+  if (L < 0 || L > c.cap) L = 0;
+  const int p0 = chunk * kScoreRows, n = min(L - p0, kScoreRows);
+  if (n <= 0) return;
+  const Parts u = parts_of(c, a, b, h);
+  constexpr int kRows = kScoreRows / kFinThreads;
+  float w[kRows] = {};
+  for (int m = 0; m < a.G; ++m) {
+    const long long hq = (long long)b * a.Hq + (long long)h * a.G + m;
+    float lse2;
+    if (u.w0 == u.w1) {
+      lse2 = a.lse2[hq];
+    } else {
+      const float2 ml = join_ml(a, u, W, MT, m, sh);
+      lse2 = ml.x + log2f(ml.y);
+    }
+    const float *src = a.s + hq * a.s_ld + p0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int p = i * kFinThreads + threadIdx.x;
+      if (p < n) w[i] += ex2(src[p] - lse2);
+    }
+  }
+  float *dst = c.scores + (long long)pair * c.scores_ld + p0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int p = i * kFinThreads + threadIdx.x;
+    if (p < n) dst[p] += w[i];
+  }
+}
+
+// Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
+struct Plan {
+  int MT, row_tiles, grid;  // grid: CTAs per row tile
+  size_t ml_off, lse_off, plan_off, s_off, total;
+};
+
+Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
+  Plan p;
+  const int G = Hq / c.Hkv;
+  p.MT = G <= 8 ? 8 : 16;
+  p.row_tiles = (G + p.MT - 1) / p.MT;
+  const long long tiles = (long long)c.B * c.Hkv * ((c.cap + kTile - 1) / kTile);
+  p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, (tiles + kMinTiles - 1) / kMinTiles));
+  const size_t rows = (size_t)p.row_tiles * p.grid * kWarps * 2 * p.MT;
+  p.ml_off = tr_align_up(rows * d * 4, 256);
+  p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
+  p.plan_off = p.lse_off + tr_align_up((size_t)c.B * Hq * 4, 256);
+  p.s_off = p.plan_off + tr_align_up((size_t)(c.B + 2) * 4, 256);
+  p.total = p.s_off + (accumulate ? (size_t)c.B * Hq * tr_align_up(c.cap, kTile) * 4 : 0);
+  return p;
+}
+
+template <int TYPE, int D, int MT>
+int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
+  constexpr int bytes = kWarps * kRingBytes;
+  TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  split_kernel<TYPE, D, MT><<<grid, kThreads, bytes, s>>>(c, a);
+  TR_LAUNCH_CHECK();
+  return TR_OK;
+}
+
+template <int TYPE, int D>
+int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
+  const dim3 grid(p.grid, p.row_tiles);
+  const int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
+  if (rc != TR_OK) return rc;
+  const int score_blocks = a.accumulate ? (c.cap + kScoreRows - 1) / kScoreRows : 0;
+  const long long blocks = (long long)c.B * a.Hq + (long long)c.B * c.Hkv * score_blocks;
+  finish_kernel<D><<<(unsigned)blocks, kFinThreads, 0, s>>>(c, a, p.grid * kWarps, p.MT, score_blocks);
+  TR_LAUNCH_CHECK();
+  return TR_OK;
 }
 
 template <int TYPE>
-void launch(int d, dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
-  if (d == 64)
-    decode_kernel<TYPE, 64><<<grid, kWarps * 32, 0, s>>>(c, a);
-  else
-    decode_kernel<TYPE, 128><<<grid, kWarps * 32, 0, s>>>(c, a);
+int launch(int d, const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
+  return d == 64 ? launch<TYPE, 64>(p, s, c, a) : launch<TYPE, 128>(p, s, c, a);
+}
+
+// Launch grids and offsets hold B * Hq in 31 bits (the cache's own limits bound the rest).
+bool fits(const KvDev &c, int Hq) {
+  return (long long)c.B * Hq + (long long)c.B * c.Hkv * ((c.cap + kScoreRows - 1) / kScoreRows) < (1LL << 31) &&
+         Hq / c.Hkv <= 65535 * 8;
 }
 
 }  // namespace
 
 extern "C" size_t tr_decode_attn_workspace_bytes(const tr_kv_cache *cache, int Hq, int accumulate) {
   KvDev c;
-  if (kv_check(cache, &c) != TR_OK || Hq < 1 || Hq % c.Hkv) return 0;
-  return accumulate ? (size_t)c.B * Hq * tr_align_up(c.cap, 16) * 4 : 256;
+  if (kv_check(cache, &c) != TR_OK || Hq < 1 || Hq % c.Hkv || !fits(c, Hq)) return 0;
+  return make_plan(c, Hq, cache->d, accumulate).total;
 }
 
 extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, float scale, float *O, float *lse,
@@ -131,29 +700,28 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   if (!Q || !O || Hq < 1 || Hq % c.Hkv || !(scale > 0.f) || !(scale < INFINITY)) return TR_E_INVAL;
   if ((((uintptr_t)Q | (uintptr_t)O) & 15) || ((uintptr_t)lse & 3)) return TR_E_INVAL;
   if (accumulate && !c.scores) return TR_E_INVAL;
-  if (!ws || ((uintptr_t)ws & 15) || ws_bytes < tr_decode_attn_workspace_bytes(cache, Hq, accumulate))
-    return TR_E_INVAL;
+  if (!fits(c, Hq)) return TR_E_UNSUPPORTED;
+  const Plan p = make_plan(c, Hq, cache->d, accumulate);
+  if (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.total) return TR_E_INVAL;
   rc = tr_check_device();
   if (rc != TR_OK) return rc;
   DecodeArgs a;
   a.Q = Q;
   a.O = O;
   a.lse = lse;
-  a.s = (float *)ws;
-  a.s_ld = (long long)tr_align_up(c.cap, 16);
+  a.part_o = (float *)ws;
+  a.part_ml = (float2 *)((char *)ws + p.ml_off);
+  a.lse2 = (float *)((char *)ws + p.lse_off);
+  a.plan = (int *)((char *)ws + p.plan_off);
+  a.s = (float *)((char *)ws + p.s_off);
+  a.s_ld = (long long)tr_align_up(c.cap, kTile);
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
-  a.accumulate = accumulate;
+  a.accumulate = accumulate != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = tr_status_dev();
-  const dim3 grid(c.Hkv, c.B);
   cudaStream_t s = (cudaStream_t)stream;
-  if (cache->type == TR_KV_BF16)
-    launch<TR_KV_BF16>(cache->d, grid, s, c, a);
-  else if (cache->type == TR_KV_F16)
-    launch<TR_KV_F16>(cache->d, grid, s, c, a);
-  else
-    launch<TR_KV_E4M3>(cache->d, grid, s, c, a);
-  TR_LAUNCH_CHECK();
-  return TR_OK;
+  if (cache->type == TR_KV_BF16) return launch<TR_KV_BF16>(cache->d, p, s, c, a);
+  if (cache->type == TR_KV_F16) return launch<TR_KV_F16>(cache->d, p, s, c, a);
+  return launch<TR_KV_E4M3>(cache->d, p, s, c, a);
 }
