@@ -5,18 +5,19 @@
 // needed once and used for the few query heads of its group, so the cache's
 // bytes bound the work (1 flop per byte for one head per group, 2 G in general).
 //
-// Split.  A pair is (sequence, KV head) with ceil(L / 16) tiles of 16 rows.  All
-// pairs' tiles are laid end to end and cut into equal ranges, one per WARP of
-// a one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
-// shared memory (cp.async) and meets no barrier on the way, whatever the mix of lengths.
-// Warps are numbered across CTAs first, so little work still spreads over
-// every SM.  A pair that lies inside one range is finished by its warp; the
-// others leave (m, l, O) partials, two slots per warp at most, that
-// finish_kernel joins in a fixed order.
+// Split.  A pair is (sequence, KV head) with ceil(L / kTile) tiles.  All pairs'
+// tiles are laid end to end and cut into equal ranges, one per WARP of a
+// one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
+// shared memory (cp.async) and meets no barrier on the way, whatever the mix of
+// lengths.  With little work only as many warps of each CTA take part as leave
+// each about kMinRows rows, so that it spreads over every SM.  A pair that lies
+// inside one range is finished by its warp.  When a CTA's whole range lies in
+// one pair its warps' sums are joined in shared memory first.  What
+// remains are (m, l, O) partials, which join_kernel joins in a fixed order.
 //
 // Tile.  S = Q K^T with m16n8k16 matrix instructions: the group's query heads
-// are the 16 rows (8 of them empty when the group has at most 8 heads), 16
-// cached rows are two columns blocks.  The contraction runs over d in an order of
+// are the 16 rows (8 of them empty when the group has at most 8 heads), cached
+// rows are the columns.  The contraction runs over d in an order of
 // its own: a lane's 16-byte piece of a row of K is used as the B fragments of
 // two (8-bit: four) instructions, and Q is loaded in the same order, so that K needs no
 // transposing load.  The accumulators of S are laid out as the A fragments of
@@ -47,9 +48,8 @@ using sm100::smem_u32;
 constexpr int kMaxB = 1024;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;               // cached rows per tile
 constexpr int kRingBytes = 24 * 1024;   // per warp
-constexpr int kMinTiles = 2;            // tiles of a warp's range, at least
+constexpr int kMinRows = 32;            // cached rows of a warp's range, about, at least
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;            // the running maximum follows once it is 2^8 behind
 
@@ -58,9 +58,9 @@ struct DecodeArgs {
   float *O, *lse;
   float *part_o;     // [row tiles][warps][2][MT][d]
   float2 *part_ml;   // [row tiles][warps][2][MT] (reference maximum, sum), log2 units
-  float *lse2;       // [B, Hq] log2 of the softmax denominator of pairs finished by one warp
+  float *lse2;       // [B, Hq] log2 of the softmax denominators
   float *s;          // [B, Hq, s_ld] logits, log2 units (accumulate)
-  int *plan;         // [0] tiles per warp, [1 + b] tiles of one head before sequence b
+  int *plan;         // tiles per warp, warps per CTA, then for each sequence the tiles of one head before it
   long long s_ld;
   int Hq, G, accumulate;
   float scale_log2;
@@ -73,6 +73,10 @@ struct Shape {
   static constexpr bool BF = TYPE == TR_KV_BF16;
   static constexpr int ROW = D * (F8 ? 1 : 2);          // bytes
   static constexpr int CPR = ROW / 16;                  // 16-byte pieces of a row
+  // cached rows per tile: 16 (one contraction step of P V), or 32 of the shorter rows, so
+  // that a tile's chain of dependent steps is paid once per 4 KB or more
+  static constexpr int KB = ROW == 256 ? 1 : 2;
+  static constexpr int kTile = 16 * KB;
   static constexpr int STAGE = 2 * kTile * ROW;         // K tile, V tile
   static constexpr int STAGES = kRingBytes / STAGE;
   static constexpr int VW = F8 && D == 128 ? 16 : 8;    // columns of a lane's piece of V
@@ -145,6 +149,7 @@ __device__ __forceinline__ void seek(Cursor &u, const Prefix &tp, const int *Ls,
   u.L = Ls[lo];
 }
 
+template <int kTile>
 __device__ __forceinline__ void step(Cursor &u, const int *Ls, int B, int Hkv) {
   if (++u.kt < u.nt) return;
   u.kt = 0;
@@ -169,11 +174,25 @@ __device__ __forceinline__ int swz_v(int r, int ch) {
   return CPR >= 8 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3);
 }
 
+// The warps that a range of pairs is cut for, from the tiles' number alone.
+struct Cut {
+  int warps, per;  // per CTA, tiles per warp
+};
+__device__ __forceinline__ Cut cut_of(int T, int ctas, int kTile) {
+  const int min_tiles = max(kMinRows / kTile, 1);
+  Cut c;
+  c.warps = min(max((T + ctas * min_tiles - 1) / (ctas * min_tiles), 1), kWarps);
+  c.per = max((T + ctas * c.warps - 1) / (ctas * c.warps), 1);
+  return c;
+}
+
 template <int TYPE, int D, int MT>
 __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const DecodeArgs a) {
   using S = Shape<TYPE, D>;
+  constexpr int kTile = S::kTile, KB = S::KB;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
+  __shared__ float2 jml[kWarps][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   // lengths and, for one head, the tiles before each sequence
@@ -204,13 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
   for (int i = 0; i < kMaxB / kThreads; ++i) tp[threadIdx.x * (kMaxB / kThreads) + i] = before + mine[i];
   if (threadIdx.x == kThreads - 1) tp[kMaxB] = before + sum;
   __syncthreads();
-  const int T = tp[c.B] * c.Hkv, W = gridDim.x * kWarps;
-  const int per = max((T + W - 1) / W, kMinTiles);
+  const int T = tp[c.B] * c.Hkv;
+  const Cut cut = cut_of(T, gridDim.x, kTile);
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i <= c.B; i += kThreads) {
-      a.plan[1 + i] = tp[i];
-      if (i == 0) a.plan[0] = per;
-    }
+    for (int i = threadIdx.x; i <= c.B + 2; i += kThreads) a.plan[i] = i == 0 ? cut.per : i == 1 ? cut.warps : tp[i - 2];
   // sequences without rows belong to no warp's range
   if (blockIdx.y == 0)
     for (int b = blockIdx.x; b < c.B; b += gridDim.x)
@@ -220,40 +236,73 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
           if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
         }
 
-  const int w = warp * gridDim.x + blockIdx.x;
-  const long long first = (long long)w * per;
-  if (first >= T) return;
-  const int t0 = (int)first, t1 = (int)min((long long)T, first + per);
+  const long long c0 = (long long)blockIdx.x * cut.warps * cut.per;  // the CTA's range
+  if (c0 >= T) return;
+  const int c1 = (int)min((long long)T, c0 + (long long)cut.warps * cut.per);
+  const int w = blockIdx.x * cut.warps + warp;
+  const int t0 = warp < cut.warps ? (int)min((long long)c1, c0 + (long long)warp * cut.per) : c1;
+  const int t1 = warp < cut.warps ? min(c1, t0 + cut.per) : c1;
   const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
   const int row0 = blockIdx.y * MT;  // first query head of this row tile inside its group
 
-  Cursor ld, cur;
-  seek(ld, tp, Ls, c.B, c.Hkv, t0);
-  cur = ld;
+  // the pair of the CTA's first tile; joined: it takes the CTA's whole range
+  Cursor cur, ld;
+  seek(cur, tp, Ls, c.B, c.Hkv, (int)c0);
+  const bool joined = cut.warps > 1 && c1 - (int)c0 <= cur.nt - cur.kt;
+  const Cursor pair = cur;
+  if (t0 >= t1 && !joined) return;
+  if (t0 < t1) seek(cur, tp, Ls, c.B, c.Hkv, t0);
+  ld = cur;
   int t_ld = t0;
 
+  // the page of row `lane` of the next tile to load, looked up a tile ahead of its use
+  auto page_of = [&]() {
+    const int p = ld.kt * kTile + lane;
+    return !c.page_table ? ld.b
+           : t_ld < t1 && lane < kTile && p < ld.L ? __ldg(c.page_table + (long long)ld.b * c.max_pages + (p >> c.page_log2))
+                                                   : 0;
+  };
+  int page = page_of();
+  const int blocks = c.page_table ? c.num_pages : c.B;
+  const bool whole_tile = !c.page_table || (1 << c.page_log2) >= kTile;  // a tile lies in one page
   auto issue = [&](int stage) {
     if (t_ld < t1) {
       const uint32_t dk = ring + stage * S::STAGE, dv = dk + kTile * S::ROW;
       const int p0 = ld.kt * kTile, ch = lane % S::CPR;
       const long long head = (long long)ld.h * c.head_stride + ch * 16;
-      const bool whole = !c.page_table || c.page_log2 >= 4;  // the tile lies in one page
-      long long blk = kv_block(c, ld.b, p0);
+      if (whole_tile) {
+        const int pg = __shfl_sync(~0u, page, 0);
+        const bool good = (unsigned)pg < (unsigned)blocks;
+        if (!good) tr_flag(a.status, TR_DEV_BAD_PAGE);
+        const long long at = (long long)pg * c.block_stride + head + kv_row(c, p0 + lane / S::CPR);
+        const char *k = c.K + at, *v = c.V + at;
+        const int left = good ? ld.L - p0 : 0;
 #pragma unroll
-      for (int i = 0; i < S::CPR / 2; ++i) {
-        const int r = lane / S::CPR + i * (32 / S::CPR), p = p0 + r;
-        bool valid = p < ld.L;
-        if (!whole && valid) blk = kv_block(c, ld.b, p);
-        if (blk < 0) {
-          if (valid) tr_flag(a.status, TR_DEV_BAD_PAGE);
-          valid = false;
+        for (int i = 0; i < KB * S::CPR / 2; ++i) {
+          const int r = lane / S::CPR + i * (32 / S::CPR);
+          const bool valid = r < left;
+          const long long off = (long long)(i * (32 / S::CPR)) * c.row_stride;
+          copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, valid ? k + off : c.K, valid);
+          copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, valid ? v + off : c.V, valid);
         }
-        const long long at = valid ? blk + head + kv_row(c, p) : 0;
-        copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
-        copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at, valid);
+      } else {
+#pragma unroll
+        for (int i = 0; i < KB * S::CPR / 2; ++i) {
+          const int r = lane / S::CPR + i * (32 / S::CPR);
+          const int pg = __shfl_sync(~0u, page, r);
+          bool valid = p0 + r < ld.L;
+          if (valid && (unsigned)pg >= (unsigned)blocks) {
+            tr_flag(a.status, TR_DEV_BAD_PAGE);
+            valid = false;
+          }
+          const long long at = valid ? (long long)pg * c.block_stride + head + kv_row(c, p0 + r) : 0;
+          copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
+          copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at, valid);
+        }
       }
-      step(ld, Ls, c.B, c.Hkv);
+      step<kTile>(ld, Ls, c.B, c.Hkv);
       ++t_ld;
+      page = page_of();
     }
     copy_commit();
   };
@@ -264,6 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
   uint32_t q[R][S::QR];
   float mul[R], m[R], l[R], o[S::NT][4];
   int kt0 = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
 
   for (int i = t0; i < t1; ++i) {
     const int stage = (i - t0) % S::STAGES;
@@ -324,12 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
     issue((i - t0 + S::STAGES - 1) % S::STAGES);  // the stage read in the previous turn
     const uint32_t sk = ring + stage * S::STAGE, sv = sk + kTile * S::ROW;
 
-    // S = Q K^T: columns j * 8 + n are the tile's rows
-    float s[2][4] = {};
+    // S = Q K^T: column n of block j is row j * 8 + n of the tile
+    float s[2 * KB][4] = {};
 #pragma unroll
     for (int e = 0; e < S::CPR / 4; ++e)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2 * KB; ++j) {
         const int r = j * 8 + g;
         const uint4 x = lds16(sk + r * S::ROW + swz_k<S::CPR>(r, e * 4 + t) * 16);
         if constexpr (S::F8) {
@@ -352,16 +406,20 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
     const int p0 = cur.kt * kTile, rows = cur.L - p0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 * KB; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) s[j][2 * r + e] = j * 8 + 2 * t + e < rows ? s[j][2 * r + e] * mul[r] : -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          s[j][2 * r + e] = j * 8 + 2 * t + e < rows ? s[j][2 * r + e] * mul[r] : -INFINITY;
+          mx = fmaxf(mx, s[j][2 * r + e]);
+        }
       if (a.accumulate && row0 + g + r * 8 < a.G) {
         float *dst = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + row0 + g + r * 8) * a.s_ld + p0 + 2 * t;
-        *reinterpret_cast<float2 *>(dst) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
-        *reinterpret_cast<float2 *>(dst + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+#pragma unroll
+        for (int j = 0; j < 2 * KB; ++j)
+          *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(s[j][2 * r], s[j][2 * r + 1]);
       }
-      float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
       const bool grow = mx > m[r] + (kOff + kLazy);
@@ -383,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
       }
       const float base = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 * KB; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           s[j][2 * r + e] = ex2(s[j][2 * r + e] - base);
@@ -391,80 +449,83 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
         }
     }
 
-    // P in parts: pt[part][r][j] holds rows 2t, 2t + 1 of half j for query row g + 8 r
-    constexpr int kParts = S::BF ? 3 : 2;
-    uint32_t pt[kParts][R][2];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int kb = 0; kb < KB; ++kb) {
+      // P of 16 rows in parts: pt[part][r][j] holds rows 2t, 2t + 1 of half j for query row g + 8 r
+      constexpr int kParts = S::BF ? 3 : 2;
+      uint32_t pt[kParts][R][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x = s[j][2 * r], y = s[j][2 * r + 1];
-        if constexpr (S::BF) {
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            pt[k][r][j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-            if (k < 2) {
-              x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-              y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+        for (int j = 0; j < 2; ++j) {
+          float x = s[2 * kb + j][2 * r], y = s[2 * kb + j][2 * r + 1];
+          if constexpr (S::BF) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              pt[k][r][j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+              if (k < 2) {
+                x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+                y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+              }
             }
+          } else {
+            pt[0][r][j] = pack_half2(x, y);
+            const __half2 h = *reinterpret_cast<const __half2 *>(&pt[0][r][j]);
+            pt[1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
           }
-        } else {
-          pt[0][r][j] = pack_half2(x, y);
-          const __half2 h = *reinterpret_cast<const __half2 *>(&pt[0][r][j]);
-          pt[1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
         }
-      }
-    auto pv = [&](float(&acc)[4], uint32_t b0, uint32_t b1) {
-      if constexpr (R == 1) {
-        mma(acc, pt[0][0][0], pt[1][0][0], pt[0][0][1], pt[1][0][1], b0, b1, S::BF);
-        if constexpr (S::BF) mma(acc, pt[kParts - 1][0][0], 0u, pt[kParts - 1][0][1], 0u, b0, b1, true);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-          mma(acc, pt[k][0][0], pt[k][R - 1][0], pt[k][0][1], pt[k][R - 1][1], b0, b1, S::BF);
-      }
-    };
-    // O += P V: column block n = VW * s + e holds columns (lane / 4 + 8 s) * VW + e
-#pragma unroll
-    for (int v = 0; v < S::VS; ++v) {
-      constexpr int NW = S::F8 ? S::VW / 4 : S::VW / 2;  // words of a piece
-      uint32_t x[4][NW];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 2 * t + (k & 1) + (k >> 1) * 8;
-        if constexpr (NW == 4) {
-          const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR>(r, g + 8 * v) * 16);
-          x[k][0] = y.x;
-          x[k][1] = y.y;
-          x[k][2] = y.z;
-          x[k][3] = y.w;
+      auto pv = [&](float(&acc)[4], uint32_t b0, uint32_t b1) {
+        if constexpr (R == 1) {
+          mma(acc, pt[0][0][0], pt[1][0][0], pt[0][0][1], pt[1][0][1], b0, b1, S::BF);
+          if constexpr (S::BF) mma(acc, pt[kParts - 1][0][0], 0u, pt[kParts - 1][0][1], 0u, b0, b1, true);
         } else {
-          const uint2 y = lds8(sv + r * S::ROW + swz_v<S::CPR>(r, g >> 1) * 16 + (g & 1) * 8);
-          x[k][0] = y.x;
-          x[k][1] = y.y;
+#pragma unroll
+          for (int k = 0; k < kParts; ++k)
+            mma(acc, pt[k][0][0], pt[k][R - 1][0], pt[k][0][1], pt[k][R - 1][1], b0, b1, S::BF);
         }
-      }
+      };
+      // O += P V: column block n = VW * s + e holds columns (lane / 4 + 8 s) * VW + e
 #pragma unroll
-      for (int e = 0; e < NW; ++e) {
-        if constexpr (S::F8) {
+      for (int v = 0; v < S::VS; ++v) {
+        constexpr int NW = S::F8 ? S::VW / 4 : S::VW / 2;  // words of a piece
+        uint32_t x[4][NW];
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint32_t sel = f ? 0x7362 : 0x5140;
-            const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
-            pv(o[v * S::VW + e * 4 + f * 2], half2_of(lo & 0xFFFFu), half2_of(hi & 0xFFFFu));
-            pv(o[v * S::VW + e * 4 + f * 2 + 1], half2_of(lo >> 16), half2_of(hi >> 16));
+        for (int k = 0; k < 4; ++k) {
+          const int r = kb * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+          if constexpr (NW == 4) {
+            const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR>(r, g + 8 * v) * 16);
+            x[k][0] = y.x;
+            x[k][1] = y.y;
+            x[k][2] = y.z;
+            x[k][3] = y.w;
+          } else {
+            const uint2 y = lds8(sv + r * S::ROW + swz_v<S::CPR>(r, g >> 1) * 16 + (g & 1) * 8);
+            x[k][0] = y.x;
+            x[k][1] = y.y;
           }
-        } else {
-          pv(o[v * S::VW + e * 2], __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
-          pv(o[v * S::VW + e * 2 + 1], __byte_perm(x[0][e], x[1][e], 0x7632), __byte_perm(x[2][e], x[3][e], 0x7632));
+        }
+#pragma unroll
+        for (int e = 0; e < NW; ++e) {
+          if constexpr (S::F8) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t sel = f ? 0x7362 : 0x5140;
+              const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
+              pv(o[v * S::VW + e * 4 + f * 2], half2_of(lo & 0xFFFFu), half2_of(hi & 0xFFFFu));
+              pv(o[v * S::VW + e * 4 + f * 2 + 1], half2_of(lo >> 16), half2_of(hi >> 16));
+            }
+          } else {
+            pv(o[v * S::VW + e * 2], __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
+            pv(o[v * S::VW + e * 2 + 1], __byte_perm(x[0][e], x[1][e], 0x7632), __byte_perm(x[2][e], x[3][e], 0x7632));
+          }
         }
       }
     }
 
-    if (cur.kt == cur.nt - 1 || i == t1 - 1) {
+    if (!joined && (cur.kt == cur.nt - 1 || i == t1 - 1)) {
       // the range leaves this pair: the result, or a partial
       const bool whole = kt0 == 0 && cur.kt == cur.nt - 1;
-      const long long slot = ((long long)blockIdx.y * W + w) * 2 + (kt0 > 0 ? 0 : 1);
+      const long long slot = ((long long)blockIdx.y * gridDim.x * kWarps + w) * 2 + (kt0 > 0 ? 0 : 1);
       const float vs = S::F8 ? __ldg(c.v_scale + cur.h) : 1.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -500,134 +561,219 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
             }
       }
     }
-    step(cur, Ls, c.B, c.Hkv);
+    step<kTile>(cur, Ls, c.B, c.Hkv);
+  }
+  if (!joined) return;
+
+  // the CTA's warps hold parts of one pair: join them through their rings
+  float *const rings = reinterpret_cast<float *>(smem);
+  copy_wait<0>();
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    l[r] += __shfl_xor_sync(~0u, l[r], 1);
+    l[r] += __shfl_xor_sync(~0u, l[r], 2);
+    if (t == 0) jml[warp][g + r * 8] = make_float2(m[r], l[r]);
+    if (t0 >= t1 || row0 + g + r * 8 >= a.G) continue;
+    float *dst = rings + warp * (kRingBytes / 4) + (g + r * 8) * D;
+#pragma unroll
+    for (int v = 0; v < S::VS; ++v)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < S::VW; e += 4) {
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float *z = o[v * S::VW + e + k];
+            y[k] = R == 1 ? z[n] + z[n + 2] : z[2 * r + n];
+          }
+          *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+  }
+  __syncthreads();
+  const bool whole = pair.kt == 0 && c1 - (int)c0 == pair.nt;
+  const long long slot = ((long long)blockIdx.y * gridDim.x * kWarps + blockIdx.x * cut.warps) * 2;
+  const float vs = S::F8 ? __ldg(c.v_scale + pair.h) : 1.f;
+  const int used = (c1 - (int)c0 + cut.per - 1) / cut.per;  // warps with tiles
+  for (int i = threadIdx.x; i < min(MT, a.G - row0) * (D / 4); i += kThreads) {
+    const int row = i / (D / 4), col = i % (D / 4) * 4;
+    float M = -INFINITY, sum = 0.f;
+    for (int k = 0; k < used; ++k) M = fmaxf(M, jml[k][row].x);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < used; ++k) {
+      const float f = jml[k][row].x == -INFINITY ? 0.f : ex2(jml[k][row].x - M);
+      const float4 x = *reinterpret_cast<const float4 *>(rings + k * (kRingBytes / 4) + row * D + col);
+      sum += jml[k][row].y * f;
+      y.x += x.x * f;
+      y.y += x.y * f;
+      y.z += x.z * f;
+      y.w += x.w * f;
+    }
+    const long long hq = (long long)pair.b * a.Hq + (long long)pair.h * a.G + row0 + row;
+    const float f = whole ? vs / sum : 1.f;
+    float *dst = whole ? a.O + hq * D : a.part_o + (slot * MT + row) * D;
+    *reinterpret_cast<float4 *>(dst + col) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    if (col == 0) {
+      if (whole) {
+        const float x = M + log2f(sum);
+        if (a.lse) a.lse[hq] = x * kLn2;
+        a.lse2[hq] = x;
+      } else {
+        a.part_ml[slot * MT + row] = make_float2(M, sum);
+      }
+    }
   }
 }
 
-// Which warps hold parts of pair (b, h): parts w0 .. w1, the first in slot 1
-// of its warp (the pair starts inside that range), the others in slot 0.
+// The parts of pair (b, h), in order.  A CTA whose range lies in the pair
+// has left one (slot 0 of its first warp); the CTAs at the pair's two ends, where
+// other pairs take part of the range, one per warp: in slot 1 where the pair starts
+// inside the warp's range, else in slot 0.
 struct Parts {
-  int w0, w1, L;
+  int per, warps;
+  int w0, w1;            // first and last warp
+  int head, mid, tail;   // parts of the first CTA, of whole CTAs, of the last one
 };
-__device__ __forceinline__ Parts parts_of(const KvDev &c, const DecodeArgs &a, int b, int h) {
-  const int per = a.plan[0], p0 = a.plan[1 + b], nt = a.plan[2 + b] - p0;
-  Parts r;
-  r.L = nt;
-  const long long first = (long long)p0 * c.Hkv + (long long)h * nt;
-  r.w0 = (int)(first / per);
-  r.w1 = (int)((first + nt - 1) / per);
-  return r;
+__device__ __forceinline__ int parts_of(const KvDev &c, const DecodeArgs &a, int b, int h, Parts &u) {
+  u.per = a.plan[0];
+  u.warps = a.plan[1];
+  const int p0 = a.plan[2 + b], nt = a.plan[3 + b] - p0;
+  const long long T = (long long)a.plan[2 + c.B] * c.Hkv;
+  const long long first = (long long)p0 * c.Hkv + (long long)h * nt, last = first + nt - 1;
+  if (nt == 0) return 0;
+  u.w0 = (int)(first / u.per);
+  u.w1 = (int)(last / u.per);
+  const long long cr = (long long)u.per * u.warps;  // tiles of a CTA
+  const int k0 = (int)(first / cr), k1 = (int)(last / cr);
+  // whole CTAs: all tiles of the CTA's range in the pair
+  const bool whole0 = u.warps > 1 && first == k0 * cr && last >= min(T, (k0 + 1) * cr) - 1;
+  const bool whole1 = u.warps > 1 && k1 > k0 && last == min(T, (k1 + 1) * cr) - 1;
+  if (u.warps == 1) {
+    u.head = u.w1 - u.w0 + 1;
+    u.mid = u.tail = 0;
+  } else if (k0 == k1) {
+    u.head = whole0 ? 0 : u.w1 - u.w0 + 1;
+    u.mid = whole0 ? 1 : 0;
+    u.tail = 0;
+  } else {
+    u.head = whole0 ? 0 : (k0 + 1) * u.warps - u.w0;
+    u.tail = whole1 ? 0 : u.w1 - k1 * u.warps + 1;
+    u.mid = k1 - k0 - 1 + (whole0 ? 1 : 0) + (whole1 ? 1 : 0);
+  }
+  return u.head + u.mid + u.tail;
+}
+// Warp slot (warp * 2 + slot) of part i.
+__device__ __forceinline__ long long part_slot(const Parts &u, int i) {
+  if (i < u.head) return (long long)(u.w0 + i) * 2 + (i == 0);
+  const int k0 = (u.w0 + u.head + u.warps - 1) / u.warps;  // first whole CTA
+  if (i < u.head + u.mid) return (long long)(k0 + i - u.head) * u.warps * 2;
+  return ((long long)(k0 + u.mid) * u.warps + (i - u.head - u.mid)) * 2;
 }
 
 constexpr int kFinThreads = 128;
 constexpr int kFinWarps = kFinThreads / 32;
-constexpr int kScoreRows = 1024;  // rows of one CTA when weights are gathered
 
-// (maximum, sum) of the parts of query head m of a pair, the same in every thread.
-__device__ __forceinline__ float2 join_ml(const DecodeArgs &a, const Parts &u, long long W, int MT, int m,
-                                          float2 *sh) {
-  const long long base = (long long)(m / MT) * W;
-  const int row = m % MT, lane = threadIdx.x & 31;
-  auto at = [&](int w) { return a.part_ml[((base + w) * 2 + (w == u.w0)) * MT + row]; };
-  float M = -INFINITY, sum = 0.f;
-  for (int w = u.w0 + threadIdx.x; w <= u.w1; w += kFinThreads) M = fmaxf(M, at(w).x);
+// Joins the partials of one query head per CTA, in the order of the warps.
+template <int D>
+__global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const DecodeArgs a, int W, int MT) {
+  __shared__ float sm[kFinWarps], sl[kFinWarps];
+  __shared__ float4 acc[kFinWarps][D / 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
+  Parts u;
+  const int parts = parts_of(c, a, b, h, u);
+  if (parts <= 1) return;  // empty, or finished by one warp or CTA
+  const long long base = (long long)(m / MT) * W * 2;
+  const int row = m % MT;
+  auto slot = [&](int i) { return (base + part_slot(u, i)) * MT + row; };
+  float M = -INFINITY;
+  for (int i = threadIdx.x; i < parts; i += kFinThreads) M = fmaxf(M, a.part_ml[slot(i)].x);
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-  if (lane == 0) sh[threadIdx.x >> 5].x = M;
+  if (lane == 0) sm[warp] = M;
   __syncthreads();
-  for (int i = 0; i < kFinWarps; ++i) M = fmaxf(M, sh[i].x);
-  for (int w = u.w0 + threadIdx.x; w <= u.w1; w += kFinThreads) {
-    const float2 x = at(w);
-    sum += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+  for (int i = 0; i < kFinWarps; ++i) M = fmaxf(M, sm[i]);
+  // each lane holds four columns; with d = 64 a warp takes two partials at a time
+  constexpr int kPer = 128 / D;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = warp * kPer + lane / (D / 4); i < parts; i += kFinWarps * kPer) {
+    const long long s = slot(i);
+    const float2 ml = a.part_ml[s];
+    const float4 y = *reinterpret_cast<const float4 *>(a.part_o + s * D + (lane % (D / 4)) * 4);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    l += ml.y * f;
+    x.x += y.x * f;
+    x.y += y.y * f;
+    x.z += y.z * f;
+    x.w += y.w * f;
   }
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (lane == 0) sh[threadIdx.x >> 5].y = sum;
+  if constexpr (kPer == 2) {
+    l += __shfl_xor_sync(~0u, l, 16);
+    x.x += __shfl_xor_sync(~0u, x.x, 16);
+    x.y += __shfl_xor_sync(~0u, x.y, 16);
+    x.z += __shfl_xor_sync(~0u, x.z, 16);
+    x.w += __shfl_xor_sync(~0u, x.w, 16);
+  }
+  if (lane < D / 4) acc[warp][lane] = x;
+  if (lane == 0) sl[warp] = l;
   __syncthreads();
-  sum = 0.f;
-  for (int i = 0; i < kFinWarps; ++i) sum += sh[i].y;
-  __syncthreads();
-  return make_float2(M, sum);
+  l = sl[0];
+  for (int i = 1; i < kFinWarps; ++i) l += sl[i];
+  if (threadIdx.x < D / 4) {
+    float4 y = acc[0][threadIdx.x];
+    for (int i = 1; i < kFinWarps; ++i) {
+      y.x += acc[i][threadIdx.x].x;
+      y.y += acc[i][threadIdx.x].y;
+      y.z += acc[i][threadIdx.x].z;
+      y.w += acc[i][threadIdx.x].w;
+    }
+    const float f = (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / l;
+    *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
+        make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+  }
+  if (threadIdx.x == 0) {
+    const float lse2 = M + log2f(l);
+    a.lse2[blockIdx.x] = lse2;
+    if (a.lse) a.lse[blockIdx.x] = lse2 * kLn2;
+  }
 }
 
-// Blocks [0, B * Hq): join the partials of one query head.  The blocks behind
-// them (accumulate): add the weights of kScoreRows rows of a pair to its scores.
-template <int D>
-__global__ void __launch_bounds__(kFinThreads) finish_kernel(const KvDev c, const DecodeArgs a, int W, int MT,
-                                                             int score_blocks) {
-  __shared__ float2 sh[kFinWarps];
-  __shared__ float4 acc[kFinWarps][D / 4];
-  const int joins = c.B * a.Hq, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if ((int)blockIdx.x < joins) {
-    const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
-    const Parts u = parts_of(c, a, b, h);
-    if (u.L == 0 || u.w0 == u.w1) return;  // empty, or finished by one warp
-    const float2 ml = join_ml(a, u, W, MT, m, sh);
-    const long long base = (long long)(m / MT) * W;
-    const int row = m % MT;
-    constexpr int kPer = 128 / D;  // partials of a warp side by side (d = 64: two)
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = u.w0 + warp * kPer + lane / (D / 4); w <= u.w1; w += kFinWarps * kPer) {
-      const long long slot = ((base + w) * 2 + (w == u.w0)) * MT + row;
-      const float pm = a.part_ml[slot].x, f = pm == -INFINITY ? 0.f : ex2(pm - ml.x);
-      const float4 y = *reinterpret_cast<const float4 *>(a.part_o + slot * D + (lane % (D / 4)) * 4);
-      x.x += y.x * f;
-      x.y += y.y * f;
-      x.z += y.z * f;
-      x.w += y.w * f;
+constexpr int kScoreRows = 128;  // rows of one CTA of score_kernel, four per lane
+
+// Adds the weights of kScoreRows rows of a pair to the rows' scores: each warp
+// sums every fourth query head, the four sums are added in order.  Bound by the
+// logits' bytes.
+__global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const DecodeArgs a) {
+  __shared__ float4 sums[kFinWarps][32];
+  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int L = c.L[b];
+  if (L < 0 || L > c.cap || (int)blockIdx.x * kScoreRows >= L) return;
+  const int p = blockIdx.x * kScoreRows + lane * 4;
+  const long long hq = (long long)b * a.Hq + (long long)h * a.G;
+  const float *src = a.s + hq * a.s_ld + p;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p < L) {
+#pragma unroll 4
+    for (int m = warp; m < a.G; m += kFinWarps) {
+      const float lse2 = __ldg(a.lse2 + hq + m);
+      const float4 x = *reinterpret_cast<const float4 *>(src + m * a.s_ld);  // behind the last row: not used
+      w.x += ex2(x.x - lse2);
+      w.y += ex2(x.y - lse2);
+      w.z += ex2(x.z - lse2);
+      w.w += ex2(x.w - lse2);
     }
-    if constexpr (kPer == 2) {
-      x.x += __shfl_xor_sync(~0u, x.x, 16);
-      x.y += __shfl_xor_sync(~0u, x.y, 16);
-      x.z += __shfl_xor_sync(~0u, x.z, 16);
-      x.w += __shfl_xor_sync(~0u, x.w, 16);
-    }
-    if (lane < D / 4) acc[warp][lane] = x;
-    __syncthreads();
-    if (threadIdx.x < D / 4) {
-      float4 y = acc[0][threadIdx.x];
-      for (int i = 1; i < kFinWarps; ++i) {
-        y.x += acc[i][threadIdx.x].x;
-        y.y += acc[i][threadIdx.x].y;
-        y.z += acc[i][threadIdx.x].z;
-        y.w += acc[i][threadIdx.x].w;
-      }
-      const float f = (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / ml.y;
-      *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
-          make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-    }
-    if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = (ml.x + log2f(ml.y)) * kLn2;
-    return;
   }
-  const int k = blockIdx.x - joins, chunk = k % score_blocks, pair = k / score_blocks;
-  const int h = pair % c.Hkv, b = pair / c.Hkv;
-  int L = c.L[b];
-  if (L < 0 || L > c.cap) L = 0;
-  const int p0 = chunk * kScoreRows, n = min(L - p0, kScoreRows);
-  if (n <= 0) return;
-  const Parts u = parts_of(c, a, b, h);
-  constexpr int kRows = kScoreRows / kFinThreads;
-  float w[kRows] = {};
-  for (int m = 0; m < a.G; ++m) {
-    const long long hq = (long long)b * a.Hq + (long long)h * a.G + m;
-    float lse2;
-    if (u.w0 == u.w1) {
-      lse2 = a.lse2[hq];
-    } else {
-      const float2 ml = join_ml(a, u, W, MT, m, sh);
-      lse2 = ml.x + log2f(ml.y);
-    }
-    const float *src = a.s + hq * a.s_ld + p0;
+  sums[warp][lane] = w;
+  __syncthreads();
+  const int r = blockIdx.x * kScoreRows + threadIdx.x;
+  if (r >= L) return;
+  const float *all = reinterpret_cast<const float *>(sums);
+  float x = all[threadIdx.x];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int p = i * kFinThreads + threadIdx.x;
-      if (p < n) w[i] += ex2(src[p] - lse2);
-    }
-  }
-  float *dst = c.scores + (long long)pair * c.scores_ld + p0;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int p = i * kFinThreads + threadIdx.x;
-    if (p < n) dst[p] += w[i];
-  }
+  for (int i = 1; i < kFinWarps; ++i) x += all[i * kScoreRows + threadIdx.x];
+  c.scores[((long long)b * c.Hkv + h) * c.scores_ld + r] += x;
 }
 
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
@@ -641,14 +787,14 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   const int G = Hq / c.Hkv;
   p.MT = G <= 8 ? 8 : 16;
   p.row_tiles = (G + p.MT - 1) / p.MT;
-  const long long tiles = (long long)c.B * c.Hkv * ((c.cap + kTile - 1) / kTile);
-  p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, (tiles + kMinTiles - 1) / kMinTiles));
+  const long long most = (long long)c.B * c.Hkv * ((c.cap + kMinRows - 1) / kMinRows);  // ranges worth a warp
+  p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, most));
   const size_t rows = (size_t)p.row_tiles * p.grid * kWarps * 2 * p.MT;
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
   p.plan_off = p.lse_off + tr_align_up((size_t)c.B * Hq * 4, 256);
-  p.s_off = p.plan_off + tr_align_up((size_t)(c.B + 2) * 4, 256);
-  p.total = p.s_off + (accumulate ? (size_t)c.B * Hq * tr_align_up(c.cap, kTile) * 4 : 0);
+  p.s_off = p.plan_off + tr_align_up((size_t)(c.B + 3) * 4, 256);
+  p.total = p.s_off + (accumulate ? (size_t)c.B * Hq * tr_align_up(c.cap, 32) * 4 : 0);
   return p;
 }
 
@@ -666,10 +812,12 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
   const int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  const int score_blocks = a.accumulate ? (c.cap + kScoreRows - 1) / kScoreRows : 0;
-  const long long blocks = (long long)c.B * a.Hq + (long long)c.B * c.Hkv * score_blocks;
-  finish_kernel<D><<<(unsigned)blocks, kFinThreads, 0, s>>>(c, a, p.grid * kWarps, p.MT, score_blocks);
+  join_kernel<D><<<(unsigned)(c.B * a.Hq), kFinThreads, 0, s>>>(c, a, p.grid * kWarps, p.MT);
   TR_LAUNCH_CHECK();
+  if (a.accumulate) {
+    score_kernel<<<dim3((c.cap + kScoreRows - 1) / kScoreRows, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
+    TR_LAUNCH_CHECK();
+  }
   return TR_OK;
 }
 
@@ -678,10 +826,9 @@ int launch(int d, const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArg
   return d == 64 ? launch<TYPE, 64>(p, s, c, a) : launch<TYPE, 128>(p, s, c, a);
 }
 
-// Launch grids and offsets hold B * Hq in 31 bits (the cache's own limits bound the rest).
+// Launch grids hold B * Hq in 31 bits and the KV heads in 16.
 bool fits(const KvDev &c, int Hq) {
-  return (long long)c.B * Hq + (long long)c.B * c.Hkv * ((c.cap + kScoreRows - 1) / kScoreRows) < (1LL << 31) &&
-         Hq / c.Hkv <= 65535 * 8;
+  return (long long)c.B * Hq < (1LL << 31) && c.Hkv <= 65535 && Hq / c.Hkv <= 65535 * 8;
 }
 
 }  // namespace
@@ -714,7 +861,7 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   a.lse2 = (float *)((char *)ws + p.lse_off);
   a.plan = (int *)((char *)ws + p.plan_off);
   a.s = (float *)((char *)ws + p.s_off);
-  a.s_ld = (long long)tr_align_up(c.cap, kTile);
+  a.s_ld = (long long)tr_align_up(c.cap, 32);
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.accumulate = accumulate != 0;
