@@ -97,7 +97,10 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes from global to shared memory, or 16 zero bytes.
+// 16 bytes from global to shared memory; of the second form 16 zero bytes where not valid.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -277,13 +280,24 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
         const long long at = (long long)pg * c.block_stride + head + kv_row(c, p0 + lane / S::CPR);
         const char *k = c.K + at, *v = c.V + at;
         const int left = good ? ld.L - p0 : 0;
+        const long long next = (32 / S::CPR) * c.row_stride;
+        if (left >= kTile) {
 #pragma unroll
-        for (int i = 0; i < KB * S::CPR / 2; ++i) {
-          const int r = lane / S::CPR + i * (32 / S::CPR);
-          const bool valid = r < left;
-          const long long off = (long long)(i * (32 / S::CPR)) * c.row_stride;
-          copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, valid ? k + off : c.K, valid);
-          copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, valid ? v + off : c.V, valid);
+          for (int i = 0; i < KB * S::CPR / 2; ++i) {
+            const int r = lane / S::CPR + i * (32 / S::CPR);
+            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, k);
+            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, v);
+            k += next;
+            v += next;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < KB * S::CPR / 2; ++i) {
+            const int r = lane / S::CPR + i * (32 / S::CPR);
+            const bool valid = r < left;
+            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, valid ? k + i * next : c.K, valid);
+            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, valid ? v + i * next : c.V, valid);
+          }
         }
       } else {
 #pragma unroll
@@ -312,11 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
   constexpr float kOff = S::BF ? 0.f : 7.f;           // fp16 weights run up to 2^15
   uint32_t q[R][S::QR];
   float mul[R], m[R], l[R], o[S::NT][4];
+  float *logits[R];  // where a lane's logits of the next tile go
   int kt0 = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
+    logits[r] = nullptr;
   }
 
   for (int i = t0; i < t1; ++i) {
@@ -331,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
         const uint4 *src = reinterpret_cast<const uint4 *>(a.Q) +
                            ((long long)cur.b * a.Hq + (long long)cur.h * a.G + m_row) * (D / 8);
         mul[r] = a.scale_log2;
+        logits[r] = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + m_row) * a.s_ld + cur.kt * kTile + 2 * t;
         if constexpr (S::F8) {
           // a lane's pieces are 16 elements; narrowed to fp16 after scaling the head's largest to 2^14
           float amax = 0.f;
@@ -403,22 +420,29 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
       }
 
     // logits in log2 units; rows behind the last get none
-    const int p0 = cur.kt * kTile, rows = cur.L - p0;
+    const int rows = cur.L - cur.kt * kTile;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 2 * KB; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[j][2 * r + e] = j * 8 + 2 * t + e < rows ? s[j][2 * r + e] * mul[r] : -INFINITY;
-          mx = fmaxf(mx, s[j][2 * r + e]);
-        }
-      if (a.accumulate && row0 + g + r * 8 < a.G) {
-        float *dst = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + row0 + g + r * 8) * a.s_ld + p0 + 2 * t;
+        for (int e = 0; e < 2; ++e) s[j][2 * r + e] *= mul[r];
+      if (rows < kTile) {
 #pragma unroll
         for (int j = 0; j < 2 * KB; ++j)
-          *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(s[j][2 * r], s[j][2 * r + 1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (j * 8 + 2 * t + e >= rows) s[j][2 * r + e] = -INFINITY;
+      }
+      float mx = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+#pragma unroll
+      for (int j = 1; j < 2 * KB; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
+      if (a.accumulate) {
+        if (row0 + g + r * 8 < a.G)
+#pragma unroll
+          for (int j = 0; j < 2 * KB; ++j)
+            *reinterpret_cast<float2 *>(logits[r] + j * 8) = make_float2(s[j][2 * r], s[j][2 * r + 1]);
+        logits[r] += kTile;
       }
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
@@ -740,23 +764,25 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
   }
 }
 
-constexpr int kScoreRows = 128;  // rows of one CTA of score_kernel, four per lane
-
-// Adds the weights of kScoreRows rows of a pair to the rows' scores: each warp
-// sums every fourth query head, the four sums are added in order.  Bound by the
-// logits' bytes.
+// Adds the weights of a pair's rows, summed over its query heads, to the
+// rows' scores; bound by the logits' bytes.  SPLIT (more than 8 heads): a CTA
+// takes 128 rows, each warp every fourth head; else 512 rows and every thread all
+// heads of four rows.  With 4 heads and 262 k rows the split form took 20 us
+// and the other 12 us; with 40 heads and 50 k rows 8 us and 19 us.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const DecodeArgs a) {
-  __shared__ float4 sums[kFinWarps][32];
+  constexpr int kRows = SPLIT ? 128 : 512;
+  __shared__ float4 sums[SPLIT ? kFinWarps : 1][32];
   const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int L = c.L[b];
-  if (L < 0 || L > c.cap || (int)blockIdx.x * kScoreRows >= L) return;
-  const int p = blockIdx.x * kScoreRows + lane * 4;
+  if (L < 0 || L > c.cap || (int)blockIdx.x * kRows >= L) return;
+  const int p = blockIdx.x * kRows + (SPLIT ? lane : threadIdx.x) * 4;
   const long long hq = (long long)b * a.Hq + (long long)h * a.G;
   const float *src = a.s + hq * a.s_ld + p;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   if (p < L) {
 #pragma unroll 4
-    for (int m = warp; m < a.G; m += kFinWarps) {
+    for (int m = SPLIT ? warp : 0; m < a.G; m += SPLIT ? kFinWarps : 1) {
       const float lse2 = __ldg(a.lse2 + hq + m);
       const float4 x = *reinterpret_cast<const float4 *>(src + m * a.s_ld);  // behind the last row: not used
       w.x += ex2(x.x - lse2);
@@ -765,15 +791,23 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
       w.w += ex2(x.w - lse2);
     }
   }
-  sums[warp][lane] = w;
-  __syncthreads();
-  const int r = blockIdx.x * kScoreRows + threadIdx.x;
-  if (r >= L) return;
-  const float *all = reinterpret_cast<const float *>(sums);
-  float x = all[threadIdx.x];
+  float *dst = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
+  if constexpr (SPLIT) {
+    sums[warp][lane] = w;
+    __syncthreads();
+    const int r = blockIdx.x * kRows + threadIdx.x;
+    if (r >= L) return;
+    const float *all = reinterpret_cast<const float *>(sums);
+    float x = all[threadIdx.x];
 #pragma unroll
-  for (int i = 1; i < kFinWarps; ++i) x += all[i * kScoreRows + threadIdx.x];
-  c.scores[((long long)b * c.Hkv + h) * c.scores_ld + r] += x;
+    for (int i = 1; i < kFinWarps; ++i) x += all[i * kRows + threadIdx.x];
+    dst[r] += x;
+  } else {
+    const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p + i < L) dst[p + i] += x[i];
+  }
 }
 
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
@@ -815,7 +849,10 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   join_kernel<D><<<(unsigned)(c.B * a.Hq), kFinThreads, 0, s>>>(c, a, p.grid * kWarps, p.MT);
   TR_LAUNCH_CHECK();
   if (a.accumulate) {
-    score_kernel<<<dim3((c.cap + kScoreRows - 1) / kScoreRows, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
+    if (a.G > 8)
+      score_kernel<true><<<dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
+    else
+      score_kernel<false><<<dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
     TR_LAUNCH_CHECK();
   }
   return TR_OK;
