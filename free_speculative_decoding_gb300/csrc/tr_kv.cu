@@ -1,5 +1,6 @@
 // Appending rows to a KV cache and evicting rows from it by accumulated
 // attention weight.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -16,15 +17,38 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;  // 16-byte pieces of K and of V per thread
 
-// Eight bf16 values divided by the head's scale and rounded to e4m3: IEEE
-// division and one rounding to nearest even (the conversion clamps to +-448).
-__device__ __forceinline__ uint2 e4m3_of(const uint4 &x, float scale) {
+// x / s rounded to the nearest fp32, as far as its rounding to e4m3 can tell, from
+// r = RN(1 / s): q0 = x r, q = q0 + r (x - q0 s) (Markstein 1990: with fused
+// multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60] and
+// |x| <= 1024 s nothing overflows, and where a remainder underflows the
+// quotient is below 2^-40, which rounds to 0 either way.
+struct Scale {
+  float s, r, most;
+  bool tame;
+  __device__ __forceinline__ explicit Scale(float v) {
+    s = v;
+    r = __frcp_rn(v);
+    most = 1024.f * v;
+    tame = v >= 0x1p-60f && v <= 0x1p60f;
+  }
+  __device__ __forceinline__ float of(float x) const {
+    if (!tame) return __fdiv_rn(x, s);
+    x = x > most ? most : x;  // beyond 448 in any case; NaN passes
+    x = x < -most ? -most : x;
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+  }
+};
+
+// Eight bf16 values divided by the head's scale and rounded to e4m3 (one
+// rounding of the fp32 quotient to nearest even, clamped to +-448).
+__device__ __forceinline__ uint2 e4m3_of(const uint4 &x, const Scale &sc) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale)), __NV_SATFINITE, __NV_E4M3);
+    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(sc.of(lo), sc.of(hi)), __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
@@ -33,7 +57,7 @@ __device__ __forceinline__ uint2 e4m3_of(const uint4 &x, float scale) {
 // Every CTA of a sequence decides alike whether the sequence can take its
 // rows; the last one to finish advances L[b], so that none reads a changed
 // length.
-template <bool E4M3>
+template <bool E4M3, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, const uint4 *Kn, const uint4 *Vn, int T,
                                                                 const int32_t *count, unsigned *counters,
                                                                 unsigned *status) {
@@ -44,14 +68,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, c
   bool bad_page = false;
   if (!bad_len && !full) bad_page = kv_bad_pages(c, b, Lb, Lb + n);
   if (!bad_len && !full && !bad_page) {
-    const int pieces = c.row_bytes / (E4M3 ? 8 : 16);  // of a row
-    const long long total = (long long)n * c.Hkv * pieces;
-    const long long base = (long long)b * T * c.Hkv * pieces;
-    const long long i0 = (long long)blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
+    constexpr int kPieces = D / 8, kOut = E4M3 ? 8 : 16;  // of a row; bytes of a piece in the cache
+    const unsigned total = (unsigned)n * c.Hkv * kPieces;
+    const long long base = (long long)b * T * c.Hkv * kPieces;
+    const unsigned i0 = blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
     uint4 kx[kAppendUnroll], vx[kAppendUnroll];
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u) {
-      const long long i = i0 + u * kAppendThreads;
+      const unsigned i = i0 + u * kAppendThreads;
       if (i < total) {
         kx[u] = __ldcs(Kn + base + i);
         vx[u] = __ldcs(Vn + base + i);
@@ -59,15 +83,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, c
     }
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u) {
-      const long long i = i0 + u * kAppendThreads;
+      const unsigned i = i0 + u * kAppendThreads;
       if (i >= total) continue;
-      const int piece = (int)(i % pieces);
-      const long long th = i / pieces;
-      const int h = (int)(th % c.Hkv), p = Lb + (int)(th / c.Hkv);
-      const long long at = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * (E4M3 ? 8 : 16);
+      const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
+      const int h = (int)(th - tok * c.Hkv), p = Lb + (int)tok;
+      const long long at = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * kOut;
       if constexpr (E4M3) {
-        *reinterpret_cast<uint2 *>(c.K + at) = e4m3_of(kx[u], __ldg(c.k_scale + h));
-        *reinterpret_cast<uint2 *>(c.V + at) = e4m3_of(vx[u], __ldg(c.v_scale + h));
+        *reinterpret_cast<uint2 *>(c.K + at) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + h)));
+        *reinterpret_cast<uint2 *>(c.V + at) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + h)));
       } else {
         *reinterpret_cast<uint4 *>(c.K + at) = kx[u];
         *reinterpret_cast<uint4 *>(c.V + at) = vx[u];
@@ -97,147 +120,224 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, c
 // eviction
 // ---------------------------------------------------------------------------
 
-constexpr int kSelThreads = 1024;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
-constexpr int kPartBytes = 64;  // columns of a row that one CTA moves
+namespace cg = cooperative_groups;
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelMaxKeys = 40960;  // of a CTA's slice, in shared memory
+constexpr int kMoveThreads = 512;
+constexpr int kMoveUnroll = 4;
 
 // Order of the scores: larger first, -0 as +0, NaN below everything.
 __device__ __forceinline__ uint32_t score_key(float s) { return s != s ? 0u : tr_ord(s); }
 
 struct SelSmem {
-  unsigned hist[256];
-  unsigned warp_sel[kSelThreads / 32], warp_eq[kSelThreads / 32];
-  unsigned prefix, need;
+  unsigned hist[3][kSelBins];
+  unsigned wsum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
+  unsigned bin, need;
+  unsigned gt, eq;  // the CTA's rows above and at the edge
 };
 
-// One CTA per (KV head, sequence).  Finds the key of the k-th largest score
-// among the rows before the protected ones (radix select, eight bits a pass),
-// then walks all rows in order, writes the positions that stay to keep and
-// moves their scores up.  A score only moves down in position and every chunk
-// is read before it is written, so the walk can work in place.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c, int budget, int recent, int32_t *keep,
-                                                                   int32_t *old_len, unsigned *status) {
+// One cluster per (KV head, sequence): finds the key of the k-th largest score
+// among the rows before the protected ones and writes the k positions that stay,
+// ascending, to keep.  Each CTA holds one slice of the keys in shared memory
+// (read from global again in every pass where the slice is too long).  The key
+// is found by a radix select, 11 + 11 + 10 bits a pass: the CTAs' histograms are
+// added through distributed shared memory and every CTA walks the sum alike.  A
+// row's place in keep is the number of rows above the edge before it plus the
+// number of edge rows taken before it, so each warp places its stretch alone.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c, int budget, int recent, int slice_keys,
+                                                                   int32_t *keep, int32_t *old_len, unsigned *status) {
+  extern __shared__ unsigned keys[];
   __shared__ SelSmem s;
-  const int h = blockIdx.x, b = blockIdx.y;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = cluster.num_blocks(), rank = cluster.block_rank();
+  const int h = blockIdx.x / CS, b = blockIdx.y;
   const int Lb = c.L[b];
   const bool bad_len = Lb < 0 || Lb > c.cap;
   const bool active = !bad_len && Lb > budget;
   const bool bad_page = active && kv_bad_pages(c, b, 0, Lb);
-  if (h == 0 && threadIdx.x == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     old_len[b] = active && !bad_page ? Lb : -1;
     if (bad_len) tr_flag(status, TR_DEV_BAD_LENGTH);
     if (bad_page) tr_flag(status, TR_DEV_BAD_PAGE);
   }
-  if (!active || bad_page) return;
-  float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
+  const int n = Lb - recent, k = budget - recent;  // k < n where active
+  if (!active || bad_page || k == 0) return;       // the same for the whole cluster
+  const float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
   keep += ((long long)b * c.Hkv + h) * budget;
-  const int n = Lb - recent, k = budget - recent;  // k < n
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = ((n + CS - 1) / CS + 31) & ~31;
+  const int lo = min(n, rank * slice), len = min(n - lo, slice);
+  sc += lo;
+  const bool held = slice <= slice_keys;
+  for (int i = threadIdx.x; i < 3 * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+  if (held)
+    for (int i = threadIdx.x; i < len; i += kSelThreads) keys[i] = score_key(sc[i]);
+  auto key_at = [&](int i) { return held ? keys[i] : score_key(sc[i]); };
+  __syncthreads();
   // key of the k-th largest: `prefix` holds its leading bits, `need` how many
   // of the rows that share them are still to be taken
   unsigned prefix = 0, need = k;
-  if (k > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) s.hist[i] = 0;
-      __syncthreads();
-      const unsigned mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int i = threadIdx.x; i < n; i += kSelThreads) {
-        const unsigned key = score_key(sc[i]);
-        if ((key & mask) == prefix) atomicAdd(&s.hist[(key >> shift) & 255], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l owns bins 255-8l .. 248-8l: running count from the largest key down
-        unsigned sum = 0;
-        for (int j = 0; j < 8; ++j) sum += s.hist[255 - 8 * lane - j];
-        unsigned incl = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned v = __shfl_up_sync(~0u, incl, o);
-          if (lane >= o) incl += v;
-        }
-        unsigned before = incl - sum;
-        if (before < need && need <= incl) {
-          int bin = 255 - 8 * lane;
-          while (before + s.hist[bin] < need) before += s.hist[bin--];
-          s.prefix = prefix | ((unsigned)bin << shift);
-          s.need = need - before;
-        }
-      }
-      __syncthreads();
-      prefix = s.prefix;
-      need = s.need;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const unsigned mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u, low = pass == 2 ? 1023u : 2047u;
+    unsigned *hist = s.hist[pass];
+    for (int i = threadIdx.x; i < len; i += kSelThreads) {
+      const unsigned key = key_at(i);
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & low], 1u);
     }
+    cluster.sync();
+    // thread i owns the bins 2047 - 4 i .. 2044 - 4 i, from the largest key down
+    constexpr int kOwn = kSelBins / kSelThreads;
+    const int top = kSelBins - 1 - kOwn * threadIdx.x;
+    unsigned cnt[kOwn] = {}, sum = 0;
+    for (int r = 0; r < CS; ++r) {
+      const unsigned *other = cluster.map_shared_rank(hist, r);
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) cnt[j] += other[top - j];
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) sum += cnt[j];
+    unsigned incl = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s.wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s.wsum[w];
+    unsigned before = incl - sum;
+    if (before < need && need <= incl) {
+      int j = 0;
+      while (before + cnt[j] < need) before += cnt[j++];
+      s.bin = top - j;
+      s.need = need - before;
+    }
+    __syncthreads();
+    prefix |= s.bin << shift;
+    need = s.need;
   }
-  // rows in order: all above the k-th key, the first `need` of those equal to it, all protected ones
-  unsigned taken = 0, equal = 0;
-  for (int i0 = 0; i0 < Lb; i0 += kSelThreads) {
-    const int i = i0 + threadIdx.x;
-    const float v = i < Lb ? sc[i] : 0.f;
-    const unsigned key = score_key(v);
-    const bool eq = k > 0 && i < n && key == prefix;
-    const unsigned eqs = __ballot_sync(~0u, eq), below = (1u << lane) - 1;
-    if (lane == 0) s.warp_eq[warp] = __popc(eqs);
-    __syncthreads();
-    unsigned eq_before = equal, eq_all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) eq_before += s.warp_eq[w];
-      eq_all += s.warp_eq[w];
+  // each warp's stretch of the slice: rows above the edge and at it
+  const int stretch = ((slice + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int w0 = min(len, warp * stretch), w1 = min(len, w0 + stretch);
+  unsigned gt = 0, eq = 0;
+  for (int i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    const unsigned key = in ? key_at(i + lane) : 0u;
+    gt += __popc(__ballot_sync(~0u, in && key > prefix));
+    eq += __popc(__ballot_sync(~0u, in && key == prefix));
+  }
+  if (lane == 0) {
+    s.wgt[warp] = gt;
+    s.weq[warp] = eq;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned x = 0, y = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      x += s.wgt[w];
+      y += s.weq[w];
     }
-    eq_before += __popc(eqs & below);
-    const bool sel = i < Lb && (i >= n || (k > 0 && (key > prefix || (eq && eq_before < need))));
-    const unsigned sels = __ballot_sync(~0u, sel);
-    if (lane == 0) s.warp_sel[warp] = __popc(sels);
-    __syncthreads();
-    unsigned at = taken, all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) at += s.warp_sel[w];
-      all += s.warp_sel[w];
-    }
-    at += __popc(sels & below);
-    if (sel) {
-      keep[at] = i;
-      sc[at] = v;
-    }
-    taken += all;
-    equal += eq_all;
-    __syncthreads();
+    s.gt = x;
+    s.eq = y;
+  }
+  cluster.sync();
+  gt = eq = 0;
+  for (int r = 0; r < rank; ++r) {
+    gt += *cluster.map_shared_rank(&s.gt, r);
+    eq += *cluster.map_shared_rank(&s.eq, r);
+  }
+  cluster.sync();  // no CTA of the cluster is read from here on
+  for (int w = 0; w < warp; ++w) {
+    gt += s.wgt[w];
+    eq += s.weq[w];
+  }
+  const unsigned below = (1u << lane) - 1;
+  for (int i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    const unsigned key = in ? key_at(i + lane) : 0u;
+    const bool above = in && key > prefix, edge = in && key == prefix;
+    const unsigned gts = __ballot_sync(~0u, above), eqs = __ballot_sync(~0u, edge);
+    const unsigned eq_before = eq + __popc(eqs & below);
+    if (above || (edge && eq_before < need)) keep[gt + __popc(gts & below) + min(eq_before, need)] = lo + i + lane;
+    gt += __popc(gts);
+    eq += __popc(eqs);
   }
 }
 
-// Moves the kept rows of K and V up, in place.  A CTA owns 64 bytes of every
-// row of one (sequence, KV head), of K or of V, so no two CTAs touch the same
-// bytes, and walks the kept rows in order.  Row r comes from keep[r] >= r:
-// writing rows [r0, r0 + n) can only hit sources of rows < r0 + n, so it is
-// enough that a batch is read before it is written, which a barrier ensures.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c, int budget, const int32_t *keep,
-                                                                  const int32_t *old_len) {
-  constexpr int kLanes = kPartBytes / 16, kRows = kMoveThreads / kLanes;
+// Moves the kept rows of K and V up, in place, and their scores.  A CTA owns
+// PART bytes of every row of one (sequence, KV head), of K or of V (or the
+// scores), so no two CTAs touch the same bytes, and walks the kept rows in
+// order.  Row r comes from keep[r] >= r.  Writing a batch of rows [r0, r1) can
+// only hit sources of rows < r1: their reads lie before the barrier that the write
+// waits for.  The next batch's sources lie at or behind r1, so it is read before the
+// barrier too, which keeps loads in flight while the batch is written.
+template <int PART>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c, int budget, int recent,
+                                                                  const int32_t *keep, const int32_t *old_len) {
+  constexpr int kLanes = PART / 16, kRows = kMoveThreads / kLanes, kBatch = kRows * kMoveUnroll;
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  if (old_len[b] < 0) return;
-  const int per = c.row_bytes / kPartBytes;
-  char *base = (part < per ? c.K : c.V) + (long long)h * c.head_stride + (part % per) * kPartBytes +
-               (threadIdx.x % kLanes) * 16;
+  const int Lb = old_len[b];
+  if (Lb < 0) return;
+  const int k = budget - recent, shift = Lb - budget;  // a protected row moves by `shift`
   keep += ((long long)b * c.Hkv + h) * budget;
-  const int row = threadIdx.x / kLanes;
-  for (int r0 = 0; r0 < budget; r0 += kRows * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    bool moves[kMoveUnroll];
+  auto source = [&](int r) { return r >= budget ? r : r < k ? __ldg(keep + r) : r + shift; };
+  const int per = c.row_bytes / PART;
+  if (part == 2 * per) {
+    float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
+    constexpr int kPer = 8;
+    for (int r0 = 0; r0 < budget; r0 += kMoveThreads * kPer) {
+      float x[kPer];
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int r = r0 + u * kRows + row;
-      const int src = r < budget ? __ldg(keep + r) : r;
-      moves[u] = src != r;
-      if (moves[u]) x[u] = *reinterpret_cast<const uint4 *>(base + kv_block(c, b, src) + kv_row(c, src));
-    }
-    __syncthreads();
+      for (int u = 0; u < kPer; ++u) {
+        const int r = r0 + u * kMoveThreads + threadIdx.x;
+        if (r < budget) x[u] = sc[source(r)];
+      }
+      __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int r = r0 + u * kRows + row;
-      if (moves[u]) *reinterpret_cast<uint4 *>(base + kv_block(c, b, r) + kv_row(c, r)) = x[u];
+      for (int u = 0; u < kPer; ++u) {
+        const int r = r0 + u * kMoveThreads + threadIdx.x;
+        if (r < budget) sc[r] = x[u];
+      }
     }
+    if (h == 0 && threadIdx.x == 0) c.L[b] = budget;
+    return;
   }
-  if (part == 0 && h == 0 && threadIdx.x == 0) c.L[b] = budget;
+  char *base = (part < per ? c.K : c.V) + (long long)h * c.head_stride + (part % per) * PART +
+               (threadIdx.x % kLanes) * 16;
+  const int row = threadIdx.x / kLanes;
+  uint4 x[2][kMoveUnroll];
+  bool moves[2][kMoveUnroll];
+  auto load = [&](int r0, uint4(&y)[kMoveUnroll], bool(&mv)[kMoveUnroll]) {
+    int src[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int r = r0 + u * kRows + row;
+      src[u] = source(r);
+      mv[u] = src[u] != r;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u)
+      if (mv[u]) y[u] = *reinterpret_cast<const uint4 *>(base + kv_block(c, b, src[u]) + kv_row(c, src[u]));
+  };
+  auto store = [&](int r0, const uint4(&y)[kMoveUnroll], const bool(&mv)[kMoveUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int r = r0 + u * kRows + row;
+      if (mv[u]) *reinterpret_cast<uint4 *>(base + kv_block(c, b, r) + kv_row(c, r)) = y[u];
+    }
+  };
+  load(0, x[0], moves[0]);
+  for (int r0 = 0; r0 < budget; r0 += 2 * kBatch) {
+    load(r0 + kBatch, x[1], moves[1]);
+    __syncthreads();
+    store(r0, x[0], moves[0]);
+    load(r0 + 2 * kBatch, x[0], moves[0]);
+    __syncthreads();
+    store(r0 + kBatch, x[1], moves[1]);
+  }
 }
 
 // Workspace: the kept positions of every (sequence, KV head), then the old
@@ -268,18 +368,20 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
   const long long pieces = (long long)T * c.Hkv * (cache->d / 8);
   const long long per = kAppendThreads * kAppendUnroll;
   const long long grid = (pieces + per - 1) / per;
-  if (grid >= (1LL << 31)) return TR_E_UNSUPPORTED;
+  if (pieces >= (1LL << 31)) return TR_E_UNSUPPORTED;
   if (grid > 1 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < tr_kv_append_workspace_bytes(cache))) return TR_E_INVAL;
   rc = tr_check_device();
   if (rc != TR_OK) return rc;
   const dim3 g((unsigned)grid, (unsigned)c.B);
   cudaStream_t s = (cudaStream_t)stream;
-  if (e4m3)
-    append_kernel<true><<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count, (unsigned *)ws,
-                                                     tr_status_dev());
+  auto run = [&](auto kernel) {
+    kernel<<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count, (unsigned *)ws,
+                                        tr_status_dev());
+  };
+  if (cache->d == 64)
+    e4m3 ? run(append_kernel<true, 64>) : run(append_kernel<false, 64>);
   else
-    append_kernel<false><<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count,
-                                                      (unsigned *)ws, tr_status_dev());
+    e4m3 ? run(append_kernel<true, 128>) : run(append_kernel<false, 128>);
   TR_LAUNCH_CHECK();
   return TR_OK;
 }
@@ -299,15 +401,40 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   if (c.Hkv > 65535) return TR_E_UNSUPPORTED;
   rc = tr_check_device();
   if (rc != TR_OK) return rc;
-  int32_t *old_len = (int32_t *)((char *)ws + keep_bytes(c, budget));
+  int32_t *keep = (int32_t *)ws, *old_len = (int32_t *)((char *)ws + keep_bytes(c, budget));
   cudaStream_t s = (cudaStream_t)stream;
+  // CTAs per (sequence, KV head): more where there are few of these and their rows are many
+  const long long pairs = (long long)c.B * c.Hkv;
+  int cs = 1;
+  while (cs < 8 && c.cap / (2 * cs) >= 4096 && pairs * 2 * cs <= 4 * tr_sm_count()) cs *= 2;
+  const long long slice = ((c.cap + cs - 1) / cs + 31) & ~31LL;
+  const int held = slice <= kSelMaxKeys ? (int)slice : 0;
+  TR_TRY_CUDA(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.Hkv * cs, c.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)held * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   // with a budget that the cache cannot exceed this still reports bad lengths
-  evict_select_kernel<<<dim3(c.Hkv, c.B), kSelThreads, 0, s>>>(c, budget, recent, (int32_t *)ws, old_len,
-                                                               tr_status_dev());
-  TR_LAUNCH_CHECK();
+  TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, evict_select_kernel, (const KvDev)c, budget, recent, held, keep, old_len,
+                                 tr_status_dev()));
   if (budget < c.cap) {
-    evict_move_kernel<<<dim3(2 * c.row_bytes / kPartBytes, c.Hkv, c.B), kMoveThreads, 0, s>>>(
-        c, budget, (const int32_t *)ws, old_len);
+    // the widest part that still gives every SM four CTAs, else the narrowest
+    const int row = c.row_bytes;
+    int part = row;
+    while (part > 32 && pairs * 2 * (row / part) < 4LL * tr_sm_count()) part /= 2;
+    const dim3 grid(2 * (row / part) + 1, c.Hkv, c.B);
+    auto run = [&](auto kernel) { kernel<<<grid, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len); };
+    if (part == 256) run(evict_move_kernel<256>);
+    else if (part == 128) run(evict_move_kernel<128>);
+    else if (part == 64) run(evict_move_kernel<64>);
+    else run(evict_move_kernel<32>);
     TR_LAUNCH_CHECK();
   }
   return TR_OK;
