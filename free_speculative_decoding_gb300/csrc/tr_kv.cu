@@ -19,24 +19,21 @@ constexpr int kAppendUnroll = 4;  // 16-byte pieces of K and of V per thread
 
 // x / s rounded to the nearest fp32, as far as its rounding to e4m3 can tell, from
 // r = RN(1 / s): q0 = x r, q = q0 + r (x - q0 s) (Markstein 1990: with fused
-// multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60] and
-// |x| <= 1024 s nothing overflows, and where a remainder underflows the
-// quotient is below 2^-40, which rounds to 0 either way.
+// multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60] a q0 of
+// 1024 or more (infinite, too) is past 448 as it is, and where the remainder
+// underflows the quotient is below 2^-40, which rounds to 0 either way.
 struct Scale {
-  float s, r, most;
+  float s, r;
   bool tame;
   __device__ __forceinline__ explicit Scale(float v) {
     s = v;
     r = __frcp_rn(v);
-    most = 1024.f * v;
     tame = v >= 0x1p-60f && v <= 0x1p60f;
   }
   __device__ __forceinline__ float of(float x) const {
     if (!tame) return __fdiv_rn(x, s);
-    x = x > most ? most : x;  // beyond 448 in any case; NaN passes
-    x = x < -most ? -most : x;
     const float q = x * r;
-    return fmaf(fmaf(-q, s, x), r, q);
+    return fabsf(q) >= 1024.f ? q : fmaf(fmaf(-q, s, x), r, q);
   }
 };
 
@@ -53,66 +50,76 @@ __device__ __forceinline__ uint2 e4m3_of(const uint4 &x, const Scale &sc) {
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
-// One thread per 16-byte piece of a new row (8 elements), K and V together.
-// Every CTA of a sequence decides alike whether the sequence can take its
-// rows; the last one to finish advances L[b], so that none reads a changed
-// length.
-template <bool E4M3, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, const uint4 *Kn, const uint4 *Vn, int T,
-                                                                const int32_t *count, unsigned *counters,
-                                                                unsigned *status) {
-  const int b = blockIdx.y;
-  const int Lb = c.L[b], n = count ? count[b] : T;
+// Whether a sequence can take its rows (the same answer in every thread of the
+// block; contains a barrier): the rows to copy, or -1 with the status bit set.
+__device__ __forceinline__ int append_rows(const KvDev &c, int b, int Lb, int n, int T, unsigned *status) {
   const bool bad_len = Lb < 0 || Lb > c.cap || n < 0 || n > T;
   const bool full = !bad_len && n > c.cap - Lb;
-  bool bad_page = false;
-  if (!bad_len && !full) bad_page = kv_bad_pages(c, b, Lb, Lb + n);
-  if (!bad_len && !full && !bad_page) {
-    constexpr int kPieces = D / 8, kOut = E4M3 ? 8 : 16;  // of a row; bytes of a piece in the cache
-    const unsigned total = (unsigned)n * c.Hkv * kPieces;
-    const long long base = (long long)b * T * c.Hkv * kPieces;
-    const unsigned i0 = blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
-    uint4 kx[kAppendUnroll], vx[kAppendUnroll];
+  const bool bad_page = kv_bad_pages(c, b, Lb, bad_len || full ? Lb : Lb + n);
+  if (!bad_len && !full && !bad_page) return n;
+  if (threadIdx.x == 0) tr_flag(status, bad_len ? TR_DEV_BAD_LENGTH : full ? TR_DEV_CACHE_FULL : TR_DEV_BAD_PAGE);
+  return -1;
+}
+
+// The checks of all sequences and their new lengths; what append_kernel has to
+// copy goes to todo[b] = (old length, rows).
+__global__ void __launch_bounds__(kAppendThreads) append_plan_kernel(const KvDev c, int T, const int32_t *count,
+                                                                     int2 *todo, unsigned *status) {
+  const int b = blockIdx.x, Lb = c.L[b];
+  const int n = append_rows(c, b, Lb, count ? count[b] : T, T, status);
+  if (threadIdx.x == 0) {
+    todo[b] = make_int2(Lb, max(n, 0));
+    if (n > 0) c.L[b] = Lb + n;
+  }
+}
+
+// One thread per 16-byte piece of a new row (8 elements), K and V together.
+// todo: the plan kernel's; NULL when a sequence's rows are one CTA's work (a
+// decoding step), which then checks and advances the length itself.
+template <bool E4M3, int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, const uint4 *Kn, const uint4 *Vn, int T,
+                                                                const int32_t *count, const int2 *todo,
+                                                                unsigned *status) {
+  constexpr int kPieces = D / 8, kOut = E4M3 ? 8 : 16;  // of a row; bytes of a piece in the cache
+  const int b = blockIdx.y;
+  int Lb, n;
+  if (todo) {
+    const int2 x = todo[b];
+    Lb = x.x;
+    n = x.y;
+  } else {
+    Lb = c.L[b];
+    n = append_rows(c, b, Lb, count ? count[b] : T, T, status);  // its barrier lies between reads and write of L
+    if (threadIdx.x == 0 && n > 0) c.L[b] = Lb + n;
+  }
+  if (n <= 0) return;
+  const unsigned total = (unsigned)n * c.Hkv * kPieces;
+  const long long base = (long long)b * T * c.Hkv * kPieces;
+  const unsigned i0 = blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
+  uint4 kx[kAppendUnroll], vx[kAppendUnroll];
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const unsigned i = i0 + u * kAppendThreads;
-      if (i < total) {
-        kx[u] = __ldcs(Kn + base + i);
-        vx[u] = __ldcs(Vn + base + i);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const unsigned i = i0 + u * kAppendThreads;
-      if (i >= total) continue;
-      const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
-      const int h = (int)(th - tok * c.Hkv), p = Lb + (int)tok;
-      const long long at = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * kOut;
-      if constexpr (E4M3) {
-        *reinterpret_cast<uint2 *>(c.K + at) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + h)));
-        *reinterpret_cast<uint2 *>(c.V + at) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + h)));
-      } else {
-        *reinterpret_cast<uint4 *>(c.K + at) = kx[u];
-        *reinterpret_cast<uint4 *>(c.V + at) = vx[u];
-      }
-      if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] = 0.f;
+  for (int u = 0; u < kAppendUnroll; ++u) {
+    const unsigned i = i0 + u * kAppendThreads;
+    if (i < total) {
+      kx[u] = __ldcs(Kn + base + i);
+      vx[u] = __ldcs(Vn + base + i);
     }
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned G = gridDim.x;
-    bool last = true;
-    if (G > 1) {
-      __threadfence();
-      last = atomicAdd(&counters[b], 1u) == G - 1;
+#pragma unroll
+  for (int u = 0; u < kAppendUnroll; ++u) {
+    const unsigned i = i0 + u * kAppendThreads;
+    if (i >= total) continue;
+    const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
+    const int h = (int)(th - tok * c.Hkv), p = Lb + (int)tok;
+    const long long at = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * kOut;
+    if constexpr (E4M3) {
+      *reinterpret_cast<uint2 *>(c.K + at) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + h)));
+      *reinterpret_cast<uint2 *>(c.V + at) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + h)));
+    } else {
+      *reinterpret_cast<uint4 *>(c.K + at) = kx[u];
+      *reinterpret_cast<uint4 *>(c.V + at) = vx[u];
     }
-    if (last) {
-      if (bad_len) tr_flag(status, TR_DEV_BAD_LENGTH);
-      else if (full) tr_flag(status, TR_DEV_CACHE_FULL);
-      else if (bad_page) tr_flag(status, TR_DEV_BAD_PAGE);
-      else c.L[b] = Lb + n;
-      if (G > 1) counters[b] = 0u;
-    }
+    if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] = 0.f;
   }
 }
 
@@ -127,13 +134,12 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 40960;  // of a CTA's slice, in shared memory
 constexpr int kMoveThreads = 512;
-constexpr int kMoveUnroll = 4;
 
 // Order of the scores: larger first, -0 as +0, NaN below everything.
 __device__ __forceinline__ uint32_t score_key(float s) { return s != s ? 0u : tr_ord(s); }
 
 struct SelSmem {
-  unsigned hist[3][kSelBins];
+  __align__(16) unsigned hist[3][kSelBins];
   unsigned wsum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
   unsigned bin, need;
   unsigned gt, eq;  // the CTA's rows above and at the edge
@@ -174,6 +180,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
   const bool held = slice <= slice_keys;
   for (int i = threadIdx.x; i < 3 * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   if (held)
+#pragma unroll 8
     for (int i = threadIdx.x; i < len; i += kSelThreads) keys[i] = score_key(sc[i]);
   auto key_at = [&](int i) { return held ? keys[i] : score_key(sc[i]); };
   __syncthreads();
@@ -186,17 +193,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
     unsigned *hist = s.hist[pass];
     for (int i = threadIdx.x; i < len; i += kSelThreads) {
       const unsigned key = key_at(i);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & low], 1u);
+      if ((key & mask) == prefix) atomicAdd(&hist[kSelBins - 1 - ((key >> shift) & low)], 1u);
     }
-    cluster.sync();
-    // thread i owns the bins 2047 - 4 i .. 2044 - 4 i, from the largest key down
+    // bins lie from the largest key down; thread i owns four of them
     constexpr int kOwn = kSelBins / kSelThreads;
-    const int top = kSelBins - 1 - kOwn * threadIdx.x;
     unsigned cnt[kOwn] = {}, sum = 0;
-    for (int r = 0; r < CS; ++r) {
-      const unsigned *other = cluster.map_shared_rank(hist, r);
+    uint4 *own_bins = reinterpret_cast<uint4 *>(hist) + threadIdx.x;
+    auto add = [&](const uint4 &x) {
+      cnt[0] += x.x;
+      cnt[1] += x.y;
+      cnt[2] += x.z;
+      cnt[3] += x.w;
+    };
+    if (CS == 1) {
+      __syncthreads();
+      add(*own_bins);
+    } else {
+      cluster.sync();
 #pragma unroll
-      for (int j = 0; j < kOwn; ++j) cnt[j] += other[top - j];
+      for (int r = 0; r < 8; ++r)
+        if (r < CS) add(*cluster.map_shared_rank(own_bins, r));
     }
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) sum += cnt[j];
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
     if (before < need && need <= incl) {
       int j = 0;
       while (before + cnt[j] < need) before += cnt[j++];
-      s.bin = top - j;
+      s.bin = kSelBins - 1 - (kOwn * threadIdx.x + j);
       s.need = need - before;
     }
     __syncthreads();
@@ -234,22 +250,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
     s.weq[warp] = eq;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned x = 0, y = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      x += s.wgt[w];
-      y += s.weq[w];
+  if (CS == 1) {
+    gt = eq = 0;
+  } else {
+    if (threadIdx.x == 0) {
+      unsigned x = 0, y = 0;
+      for (int w = 0; w < kSelWarps; ++w) {
+        x += s.wgt[w];
+        y += s.weq[w];
+      }
+      s.gt = x;
+      s.eq = y;
     }
-    s.gt = x;
-    s.eq = y;
+    cluster.sync();
+    gt = eq = 0;
+    for (int r = 0; r < rank; ++r) {
+      gt += *cluster.map_shared_rank(&s.gt, r);
+      eq += *cluster.map_shared_rank(&s.eq, r);
+    }
+    cluster.sync();  // no CTA of the cluster is read from here on
   }
-  cluster.sync();
-  gt = eq = 0;
-  for (int r = 0; r < rank; ++r) {
-    gt += *cluster.map_shared_rank(&s.gt, r);
-    eq += *cluster.map_shared_rank(&s.eq, r);
-  }
-  cluster.sync();  // no CTA of the cluster is read from here on
   for (int w = 0; w < warp; ++w) {
     gt += s.wgt[w];
     eq += s.weq[w];
@@ -273,8 +293,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
 // order.  Row r comes from keep[r] >= r.  Writing a batch of rows [r0, r1) can
 // only hit sources of rows < r1: their reads lie before the barrier that the write
 // waits for.  The next batch's sources lie at or behind r1, so it is read before the
-// barrier too, which keeps loads in flight while the batch is written.
-template <int PART>
+// barrier too, which keeps loads in flight while the batch is written; its
+// addresses come from keep and the page table, read one and two batches before that.
+template <int PART, int kMoveUnroll>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c, int budget, int recent,
                                                                   const int32_t *keep, const int32_t *old_len) {
   constexpr int kLanes = PART / 16, kRows = kMoveThreads / kLanes, kBatch = kRows * kMoveUnroll;
@@ -309,34 +330,47 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c,
                (threadIdx.x % kLanes) * 16;
   const int row = threadIdx.x / kLanes;
   uint4 x[2][kMoveUnroll];
-  bool moves[2][kMoveUnroll];
-  auto load = [&](int r0, uint4(&y)[kMoveUnroll], bool(&mv)[kMoveUnroll]) {
-    int src[kMoveUnroll];
+  long long from[2][kMoveUnroll];  // byte offset of the source, -1: the row stays
+  int src[kMoveUnroll];
+  auto sources = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int r = r0 + u * kRows + row;
-      src[u] = source(r);
-      mv[u] = src[u] != r;
-    }
+    for (int u = 0; u < kMoveUnroll; ++u) src[u] = source(r0 + u * kRows + row);
+  };
+  auto offsets = [&](int r0, long long(&f)[kMoveUnroll]) {
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u)
-      if (mv[u]) y[u] = *reinterpret_cast<const uint4 *>(base + kv_block(c, b, src[u]) + kv_row(c, src[u]));
+      f[u] = src[u] == r0 + u * kRows + row ? -1 : kv_block(c, b, src[u]) + kv_row(c, src[u]);
   };
-  auto store = [&](int r0, const uint4(&y)[kMoveUnroll], const bool(&mv)[kMoveUnroll]) {
+  auto load = [&](const long long(&f)[kMoveUnroll], uint4(&y)[kMoveUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u)
+      if (f[u] >= 0) y[u] = *reinterpret_cast<const uint4 *>(base + f[u]);
+  };
+  auto store = [&](int r0, const long long(&f)[kMoveUnroll], const uint4(&y)[kMoveUnroll]) {
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
       const int r = r0 + u * kRows + row;
-      if (mv[u]) *reinterpret_cast<uint4 *>(base + kv_block(c, b, r) + kv_row(c, r)) = y[u];
+      if (f[u] >= 0) *reinterpret_cast<uint4 *>(base + kv_block(c, b, r) + kv_row(c, r)) = y[u];
     }
   };
-  load(0, x[0], moves[0]);
+  // on entry of a turn: batch r0 loaded, offsets of r0 + kBatch and sources of r0 + 2 kBatch at hand
+  sources(0);
+  offsets(0, from[0]);
+  load(from[0], x[0]);
+  sources(kBatch);
+  offsets(kBatch, from[1]);
+  sources(2 * kBatch);
+  auto turn = [&](int r0, long long(&f)[kMoveUnroll], uint4(&y)[kMoveUnroll], long long(&nf)[kMoveUnroll],
+                  uint4(&ny)[kMoveUnroll]) {
+    load(nf, ny);
+    __syncthreads();
+    store(r0, f, y);
+    offsets(r0 + 2 * kBatch, f);
+    sources(r0 + 3 * kBatch);
+  };
   for (int r0 = 0; r0 < budget; r0 += 2 * kBatch) {
-    load(r0 + kBatch, x[1], moves[1]);
-    __syncthreads();
-    store(r0, x[0], moves[0]);
-    load(r0 + 2 * kBatch, x[0], moves[0]);
-    __syncthreads();
-    store(r0 + kBatch, x[1], moves[1]);
+    turn(r0, from[0], x[0], from[1], x[1]);
+    turn(r0 + kBatch, from[1], x[1], from[0], x[0]);
   }
 }
 
@@ -355,7 +389,7 @@ size_t evict_bytes(const KvDev &c, int budget) { return keep_bytes(c, budget) + 
 // ---------------------------------------------------------------------------
 
 extern "C" size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache) {
-  return cache && cache->B > 0 ? tr_align_up((size_t)cache->B * 4, 256) : 0;
+  return cache && cache->B > 0 ? tr_align_up((size_t)cache->B * sizeof(int2), 256) : 0;
 }
 
 extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t *count, const tr_kv_cache *cache,
@@ -374,9 +408,13 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
   if (rc != TR_OK) return rc;
   const dim3 g((unsigned)grid, (unsigned)c.B);
   cudaStream_t s = (cudaStream_t)stream;
+  int2 *todo = grid > 1 ? (int2 *)ws : nullptr;
+  if (todo) {
+    append_plan_kernel<<<c.B, kAppendThreads, 0, s>>>(c, T, count, todo, tr_status_dev());
+    TR_LAUNCH_CHECK();
+  }
   auto run = [&](auto kernel) {
-    kernel<<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count, (unsigned *)ws,
-                                        tr_status_dev());
+    kernel<<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count, todo, tr_status_dev());
   };
   if (cache->d == 64)
     e4m3 ? run(append_kernel<true, 64>) : run(append_kernel<false, 64>);
@@ -431,10 +469,10 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
     while (part > 32 && pairs * 2 * (row / part) < 4LL * tr_sm_count()) part /= 2;
     const dim3 grid(2 * (row / part) + 1, c.Hkv, c.B);
     auto run = [&](auto kernel) { kernel<<<grid, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len); };
-    if (part == 256) run(evict_move_kernel<256>);
-    else if (part == 128) run(evict_move_kernel<128>);
-    else if (part == 64) run(evict_move_kernel<64>);
-    else run(evict_move_kernel<32>);
+    if (part == 256) run(evict_move_kernel<256, 4>);
+    else if (part == 128) run(evict_move_kernel<128, 4>);
+    else if (part == 64) run(evict_move_kernel<64, 4>);
+    else run(evict_move_kernel<32, 8>);  // few CTAs: more in flight for each
     TR_LAUNCH_CHECK();
   }
   return TR_OK;

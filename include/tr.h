@@ -390,8 +390,8 @@ size_t tr_decode_attn_workspace_bytes(const tr_kv_cache *cache, int Hq, int accu
  * A sequence whose L[b] or count[b] is out of range (TR_DEV_BAD_LENGTH), whose
  * rows would not fit (TR_DEV_CACHE_FULL) or need a bad page (TR_DEV_BAD_PAGE)
  * is left untouched.
- * ws: tr_kv_append_workspace_bytes bytes, zeroed once before first use; every
- * call leaves its counters at zero again. */
+ * ws: tr_kv_append_workspace_bytes bytes, 16-byte aligned; its contents do not
+ * matter and nothing is kept in it between calls. */
 int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t *count, const tr_kv_cache *cache, void *ws,
                  size_t ws_bytes, tr_stream_t stream);
 size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache);

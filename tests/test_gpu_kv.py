@@ -469,9 +469,8 @@ def check_append(c, T, count):
         new[1][0, 0, 0, :4] = torch.tensor([2.0625 * s, 2.1875 * s, 2 ** -10 * s, 3 * 2 ** -10 * s])
     old = [raw(c.K).clone(), raw(c.V).clone(), c.scores.clone()]
     cnt = None if count is None else torch.tensor(count, dtype=torch.int32, device="cuda")
-    ws = c.tr.workspace(c.tr.tr_kv_append_workspace_bytes(c.cache))
+    ws = torch.full((c.tr.tr_kv_append_workspace_bytes(c.cache),), 0xA5, dtype=torch.uint8, device="cuda")
     c.tr.tr_kv_append(new[0].cuda(), new[1].cuda(), c.cache, ws, count=cnt)
-    assert not ws.any(), "the counters are left at zero"
     count = [T] * B if count is None else count
     want = [raw(c.K).clone(), raw(c.V).clone(), c.scores.clone()]
     for w, o in zip(want, old):
@@ -536,13 +535,13 @@ def test_append_bad_inputs_are_reported(tr, T):
         c.L.copy_(torch.tensor(L, dtype=torch.int32))
         tr.tr_kv_append(n, n, c.cache, ws, count=torch.tensor(cnt, dtype=torch.int32, device="cuda"))
         assert tr.tr_get_status() == bit
-        assert c.L.tolist() == L and torch.equal(raw(c.K), old) and not ws.any()
+        assert c.L.tolist() == L and torch.equal(raw(c.K), old)
     c.L.fill_(20)
     c.pt[1, 1] = -1      # the page that row 20 goes to
     c.pt[2, 0] = -1      # a page that no new row needs
     tr.tr_kv_append(n, n, c.cache, ws)
     assert tr.tr_get_status() == tr.TR_DEV_BAD_PAGE
-    assert c.L.tolist() == [20 + T, 20, 20 + T, 20 + T] and not ws.any()
+    assert c.L.tolist() == [20 + T, 20, 20 + T, 20 + T]
 
 
 def test_append_into_graph(tr):
@@ -619,6 +618,37 @@ def test_evict(tr, type, d, layout, budget, recent):
 def test_evict_long(tr, n, budget, recent):
     c = Made(tr, np.random.default_rng(31), "bf16", 64, [n, n // 2 + 1], 2, 64)
     check_evict(c, budget, recent)
+
+
+@pytest.mark.parametrize("n,budget,recent", [(400_000, 150_000, 1000), (330_000, 329_999, 5), (70_000, 1, 0)])
+def test_evict_very_long(tr, n, budget, recent):
+    """More rows than the shared memory of a whole cluster holds scores of (8 x 40960), and up to that many."""
+    c = Made(tr, np.random.default_rng(35), "e4m3", 256, [n], 1, 64)
+    c.scores.copy_((c.scores * 500).round() / 500)   # ties
+    check_evict(c, budget, recent)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 1e-3, 3e-19, 1e-25, 7e18, 2e30])
+def test_append_divides_exactly(tr, scale):
+    """Every quotient that decides between two 8-bit values: the rows lie on and next to the rounding borders."""
+    T, d = 64, 128
+    K = torch.zeros(1, 1, 128, d, device="cuda").to(TYPES["e4m3"])
+    V, L = K.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ks = torch.tensor([scale], device="cuda")
+    cache = tr.KVCache(K, V, L, k_scale=ks, v_scale=ks * 1.7)
+    grid = torch.arange(127, dtype=torch.uint8).view(TYPES["e4m3"]).double()
+    grid = torch.cat([grid, torch.tensor([480.0, 1000.0, 1025.0, 1e6], dtype=torch.float64)])
+    mid = (grid[1:] + grid[:-1]) / 2
+    x = torch.cat([grid, mid, -mid]) * float(ks)                  # borders, as near as bf16 comes
+    x = x.bfloat16().view(torch.int16)
+    x = torch.cat([x, x + 1, x - 1, x + 2]).view(torch.bfloat16)
+    rng = torch.Generator().manual_seed(1)
+    more = torch.randn(T * d - len(x), generator=rng, dtype=torch.float64) * 10 ** (torch.rand(T * d - len(x), generator=rng) * 6 - 3)
+    x = torch.cat([x, (more * float(ks)).bfloat16()]).view(1, T, 1, d)
+    tr.tr_kv_append(x.cuda(), x.cuda(), cache, tr.workspace(tr.tr_kv_append_workspace_bytes(cache)))
+    for got, s in ((K, ks), (V, ks * 1.7)):
+        want = oracle.e4m3_round((x[0, :, 0].float() / s.cpu()).numpy())
+        assert np.array_equal(got[0, 0, :T].double().cpu().numpy(), want, equal_nan=True)
 
 
 @pytest.mark.parametrize("kind", ["equal", "zeros", "few", "special", "negative", "sorted", "reversed", "tiny"])
