@@ -9,6 +9,16 @@ no arithmetic itself.  A step is
     ... the target produces logits (or hidden states) for state.tree_tok ...
     state.finish(logits=...)         # top-K, accept, update, KV commit, next tree
 
+or, without a draft (one token per sequence, the root's),
+
+    state.decode(Q, Kn, Vn)          # append the root's K/V, attention of one token
+    state.finish_decode(logits)      # top-K, update of the root's row, next root and tree
+
+and the two may alternate.  With ``budget`` the attention weights that the
+cached rows gather in decode are kept, and evict() cuts every sequence longer
+than the budget down to it.  L then no longer is a token's position: a program
+that needs positions (rotary embeddings) keeps count of them itself.
+
 Every call is asynchronous and allocation-free after construction, so whole
 loops can be captured in a CUDA graph.
 """
@@ -16,14 +26,16 @@ from __future__ import annotations
 
 import torch
 
-from . import (TR_INIT_INHERIT, TR_UPD_ALL, Tree, make_step_args, tr_get_status, tr_init_matrix, tr_retrieve,
-               tr_step, tr_step_sampled, tr_step_workspace_bytes, tr_verify_attn, tr_verify_attn_workspace_bytes,
-               workspace)
+from . import (TR_INIT_INHERIT, TR_UPD_ALL, KVCache, Tree, make_step_args, tr_accept, tr_decode_attn,
+               tr_decode_attn_workspace_bytes, tr_get_status, tr_init_matrix, tr_kv_append,
+               tr_kv_append_workspace_bytes, tr_kv_evict, tr_kv_evict_workspace_bytes, tr_retrieve, tr_step,
+               tr_step_sampled, tr_step_workspace_bytes, tr_topk, tr_topk_workspace_bytes, tr_update, tr_verify_attn,
+               tr_verify_attn_workspace_bytes, workspace)
 
 
 class TRState:
     def __init__(self, tree: Tree, B: int, V: int, m_dtype=torch.int64, Hq=0, Hkv=0, d=128, cap=0,
-                 logits_dtype=torch.float32, D=0, device="cuda"):
+                 logits_dtype=torch.float32, D=0, device="cuda", budget=0, recent=0):
         self.tree = tree
         self.B, self.V, self.K, self.N = B, V, tree.K, tree.N
         self.Dmax = tree.max_depth
@@ -48,12 +60,35 @@ class TRState:
             self.O = torch.zeros(B, self.N, Hq, d, dtype=torch.float32, **dev)
             self.ws_attn = workspace(tr_verify_attn_workspace_bytes(B, Hq, Hkv, d, cap, tree), device)
             self.scale = d ** -0.5
+            self._init_decode(budget, recent, dev)
+        elif budget:
+            raise ValueError("a budget needs a cache (Hq > 0)")
         self._args = make_step_args(tree, self.M, self.tree_tok, self.ids, self.vals, self.acc_len, self.path,
                                     self.committed, self.root, self.L,
                                     logits=torch.empty(1, V, dtype=logits_dtype, **dev) if D == 0 else None,
                                     H=torch.empty(1, max(D, 64), dtype=torch.bfloat16, **dev) if D else None,
                                     Wt=torch.empty(1, max(D, 64), dtype=torch.bfloat16, **dev) if D else None)
         self.ws_step = workspace(tr_step_workspace_bytes(self._args), device)
+
+    def _init_decode(self, budget, recent, dev):
+        """What single-token steps and eviction need."""
+        B, Hq = self.B, self.Hq
+        self.budget, self.recent = budget, recent
+        # a row that no query has looked at has gathered nothing: scores behind L are always 0
+        self.scores = torch.zeros(B, self.Hkv, self.cap, dtype=torch.float32, **dev) if budget else None
+        self.cache = KVCache(self.Kc, self.Vc, self.L, scores=self.scores)
+        self.O1 = torch.zeros(B, Hq, self.d, dtype=torch.float32, **dev)
+        self.ws_decode = workspace(tr_decode_attn_workspace_bytes(self.cache, Hq, bool(budget)), self.device)
+        self.ws_append = workspace(tr_kv_append_workspace_bytes(self.cache), self.device)
+        if budget:
+            if not 0 <= recent <= budget:
+                raise ValueError("recent must be in [0, budget]")
+            self.ws_evict = workspace(tr_kv_evict_workspace_bytes(self.cache, budget), self.device)
+        self.tree1 = Tree((0,), self.K)   # the root alone
+        self.ids1 = torch.zeros(B, self.K, dtype=torch.int32, **dev)
+        self.path1 = torch.zeros(B, 1, dtype=torch.int32, **dev)
+        self.committed1 = torch.zeros(B, 1, dtype=torch.int32, **dev)
+        self.ws_topk1 = workspace(tr_topk_workspace_bytes(B, self.V, self.K), self.device)
 
     def start(self, root, L, M_src=None, mode=TR_INIT_INHERIT, seed=0):
         """Set the roots and cache lengths, initialise M, retrieve the first tree.
@@ -64,6 +99,8 @@ class TRState:
         already is."""
         self.root.copy_(torch.as_tensor(root, dtype=torch.int32))
         self.L.copy_(torch.as_tensor(L, dtype=torch.int32))
+        if self.attention and self.scores is not None:
+            self.scores.zero_()
         if M_src is not None and M_src.dim() == 3:
             self.M.copy_(M_src)
         elif mode is not None:
@@ -86,6 +123,31 @@ class TRState:
             tr_step(a)
         else:
             tr_step_sampled(a, temperature, U)
+
+    def decode(self, Q, Kn, Vn):
+        """A step without a draft: appends the root's Kn, Vn [B, Hkv, d] to the cache
+        and attends with Q [B, Hq, d] over all its rows (the root's own among
+        them); with a budget the rows' weights are gathered."""
+        tr_kv_append(Kn.unsqueeze(1), Vn.unsqueeze(1), self.cache, self.ws_append)
+        tr_decode_attn(Q, self.cache, self.O1, self.scale, self.ws_decode, accumulate=self.scores is not None)
+        return self.O1
+
+    def finish_decode(self, logits):
+        """The end of a step without a draft, from the roots' logits [B, V]: the root's
+        row of M becomes its top-K, its first token the next root (committed1)."""
+        tr_topk(logits, self.K, self.ids1, None, self.ws_topk1, V=self.V)
+        tok = self.root.unsqueeze(1)
+        tr_update(self.M, self.tree1, tok, self.ids1)
+        tr_accept(self.tree1, tok, self.ids1, self.acc_len, self.path1, self.committed1, self.root)
+        tr_retrieve(self.M, self.tree, self.root, self.tree_tok)
+
+    def evict(self):
+        """Cuts every sequence longer than the budget down to it: the last ``recent`` rows
+        and, for each KV head, those with the most gathered weight."""
+        if self.scores is None:
+            raise ValueError("evict needs a budget")
+        tr_kv_evict(self.cache, self.budget, self.recent, self.ws_evict)
+        self.scores[:, :, self.budget:].zero_()   # rows appended there next start from nothing
 
     def status(self):
         return tr_get_status()

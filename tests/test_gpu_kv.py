@@ -741,3 +741,81 @@ def test_decoding_steps_with_eviction(tr, type, layout):
         c.check(Q, 0.125, O, lse, before)
         if max(c.lengths) > 48:
             check_evict(c, 32, 8)
+
+
+@pytest.mark.parametrize("budget", [0, 100])
+def test_engine_alternates_tree_and_single_token_steps(tr, budget):
+    """TRState: tree steps and steps without a draft on one state, evictions between them, against the oracle's loop
+    (a step without a draft is the loop's step on a one-node tree); the committed tokens are plain greedy decoding."""
+    import synth
+    from free_speculative_decoding_gb300.engine import TRState
+    from gpu_util import ATTN_TOL, gpu_start, oracle_qkv, oracle_states, rows_rel_err, target_fn
+    from synth import device as sd
+
+    w = synth.WORKLOADS["tiny"].scaled(prefix=(100, 140), B=2, Hq=8, Hkv=4, V=5000, steps=24)
+    tree, plan, plan1 = tr.Tree(w.child_counts, w.K), oracle.TreePlan(w.child_counts, w.K), oracle.TreePlan((0,), w.K)
+    st = TRState(tree, w.B, w.V, Hq=w.Hq, Hkv=w.Hkv, d=w.d, cap=w.capacity(), budget=budget, recent=20 if budget else 0)
+    sd.fill_cache(w, st)
+    gpu_start(w, st)
+    states, target, qkv = oracle_states(w), target_fn(w), oracle_qkv(w)
+    tgt, logits1 = sd.DeviceTarget(w, tree), torch.empty(w.B, w.V, device="cuda")
+    gathered = [np.zeros((w.Hkv, w.capacity())) for _ in range(w.B)]
+    evicted = 0
+    for s in range(w.steps):
+        q, kt, vt = sd.step_qkv(w, s, tree.N)
+        plain, recs = s % 3 != 0, {}
+        before = [(x.kc.copy(), x.vc.copy(), x.L) for x in states]
+        qo, ko, vo = qkv(s)
+        one = (qo[:, :1], ko[:, :1], vo[:, :1]) if plain else (qo, ko, vo)
+        oracle.tr_loop(plan1 if plain else plan, states, target, 1, w.K, qkv=lambda _: one, scale=w.d ** -0.5,
+                       on_step=lambda _, b, rec: recs.__setitem__(b, rec))
+        if plain:
+            tr.trsyn_logits(w.seed, st.tree1, st.root.unsqueeze(1), st.L, logits1)
+            O = st.decode(q[:, 0].contiguous(), kt[:, 0].contiguous(), vt[:, 0].contiguous())
+            got_O = O.cpu().numpy()[:, None]
+            st.finish_decode(logits1)
+            for b in range(w.B):
+                kc, vc, L = before[b]
+                kc[:, L], vc[:, L] = ko[b, 0], vo[b, 0]
+                _, _, W = oracle.decode_attention(qo[b, 0], kc[:, :L + 1], vc[:, :L + 1], w.d ** -0.5)
+                gathered[b][:, :L + 1] += W.reshape(w.Hkv, -1, L + 1).sum(1)
+                assert st.committed1[b].tolist() == recs[b]["committed"]
+        else:
+            got_O = st.verify(q, kt, vt).cpu().numpy()
+            st.finish(logits=tgt.logits_for(st), Kt=kt, Vt=vt)
+        for b in range(w.B):
+            assert rows_rel_err(got_O[b], recs[b]["O"]) <= ATTN_TOL
+            assert st.acc_len[b].item() == recs[b]["acc_len"]
+            assert np.array_equal(st.M[b].cpu().numpy(), states[b].M)
+            assert st.root[b].item() == states[b].root and st.L[b].item() == states[b].L
+            assert np.array_equal(st.tree_tok[b].cpu().numpy(), oracle.retrieve(states[b].M, states[b].root, plan))
+        if budget:
+            sc = st.scores.cpu().numpy()
+            for b in range(w.B):
+                assert np.allclose(sc[b], gathered[b], rtol=1e-5, atol=1e-7)
+            if s % 5 == 4:
+                lens = [x.L for x in states]
+                st.evict()
+                for b, x in enumerate(states):
+                    if x.L > budget:
+                        evicted += 1
+                        for h in range(w.Hkv):
+                            keep = oracle.evict_keep(sc[b, h, :x.L], budget, 20)
+                            for t in (x.kc, x.vc):
+                                t[h, :budget] = t[h, keep]
+                            gathered[b][h, :budget] = sc[b, h, keep]
+                        x.L = budget
+                    gathered[b][:, x.L:] = 0
+                    assert st.L[b].item() == min(lens[b], budget)
+    assert not budget or evicted >= 4
+    if not budget:
+        L0, roots = w.prefix_lengths(), synth.initial_roots(w)
+        for b in range(w.B):
+            out = states[b].emitted
+            top1 = lambda pos, tok: np.argmax(target(b, np.array([pos]), np.array([tok]))[0])
+            assert out == oracle.greedy_decode(top1, int(roots[b]), int(L0[b]), len(out))
+    with pytest.raises(ValueError):
+        TRState(tree, 1, 100, budget=5)
+    if not budget:
+        with pytest.raises(ValueError, match="budget"):
+            st.evict()
