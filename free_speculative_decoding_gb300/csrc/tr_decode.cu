@@ -46,9 +46,8 @@ using sm100::ex2;
 using sm100::smem_u32;
 
 constexpr int kMaxB = 1024;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRingBytes = 24 * 1024;   // per warp
+constexpr int kMaxWarps = 12;            // of any split kernel's CTA
+constexpr int kRings = 192 * 1024;       // bytes of a CTA's rings
 constexpr int kMinRows = 32;            // cached rows of a warp's range, about, at least
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;            // the running maximum follows once it is 2^8 behind
@@ -78,7 +77,10 @@ struct Shape {
   static constexpr int KB = ROW == 256 ? 1 : 2;
   static constexpr int kTile = 16 * KB;
   static constexpr int STAGE = 2 * kTile * ROW;         // K tile, V tile
-  static constexpr int STAGES = kRingBytes / STAGE;
+  static constexpr int WARPS = F8 && D == 128 ? 12 : 8;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int RING = kRings / WARPS;           // bytes of a warp's ring
+  static constexpr int STAGES = RING / STAGE;
   static constexpr int VW = F8 && D == 128 ? 16 : 8;    // columns of a lane's piece of V
   static constexpr int VS = D / (8 * VW);               // pieces of V per lane and row
   static constexpr int NT = D / 8;                      // column blocks of O
@@ -181,34 +183,35 @@ __device__ __forceinline__ int swz_v(int r, int ch) {
 struct Cut {
   int warps, per;  // per CTA, tiles per warp
 };
-__device__ __forceinline__ Cut cut_of(int T, int ctas, int kTile) {
+__device__ __forceinline__ Cut cut_of(int T, int ctas, int kTile, int most) {
   const int min_tiles = max(kMinRows / kTile, 1);
   Cut c;
-  c.warps = min(max((T + ctas * min_tiles - 1) / (ctas * min_tiles), 1), kWarps);
+  c.warps = min(max((T + ctas * min_tiles - 1) / (ctas * min_tiles), 1), most);
   c.per = max((T + ctas * c.warps - 1) / (ctas * c.warps), 1);
   return c;
 }
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const DecodeArgs a) {
+__global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const KvDev c, const DecodeArgs a) {
   using S = Shape<TYPE, D>;
-  constexpr int kTile = S::kTile, KB = S::KB;
+  constexpr int kTile = S::kTile, KB = S::KB, kWarps = S::WARPS, kThreads = S::THREADS;
+  constexpr int kOwn = (kMaxB + kThreads - 1) / kThreads;  // sequences of a thread, in the prefix sum
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
   __shared__ float2 jml[kWarps][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   // lengths and, for one head, the tiles before each sequence
-  int mine[kMaxB / kThreads], sum = 0;
+  int mine[kOwn], sum = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxB / kThreads; ++i) {
-    const int b = threadIdx.x * (kMaxB / kThreads) + i;
+  for (int i = 0; i < kOwn; ++i) {
+    const int b = threadIdx.x * kOwn + i;
     int L = b < c.B ? c.L[b] : 0;
     if (L < 0 || L > c.cap) {
       if (blockIdx.x == 0 && blockIdx.y == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
       L = 0;
     }
-    Ls[b] = L;
+    if (b < kMaxB) Ls[b] = L;
     mine[i] = sum;
     sum += (L + kTile - 1) / kTile;
   }
@@ -223,11 +226,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
   int before = incl - sum;
   for (int w = 0; w < warp; ++w) before += wsum[w];
 #pragma unroll
-  for (int i = 0; i < kMaxB / kThreads; ++i) tp[threadIdx.x * (kMaxB / kThreads) + i] = before + mine[i];
-  if (threadIdx.x == kThreads - 1) tp[kMaxB] = before + sum;
+  for (int i = 0; i < kOwn; ++i)
+    if (threadIdx.x * kOwn + i <= kMaxB) tp[threadIdx.x * kOwn + i] = before + mine[i];
+  if (threadIdx.x == kThreads - 1 && kThreads * kOwn == kMaxB) tp[kMaxB] = before + sum;
   __syncthreads();
   const int T = tp[c.B] * c.Hkv;
-  const Cut cut = cut_of(T, gridDim.x, kTile);
+  const Cut cut = cut_of(T, gridDim.x, kTile, kWarps);
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i <= c.B + 2; i += kThreads) a.plan[i] = i == 0 ? cut.per : i == 1 ? cut.warps : tp[i - 2];
   // sequences without rows belong to no warp's range
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
   const int w = blockIdx.x * cut.warps + warp;
   const int t0 = warp < cut.warps ? (int)min((long long)c1, c0 + (long long)warp * cut.per) : c1;
   const int t1 = warp < cut.warps ? min(c1, t0 + cut.per) : c1;
-  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+  const uint32_t ring = smem_u32(smem) + warp * S::RING;
   const int row0 = blockIdx.y * MT;  // first query head of this row tile inside its group
 
   // the pair of the CTA's first tile; joined: it takes the CTA's whole range
@@ -419,14 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
         }
       }
 
-    // logits in log2 units; rows behind the last get none
+    // softmax weights, relative to a maximum that follows lazily; rows behind the last get none
     const int rows = cur.L - cur.kt * kTile;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int j = 0; j < 2 * KB; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) s[j][2 * r + e] *= mul[r];
       if (rows < kTile) {
 #pragma unroll
         for (int j = 0; j < 2 * KB; ++j)
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
         if (row0 + g + r * 8 < a.G)
 #pragma unroll
           for (int j = 0; j < 2 * KB; ++j)
-            *reinterpret_cast<float2 *>(logits[r] + j * 8) = make_float2(s[j][2 * r], s[j][2 * r + 1]);
+            *reinterpret_cast<float2 *>(logits[r] + j * 8) = make_float2(s[j][2 * r] * mul[r], s[j][2 * r + 1] * mul[r]);
         logits[r] += kTile;
       }
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * mul[r];
       const bool grow = mx > m[r] + (kOff + kLazy);
       if (__any_sync(~0u, grow)) {
         const float mn = grow ? mx - kOff : m[r];
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
       for (int j = 0; j < 2 * KB; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[j][2 * r + e] = ex2(s[j][2 * r + e] - base);
+          s[j][2 * r + e] = ex2(fmaf(s[j][2 * r + e], mul[r], -base));
           l[r] += s[j][2 * r + e];
         }
     }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
     l[r] += __shfl_xor_sync(~0u, l[r], 2);
     if (t == 0) jml[warp][g + r * 8] = make_float2(m[r], l[r]);
     if (t0 >= t1 || row0 + g + r * 8 >= a.G) continue;
-    float *dst = rings + warp * (kRingBytes / 4) + (g + r * 8) * D;
+    float *dst = rings + warp * (S::RING / 4) + (g + r * 8) * D;
 #pragma unroll
     for (int v = 0; v < S::VS; ++v)
 #pragma unroll
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const KvDev c, const
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < used; ++k) {
       const float f = jml[k][row].x == -INFINITY ? 0.f : ex2(jml[k][row].x - M);
-      const float4 x = *reinterpret_cast<const float4 *>(rings + k * (kRingBytes / 4) + row * D + col);
+      const float4 x = *reinterpret_cast<const float4 *>(rings + k * (S::RING / 4) + row * D + col);
       sum += jml[k][row].y * f;
       y.x += x.x * f;
       y.y += x.y * f;
@@ -823,7 +823,7 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   p.row_tiles = (G + p.MT - 1) / p.MT;
   const long long most = (long long)c.B * c.Hkv * ((c.cap + kMinRows - 1) / kMinRows);  // ranges worth a warp
   p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, most));
-  const size_t rows = (size_t)p.row_tiles * p.grid * kWarps * 2 * p.MT;
+  const size_t rows = (size_t)p.row_tiles * p.grid * kMaxWarps * 2 * p.MT;
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
   p.plan_off = p.lse_off + tr_align_up((size_t)c.B * Hq * 4, 256);
@@ -834,9 +834,8 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
 
 template <int TYPE, int D, int MT>
 int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
-  constexpr int bytes = kWarps * kRingBytes;
-  TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  split_kernel<TYPE, D, MT><<<grid, kThreads, bytes, s>>>(c, a);
+  TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
+  split_kernel<TYPE, D, MT><<<grid, Shape<TYPE, D>::THREADS, kRings, s>>>(c, a);
   TR_LAUNCH_CHECK();
   return TR_OK;
 }
@@ -846,7 +845,7 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
   const int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  join_kernel<D><<<(unsigned)(c.B * a.Hq), kFinThreads, 0, s>>>(c, a, p.grid * kWarps, p.MT);
+  join_kernel<D><<<(unsigned)(c.B * a.Hq), kFinThreads, 0, s>>>(c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
   TR_LAUNCH_CHECK();
   if (a.accumulate) {
     if (a.G > 8)
