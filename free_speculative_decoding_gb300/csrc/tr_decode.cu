@@ -33,7 +33,6 @@
 // An 8-bit row is widened to fp16 (exact); Q is scaled by a power of two per
 // head so that narrowing bf16 to fp16 is exact for all but negligible elements.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
@@ -123,9 +122,16 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t half2_of(uint32_t e4m3x2) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Two e4m3 values widened to fp16 (exact): those in the low, or high, half of w.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           for (int f = 0; f < 4; ++f) {
             const int at = e * 8 + f * 2;
             mma(s[j], q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u,
-                half2_of(y[f] & 0xFFFFu), half2_of(y[f] >> 16), false);
+                widen_lo(y[f]), widen_hi(y[f]), false);
           }
         } else {
           const int at = e * 4;
@@ -535,8 +541,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
             for (int f = 0; f < 2; ++f) {
               const uint32_t sel = f ? 0x7362 : 0x5140;
               const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
-              pv(o[v * S::VW + e * 4 + f * 2], half2_of(lo & 0xFFFFu), half2_of(hi & 0xFFFFu));
-              pv(o[v * S::VW + e * 4 + f * 2 + 1], half2_of(lo >> 16), half2_of(hi >> 16));
+              pv(o[v * S::VW + e * 4 + f * 2], widen_lo(lo), widen_lo(hi));
+              pv(o[v * S::VW + e * 4 + f * 2 + 1], widen_hi(lo), widen_hi(hi));
             }
           } else {
             pv(o[v * S::VW + e * 2], __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
