@@ -281,44 +281,37 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   auto issue = [&](int stage) {
     if (t_ld < t1) {
       const uint32_t dk = ring + stage * S::STAGE, dv = dk + kTile * S::ROW;
-      const int p0 = ld.kt * kTile, ch = lane % S::CPR;
+      const int p0 = ld.kt * kTile, ch = lane % S::CPR, r0 = lane / S::CPR, left = ld.L - p0;
       const long long head = (long long)ld.h * c.head_stride + ch * 16;
-      if (whole_tile) {
-        const int pg = __shfl_sync(~0u, page, 0);
-        const bool good = (unsigned)pg < (unsigned)blocks;
-        if (!good) tr_flag(a.status, TR_DEV_BAD_PAGE);
-        const long long at = (long long)pg * c.block_stride + head + kv_row(c, p0 + lane / S::CPR);
-        const char *k = c.K + at, *v = c.V + at;
-        const int left = good ? ld.L - p0 : 0;
-        const long long next = (32 / S::CPR) * c.row_stride;
-        if (left >= kTile) {
+      constexpr int kCopies = KB * S::CPR / 2, kStep = 32 / S::CPR;  // per lane and tensor; rows apart
+      const bool bad = lane < min(kTile, left) && (unsigned)page >= (unsigned)blocks;
+      if (left >= kTile && !__any_sync(~0u, bad)) {
+        if (whole_tile) {
+          const long long at = (long long)__shfl_sync(~0u, page, 0) * c.block_stride + head + kv_row(c, p0 + r0);
+          const char *k = c.K + at, *v = c.V + at;
 #pragma unroll
-          for (int i = 0; i < KB * S::CPR / 2; ++i) {
-            const int r = lane / S::CPR + i * (32 / S::CPR);
+          for (int i = 0; i < kCopies; ++i) {
+            const int r = r0 + i * kStep;
             copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, k);
             copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, v);
-            k += next;
-            v += next;
+            k += kStep * c.row_stride;
+            v += kStep * c.row_stride;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < KB * S::CPR / 2; ++i) {
-            const int r = lane / S::CPR + i * (32 / S::CPR);
-            const bool valid = r < left;
-            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, valid ? k + i * next : c.K, valid);
-            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, valid ? v + i * next : c.V, valid);
+          for (int i = 0; i < kCopies; ++i) {
+            const int r = r0 + i * kStep;
+            const long long at = (long long)__shfl_sync(~0u, page, r) * c.block_stride + head + kv_row(c, p0 + r);
+            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at);
+            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at);
           }
         }
-      } else {
+      } else {  // a pair's last tile, or a page that is not there: row by row
+        if (bad) tr_flag(a.status, TR_DEV_BAD_PAGE);
 #pragma unroll
-        for (int i = 0; i < KB * S::CPR / 2; ++i) {
-          const int r = lane / S::CPR + i * (32 / S::CPR);
-          const int pg = __shfl_sync(~0u, page, r);
-          bool valid = p0 + r < ld.L;
-          if (valid && (unsigned)pg >= (unsigned)blocks) {
-            tr_flag(a.status, TR_DEV_BAD_PAGE);
-            valid = false;
-          }
+        for (int i = 0; i < kCopies; ++i) {
+          const int r = r0 + i * kStep, pg = __shfl_sync(~0u, page, r);
+          const bool valid = r < left && (unsigned)pg < (unsigned)blocks;
           const long long at = valid ? (long long)pg * c.block_stride + head + kv_row(c, p0 + r) : 0;
           copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
           copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at, valid);
