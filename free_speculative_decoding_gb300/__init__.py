@@ -415,18 +415,22 @@ class KVCache:
         c.scores_ld = scores.shape[2] if scores is not None else 0
         self.struct = c
         self._ref = ctypes.byref(c)
+        self._index = K.get_device()
 
     def _stream(self):
-        if self.device.index != torch.cuda.current_device():
+        if self._index != torch.cuda.current_device():
             raise ValueError("the cache must live on the current CUDA device")
-        return _stream()
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def _arg(self, t, name, dtype):
+        # one step of decoding is a few microseconds on the device: no objects are made here
         if t.dtype != dtype:
             raise ValueError("%s must be %s" % (name, dtype))
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError("%s must live on the cache's device" % name)
-        return _ptr(t)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
 
 
 def tr_decode_attn_workspace_bytes(cache, Hq, accumulate=False):

@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tr_kv.cuh"
 #include "tr_sm100.cuh"
@@ -97,6 +98,11 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// Programmatic dependent launch: the next kernel of the call may be set up from
+// here on; it waits for this one's results with wait_for_previous.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 16 bytes from global to shared memory; of the second form 16 zero bytes where not valid.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -206,6 +212,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
   __shared__ float2 jml[kWarps][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  let_next_start();
 
   // lengths and, for one head, the tiles before each sequence
   int mine[kOwn], sum = 0;
@@ -704,6 +711,8 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
   __shared__ float4 acc[kFinWarps][D / 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
+  let_next_start();
+  wait_for_previous();
   Parts u;
   const int parts = parts_of(c, a, b, h, u);
   if (parts <= 1) return;  // empty, or finished by one warp or CTA
@@ -774,6 +783,7 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   __shared__ float4 sums[SPLIT ? kFinWarps : 1][32];
   const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int L = c.L[b];
+  wait_for_previous();
   if (L < 0 || L > c.cap || (int)blockIdx.x * kRows >= L) return;
   const int p = blockIdx.x * kRows + (SPLIT ? lane : threadIdx.x) * 4;
   const long long hq = (long long)b * a.Hq + (long long)h * a.G;
@@ -831,9 +841,31 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   return p;
 }
 
+// A launch that may be set up while the previous kernel on the stream still runs.
+template <typename... P, typename... A>
+int launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return TR_OK;
+}
+
 template <int TYPE, int D, int MT>
 int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
-  TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  TR_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
   split_kernel<TYPE, D, MT><<<grid, Shape<TYPE, D>::THREADS, kRings, s>>>(c, a);
   TR_LAUNCH_CHECK();
   return TR_OK;
@@ -842,18 +874,12 @@ int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a)
 template <int TYPE, int D>
 int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
-  const int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
+  int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  join_kernel<D><<<(unsigned)(c.B * a.Hq), kFinThreads, 0, s>>>(c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
-  TR_LAUNCH_CHECK();
-  if (a.accumulate) {
-    if (a.G > 8)
-      score_kernel<true><<<dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
-    else
-      score_kernel<false><<<dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, 0, s>>>(c, a);
-    TR_LAUNCH_CHECK();
-  }
-  return TR_OK;
+  rc = launch_next(join_kernel<D>, dim3(c.B * a.Hq), kFinThreads, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
+  if (rc != TR_OK || !a.accumulate) return rc;
+  return a.G > 8 ? launch_next(score_kernel<true>, dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, s, c, a)
+                 : launch_next(score_kernel<false>, dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, s, c, a);
 }
 
 template <int TYPE>

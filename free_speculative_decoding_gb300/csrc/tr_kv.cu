@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tr_kv.cuh"
 
@@ -447,7 +448,13 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   while (cs < 8 && c.cap / (2 * cs) >= 4096 && pairs * 2 * cs <= 4 * tr_sm_count()) cs *= 2;
   const long long slice = ((c.cap + cs - 1) / cs + 31) & ~31LL;
   const int held = slice <= kSelMaxKeys ? (int)slice : 0;
-  TR_TRY_CUDA(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4));
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  TR_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    TR_TRY_CUDA(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4));
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.Hkv * cs, c.B);
   cfg.blockDim = dim3(kSelThreads);
