@@ -4,9 +4,6 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <algorithm>
-#include <atomic>
-
 #include "tr_kv.cuh"
 
 namespace {
@@ -132,73 +129,113 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;
-constexpr int kSelMaxKeys = 40960;  // of a CTA's slice, in shared memory
+constexpr int kSelMost = 32;  // keys of a thread in registers, at most
 constexpr int kMoveThreads = 512;
 
 // Order of the scores: larger first, -0 as +0, NaN below everything.
 __device__ __forceinline__ uint32_t score_key(float s) { return s != s ? 0u : tr_ord(s); }
 
+template <int BITS>
 struct SelSmem {
-  __align__(16) unsigned hist[3][kSelBins];
-  unsigned wsum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
+  __align__(16) unsigned hist[(32 + BITS - 1) / BITS][1 << BITS];
+  unsigned wsum[kSelWarps];
+  unsigned cnt[kSelMost * kSelWarps];  // (rows above the edge << 16) + rows at it, of 32 rows
+  unsigned wgt[kSelWarps], weq[kSelWarps];
   unsigned bin, need;
-  unsigned gt, eq;  // the CTA's rows above and at the edge
+  unsigned gt, eq;  // of the CTA
 };
+
+// Inclusive sum over the block's threads (two barriers).
+__device__ __forceinline__ unsigned block_sum(unsigned v, unsigned *wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) wsum[warp] = v;
+  __syncthreads();
+  unsigned w = lane < kSelWarps ? wsum[lane] : 0u;
+#pragma unroll
+  for (int o = 1; o < kSelWarps; o <<= 1) {
+    const unsigned x = __shfl_up_sync(~0u, w, o);
+    if (lane >= o) w += x;
+  }
+  w = __shfl_sync(~0u, w, max(warp - 1, 0));
+  __syncthreads();
+  return v + (warp ? w : 0u);
+}
 
 // One cluster per (KV head, sequence): finds the key of the k-th largest score
 // among the rows before the protected ones and writes the k positions that stay,
-// ascending, to keep.  Each CTA holds one slice of the keys in shared memory
-// (read from global again in every pass where the slice is too long).  The key
-// is found by a radix select, 11 + 11 + 10 bits a pass: the CTAs' histograms are
-// added through distributed shared memory and every CTA walks the sum alike.  A
+// ascending, to keep.  Each CTA holds one slice of the keys, KPT to a thread in
+// registers (a slice that is longer is read again in every pass).  The key is
+// found by a radix select, BITS a pass: the CTAs' histograms are added through
+// distributed shared memory and every CTA walks the sum alike.  11 bits (three
+// passes) suit one CTA, 8 bits (four) a cluster, whose exchange is an eighth.  A
 // row's place in keep is the number of rows above the edge before it plus the
-// number of edge rows taken before it, so each warp places its stretch alone.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c, int budget, int recent, int slice_keys,
-                                                                   int32_t *keep, int32_t *old_len, unsigned *status) {
-  extern __shared__ unsigned keys[];
-  __shared__ SelSmem s;
+// number of edge rows taken before it.  split[pair], where asked for, gets the
+// number of kept rows at positions below the budget.
+template <int KPT, int BITS>
+__global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
+    evict_select_kernel(const KvDev c, int budget, int recent, int32_t *keep, int32_t *old_len, int32_t *split,
+                        unsigned *status) {
+  constexpr int kSelBins = 1 << BITS, kPasses = (32 + BITS - 1) / BITS;
+  __shared__ SelSmem<BITS> s;
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int h = blockIdx.x / CS, b = blockIdx.y;
   const int Lb = c.L[b];
   const bool bad_len = Lb < 0 || Lb > c.cap;
   const bool active = !bad_len && Lb > budget;
+  const int n = Lb - recent, k = budget - recent;  // k < n where active
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = active ? ((n + CS - 1) / CS + 31) & ~31 : 0;
+  const int lo = active ? min(n, rank * slice) : 0, len = active ? min(n - lo, slice) : 0;
+  const float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld + lo;
+  const bool held = slice <= KPT * kSelThreads;
+  unsigned keys[KPT];  // rows threadIdx.x + j * kSelThreads, read while the pages are looked over
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const int i = threadIdx.x + j * kSelThreads;
+      keys[j] = i < len ? __float_as_uint(sc[i]) : 0u;
+    }
+  }
+  for (int i = threadIdx.x; i < kPasses * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   const bool bad_page = active && kv_bad_pages(c, b, 0, Lb);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     old_len[b] = active && !bad_page ? Lb : -1;
     if (bad_len) tr_flag(status, TR_DEV_BAD_LENGTH);
     if (bad_page) tr_flag(status, TR_DEV_BAD_PAGE);
   }
-  const int n = Lb - recent, k = budget - recent;  // k < n where active
-  if (!active || bad_page || k == 0) return;       // the same for the whole cluster
-  const float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
+  if (!active || bad_page || k == 0) return;  // the same for the whole cluster
   keep += ((long long)b * c.Hkv + h) * budget;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slice = ((n + CS - 1) / CS + 31) & ~31;
-  const int lo = min(n, rank * slice), len = min(n - lo, slice);
-  sc += lo;
-  const bool held = slice <= slice_keys;
-  for (int i = threadIdx.x; i < 3 * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
-  if (held)
-#pragma unroll 8
-    for (int i = threadIdx.x; i < len; i += kSelThreads) keys[i] = score_key(sc[i]);
-  auto key_at = [&](int i) { return held ? keys[i] : score_key(sc[i]); };
-  __syncthreads();
-  // key of the k-th largest: `prefix` holds its leading bits, `need` how many
-  // of the rows that share them are still to be taken
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) keys[j] = score_key(__uint_as_float(keys[j]));
+  }
+  // `prefix` holds the leading bits of the key of the k-th largest, `need` how
+  // many of the rows that share them are still to be taken
   unsigned prefix = 0, need = k;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const unsigned mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u, low = pass == 2 ? 1023u : 2047u;
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int shift = max(32 - BITS * (pass + 1), 0), width = min(BITS, 32 - BITS * pass);
+    const unsigned mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + width), low = (1u << width) - 1u;
     unsigned *hist = s.hist[pass];
-    for (int i = threadIdx.x; i < len; i += kSelThreads) {
-      const unsigned key = key_at(i);
+    auto count = [&](unsigned key) {
       if ((key & mask) == prefix) atomicAdd(&hist[kSelBins - 1 - ((key >> shift) & low)], 1u);
+    };
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (threadIdx.x + j * kSelThreads < len) count(keys[j]);
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < len; i += kSelThreads) count(score_key(sc[i]));
     }
-    // bins lie from the largest key down; thread i owns four of them
-    constexpr int kOwn = kSelBins / kSelThreads;
-    unsigned cnt[kOwn] = {}, sum = 0;
+    // bins lie from the largest key down; a thread owns four of them
+    constexpr int kOwners = kSelBins / 4;
+    unsigned cnt[4] = {}, sum = 0;
     uint4 *own_bins = reinterpret_cast<uint4 *>(hist) + threadIdx.x;
     auto add = [&](const uint4 &x) {
       cnt[0] += x.x;
@@ -206,54 +243,72 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
       cnt[2] += x.z;
       cnt[3] += x.w;
     };
-    if (CS == 1) {
-      __syncthreads();
-      add(*own_bins);
-    } else {
-      cluster.sync();
+    if (CS == 1) __syncthreads();
+    else cluster.sync();
+    if (threadIdx.x < kOwners) {
+      if (CS == 1) {
+        add(*own_bins);
+      } else {
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < CS) add(*cluster.map_shared_rank(own_bins, r));
+        for (int r = 0; r < 8; ++r)
+          if (r < CS) add(*cluster.map_shared_rank(own_bins, r));
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kOwn; ++j) sum += cnt[j];
-    unsigned incl = sum;
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned v = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) s.wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += s.wsum[w];
+    for (int j = 0; j < 4; ++j) sum += cnt[j];
+    const unsigned incl = block_sum(sum, s.wsum);
     unsigned before = incl - sum;
     if (before < need && need <= incl) {
-      int j = 0;
-      while (before + cnt[j] < need) before += cnt[j++];
-      s.bin = kSelBins - 1 - (kOwn * threadIdx.x + j);
+      int bin = kSelBins - 1 - 4 * threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (before + cnt[j] < need) {
+          before += cnt[j];
+          --bin;
+        } else {
+          break;
+        }
+      s.bin = bin;
       s.need = need - before;
     }
     __syncthreads();
     prefix |= s.bin << shift;
     need = s.need;
   }
-  // each warp's stretch of the slice: rows above the edge and at it
-  const int stretch = ((slice + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  // rows above the edge and at it before each 32 rows of the slice
+  unsigned gt = 0, eq = 0;  // of the CTA, then before its slice
+  const unsigned below = (1u << lane) - 1;
+  const int stretch = ((slice + kSelWarps - 1) / kSelWarps + 31) & ~31;  // of a warp, where the slice is not held
   const int w0 = min(len, warp * stretch), w1 = min(len, w0 + stretch);
-  unsigned gt = 0, eq = 0;
-  for (int i = w0; i < w1; i += 32) {
-    const bool in = i + lane < w1;
-    const unsigned key = in ? key_at(i + lane) : 0u;
-    gt += __popc(__ballot_sync(~0u, in && key > prefix));
-    eq += __popc(__ballot_sync(~0u, in && key == prefix));
-  }
-  if (lane == 0) {
-    s.wgt[warp] = gt;
-    s.weq[warp] = eq;
-  }
-  __syncthreads();
-  if (CS == 1) {
-    gt = eq = 0;
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const bool in = threadIdx.x + j * kSelThreads < len;
+      const unsigned x = __popc(__ballot_sync(~0u, in && keys[j] > prefix)),
+                     y = __popc(__ballot_sync(~0u, in && keys[j] == prefix));
+      if (lane == 0) s.cnt[j * kSelWarps + warp] = (x << 16) + y;
+    }
+    __syncthreads();
+    const unsigned v = threadIdx.x < KPT * kSelWarps ? s.cnt[threadIdx.x] : 0u;
+    const unsigned incl = block_sum(v, s.wsum);
+    if (threadIdx.x < KPT * kSelWarps) s.cnt[threadIdx.x] = incl - v;
+    if (threadIdx.x == kSelThreads - 1) {
+      s.gt = incl >> 16;
+      s.eq = incl & 0xFFFFu;
+    }
   } else {
+#pragma unroll 2
+    for (int i = w0; i < w1; i += 32) {
+      const bool in = i + lane < w1;
+      const unsigned key = in ? score_key(sc[i + lane]) : 0u;
+      gt += __popc(__ballot_sync(~0u, in && key > prefix));
+      eq += __popc(__ballot_sync(~0u, in && key == prefix));
+    }
+    if (lane == 0) {
+      s.wgt[warp] = gt;
+      s.weq[warp] = eq;
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
       unsigned x = 0, y = 0;
       for (int w = 0; w < kSelWarps; ++w) {
@@ -263,28 +318,93 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
       s.gt = x;
       s.eq = y;
     }
+  }
+  gt = eq = 0;
+  if (CS == 1) {
+    __syncthreads();
+  } else {
     cluster.sync();
-    gt = eq = 0;
     for (int r = 0; r < rank; ++r) {
       gt += *cluster.map_shared_rank(&s.gt, r);
       eq += *cluster.map_shared_rank(&s.eq, r);
     }
     cluster.sync();  // no CTA of the cluster is read from here on
   }
-  for (int w = 0; w < warp; ++w) {
-    gt += s.wgt[w];
-    eq += s.weq[w];
-  }
-  const unsigned below = (1u << lane) - 1;
-  for (int i = w0; i < w1; i += 32) {
-    const bool in = i + lane < w1;
-    const unsigned key = in ? key_at(i + lane) : 0u;
+  auto place = [&](int i, bool in, unsigned key) {
     const bool above = in && key > prefix, edge = in && key == prefix;
     const unsigned gts = __ballot_sync(~0u, above), eqs = __ballot_sync(~0u, edge);
     const unsigned eq_before = eq + __popc(eqs & below);
-    if (above || (edge && eq_before < need)) keep[gt + __popc(gts & below) + min(eq_before, need)] = lo + i + lane;
+    const unsigned at = gt + __popc(gts & below) + min(eq_before, need);
+    if (above || (edge && eq_before < need)) keep[at] = lo + i;
+    if (split && in && lo + i == budget) split[(long long)b * c.Hkv + h] = at;
     gt += __popc(gts);
     eq += __popc(eqs);
+  };
+  if (held) {
+    const unsigned gt0 = gt, eq0 = eq;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const unsigned x = s.cnt[j * kSelWarps + warp];
+      gt = gt0 + (x >> 16);
+      eq = eq0 + (x & 0xFFFFu);
+      const int i = threadIdx.x + j * kSelThreads;
+      place(i, i < len, keys[j]);
+    }
+  } else {
+    for (int w = 0; w < warp; ++w) {
+      gt += s.wgt[w];
+      eq += s.weq[w];
+    }
+    for (int i = w0; i < w1; i += 32) {
+      const bool in = i + lane < w1;
+      place(i + lane, in, in ? score_key(sc[i + lane]) : 0u);
+    }
+  }
+}
+
+// The first kept row that comes from a position at or behind the budget: it and
+// all after it come from where nothing is written.
+__device__ __forceinline__ int first_apart(int budget, int k, int Lb, const int32_t *split) {
+  return k > 0 && budget < Lb - (budget - k) ? *split : max(0, 2 * budget - Lb);
+}
+
+// Moves the kept rows that come from behind the budget, in any order: 16 bytes
+// of K or of V per thread and turn.
+constexpr int kApartUnroll = 4;
+template <int ROW>
+__global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c, int budget, int recent,
+                                                                   const int32_t *keep, const int32_t *old_len,
+                                                                   const int32_t *split) {
+  constexpr int kLanes = ROW / 16, kRows = kMoveThreads / kLanes;
+  const int h = blockIdx.y, b = blockIdx.z, Lb = old_len[b];
+  if (Lb < 0) return;
+  const int k = budget - recent, shift = Lb - budget;
+  const long long pair = (long long)b * c.Hkv + h;
+  keep += pair * budget;
+  const int first = first_apart(budget, k, Lb, split + pair);
+  const long long head = (long long)h * c.head_stride + (threadIdx.x % kLanes) * 16;
+  for (int r0 = first + blockIdx.x * kRows * kApartUnroll; r0 < budget; r0 += gridDim.x * kRows * kApartUnroll) {
+    long long from[kApartUnroll];
+    uint4 x[kApartUnroll], y[kApartUnroll];
+#pragma unroll
+    for (int u = 0; u < kApartUnroll; ++u) {
+      const int r = r0 + u * kRows + threadIdx.x / kLanes;
+      const int src = r >= budget ? 0 : r < k ? __ldg(keep + r) : r + shift;
+      from[u] = head + kv_block(c, b, src) + kv_row(c, src);
+    }
+#pragma unroll
+    for (int u = 0; u < kApartUnroll; ++u) {
+      x[u] = __ldcs(reinterpret_cast<const uint4 *>(c.K + from[u]));
+      y[u] = __ldcs(reinterpret_cast<const uint4 *>(c.V + from[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < kApartUnroll; ++u) {
+      const int r = r0 + u * kRows + threadIdx.x / kLanes;
+      if (r >= budget) continue;
+      const long long to = head + kv_block(c, b, r) + kv_row(c, r);
+      *reinterpret_cast<uint4 *>(c.K + to) = x[u];
+      *reinterpret_cast<uint4 *>(c.V + to) = y[u];
+    }
   }
 }
 
@@ -296,15 +416,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const KvDev c
 // waits for.  The next batch's sources lie at or behind r1, so it is read before the
 // barrier too, which keeps loads in flight while the batch is written; its
 // addresses come from keep and the page table, read one and two batches before that.
+// With few pairs (split given) it ends where evict_apart_kernel takes over.
 template <int PART, int kMoveUnroll>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c, int budget, int recent,
-                                                                  const int32_t *keep, const int32_t *old_len) {
+                                                                  const int32_t *keep, const int32_t *old_len,
+                                                                  const int32_t *split) {
   constexpr int kLanes = PART / 16, kRows = kMoveThreads / kLanes, kBatch = kRows * kMoveUnroll;
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int Lb = old_len[b];
   if (Lb < 0) return;
   const int k = budget - recent, shift = Lb - budget;  // a protected row moves by `shift`
   keep += ((long long)b * c.Hkv + h) * budget;
+  const int rows = split ? first_apart(budget, k, Lb, split + (long long)b * c.Hkv + h) : budget;
   auto source = [&](int r) { return r >= budget ? r : r < k ? __ldg(keep + r) : r + shift; };
   const int per = c.row_bytes / PART;
   if (part == 2 * per) {
@@ -335,7 +458,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c,
   int src[kMoveUnroll];
   auto sources = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) src[u] = source(r0 + u * kRows + row);
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int r = r0 + u * kRows + row;
+      src[u] = r < rows ? source(r) : r;
+    }
   };
   auto offsets = [&](int r0, long long(&f)[kMoveUnroll]) {
 #pragma unroll
@@ -369,19 +495,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c,
     offsets(r0 + 2 * kBatch, f);
     sources(r0 + 3 * kBatch);
   };
-  for (int r0 = 0; r0 < budget; r0 += 2 * kBatch) {
+  for (int r0 = 0; r0 < rows; r0 += 2 * kBatch) {
     turn(r0, from[0], x[0], from[1], x[1]);
     turn(r0 + kBatch, from[1], x[1], from[0], x[0]);
   }
 }
 
 // Workspace: the kept positions of every (sequence, KV head), then the old
-// lengths.  A budget that no sequence can exceed keeps no positions.
+// lengths, then each pair's first row to come from behind the budget.  A budget that no sequence can exceed keeps no positions.
 size_t keep_bytes(const KvDev &c, int budget) {
   return budget < c.cap ? tr_align_up((size_t)c.B * c.Hkv * (size_t)budget * 4, 256) : 0;
 }
 
-size_t evict_bytes(const KvDev &c, int budget) { return keep_bytes(c, budget) + tr_align_up((size_t)c.B * 4, 256); }
+size_t evict_bytes(const KvDev &c, int budget) {
+  return keep_bytes(c, budget) + tr_align_up((size_t)c.B * 4, 256) + tr_align_up((size_t)c.B * c.Hkv * 4, 256);
+}
 
 }  // namespace
 
@@ -446,41 +574,55 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   const long long pairs = (long long)c.B * c.Hkv;
   int cs = 1;
   while (cs < 8 && c.cap / (2 * cs) >= 4096 && pairs * 2 * cs <= 4 * tr_sm_count()) cs *= 2;
-  const long long slice = ((c.cap + cs - 1) / cs + 31) & ~31LL;
-  const int held = slice <= kSelMaxKeys ? (int)slice : 0;
-  static std::atomic<bool> set[64];  // per device
-  int dev = 0;
-  TR_TRY_CUDA(cudaGetDevice(&dev));
-  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    TR_TRY_CUDA(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4));
-    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c.Hkv * cs, c.B);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = (size_t)held * 4;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  auto run = [&](auto kernel, dim3 grid, int cluster, int threads, auto... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+  };
+  // whole rows where the pairs alone give every SM two CTAs; else narrow columns,
+  // many CTAs, for the rows that move within the budget and the others apart
+  const bool few = pairs * 2 < 2LL * tr_sm_count();
+  int32_t *split = few ? (int32_t *)((char *)old_len + tr_align_up((size_t)c.B * 4, 256)) : nullptr;
   // with a budget that the cache cannot exceed this still reports bad lengths
-  TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, evict_select_kernel, (const KvDev)c, budget, recent, held, keep, old_len,
-                                 tr_status_dev()));
-  if (budget < c.cap) {
-    // the widest part that still gives every SM four CTAs, else the narrowest
-    const int row = c.row_bytes;
-    int part = row;
-    while (part > 32 && pairs * 2 * (row / part) < 4LL * tr_sm_count()) part /= 2;
-    const dim3 grid(2 * (row / part) + 1, c.Hkv, c.B);
-    auto run = [&](auto kernel) { kernel<<<grid, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len); };
-    if (part == 256) run(evict_move_kernel<256, 4>);
-    else if (part == 128) run(evict_move_kernel<128, 4>);
-    else if (part == 64) run(evict_move_kernel<64, 4>);
-    else run(evict_move_kernel<32, 8>);  // few CTAs: more in flight for each
-    TR_LAUNCH_CHECK();
+  const dim3 select(c.Hkv * cs, c.B);
+  auto pick = [&](auto kernel) {
+    return run(kernel, select, cs, kSelThreads, c, budget, recent, keep, old_len, split, tr_status_dev());
+  };
+  const bool small = c.cap <= (long long)cs * 8 * kSelThreads;
+  TR_TRY_CUDA(cs == 1 ? (small ? pick(evict_select_kernel<8, 11>) : pick(evict_select_kernel<kSelMost, 11>))
+                      : (small ? pick(evict_select_kernel<8, 8>) : pick(evict_select_kernel<kSelMost, 8>)));
+  if (budget >= c.cap) return TR_OK;
+  const int row = c.row_bytes;
+  int part = row;
+  while (few && part > 32 && pairs * 2 * (row / part) < 2LL * tr_sm_count()) part /= 2;
+  const dim3 move(2 * (row / part) + 1, c.Hkv, c.B);
+  auto go = [&](auto kernel) {
+    kernel<<<move, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len, split);
+    return cudaGetLastError();
+  };
+  TR_TRY_CUDA(part == 256   ? go(evict_move_kernel<256, 4>)
+              : part == 128 ? go(evict_move_kernel<128, 4>)
+              : part == 64  ? go(evict_move_kernel<64, 4>)
+                            : go(evict_move_kernel<32, 8>));  // few CTAs: more in flight for each
+  if (few) {
+    const long long rows = kMoveThreads / (row / 16) * kApartUnroll;  // of one turn of a CTA
+    const long long turns = (budget + rows - 1) / rows, fill = (4LL * tr_sm_count() + pairs - 1) / pairs;
+    const dim3 apart((unsigned)(turns < fill ? turns : fill), c.Hkv, c.B);
+    auto rest = [&](auto kernel) {
+      kernel<<<apart, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len, split);
+      return cudaGetLastError();
+    };
+    TR_TRY_CUDA(row == 256   ? rest(evict_apart_kernel<256>)
+                : row == 128 ? rest(evict_apart_kernel<128>)
+                             : rest(evict_apart_kernel<64>));
   }
   return TR_OK;
 }

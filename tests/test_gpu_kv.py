@@ -620,6 +620,21 @@ def test_evict_long(tr, n, budget, recent):
     check_evict(c, budget, recent)
 
 
+@pytest.mark.parametrize("type,d,layout", [("bf16", 128, "dense"), ("e4m3", 64, 16), ("f16", 64, "nhd64")])
+@pytest.mark.parametrize("budget,recent", [(300, 40), (64, 64), (900, 0)])
+def test_evict_many_pairs(tr, type, d, layout, budget, recent):
+    """More (sequence, head) pairs than SMs: whole rows by one CTA each."""
+    c = Made(tr, np.random.default_rng(36), type, layout, [37 * b % 1200 for b in range(44)], 4, d)
+    check_evict(c, budget, recent)
+
+
+@pytest.mark.parametrize("budget,recent", [(2000, 10), (6000, 5000), (7900, 100), (4096, 0), (8191, 0)])
+def test_evict_around_the_halfway_mark(tr, budget, recent):
+    """Few pairs: rows from behind the budget move apart from the others, whatever part of the kept ones they are."""
+    c = Made(tr, np.random.default_rng(37), "bf16", "dense", [8192, 4097, 8000], 2, 64)
+    check_evict(c, budget, recent)
+
+
 @pytest.mark.parametrize("n,budget,recent", [(400_000, 150_000, 1000), (330_000, 329_999, 5), (70_000, 1, 0)])
 def test_evict_very_long(tr, n, budget, recent):
     """More rows than the shared memory of a whole cluster holds scores of (8 x 40960), and up to that many."""
