@@ -99,11 +99,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Programmatic dependent launch: the next kernel of the call may be set up from
-// here on; it waits for this one's results with wait_for_previous.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // 16 bytes from global to shared memory; of the second form 16 zero bytes where not valid.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -212,7 +207,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
   __shared__ float2 jml[kWarps][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  let_next_start();
+  tr_let_next_start();
 
   // lengths and, for one head, the tiles before each sequence
   int mine[kOwn], sum = 0;
@@ -711,8 +706,8 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
   __shared__ float4 acc[kFinWarps][D / 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
-  let_next_start();
-  wait_for_previous();
+  tr_let_next_start();
+  tr_wait_for_previous();
   Parts u;
   const int parts = parts_of(c, a, b, h, u);
   if (parts <= 1) return;  // empty, or finished by one warp or CTA
@@ -783,7 +778,7 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   __shared__ float4 sums[SPLIT ? kFinWarps : 1][32];
   const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int L = c.L[b];
-  wait_for_previous();
+  tr_wait_for_previous();
   if (L < 0 || L > c.cap || (int)blockIdx.x * kRows >= L) return;
   const int p = blockIdx.x * kRows + (SPLIT ? lane : threadIdx.x) * 4;
   const long long hq = (long long)b * a.Hq + (long long)h * a.G;
@@ -841,22 +836,6 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   return p;
 }
 
-// A launch that may be set up while the previous kernel on the stream still runs.
-template <typename... P, typename... A>
-int launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
-  return TR_OK;
-}
-
 template <int TYPE, int D, int MT>
 int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   static std::atomic<bool> set[64];  // per device
@@ -876,10 +855,10 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
   int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  rc = launch_next(join_kernel<D>, dim3(c.B * a.Hq), kFinThreads, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
+  rc = tr_launch_next(join_kernel<D>, dim3(c.B * a.Hq), kFinThreads, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
   if (rc != TR_OK || !a.accumulate) return rc;
-  return a.G > 8 ? launch_next(score_kernel<true>, dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, s, c, a)
-                 : launch_next(score_kernel<false>, dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, s, c, a);
+  return a.G > 8 ? tr_launch_next(score_kernel<true>, dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, s, c, a)
+                 : tr_launch_next(score_kernel<false>, dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, s, c, a);
 }
 
 template <int TYPE>

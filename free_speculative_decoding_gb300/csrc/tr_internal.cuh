@@ -81,6 +81,28 @@ int tr_sm_count();
     if (cudaGetLastError() != cudaSuccess) return TR_E_CUDA; \
   } while (0)
 
+// Programmatic dependent launch: a kernel launched with tr_launch_next may be
+// set up while the previous one on the stream still runs, once all of that one's
+// CTAs have called tr_let_next_start (or ended); tr_wait_for_previous waits for
+// the previous kernel's end and its writes.
+__device__ __forceinline__ void tr_let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void tr_wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+static inline int tr_launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return TR_OK;
+}
+
 static inline size_t tr_align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // smallest supported register-list width for K

@@ -63,6 +63,7 @@ __device__ __forceinline__ int append_rows(const KvDev &c, int b, int Lb, int n,
 // copy goes to todo[b] = (old length, rows).
 __global__ void __launch_bounds__(kAppendThreads) append_plan_kernel(const KvDev c, int T, const int32_t *count,
                                                                      int2 *todo, unsigned *status) {
+  tr_let_next_start();
   const int b = blockIdx.x, Lb = c.L[b];
   const int n = append_rows(c, b, Lb, count ? count[b] : T, T, status);
   if (threadIdx.x == 0) {
@@ -75,13 +76,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_plan_kernel(const KvDev
 // todo: the plan kernel's; NULL when a sequence's rows are one CTA's work (a
 // decoding step), which then checks and advances the length itself.
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, const uint4 *Kn, const uint4 *Vn, int T,
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c, const uint4 *Kn, const uint4 *Vn, int T,
                                                                 const int32_t *count, const int2 *todo,
                                                                 unsigned *status) {
   constexpr int kPieces = D / 8, kOut = E4M3 ? 8 : 16;  // of a row; bytes of a piece in the cache
   const int b = blockIdx.y;
   int Lb, n;
   if (todo) {
+    tr_wait_for_previous();
     const int2 x = todo[b];
     Lb = x.x;
     n = x.y;
@@ -90,34 +92,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvDev c, c
     n = append_rows(c, b, Lb, count ? count[b] : T, T, status);  // its barrier lies between reads and write of L
     if (threadIdx.x == 0 && n > 0) c.L[b] = Lb + n;
   }
-  if (n <= 0) return;
+  if (n <= 0 || blockIdx.x * (kAppendThreads * kAppendUnroll) >= (unsigned)n * c.Hkv * kPieces) return;
   const unsigned total = (unsigned)n * c.Hkv * kPieces;
   const long long base = (long long)b * T * c.Hkv * kPieces;
   const unsigned i0 = blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
   uint4 kx[kAppendUnroll], vx[kAppendUnroll];
+  long long at[kAppendUnroll];
+  int head[kAppendUnroll];
 #pragma unroll
-  for (int u = 0; u < kAppendUnroll; ++u) {
-    const unsigned i = i0 + u * kAppendThreads;
-    if (i < total) {
-      kx[u] = __ldcs(Kn + base + i);
-      vx[u] = __ldcs(Vn + base + i);
-    }
+  for (int u = 0; u < kAppendUnroll; ++u) {  // a piece behind the last one is read twice, and not written
+    const unsigned i = min(i0 + u * kAppendThreads, total - 1);
+    kx[u] = __ldcs(Kn + base + i);
+    vx[u] = __ldcs(Vn + base + i);
+    const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
+    const int p = Lb + (int)tok;
+    head[u] = (int)(th - tok * c.Hkv);
+    at[u] = kv_block(c, b, p) + (long long)head[u] * c.head_stride + kv_row(c, p) + piece * kOut;
+    if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + head[u]) * c.scores_ld + p] = 0.f;
   }
 #pragma unroll
   for (int u = 0; u < kAppendUnroll; ++u) {
-    const unsigned i = i0 + u * kAppendThreads;
-    if (i >= total) continue;
-    const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
-    const int h = (int)(th - tok * c.Hkv), p = Lb + (int)tok;
-    const long long at = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * kOut;
+    if (i0 + u * kAppendThreads >= total) continue;
     if constexpr (E4M3) {
-      *reinterpret_cast<uint2 *>(c.K + at) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + h)));
-      *reinterpret_cast<uint2 *>(c.V + at) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + h)));
+      *reinterpret_cast<uint2 *>(c.K + at[u]) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + head[u])));
+      *reinterpret_cast<uint2 *>(c.V + at[u]) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + head[u])));
     } else {
-      *reinterpret_cast<uint4 *>(c.K + at) = kx[u];
-      *reinterpret_cast<uint4 *>(c.V + at) = vx[u];
+      *reinterpret_cast<uint4 *>(c.K + at[u]) = kx[u];
+      *reinterpret_cast<uint4 *>(c.V + at[u]) = vx[u];
     }
-    if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] = 0.f;
   }
 }
 
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
                         unsigned *status) {
   constexpr int kSelBins = 1 << BITS, kPasses = (32 + BITS - 1) / BITS;
   __shared__ SelSmem<BITS> s;
+  tr_let_next_start();
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int h = blockIdx.x / CS, b = blockIdx.y;
@@ -362,35 +365,61 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
   }
 }
 
-// The first kept row that comes from a position at or behind the budget: it and
-// all after it come from where nothing is written.
-__device__ __forceinline__ int first_apart(int budget, int k, int Lb, const int32_t *split) {
-  return k > 0 && budget < Lb - (budget - k) ? *split : max(0, 2 * budget - Lb);
+// Where there are few pairs, the kept rows of one are cut at two places: rows
+// [one, budget) come from positions at or behind the budget, rows [two, one) from
+// positions at or behind one, so that within either stretch nothing is read
+// where something is written, and each can be moved in any order once the
+// stretches before it have been read.  two is the first eighth of one that will do.
+struct Cuts {
+  int two, one;
+};
+__device__ __forceinline__ Cuts cuts_of(int budget, int k, int Lb, const int32_t *keep, const int32_t *split) {
+  Cuts u;
+  u.one = k > 0 && budget < Lb - (budget - k) ? *split : max(0, 2 * budget - Lb);
+  u.two = u.one;
+  int at[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (int)((long long)u.one * i / 8);
+    at[i] = r < k ? __ldg(keep + r) : r + Lb - budget;
+  }
+#pragma unroll
+  for (int i = 7; i >= 0; --i)
+    if (at[i] >= u.one) u.two = (int)((long long)u.one * i / 8);
+  return u;
 }
 
-// Moves the kept rows that come from behind the budget, in any order: 16 bytes
-// of K or of V per thread and turn.
+// Moves one of the two stretches, scores included: 16 bytes of K and of V per
+// thread and turn.
 constexpr int kApartUnroll = 4;
 template <int ROW>
-__global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c, int budget, int recent,
+__global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c, int budget, int recent, bool second,
                                                                    const int32_t *keep, const int32_t *old_len,
                                                                    const int32_t *split) {
   constexpr int kLanes = ROW / 16, kRows = kMoveThreads / kLanes;
-  const int h = blockIdx.y, b = blockIdx.z, Lb = old_len[b];
+  const int h = blockIdx.y, b = blockIdx.z;
+  tr_let_next_start();
+  tr_wait_for_previous();
+  const int Lb = old_len[b];
   if (Lb < 0) return;
   const int k = budget - recent, shift = Lb - budget;
   const long long pair = (long long)b * c.Hkv + h;
   keep += pair * budget;
-  const int first = first_apart(budget, k, Lb, split + pair);
+  const Cuts cuts = cuts_of(budget, k, Lb, keep, split + pair);
+  const int first = second ? cuts.two : cuts.one, last = second ? cuts.one : budget;
   const long long head = (long long)h * c.head_stride + (threadIdx.x % kLanes) * 16;
-  for (int r0 = first + blockIdx.x * kRows * kApartUnroll; r0 < budget; r0 += gridDim.x * kRows * kApartUnroll) {
+  float *sc = c.scores + pair * c.scores_ld;
+  const bool scorer = threadIdx.x % kLanes == 0;
+  for (int r0 = first + blockIdx.x * kRows * kApartUnroll; r0 < last; r0 += gridDim.x * kRows * kApartUnroll) {
     long long from[kApartUnroll];
     uint4 x[kApartUnroll], y[kApartUnroll];
+    float z[kApartUnroll];
 #pragma unroll
-    for (int u = 0; u < kApartUnroll; ++u) {
-      const int r = r0 + u * kRows + threadIdx.x / kLanes;
-      const int src = r >= budget ? 0 : r < k ? __ldg(keep + r) : r + shift;
+    for (int u = 0; u < kApartUnroll; ++u) {  // a row behind the last one is read twice, and not written
+      const int r = min(r0 + u * kRows + (int)threadIdx.x / kLanes, last - 1);
+      const int src = r < k ? __ldg(keep + r) : r + shift;
       from[u] = head + kv_block(c, b, src) + kv_row(c, src);
+      if (scorer) z[u] = sc[src];
     }
 #pragma unroll
     for (int u = 0; u < kApartUnroll; ++u) {
@@ -400,10 +429,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c
 #pragma unroll
     for (int u = 0; u < kApartUnroll; ++u) {
       const int r = r0 + u * kRows + threadIdx.x / kLanes;
-      if (r >= budget) continue;
+      if (r >= last) continue;
       const long long to = head + kv_block(c, b, r) + kv_row(c, r);
       *reinterpret_cast<uint4 *>(c.K + to) = x[u];
       *reinterpret_cast<uint4 *>(c.V + to) = y[u];
+      if (scorer) sc[r] = z[u];
     }
   }
 }
@@ -416,35 +446,38 @@ __global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c
 // waits for.  The next batch's sources lie at or behind r1, so it is read before the
 // barrier too, which keeps loads in flight while the batch is written; its
 // addresses come from keep and the page table, read one and two batches before that.
-// With few pairs (split given) it ends where evict_apart_kernel takes over.
+// With few pairs (split given) it ends where evict_apart_kernel takes over.  The
+// first CTA of a sequence sets its new length.
 template <int PART, int kMoveUnroll>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c, int budget, int recent,
                                                                   const int32_t *keep, const int32_t *old_len,
                                                                   const int32_t *split) {
   constexpr int kLanes = PART / 16, kRows = kMoveThreads / kLanes, kBatch = kRows * kMoveUnroll;
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  tr_let_next_start();
+  tr_wait_for_previous();
   const int Lb = old_len[b];
   if (Lb < 0) return;
   const int k = budget - recent, shift = Lb - budget;  // a protected row moves by `shift`
   keep += ((long long)b * c.Hkv + h) * budget;
-  const int rows = split ? first_apart(budget, k, Lb, split + (long long)b * c.Hkv + h) : budget;
+  const int rows = split ? cuts_of(budget, k, Lb, keep, split + (long long)b * c.Hkv + h).two : budget;
   auto source = [&](int r) { return r >= budget ? r : r < k ? __ldg(keep + r) : r + shift; };
   const int per = c.row_bytes / PART;
   if (part == 2 * per) {
     float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;
     constexpr int kPer = 8;
-    for (int r0 = 0; r0 < budget; r0 += kMoveThreads * kPer) {
+    for (int r0 = 0; r0 < rows; r0 += kMoveThreads * kPer) {
       float x[kPer];
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int r = r0 + u * kMoveThreads + threadIdx.x;
-        if (r < budget) x[u] = sc[source(r)];
+        if (r < rows) x[u] = sc[source(r)];
       }
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int r = r0 + u * kMoveThreads + threadIdx.x;
-        if (r < budget) sc[r] = x[u];
+        if (r < rows) sc[r] = x[u];
       }
     }
     if (h == 0 && threadIdx.x == 0) c.L[b] = budget;
@@ -543,14 +576,13 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
     TR_LAUNCH_CHECK();
   }
   auto run = [&](auto kernel) {
-    kernel<<<g, kAppendThreads, 0, s>>>(c, (const uint4 *)Kn, (const uint4 *)Vn, T, count, todo, tr_status_dev());
+    const uint4 *k = (const uint4 *)Kn, *v = (const uint4 *)Vn;
+    if (todo) return tr_launch_next(kernel, g, kAppendThreads, s, c, k, v, T, count, todo, tr_status_dev());
+    kernel<<<g, kAppendThreads, 0, s>>>(c, k, v, T, count, todo, tr_status_dev());
+    return cudaGetLastError() == cudaSuccess ? (int)TR_OK : (int)TR_E_CUDA;
   };
-  if (cache->d == 64)
-    e4m3 ? run(append_kernel<true, 64>) : run(append_kernel<false, 64>);
-  else
-    e4m3 ? run(append_kernel<true, 128>) : run(append_kernel<false, 128>);
-  TR_LAUNCH_CHECK();
-  return TR_OK;
+  if (cache->d == 64) return e4m3 ? run(append_kernel<true, 64>) : run(append_kernel<false, 64>);
+  return e4m3 ? run(append_kernel<true, 128>) : run(append_kernel<false, 128>);
 }
 
 extern "C" size_t tr_kv_evict_workspace_bytes(const tr_kv_cache *cache, int budget) {
@@ -605,24 +637,23 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   while (few && part > 32 && pairs * 2 * (row / part) < 2LL * tr_sm_count()) part /= 2;
   const dim3 move(2 * (row / part) + 1, c.Hkv, c.B);
   auto go = [&](auto kernel) {
-    kernel<<<move, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len, split);
-    return cudaGetLastError();
+    return tr_launch_next(kernel, move, kMoveThreads, s, c, budget, recent, keep, old_len, split);
   };
-  TR_TRY_CUDA(part == 256   ? go(evict_move_kernel<256, 4>)
-              : part == 128 ? go(evict_move_kernel<128, 4>)
-              : part == 64  ? go(evict_move_kernel<64, 4>)
-                            : go(evict_move_kernel<32, 8>));  // few CTAs: more in flight for each
-  if (few) {
-    const long long rows = kMoveThreads / (row / 16) * kApartUnroll;  // of one turn of a CTA
-    const long long turns = (budget + rows - 1) / rows, fill = (4LL * tr_sm_count() + pairs - 1) / pairs;
-    const dim3 apart((unsigned)(turns < fill ? turns : fill), c.Hkv, c.B);
+  rc = part == 256   ? go(evict_move_kernel<256, 4>)
+       : part == 128 ? go(evict_move_kernel<128, 4>)
+       : part == 64  ? go(evict_move_kernel<64, 4>)
+                     : go(evict_move_kernel<32, 8>);  // few CTAs: more in flight for each
+  if (!few) return rc;
+  const long long rows = kMoveThreads / (row / 16) * kApartUnroll;  // of one turn of a CTA
+  const long long turns = (budget + rows - 1) / rows, fill = (4LL * tr_sm_count() + pairs - 1) / pairs;
+  const dim3 apart((unsigned)(turns < fill ? turns : fill), c.Hkv, c.B);
+  for (int level = 2; level >= 1 && rc == TR_OK; --level) {
     auto rest = [&](auto kernel) {
-      kernel<<<apart, kMoveThreads, 0, s>>>(c, budget, recent, keep, old_len, split);
-      return cudaGetLastError();
+      return tr_launch_next(kernel, apart, kMoveThreads, s, c, budget, recent, level == 2, keep, old_len, split);
     };
-    TR_TRY_CUDA(row == 256   ? rest(evict_apart_kernel<256>)
-                : row == 128 ? rest(evict_apart_kernel<128>)
-                             : rest(evict_apart_kernel<64>));
+    rc = row == 256   ? rest(evict_apart_kernel<256>)
+         : row == 128 ? rest(evict_apart_kernel<128>)
+                      : rest(evict_apart_kernel<64>);
   }
-  return TR_OK;
+  return rc;
 }
