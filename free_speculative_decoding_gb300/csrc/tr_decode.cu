@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   __shared__ float2 jml[kWarps][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   tr_let_next_start();
+  tr_wait_for_previous();
 
   // lengths and, for one head, the tiles before each sequence
   int mine[kOwn], sum = 0;
@@ -777,8 +778,8 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   constexpr int kRows = SPLIT ? 128 : 512;
   __shared__ float4 sums[SPLIT ? kFinWarps : 1][32];
   const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int L = c.L[b];
   tr_wait_for_previous();
+  const int L = c.L[b];
   if (L < 0 || L > c.cap || (int)blockIdx.x * kRows >= L) return;
   const int p = blockIdx.x * kRows + (SPLIT ? lane : threadIdx.x) * 4;
   const long long hq = (long long)b * a.Hq + (long long)h * a.G;
@@ -845,9 +846,7 @@ int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a)
     TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  split_kernel<TYPE, D, MT><<<grid, Shape<TYPE, D>::THREADS, kRings, s>>>(c, a);
-  TR_LAUNCH_CHECK();
-  return TR_OK;
+  return tr_launch_next(split_kernel<TYPE, D, MT>, {grid, Shape<TYPE, D>::THREADS, kRings}, s, c, a);
 }
 
 template <int TYPE, int D>
@@ -855,10 +854,10 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
   int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  rc = tr_launch_next(join_kernel<D>, dim3(c.B * a.Hq), kFinThreads, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
+  rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
   if (rc != TR_OK || !a.accumulate) return rc;
-  return a.G > 8 ? tr_launch_next(score_kernel<true>, dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads, s, c, a)
-                 : tr_launch_next(score_kernel<false>, dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads, s, c, a);
+  return a.G > 8 ? tr_launch_next(score_kernel<true>, {dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads}, s, c, a)
+                 : tr_launch_next(score_kernel<false>, {dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads}, s, c, a);
 }
 
 template <int TYPE>

@@ -88,17 +88,27 @@ int tr_sm_count();
 __device__ __forceinline__ void tr_let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void tr_wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+struct LaunchShape {
+  dim3 grid;
+  int threads;
+  size_t smem = 0;
+  int cluster = 1;  // CTAs of a cluster, along x
+};
 template <typename... P, typename... A>
-static inline int tr_launch_next(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
+static inline int tr_launch_next(void (*kernel)(P...), const LaunchShape &l, cudaStream_t s, const A &...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = l.grid;
+  cfg.blockDim = dim3(l.threads);
+  cfg.dynamicSmemBytes = l.smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = l.cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = l.cluster > 1 ? 2 : 1;
   TR_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
   return TR_OK;
 }

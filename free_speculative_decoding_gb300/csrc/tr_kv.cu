@@ -64,6 +64,7 @@ __device__ __forceinline__ int append_rows(const KvDev &c, int b, int Lb, int n,
 __global__ void __launch_bounds__(kAppendThreads) append_plan_kernel(const KvDev c, int T, const int32_t *count,
                                                                      int2 *todo, unsigned *status) {
   tr_let_next_start();
+  tr_wait_for_previous();
   const int b = blockIdx.x, Lb = c.L[b];
   const int n = append_rows(c, b, Lb, count ? count[b] : T, T, status);
   if (threadIdx.x == 0) {
@@ -81,9 +82,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
                                                                 unsigned *status) {
   constexpr int kPieces = D / 8, kOut = E4M3 ? 8 : 16;  // of a row; bytes of a piece in the cache
   const int b = blockIdx.y;
+  tr_let_next_start();
+  tr_wait_for_previous();
   int Lb, n;
   if (todo) {
-    tr_wait_for_previous();
     const int2 x = todo[b];
     Lb = x.x;
     n = x.y;
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
   constexpr int kSelBins = 1 << BITS, kPasses = (32 + BITS - 1) / BITS;
   __shared__ SelSmem<BITS> s;
   tr_let_next_start();
+  tr_wait_for_previous();
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int h = blockIdx.x / CS, b = blockIdx.y;
@@ -572,14 +575,12 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
   cudaStream_t s = (cudaStream_t)stream;
   int2 *todo = grid > 1 ? (int2 *)ws : nullptr;
   if (todo) {
-    append_plan_kernel<<<c.B, kAppendThreads, 0, s>>>(c, T, count, todo, tr_status_dev());
-    TR_LAUNCH_CHECK();
+    rc = tr_launch_next(append_plan_kernel, {dim3(c.B), kAppendThreads}, s, c, T, count, todo, tr_status_dev());
+    if (rc != TR_OK) return rc;
   }
   auto run = [&](auto kernel) {
-    const uint4 *k = (const uint4 *)Kn, *v = (const uint4 *)Vn;
-    if (todo) return tr_launch_next(kernel, g, kAppendThreads, s, c, k, v, T, count, todo, tr_status_dev());
-    kernel<<<g, kAppendThreads, 0, s>>>(c, k, v, T, count, todo, tr_status_dev());
-    return cudaGetLastError() == cudaSuccess ? (int)TR_OK : (int)TR_E_CUDA;
+    return tr_launch_next(kernel, {g, kAppendThreads}, s, c, (const uint4 *)Kn, (const uint4 *)Vn, T, count,
+                          (const int2 *)todo, tr_status_dev());
   };
   if (cache->d == 64) return e4m3 ? run(append_kernel<true, 64>) : run(append_kernel<false, 64>);
   return e4m3 ? run(append_kernel<true, 128>) : run(append_kernel<false, 128>);
@@ -606,19 +607,6 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   const long long pairs = (long long)c.B * c.Hkv;
   int cs = 1;
   while (cs < 8 && c.cap / (2 * cs) >= 4096 && pairs * 2 * cs <= 4 * tr_sm_count()) cs *= 2;
-  auto run = [&](auto kernel, dim3 grid, int cluster, int threads, auto... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-  };
   // whole rows where the pairs alone give every SM two CTAs; else narrow columns,
   // many CTAs, for the rows that move within the budget and the others apart
   const bool few = pairs * 2 < 2LL * tr_sm_count();
@@ -626,18 +614,19 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   // with a budget that the cache cannot exceed this still reports bad lengths
   const dim3 select(c.Hkv * cs, c.B);
   auto pick = [&](auto kernel) {
-    return run(kernel, select, cs, kSelThreads, c, budget, recent, keep, old_len, split, tr_status_dev());
+    return tr_launch_next(kernel, {select, kSelThreads, 0, cs}, s, c, budget, recent, keep, old_len, split,
+                          tr_status_dev());
   };
   const bool small = c.cap <= (long long)cs * 8 * kSelThreads;
-  TR_TRY_CUDA(cs == 1 ? (small ? pick(evict_select_kernel<8, 11>) : pick(evict_select_kernel<kSelMost, 11>))
-                      : (small ? pick(evict_select_kernel<8, 8>) : pick(evict_select_kernel<kSelMost, 8>)));
-  if (budget >= c.cap) return TR_OK;
+  rc = cs == 1 ? (small ? pick(evict_select_kernel<8, 11>) : pick(evict_select_kernel<kSelMost, 11>))
+               : (small ? pick(evict_select_kernel<8, 8>) : pick(evict_select_kernel<kSelMost, 8>));
+  if (rc != TR_OK || budget >= c.cap) return rc;
   const int row = c.row_bytes;
   int part = row;
   while (few && part > 32 && pairs * 2 * (row / part) < 2LL * tr_sm_count()) part /= 2;
   const dim3 move(2 * (row / part) + 1, c.Hkv, c.B);
   auto go = [&](auto kernel) {
-    return tr_launch_next(kernel, move, kMoveThreads, s, c, budget, recent, keep, old_len, split);
+    return tr_launch_next(kernel, {move, kMoveThreads}, s, c, budget, recent, keep, old_len, split);
   };
   rc = part == 256   ? go(evict_move_kernel<256, 4>)
        : part == 128 ? go(evict_move_kernel<128, 4>)
@@ -649,7 +638,7 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   const dim3 apart((unsigned)(turns < fill ? turns : fill), c.Hkv, c.B);
   for (int level = 2; level >= 1 && rc == TR_OK; --level) {
     auto rest = [&](auto kernel) {
-      return tr_launch_next(kernel, apart, kMoveThreads, s, c, budget, recent, level == 2, keep, old_len, split);
+      return tr_launch_next(kernel, {apart, kMoveThreads}, s, c, budget, recent, level == 2, keep, old_len, split);
     };
     rc = row == 256   ? rest(evict_apart_kernel<256>)
          : row == 128 ? rest(evict_apart_kernel<128>)
