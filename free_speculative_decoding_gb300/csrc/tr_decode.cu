@@ -9,7 +9,8 @@
 // tiles are laid end to end and cut into equal ranges, one per WARP of a
 // one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
 // shared memory (cp.async) and meets no barrier on the way, whatever the mix of
-// lengths.  With little work only as many warps of each CTA take part as leave
+// lengths.  Where all pairs of a small cache fit on the SMs at once each is one
+// CTA's work, and nothing is left to join.  With little work only as many warps of each CTA take part as leave
 // each about kMinRows rows, so that it spreads over every SM.  A pair that lies
 // inside one range is finished by its warp.  When a CTA's whole range lies in
 // one pair its warps' sums are joined in shared memory first.  What
@@ -62,6 +63,7 @@ struct DecodeArgs {
   int *plan;         // tiles per warp, warps per CTA, then for each sequence the tiles of one head before it
   long long s_ld;
   int Hq, G, accumulate;
+  bool own;          // one CTA per pair and row tile
   float scale_log2;
   unsigned *status;
 };
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   if (threadIdx.x == kThreads - 1 && kThreads * kOwn == kMaxB) tp[kMaxB] = before + sum;
   __syncthreads();
   const int T = tp[c.B] * c.Hkv;
-  const Cut cut = cut_of(T, gridDim.x, kTile, kWarps);
+  Cut cut = cut_of(T, gridDim.x, kTile, kWarps);
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i <= c.B + 2; i += kThreads) a.plan[i] = i == 0 ? cut.per : i == 1 ? cut.warps : tp[i - 2];
   // sequences without rows belong to no warp's range
@@ -252,22 +254,40 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
         }
 
-  const long long c0 = (long long)blockIdx.x * cut.warps * cut.per;  // the CTA's range
-  if (c0 >= T) return;
-  const int c1 = (int)min((long long)T, c0 + (long long)cut.warps * cut.per);
+  // the CTA's range of tiles, and its first pair
+  long long c0 = (long long)blockIdx.x * cut.warps * cut.per;
+  Cursor cur, ld;
+  int c1;
+  if (a.own) {
+    cur.b = blockIdx.x / c.Hkv;
+    cur.h = blockIdx.x % c.Hkv;
+    cur.kt = 0;
+    cur.L = Ls[cur.b];
+    cur.nt = tp[cur.b + 1] - tp[cur.b];
+    if (cur.nt == 0) return;
+    c0 = (long long)tp[cur.b] * c.Hkv + cur.h * cur.nt;
+    c1 = (int)c0 + cur.nt;
+    cut.warps = kWarps;
+    cut.per = (cur.nt + kWarps - 1) / kWarps;
+  } else {
+    if (c0 >= T) return;
+    c1 = (int)min((long long)T, c0 + (long long)cut.warps * cut.per);
+    seek(cur, tp, Ls, c.B, c.Hkv, (int)c0);
+  }
   const int w = blockIdx.x * cut.warps + warp;
   const int t0 = warp < cut.warps ? (int)min((long long)c1, c0 + (long long)warp * cut.per) : c1;
   const int t1 = warp < cut.warps ? min(c1, t0 + cut.per) : c1;
   const uint32_t ring = smem_u32(smem) + warp * S::RING;
   const int row0 = blockIdx.y * MT;  // first query head of this row tile inside its group
 
-  // the pair of the CTA's first tile; joined: it takes the CTA's whole range
-  Cursor cur, ld;
-  seek(cur, tp, Ls, c.B, c.Hkv, (int)c0);
+  // joined: the CTA's whole range lies in its first pair
   const bool joined = cut.warps > 1 && c1 - (int)c0 <= cur.nt - cur.kt;
   const Cursor pair = cur;
   if (t0 >= t1 && !joined) return;
-  if (t0 < t1) seek(cur, tp, Ls, c.B, c.Hkv, t0);
+  if (t0 < t1) {
+    if (joined) cur.kt += t0 - (int)c0;
+    else seek(cur, tp, Ls, c.B, c.Hkv, t0);
+  }
   ld = cur;
   int t_ld = t0;
 
@@ -665,13 +685,13 @@ __device__ __forceinline__ int parts_of(const KvDev &c, const DecodeArgs &a, int
   u.per = a.plan[0];
   u.warps = a.plan[1];
   const int p0 = a.plan[2 + b], nt = a.plan[3 + b] - p0;
-  const long long T = (long long)a.plan[2 + c.B] * c.Hkv;
-  const long long first = (long long)p0 * c.Hkv + (long long)h * nt, last = first + nt - 1;
+  const int T = a.plan[2 + c.B] * c.Hkv;  // tiles are at most 2^27
+  const int first = p0 * c.Hkv + h * nt, last = first + nt - 1;
   if (nt == 0) return 0;
-  u.w0 = (int)(first / u.per);
-  u.w1 = (int)(last / u.per);
-  const long long cr = (long long)u.per * u.warps;  // tiles of a CTA
-  const int k0 = (int)(first / cr), k1 = (int)(last / cr);
+  u.w0 = first / u.per;
+  u.w1 = last / u.per;
+  const int cr = u.per * u.warps;  // tiles of a CTA
+  const int k0 = first / cr, k1 = last / cr;
   // whole CTAs: all tiles of the CTA's range in the pair
   const bool whole0 = u.warps > 1 && first == k0 * cr && last >= min(T, (k0 + 1) * cr) - 1;
   const bool whole1 = u.warps > 1 && k1 > k0 && last == min(T, (k1 + 1) * cr) - 1;
@@ -715,47 +735,58 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
   const long long base = (long long)(m / MT) * W * 2;
   const int row = m % MT;
   auto slot = [&](int i) { return (base + part_slot(u, i)) * MT + row; };
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kFinThreads) M = fmaxf(M, a.part_ml[slot(i)].x);
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-  if (lane == 0) sm[warp] = M;
-  __syncthreads();
-  for (int i = 0; i < kFinWarps; ++i) M = fmaxf(M, sm[i]);
-  // each lane holds four columns; with d = 64 a warp takes two partials at a time
+  // each lane holds four columns; with d = 64 a warp takes two partials at a time.  Parts
+  // are read once: a warp's sums follow its own maximum, the four are levelled at the end
   constexpr int kPer = 128 / D;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  float l = 0.f, M = -INFINITY;
 #pragma unroll 4
   for (int i = warp * kPer + lane / (D / 4); i < parts; i += kFinWarps * kPer) {
     const long long s = slot(i);
     const float2 ml = a.part_ml[s];
     const float4 y = *reinterpret_cast<const float4 *>(a.part_o + s * D + (lane % (D / 4)) * 4);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    l += ml.y * f;
-    x.x += y.x * f;
-    x.y += y.y * f;
-    x.z += y.z * f;
-    x.w += y.w * f;
+    const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
+    const float e = ex2(M - base), f = ex2(ml.x - base);
+    M = mn;
+    l = l * e + ml.y * f;
+    x.x = x.x * e + y.x * f;
+    x.y = x.y * e + y.y * f;
+    x.z = x.z * e + y.z * f;
+    x.w = x.w * e + y.w * f;
   }
   if constexpr (kPer == 2) {
+    const float mn = fmaxf(M, __shfl_xor_sync(~0u, M, 16));
+    const float e = ex2(M - (mn == -INFINITY ? 0.f : mn));
+    M = mn;
+    l *= e;
     l += __shfl_xor_sync(~0u, l, 16);
+    x = make_float4(x.x * e, x.y * e, x.z * e, x.w * e);
     x.x += __shfl_xor_sync(~0u, x.x, 16);
     x.y += __shfl_xor_sync(~0u, x.y, 16);
     x.z += __shfl_xor_sync(~0u, x.z, 16);
     x.w += __shfl_xor_sync(~0u, x.w, 16);
   }
+  if (lane == 0) sm[warp] = M;
   if (lane < D / 4) acc[warp][lane] = x;
   if (lane == 0) sl[warp] = l;
   __syncthreads();
-  l = sl[0];
-  for (int i = 1; i < kFinWarps; ++i) l += sl[i];
+  float f4[kFinWarps];
+  M = sm[0];
+  for (int i = 1; i < kFinWarps; ++i) M = fmaxf(M, sm[i]);
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFinWarps; ++i) {
+    f4[i] = ex2(sm[i] - (M == -INFINITY ? 0.f : M));
+    l += sl[i] * f4[i];
+  }
   if (threadIdx.x < D / 4) {
-    float4 y = acc[0][threadIdx.x];
-    for (int i = 1; i < kFinWarps; ++i) {
-      y.x += acc[i][threadIdx.x].x;
-      y.y += acc[i][threadIdx.x].y;
-      y.z += acc[i][threadIdx.x].z;
-      y.w += acc[i][threadIdx.x].w;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kFinWarps; ++i) {
+      y.x += acc[i][threadIdx.x].x * f4[i];
+      y.y += acc[i][threadIdx.x].y * f4[i];
+      y.z += acc[i][threadIdx.x].z * f4[i];
+      y.w += acc[i][threadIdx.x].w * f4[i];
     }
     const float f = (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / l;
     *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
@@ -815,9 +846,13 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   }
 }
 
+// A pair's bytes up to which one CTA per pair is used (where all fit on the SMs).
+constexpr long long kOwnBytes = 256 * 1024;
+
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
 struct Plan {
   int MT, row_tiles, grid;  // grid: CTAs per row tile
+  bool own;
   size_t ml_off, lse_off, plan_off, s_off, total;
 };
 
@@ -828,6 +863,8 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   p.row_tiles = (G + p.MT - 1) / p.MT;
   const long long most = (long long)c.B * c.Hkv * ((c.cap + kMinRows - 1) / kMinRows);  // ranges worth a warp
   p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, most));
+  p.own = (long long)c.B * c.Hkv * p.row_tiles <= tr_sm_count() && (long long)c.cap * c.row_bytes * 2 <= kOwnBytes;
+  if (p.own) p.grid = c.B * c.Hkv;
   const size_t rows = (size_t)p.row_tiles * p.grid * kMaxWarps * 2 * p.MT;
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
@@ -854,7 +891,8 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   const dim3 grid(p.grid, p.row_tiles);
   int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
   if (rc != TR_OK) return rc;
-  rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
+  if (!p.own)
+    rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
   if (rc != TR_OK || !a.accumulate) return rc;
   return a.G > 8 ? tr_launch_next(score_kernel<true>, {dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads}, s, c, a)
                  : tr_launch_next(score_kernel<false>, {dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads}, s, c, a);
@@ -904,6 +942,7 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
   a.accumulate = accumulate != 0;
+  a.own = p.own;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = tr_status_dev();
   cudaStream_t s = (cudaStream_t)stream;

@@ -19,32 +19,44 @@ constexpr int kAppendUnroll = 4;  // 16-byte pieces of K and of V per thread
 // r = RN(1 / s): q0 = x r, q = q0 + r (x - q0 s) (Markstein 1990: with fused
 // multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60] a q0 of
 // 1024 or more (infinite, too) is past 448 as it is, and where the remainder
-// underflows the quotient is below 2^-40, which rounds to 0 either way.
+// underflows the quotient is below 2^-40, which rounds to 0 either way.  Other
+// scales (r = 0) take the division itself, which costs two to three times as much.
 struct Scale {
   float s, r;
-  bool tame;
-  __device__ __forceinline__ explicit Scale(float v) {
-    s = v;
-    r = __frcp_rn(v);
-    tame = v >= 0x1p-60f && v <= 0x1p60f;
-  }
-  __device__ __forceinline__ float of(float x) const {
-    if (!tame) return __fdiv_rn(x, s);
-    const float q = x * r;
-    return fabsf(q) >= 1024.f ? q : fmaf(fmaf(-q, s, x), r, q);
-  }
 };
+__device__ __forceinline__ Scale make_scale(float s) {
+  return {s, s >= 0x1p-60f && s <= 0x1p60f ? __frcp_rn(s) : 0.f};
+}
 
 // Eight bf16 values divided by the head's scale and rounded to e4m3 (one
 // rounding of the fp32 quotient to nearest even, clamped to +-448).
 __device__ __forceinline__ uint2 e4m3_of(const uint4 &x, const Scale &sc) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r[4];
+  float q[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(sc.of(lo), sc.of(hi)), __NV_SATFINITE, __NV_E4M3);
+    q[2 * i] = __uint_as_float(w[i] << 16);
+    q[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+  if (sc.r != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = q[i] * sc.r, q1 = fmaf(fmaf(-q0, sc.s, q[i]), sc.r, q0);
+      q[i] = fabsf(q0) >= 1024.f ? q0 : q1;
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      // one division's code for all eight: q turns round
+      const float d = __fdiv_rn(q[0], sc.s);
+#pragma unroll
+      for (int j = 0; j < 7; ++j) q[j] = q[j + 1];
+      q[7] = d;
+    }
+  }
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -95,6 +107,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
     if (threadIdx.x == 0 && n > 0) c.L[b] = Lb + n;
   }
   if (n <= 0 || blockIdx.x * (kAppendThreads * kAppendUnroll) >= (unsigned)n * c.Hkv * kPieces) return;
+  // the heads' scales and their reciprocals, once per CTA where they fit
+  constexpr int kHeads = E4M3 ? 256 : 1;
+  __shared__ Scale scales[2][kHeads];
+  const bool shared_scales = c.Hkv <= kHeads;
   const unsigned total = (unsigned)n * c.Hkv * kPieces;
   const long long base = (long long)b * T * c.Hkv * kPieces;
   const unsigned i0 = blockIdx.x * (kAppendThreads * kAppendUnroll) + threadIdx.x;
@@ -112,12 +128,23 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
     at[u] = kv_block(c, b, p) + (long long)head[u] * c.head_stride + kv_row(c, p) + piece * kOut;
     if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + head[u]) * c.scores_ld + p] = 0.f;
   }
+  if constexpr (E4M3) {
+    if (shared_scales) {
+      if ((int)threadIdx.x < c.Hkv) {
+        scales[0][threadIdx.x] = make_scale(__ldg(c.k_scale + threadIdx.x));
+        scales[1][threadIdx.x] = make_scale(__ldg(c.v_scale + threadIdx.x));
+      }
+      __syncthreads();
+    }
+  }
 #pragma unroll
   for (int u = 0; u < kAppendUnroll; ++u) {
     if (i0 + u * kAppendThreads >= total) continue;
     if constexpr (E4M3) {
-      *reinterpret_cast<uint2 *>(c.K + at[u]) = e4m3_of(kx[u], Scale(__ldg(c.k_scale + head[u])));
-      *reinterpret_cast<uint2 *>(c.V + at[u]) = e4m3_of(vx[u], Scale(__ldg(c.v_scale + head[u])));
+      const Scale ks = shared_scales ? scales[0][head[u]] : make_scale(__ldg(c.k_scale + head[u]));
+      const Scale vs = shared_scales ? scales[1][head[u]] : make_scale(__ldg(c.v_scale + head[u]));
+      *reinterpret_cast<uint2 *>(c.K + at[u]) = e4m3_of(kx[u], ks);
+      *reinterpret_cast<uint2 *>(c.V + at[u]) = e4m3_of(vx[u], vs);
     } else {
       *reinterpret_cast<uint4 *>(c.K + at[u]) = kx[u];
       *reinterpret_cast<uint4 *>(c.V + at[u]) = vx[u];
