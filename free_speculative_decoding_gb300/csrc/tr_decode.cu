@@ -30,7 +30,11 @@
 // p is split exactly into three bf16 parts (8 + 8 + 8 bits), or into two fp16 parts
 // (22 bits, p scaled up to 2^15 so that small weights stay normal numbers), and
 // each part is multiplied with V.  With at most 8 heads the empty half of the
-// instruction's rows carries the second part at no extra cost.
+// instruction's rows carries the second part at no extra cost.  The matrix
+// unit's own adds cut off what does not fit, always towards zero, so its sums
+// last 16 rows only and are added to O with rounded adds (kept in the unit over a
+// whole range, the loss grew with the range: 7e-6 of the result's norm at 3400
+// rows a warp against 1e-6 for fp32 products and sums).
 // An 8-bit row is widened to fp16 (exact); Q is scaled by a power of two per
 // head so that narrowing bf16 to fp16 is exact for all but negligible elements.
 #include <cuda_fp16.h>
@@ -92,13 +96,20 @@ struct Shape {
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1, bool bf) {
   if (bf)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// a + b, two fp32 values in one instruction.
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+  asm("{ .reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; add.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
 }
 
 // 16 bytes from global to shared memory; of the second form 16 zero bytes where not valid.
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   constexpr int R = MT / 8;                           // query rows of a lane: g, g + 8
   constexpr float kOff = S::BF ? 0.f : 7.f;           // fp16 weights run up to 2^15
   uint32_t q[R][S::QR];
-  float mul[R], m[R], l[R], o[S::NT][4];
+  float mul[R], m[R], l[R], o[S::NT][2 * R];
   float *logits[R];  // where a lane's logits of the next tile go
   int kt0 = 0;
 #pragma unroll
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
 #pragma unroll
       for (int n = 0; n < S::NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        for (int e = 0; e < 2 * R; ++e) o[n][e] = 0.f;
     }
 
     copy_wait<S::STAGES - 2>();
@@ -476,13 +487,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
         l[r] *= f;
 #pragma unroll
         for (int n = 0; n < S::NT; ++n) {
-          if constexpr (R == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= f;
-          } else {
-            o[n][2 * r] *= f;
-            o[n][2 * r + 1] *= f;
-          }
+          o[n][2 * r] *= f;
+          o[n][2 * r + 1] *= f;
         }
       }
       const float base = m[r] == -INFINITY ? 0.f : m[r];
@@ -495,11 +501,11 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
         }
     }
 
+    // P in parts: pt[kb][part][r][j] holds rows 2t, 2t + 1 of half j of 16 rows for query row g + 8 r
+    constexpr int kParts = S::BF ? 3 : 2;
+    uint32_t pt[KB][kParts][R][2];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      // P of 16 rows in parts: pt[part][r][j] holds rows 2t, 2t + 1 of half j for query row g + 8 r
-      constexpr int kParts = S::BF ? 3 : 2;
-      uint32_t pt[kParts][R][2];
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -508,29 +514,36 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           if constexpr (S::BF) {
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-              pt[k][r][j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+              pt[kb][k][r][j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
               if (k < 2) {
                 x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
                 y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
               }
             }
           } else {
-            pt[0][r][j] = pack_half2(x, y);
-            const __half2 h = *reinterpret_cast<const __half2 *>(&pt[0][r][j]);
-            pt[1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
+            pt[kb][0][r][j] = pack_half2(x, y);
+            const __half2 h = *reinterpret_cast<const __half2 *>(&pt[kb][0][r][j]);
+            pt[kb][1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
           }
         }
-      auto pv = [&](float(&acc)[4], uint32_t b0, uint32_t b1) {
-        if constexpr (R == 1) {
-          mma(acc, pt[0][0][0], pt[1][0][0], pt[0][0][1], pt[1][0][1], b0, b1, S::BF);
-          if constexpr (S::BF) mma(acc, pt[kParts - 1][0][0], 0u, pt[kParts - 1][0][1], 0u, b0, b1, true);
-        } else {
+    // O += P V of 16 rows: column block n = VW * v + e holds columns (lane / 4 + 8 v) * VW + e
+    auto pv = [&](float(&to)[2 * R], int kb, uint32_t b0, uint32_t b1) {
+      const uint32_t(&p)[kParts][R][2] = pt[kb];
+      float acc[4] = {};
+      if constexpr (R == 1) {
+        mma(acc, p[0][0][0], p[1][0][0], p[0][0][1], p[1][0][1], b0, b1, S::BF);
+        if constexpr (S::BF) mma(acc, p[kParts - 1][0][0], 0u, p[kParts - 1][0][1], 0u, b0, b1, true);
+        add2(acc[0], acc[1], acc[2], acc[3]);
+        add2(to[0], to[1], acc[0], acc[1]);
+      } else {
 #pragma unroll
-          for (int k = 0; k < kParts; ++k)
-            mma(acc, pt[k][0][0], pt[k][R - 1][0], pt[k][0][1], pt[k][R - 1][1], b0, b1, S::BF);
-        }
-      };
-      // O += P V: column block n = VW * s + e holds columns (lane / 4 + 8 s) * VW + e
+        for (int k = 0; k < kParts; ++k) mma(acc, p[k][0][0], p[k][R - 1][0], p[k][0][1], p[k][R - 1][1], b0, b1, S::BF);
+        add2(to[0], to[1], acc[0], acc[1]);
+        add2(to[2 * R - 2], to[2 * R - 1], acc[2], acc[3]);
+      }
+    };
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int v = 0; v < S::VS; ++v) {
         constexpr int NW = S::F8 ? S::VW / 4 : S::VW / 2;  // words of a piece
@@ -557,16 +570,16 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
             for (int f = 0; f < 2; ++f) {
               const uint32_t sel = f ? 0x7362 : 0x5140;
               const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
-              pv(o[v * S::VW + e * 4 + f * 2], widen_lo(lo), widen_lo(hi));
-              pv(o[v * S::VW + e * 4 + f * 2 + 1], widen_hi(lo), widen_hi(hi));
+              pv(o[v * S::VW + e * 4 + f * 2], kb, widen_lo(lo), widen_lo(hi));
+              pv(o[v * S::VW + e * 4 + f * 2 + 1], kb, widen_hi(lo), widen_hi(hi));
             }
           } else {
-            pv(o[v * S::VW + e * 2], __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
-            pv(o[v * S::VW + e * 2 + 1], __byte_perm(x[0][e], x[1][e], 0x7632), __byte_perm(x[2][e], x[3][e], 0x7632));
+            pv(o[v * S::VW + e * 2], kb, __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
+            pv(o[v * S::VW + e * 2 + 1], kb, __byte_perm(x[0][e], x[1][e], 0x7632),
+               __byte_perm(x[2][e], x[3][e], 0x7632));
           }
         }
       }
-    }
 
     if (!joined && (cur.kt == cur.nt - 1 || i == t1 - 1)) {
       // the range leaves this pair: the result, or a partial
@@ -600,8 +613,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
               float y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float *z = o[v * S::VW + e + k];
-                y[k] = (R == 1 ? z[n] + z[n + 2] : z[2 * r + n]) * f;
+                y[k] = o[v * S::VW + e + k][2 * r + n] * f;
               }
               *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
             }
@@ -631,8 +643,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           float y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float *z = o[v * S::VW + e + k];
-            y[k] = R == 1 ? z[n] + z[n + 2] : z[2 * r + n];
+            y[k] = o[v * S::VW + e + k][2 * r + n];
           }
           *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
         }
