@@ -17,46 +17,64 @@ constexpr int kAppendUnroll = 4;  // 16-byte pieces of K and of V per thread
 
 // x / s rounded to the nearest fp32, as far as its rounding to e4m3 can tell, from
 // r = RN(1 / s): q0 = x r, q = q0 + r (x - q0 s) (Markstein 1990: with fused
-// multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60] a q0 of
-// 1024 or more (infinite, too) is past 448 as it is, and where the remainder
+// multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60]: x is
+// first held to +-most, a bf16 number between 1024 s and 1033 s (the quotient is
+// past 448 either way, and nothing overflows; NaN stays), and where the remainder
 // underflows the quotient is below 2^-40, which rounds to 0 either way.  Other
 // scales (r = 0) take the division itself, which costs two to three times as much.
 struct Scale {
   float s, r;
+  uint32_t most;  // twice
 };
 __device__ __forceinline__ Scale make_scale(float s) {
-  return {s, s >= 0x1p-60f && s <= 0x1p60f ? __frcp_rn(s) : 0.f};
+  const uint32_t m = (__float_as_uint(1024.f * s) + 0xFFFFu) >> 16;
+  return {s, s >= 0x1p-60f && s <= 0x1p60f ? __frcp_rn(s) : 0.f, m | (m << 16)};
+}
+
+// Two fp32 values in one instruction: a * b, and a * b + c.
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b, float m) {
+  asm("{ .reg .b64 p, q; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %4}; mul.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(m));
+}
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float m, float c, float d) {
+  asm("{ .reg .b64 p, q, r; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %4}; mov.b64 r, {%5, %6};"
+      " fma.rn.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(m), "f"(c), "f"(d));
+}
+// bf16 pairs held to +-most; NaN stays.
+__device__ __forceinline__ uint32_t hold2(uint32_t x, uint32_t most) {
+  uint32_t r;
+  asm("{ .reg .b32 p; min.NaN.bf16x2 p, %1, %2; max.NaN.bf16x2 %0, p, %3; }"
+      : "=r"(r)
+      : "r"(x), "r"(most), "r"(most | 0x80008000u));
+  return r;
 }
 
 // Eight bf16 values divided by the head's scale and rounded to e4m3 (one
 // rounding of the fp32 quotient to nearest even, clamped to +-448).
 __device__ __forceinline__ uint2 e4m3_of(const uint4 &x, const Scale &sc) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    q[2 * i] = __uint_as_float(w[i] << 16);
-    q[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  uint32_t r[4];
   if (sc.r != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q0 = q[i] * sc.r, q1 = fmaf(fmaf(-q0, sc.s, q[i]), sc.r, q0);
-      q[i] = fabsf(q0) >= 1024.f ? q0 : q1;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = hold2(w[i], sc.most);
+      const float lo = __uint_as_float(h << 16), hi = __uint_as_float(h & 0xFFFF0000u);
+      float p, q, u, v;
+      mul2(p, q, lo, hi, sc.r);
+      fma2(u, v, p, q, -sc.s, lo, hi);
+      fma2(p, q, u, v, sc.r, p, q);
+      r[i] = __nv_cvt_float2_to_fp8x2(make_float2(p, q), __NV_SATFINITE, __NV_E4M3);
     }
   } else {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      // one division's code for all eight: q turns round
-      const float d = __fdiv_rn(q[0], sc.s);
 #pragma unroll
-      for (int j = 0; j < 7; ++j) q[j] = q[j + 1];
-      q[7] = d;
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+      r[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(lo, sc.s), __fdiv_rn(hi, sc.s)), __NV_SATFINITE, __NV_E4M3);
     }
   }
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -117,16 +135,27 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
   uint4 kx[kAppendUnroll], vx[kAppendUnroll];
   long long at[kAppendUnroll];
   int head[kAppendUnroll];
+  // row th = token * Hkv + head; the next piece of this thread is kAppendThreads / kPieces rows on
+  constexpr unsigned kNext = kAppendThreads / kPieces;
+  const unsigned piece = threadIdx.x % kPieces, tok_next = kNext / (unsigned)c.Hkv, h_next = kNext % (unsigned)c.Hkv;
+  unsigned th = i0 / kPieces, tok = th / (unsigned)c.Hkv, h = th - tok * c.Hkv;
 #pragma unroll
-  for (int u = 0; u < kAppendUnroll; ++u) {  // a piece behind the last one is read twice, and not written
-    const unsigned i = min(i0 + u * kAppendThreads, total - 1);
-    kx[u] = __ldcs(Kn + base + i);
-    vx[u] = __ldcs(Vn + base + i);
-    const unsigned piece = i % kPieces, th = i / kPieces, tok = th / (unsigned)c.Hkv;
-    const int p = Lb + (int)tok;
-    head[u] = (int)(th - tok * c.Hkv);
-    at[u] = kv_block(c, b, p) + (long long)head[u] * c.head_stride + kv_row(c, p) + piece * kOut;
-    if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + head[u]) * c.scores_ld + p] = 0.f;
+  for (int u = 0; u < kAppendUnroll; ++u) {
+    head[u] = h;
+    if (i0 + u * kAppendThreads < total) {
+      const unsigned i = i0 + u * kAppendThreads;
+      kx[u] = __ldcs(Kn + base + i);
+      vx[u] = __ldcs(Vn + base + i);
+      const int p = Lb + (int)tok;
+      at[u] = kv_block(c, b, p) + (long long)h * c.head_stride + kv_row(c, p) + piece * kOut;
+      if (c.scores && piece == 0) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] = 0.f;
+    }
+    tok += tok_next;
+    h += h_next;
+    if (h >= (unsigned)c.Hkv) {
+      h -= c.Hkv;
+      ++tok;
+    }
   }
   if constexpr (E4M3) {
     if (shared_scales) {
