@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   auto page_of = [&]() {
     const int p = ld.kt * kTile + lane;
     return !c.page_table ? ld.b
-           : t_ld < t1 && lane < kTile && p < ld.L ? __ldg(c.page_table + (long long)ld.b * c.max_pages + (p >> c.page_log2))
+           : t_ld < t1 && lane < kTile && p < ld.L ? c.page_table[(long long)ld.b * c.max_pages + (p >> c.page_log2)]
                                                    : 0;
   };
   int page = page_of();
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           for (int s = 0; s < D / 64; ++s)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint4 x = valid ? __ldg(src + (4 * s + t) * 2 + j) : make_uint4(0, 0, 0, 0);
+              const uint4 x = valid ? src[(4 * s + t) * 2 + j] : make_uint4(0, 0, 0, 0);
               const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -407,11 +407,11 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           for (int e = 0; e < S::QR; ++e)
             q[r][e] = pack_half2(scalbnf(__uint_as_float(q[r][e] << 16), up),
                                  scalbnf(__uint_as_float(q[r][e] & 0xFFFF0000u), up));
-          mul[r] = scalbnf(a.scale_log2 * __ldg(c.k_scale + cur.h), -up);
+          mul[r] = scalbnf(a.scale_log2 * c.k_scale[cur.h], -up);
         } else {
 #pragma unroll
           for (int s = 0; s < D / 32; ++s) {
-            const uint4 x = valid ? __ldg(src + 4 * s + t) : make_uint4(0, 0, 0, 0);
+            const uint4 x = valid ? src[4 * s + t] : make_uint4(0, 0, 0, 0);
             q[r][s * 4] = x.x;
             q[r][s * 4 + 1] = x.y;
             q[r][s * 4 + 2] = x.z;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
       // the range leaves this pair: the result, or a partial
       const bool whole = kt0 == 0 && cur.kt == cur.nt - 1;
       const long long slot = ((long long)blockIdx.y * gridDim.x * kWarps + w) * 2 + (kt0 > 0 ? 0 : 1);
-      const float vs = S::F8 ? __ldg(c.v_scale + cur.h) : 1.f;
+      const float vs = S::F8 ? c.v_scale[cur.h] : 1.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         l[r] += __shfl_xor_sync(~0u, l[r], 1);
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   __syncthreads();
   const bool whole = pair.kt == 0 && c1 - (int)c0 == pair.nt;
   const long long slot = ((long long)blockIdx.y * gridDim.x * kWarps + blockIdx.x * cut.warps) * 2;
-  const float vs = S::F8 ? __ldg(c.v_scale + pair.h) : 1.f;
+  const float vs = S::F8 ? c.v_scale[pair.h] : 1.f;
   const int used = (c1 - (int)c0 + cut.per - 1) / cut.per;  // warps with tiles
   for (int i = threadIdx.x; i < min(MT, a.G - row0) * (D / 4); i += kThreads) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
@@ -754,8 +754,8 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
 #pragma unroll 4
   for (int i = warp * kPer + lane / (D / 4); i < parts; i += kFinWarps * kPer) {
     const long long s = slot(i);
-    const float2 ml = a.part_ml[s];
-    const float4 y = *reinterpret_cast<const float4 *>(a.part_o + s * D + (lane % (D / 4)) * 4);
+    const float2 ml = __ldcg(a.part_ml + s);
+    const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + s * D + (lane % (D / 4)) * 4));
     const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
     const float e = ex2(M - base), f = ex2(ml.x - base);
     M = mn;
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
       y.z += acc[i][threadIdx.x].z * f4[i];
       y.w += acc[i][threadIdx.x].w * f4[i];
     }
-    const float f = (c.v_scale ? __ldg(c.v_scale + h) : 1.f) / l;
+    const float f = (c.v_scale ? c.v_scale[h] : 1.f) / l;
     *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
         make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
   }
@@ -830,8 +830,8 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   if (p < L) {
 #pragma unroll 4
     for (int m = SPLIT ? warp : 0; m < a.G; m += SPLIT ? kFinWarps : 1) {
-      const float lse2 = __ldg(a.lse2 + hq + m);
-      const float4 x = *reinterpret_cast<const float4 *>(src + m * a.s_ld);  // behind the last row: not used
+      const float lse2 = __ldcg(a.lse2 + hq + m);
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + m * a.s_ld));  // behind the last row: not used
       w.x += ex2(x.x - lse2);
       w.y += ex2(x.y - lse2);
       w.z += ex2(x.z - lse2);

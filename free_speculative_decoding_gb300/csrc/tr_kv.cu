@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
   if constexpr (E4M3) {
     if (shared_scales) {
       if ((int)threadIdx.x < c.Hkv) {
-        scales[0][threadIdx.x] = make_scale(__ldg(c.k_scale + threadIdx.x));
-        scales[1][threadIdx.x] = make_scale(__ldg(c.v_scale + threadIdx.x));
+        scales[0][threadIdx.x] = make_scale(c.k_scale[threadIdx.x]);
+        scales[1][threadIdx.x] = make_scale(c.v_scale[threadIdx.x]);
       }
       __syncthreads();
     }
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvDev c
   for (int u = 0; u < kAppendUnroll; ++u) {
     if (i0 + u * kAppendThreads >= total) continue;
     if constexpr (E4M3) {
-      const Scale ks = shared_scales ? scales[0][head[u]] : make_scale(__ldg(c.k_scale + head[u]));
-      const Scale vs = shared_scales ? scales[1][head[u]] : make_scale(__ldg(c.v_scale + head[u]));
+      const Scale ks = shared_scales ? scales[0][head[u]] : make_scale(c.k_scale[head[u]]);
+      const Scale vs = shared_scales ? scales[1][head[u]] : make_scale(c.v_scale[head[u]]);
       *reinterpret_cast<uint2 *>(c.K + at[u]) = e4m3_of(kx[u], ks);
       *reinterpret_cast<uint2 *>(c.V + at[u]) = e4m3_of(vx[u], vs);
     } else {
@@ -440,7 +440,7 @@ __device__ __forceinline__ Cuts cuts_of(int budget, int k, int Lb, const int32_t
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = (int)((long long)u.one * i / 8);
-    at[i] = r < k ? __ldg(keep + r) : r + Lb - budget;
+    at[i] = r < k ? __ldcg(keep + r) : r + Lb - budget;
   }
 #pragma unroll
   for (int i = 7; i >= 0; --i)
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_apart_kernel(const KvDev c
 #pragma unroll
     for (int u = 0; u < kApartUnroll; ++u) {  // a row behind the last one is read twice, and not written
       const int r = min(r0 + u * kRows + (int)threadIdx.x / kLanes, last - 1);
-      const int src = r < k ? __ldg(keep + r) : r + shift;
+      const int src = r < k ? __ldcg(keep + r) : r + shift;
       from[u] = head + kv_block(c, b, src) + kv_row(c, src);
       if (scorer) z[u] = sc[src];
     }
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const KvDev c,
   const int k = budget - recent, shift = Lb - budget;  // a protected row moves by `shift`
   keep += ((long long)b * c.Hkv + h) * budget;
   const int rows = split ? cuts_of(budget, k, Lb, keep, split + (long long)b * c.Hkv + h).two : budget;
-  auto source = [&](int r) { return r >= budget ? r : r < k ? __ldg(keep + r) : r + shift; };
+  auto source = [&](int r) { return r >= budget ? r : r < k ? __ldcg(keep + r) : r + shift; };
   const int per = c.row_bytes / PART;
   if (part == 2 * per) {
     float *sc = c.scores + ((long long)b * c.Hkv + h) * c.scores_ld;

@@ -5,6 +5,8 @@
 #include "tr_internal.cuh"
 
 // A cache as the kernels see it: strides in bytes, the page size as a shift.
+// The kernels may be set up before the one before them ends (tr_launch_next), so
+// nothing that it can have written is read through the non-coherent path (__ldg).
 struct KvDev {
   char *K, *V;
   int B, Hkv;
@@ -23,7 +25,7 @@ struct KvDev {
 // sequence b, -1 for a page table entry that points nowhere.
 __device__ __forceinline__ long long kv_block(const KvDev &c, int b, int p) {
   if (!c.page_table) return (long long)b * c.block_stride;
-  const int page = __ldg(c.page_table + (long long)b * c.max_pages + (p >> c.page_log2));
+  const int page = c.page_table[(long long)b * c.max_pages + (p >> c.page_log2)];
   return (unsigned)page < (unsigned)c.num_pages ? (long long)page * c.block_stride : -1;
 }
 
@@ -38,7 +40,7 @@ __device__ __forceinline__ bool kv_bad_pages(const KvDev &c, int b, int p0, int 
   int bad = 0;
   if (c.page_table && p1 > p0)
     for (int i = (p0 >> c.page_log2) + threadIdx.x; i <= (p1 - 1) >> c.page_log2; i += blockDim.x)
-      bad |= (unsigned)__ldg(c.page_table + (long long)b * c.max_pages + i) >= (unsigned)c.num_pages;
+      bad |= (unsigned)c.page_table[(long long)b * c.max_pages + i] >= (unsigned)c.num_pages;
   return __syncthreads_or(bad);
 }
 

@@ -14,7 +14,7 @@ or, without a draft (one token per sequence, the root's),
     state.decode(Q, Kn, Vn)          # append the root's K/V, attention of one token
     state.finish_decode(logits)      # top-K, update of the root's row, next root and tree
 
-and the two may alternate.  With ``budget`` the attention weights that the
+and the two may alternate (``single_token=True``).  With ``budget`` the attention weights that the
 cached rows gather in decode are kept, and evict() cuts every sequence longer
 than the budget down to it.  L then no longer is a token's position: a program
 that needs positions (rotary embeddings) keeps count of them itself.
@@ -35,7 +35,7 @@ from . import (TR_INIT_INHERIT, TR_UPD_ALL, KVCache, Tree, make_step_args, tr_ac
 
 class TRState:
     def __init__(self, tree: Tree, B: int, V: int, m_dtype=torch.int64, Hq=0, Hkv=0, d=128, cap=0,
-                 logits_dtype=torch.float32, D=0, device="cuda", budget=0, recent=0):
+                 logits_dtype=torch.float32, D=0, device="cuda", single_token=False, budget=0, recent=0):
         self.tree = tree
         self.B, self.V, self.K, self.N = B, V, tree.K, tree.N
         self.Dmax = tree.max_depth
@@ -60,9 +60,11 @@ class TRState:
             self.O = torch.zeros(B, self.N, Hq, d, dtype=torch.float32, **dev)
             self.ws_attn = workspace(tr_verify_attn_workspace_bytes(B, Hq, Hkv, d, cap, tree), device)
             self.scale = d ** -0.5
-            self._init_decode(budget, recent, dev)
-        elif budget:
-            raise ValueError("a budget needs a cache (Hq > 0)")
+        self.budget, self.recent, self.scores = budget, recent, None
+        if single_token or budget:
+            if not self.attention:
+                raise ValueError("single-token steps need a cache (Hq > 0)")
+            self._init_single_token(dev)
         self._args = make_step_args(tree, self.M, self.tree_tok, self.ids, self.vals, self.acc_len, self.path,
                                     self.committed, self.root, self.L,
                                     logits=torch.empty(1, V, dtype=logits_dtype, **dev) if D == 0 else None,
@@ -70,19 +72,19 @@ class TRState:
                                     Wt=torch.empty(1, max(D, 64), dtype=torch.bfloat16, **dev) if D else None)
         self.ws_step = workspace(tr_step_workspace_bytes(self._args), device)
 
-    def _init_decode(self, budget, recent, dev):
-        """What single-token steps and eviction need."""
-        B, Hq = self.B, self.Hq
-        self.budget, self.recent = budget, recent
-        # a row that no query has looked at has gathered nothing: scores behind L are always 0
-        self.scores = torch.zeros(B, self.Hkv, self.cap, dtype=torch.float32, **dev) if budget else None
+    def _init_single_token(self, dev):
+        """What steps without a draft and eviction need."""
+        B, Hq, budget = self.B, self.Hq, self.budget
+        if budget:
+            if not 0 <= self.recent <= budget:
+                raise ValueError("recent must be in [0, budget]")
+            # a row that no query has looked at has gathered nothing: scores behind L are always 0
+            self.scores = torch.zeros(B, self.Hkv, self.cap, dtype=torch.float32, **dev)
         self.cache = KVCache(self.Kc, self.Vc, self.L, scores=self.scores)
         self.O1 = torch.zeros(B, Hq, self.d, dtype=torch.float32, **dev)
         self.ws_decode = workspace(tr_decode_attn_workspace_bytes(self.cache, Hq, bool(budget)), self.device)
         self.ws_append = workspace(tr_kv_append_workspace_bytes(self.cache), self.device)
         if budget:
-            if not 0 <= recent <= budget:
-                raise ValueError("recent must be in [0, budget]")
             self.ws_evict = workspace(tr_kv_evict_workspace_bytes(self.cache, budget), self.device)
         self.tree1 = Tree((0,), self.K)   # the root alone
         self.ids1 = torch.zeros(B, self.K, dtype=torch.int32, **dev)
@@ -99,7 +101,7 @@ class TRState:
         already is."""
         self.root.copy_(torch.as_tensor(root, dtype=torch.int32))
         self.L.copy_(torch.as_tensor(L, dtype=torch.int32))
-        if self.attention and self.scores is not None:
+        if self.scores is not None:
             self.scores.zero_()
         if M_src is not None and M_src.dim() == 3:
             self.M.copy_(M_src)

@@ -11,11 +11,17 @@ off by delta (plus 2^-22 of the hardware's 2^x), relative.  Sums over the rows
 run as chains of at most L / 8 + 64 adds.  So every output element is within
 eps = 2 * (delta + 2^-22 + (L / 8 + 64) * 2u) of sum_p w_p |v_p|, and lse within
 delta + 2^-22 + (L / 8 + 64) * 2u + 4u |lse|."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import oracle
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 pytestmark = pytest.mark.gpu
 
@@ -735,6 +741,74 @@ def test_evict_in_a_graph(tr):
 # together
 # ----------------------------------------------------------------------------
 
+FIRST_CALLS = """
+import torch, free_speculative_decoding_gb300 as tr
+B, H, cap, d = 2, 3, 9000, 64
+K = torch.randn(B, H, cap, d, device="cuda").bfloat16()
+V, sc = K.clone(), torch.rand(B, H, cap, device="cuda")
+L0 = torch.tensor([8000, 77], dtype=torch.int32, device="cuda")
+L = L0.clone()
+c = tr.KVCache(K, V, L, scores=sc)
+Q, O = torch.randn(B, 6, d, device="cuda").bfloat16(), torch.zeros(B, 6, d, device="cuda")
+n = torch.randn(B, 500, H, d, device="cuda").bfloat16()
+ws = [tr.workspace(x) for x in (tr.tr_kv_append_workspace_bytes(c), tr.tr_decode_attn_workspace_bytes(c, 6, True),
+                                tr.tr_kv_evict_workspace_bytes(c, 300))]
+def step():
+    tr.tr_kv_append(n, n, c, ws[0])
+    tr.tr_decode_attn(Q, c, O, 0.125, ws[1], accumulate=True)
+    tr.tr_kv_evict(c, 300, 40, ws[2])
+K0, V0, s0 = K.clone(), V.clone(), sc.clone()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (O, K, V, sc, L)]
+for x, y in ((K, K0), (V, V0), (sc, s0), (L, L0)):
+    x.copy_(y)
+O.zero_()
+step()
+assert all(torch.equal(x, y) for x, y in zip(got, (O, K, V, sc, L)))
+assert L.tolist() == [300, 300] and tr.tr_get_status() == 0
+print("fine")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(tr):
+    """Nothing has to run before a capture: all three calls are captured as a process's first, and replay to what
+    they do eagerly."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("layout", ["dense", 16])
+def test_back_to_back_calls_see_each_other(tr, layout):
+    """Append, attention and eviction queued without a pause between them (each may be set up while the one before it
+    ends) read what the one before wrote: the same as with a synchronisation after every call."""
+    outs = []
+    for wait in (False, True):
+        c = Made(tr, np.random.default_rng(41), "bf16", layout, [700, 3, 0, 1500], 4, 128, extra=1200)
+        Q = [c.queries(8, 2.0).cuda() for _ in range(60)]
+        new = [torch.randn(4, 1 + i % 40, 4, 128, generator=c.g).bfloat16().cuda() for i in range(60)]
+        ws = [tr.workspace(x) for x in (tr.tr_kv_append_workspace_bytes(c.cache),
+                                        tr.tr_decode_attn_workspace_bytes(c.cache, 8, True),
+                                        tr.tr_kv_evict_workspace_bytes(c.cache, 600))]
+        O = [torch.empty(4, 8, 128, device="cuda") for _ in range(60)]
+        pause = torch.cuda.synchronize if wait else lambda: None
+        pause()
+        for i in range(60):
+            tr.tr_kv_append(new[i], new[i], c.cache, ws[0])
+            pause()
+            tr.tr_decode_attn(Q[i], c.cache, O[i], 0.09, ws[1], accumulate=True)
+            pause()
+            if i % 3 == 2:
+                tr.tr_kv_evict(c.cache, 600, 100, ws[2])
+                pause()
+        torch.cuda.synchronize()
+        outs.append(O + [c.scores, c.L, raw(c.K), raw(c.V)])
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
 @pytest.mark.parametrize("type,layout", [("bf16", "dense"), ("bf16", 16), ("e4m3", 16), ("f16", "nhd4")])
 def test_decoding_steps_with_eviction(tr, type, layout):
     """Prompt, then steps of append + attention with weights gathered, cut back whenever a sequence passes 48 rows;
@@ -769,7 +843,8 @@ def test_engine_alternates_tree_and_single_token_steps(tr, budget):
 
     w = synth.WORKLOADS["tiny"].scaled(prefix=(100, 140), B=2, Hq=8, Hkv=4, V=5000, steps=24)
     tree, plan, plan1 = tr.Tree(w.child_counts, w.K), oracle.TreePlan(w.child_counts, w.K), oracle.TreePlan((0,), w.K)
-    st = TRState(tree, w.B, w.V, Hq=w.Hq, Hkv=w.Hkv, d=w.d, cap=w.capacity(), budget=budget, recent=20 if budget else 0)
+    st = TRState(tree, w.B, w.V, Hq=w.Hq, Hkv=w.Hkv, d=w.d, cap=w.capacity(), single_token=True, budget=budget,
+                 recent=20 if budget else 0)
     sd.fill_cache(w, st)
     gpu_start(w, st)
     states, target, qkv = oracle_states(w), target_fn(w), oracle_qkv(w)
