@@ -9,8 +9,9 @@
 // tiles are laid end to end and cut into equal ranges, one per WARP of a
 // one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
 // shared memory (cp.async) and meets no barrier on the way, whatever the mix of
-// lengths.  Where all pairs of a small cache fit on the SMs at once each is one
-// CTA's work, and nothing is left to join.  With little work only as many warps of each CTA take part as leave
+// lengths.  Where all pairs of a small cache fit on the SMs at once each is the
+// work of one CTA, or of a cluster whose CTAs join their parts through distributed
+// shared memory, and nothing is left for a second kernel.  With little work only as many warps of each CTA take part as leave
 // each about kMinRows rows, so that it spreads over every SM.  A pair that lies
 // inside one range is finished by its warp.  When a CTA's whole range lies in
 // one pair its warps' sums are joined in shared memory first.  What
@@ -42,16 +43,20 @@
 #include <algorithm>
 #include <atomic>
 
+#include <cooperative_groups.h>
+
 #include "tr_kv.cuh"
 #include "tr_sm100.cuh"
 
 namespace {
 
+namespace cg = cooperative_groups;
 using sm100::ex2;
 using sm100::smem_u32;
 
 constexpr int kMaxB = 1024;
 constexpr int kMaxWarps = 12;            // of any split kernel's CTA
+constexpr int kMaxOwn = 8;               // CTAs of a cluster that share a pair
 constexpr int kRings = 192 * 1024;       // bytes of a CTA's rings
 constexpr int kMinRows = 32;            // cached rows of a warp's range, about, at least
 constexpr float kLn2 = 0.6931471805599453f;
@@ -67,12 +72,12 @@ struct DecodeArgs {
   int *plan;         // tiles per warp, warps per CTA, then for each sequence the tiles of one head before it
   long long s_ld;
   int Hq, G, accumulate;
-  bool own;          // one CTA per pair and row tile
+  int own;           // CTAs (a cluster) that share one pair and row tile; 0: ranges over all pairs
   float scale_log2;
   unsigned *status;
 };
 
-template <int TYPE, int D>
+template <int TYPE, int D, int NW>
 struct Shape {
   static constexpr bool F8 = TYPE == TR_KV_E4M3;
   static constexpr bool BF = TYPE == TR_KV_BF16;
@@ -83,7 +88,7 @@ struct Shape {
   static constexpr int KB = ROW == 256 ? 1 : 2;
   static constexpr int kTile = 16 * KB;
   static constexpr int STAGE = 2 * kTile * ROW;         // K tile, V tile
-  static constexpr int WARPS = F8 && D == 128 ? 12 : 8;
+  static constexpr int WARPS = NW;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int RING = kRings / WARPS;           // bytes of a warp's ring
   static constexpr int STAGES = RING / STAGE;
@@ -211,14 +216,14 @@ __device__ __forceinline__ Cut cut_of(int T, int ctas, int kTile, int most) {
   return c;
 }
 
-template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const KvDev c, const DecodeArgs a) {
-  using S = Shape<TYPE, D>;
+template <int TYPE, int D, int MT, int NW>
+__global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const DecodeArgs a) {
+  using S = Shape<TYPE, D, NW>;
   constexpr int kTile = S::kTile, KB = S::KB, kWarps = S::WARPS, kThreads = S::THREADS;
   constexpr int kOwn = (kMaxB + kThreads - 1) / kThreads;  // sequences of a thread, in the prefix sum
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int Ls[kMaxB], tp[kMaxB + 1], wsum[kWarps];
-  __shared__ float2 jml[kWarps][MT];
+  __shared__ float2 jml[kWarps][MT], cml[MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   tr_let_next_start();
   tr_wait_for_previous();
@@ -270,16 +275,17 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   Cursor cur, ld;
   int c1;
   if (a.own) {
-    cur.b = blockIdx.x / c.Hkv;
-    cur.h = blockIdx.x % c.Hkv;
-    cur.kt = 0;
+    const int pair_id = blockIdx.x / a.own, part = blockIdx.x % a.own;
+    cur.b = pair_id / c.Hkv;
+    cur.h = pair_id % c.Hkv;
     cur.L = Ls[cur.b];
     cur.nt = tp[cur.b + 1] - tp[cur.b];
-    if (cur.nt == 0) return;
-    c0 = (long long)tp[cur.b] * c.Hkv + cur.h * cur.nt;
-    c1 = (int)c0 + cur.nt;
+    if (cur.nt == 0) return;  // the whole cluster
     cut.warps = kWarps;
-    cut.per = (cur.nt + kWarps - 1) / kWarps;
+    cut.per = (cur.nt + a.own * kWarps - 1) / (a.own * kWarps);
+    cur.kt = min(cur.nt, part * kWarps * cut.per);
+    c0 = (long long)tp[cur.b] * c.Hkv + cur.h * cur.nt + cur.kt;
+    c1 = (int)c0 + min(cur.nt - cur.kt, kWarps * cut.per);
   } else {
     if (c0 >= T) return;
     c1 = (int)min((long long)T, c0 + (long long)cut.warps * cut.per);
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
   const int row0 = blockIdx.y * MT;  // first query head of this row tile inside its group
 
   // joined: the CTA's whole range lies in its first pair
-  const bool joined = cut.warps > 1 && c1 - (int)c0 <= cur.nt - cur.kt;
+  const bool joined = a.own || (cut.warps > 1 && c1 - (int)c0 <= cur.nt - cur.kt);
   const Cursor pair = cur;
   if (t0 >= t1 && !joined) return;
   if (t0 < t1) {
@@ -429,32 +435,43 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
 
     copy_wait<S::STAGES - 2>();
     __syncwarp();
-    issue((i - t0 + S::STAGES - 1) % S::STAGES);  // the stage read in the previous turn
     const uint32_t sk = ring + stage * S::STAGE, sv = sk + kTile * S::ROW;
 
-    // S = Q K^T: column n of block j is row j * 8 + n of the tile
-    float s[2 * KB][4] = {};
+    // S = Q K^T: column n of block j is row j * 8 + n of the tile.  With two blocks only the
+    // contraction runs in two halves, so that four chains of instructions are under way
+    constexpr int kHalves = KB == 1 ? 2 : 1, kPieces = S::CPR / 4;
+    float s2[kHalves][2 * KB][4] = {};
 #pragma unroll
-    for (int e = 0; e < S::CPR / 4; ++e)
+    for (int e = 0; e < kPieces / kHalves; ++e)
 #pragma unroll
-      for (int j = 0; j < 2 * KB; ++j) {
-        const int r = j * 8 + g;
-        const uint4 x = lds16(sk + r * S::ROW + swz_k<S::CPR>(r, e * 4 + t) * 16);
-        if constexpr (S::F8) {
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+      for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int at = e * 8 + f * 2;
-            mma(s[j], q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u,
-                widen_lo(y[f]), widen_hi(y[f]), false);
+        for (int j = 0; j < 2 * KB; ++j) {
+          const int r = j * 8 + g, pc = hf * (kPieces / kHalves) + e;
+          const uint4 x = lds16(sk + r * S::ROW + swz_k<S::CPR>(r, pc * 4 + t) * 16);
+          auto &acc = s2[hf][j];
+          if constexpr (S::F8) {
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int at = pc * 8 + f * 2;
+              mma(acc, q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u,
+                  widen_lo(y[f]), widen_hi(y[f]), false);
+            }
+          } else {
+            const int at = pc * 4;
+            mma(acc, q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u, x.x, x.y, S::BF);
+            mma(acc, q[0][at + 2], R > 1 ? q[R - 1][at + 2] : 0u, q[0][at + 3], R > 1 ? q[R - 1][at + 3] : 0u, x.z, x.w,
+                S::BF);
           }
-        } else {
-          const int at = e * 4;
-          mma(s[j], q[0][at], R > 1 ? q[R - 1][at] : 0u, q[0][at + 1], R > 1 ? q[R - 1][at + 1] : 0u, x.x, x.y, S::BF);
-          mma(s[j], q[0][at + 2], R > 1 ? q[R - 1][at + 2] : 0u, q[0][at + 3], R > 1 ? q[R - 1][at + 3] : 0u, x.z, x.w,
-              S::BF);
         }
-      }
+    // the stage read in the previous turn; its addresses are worked out while the products are under way
+    issue((i - t0 + S::STAGES - 1) % S::STAGES);
+    float s[2 * KB][4];
+#pragma unroll
+    for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = kHalves == 2 ? s2[0][j][e] + s2[kHalves - 1][j][e] : s2[0][j][e];
 
     // softmax weights, relative to a maximum that follows lazily; rows behind the last get none
     const int rows = cur.L - cur.kt * kTile;
@@ -546,12 +563,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int v = 0; v < S::VS; ++v) {
-        constexpr int NW = S::F8 ? S::VW / 4 : S::VW / 2;  // words of a piece
-        uint32_t x[4][NW];
+        constexpr int kWords = S::F8 ? S::VW / 4 : S::VW / 2;  // of a piece
+        uint32_t x[4][kWords];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int r = kb * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
-          if constexpr (NW == 4) {
+          if constexpr (kWords == 4) {
             const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR>(r, g + 8 * v) * 16);
             x[k][0] = y.x;
             x[k][1] = y.y;
@@ -564,7 +581,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
           }
         }
 #pragma unroll
-        for (int e = 0; e < NW; ++e) {
+        for (int e = 0; e < kWords; ++e) {
           if constexpr (S::F8) {
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
@@ -649,11 +666,17 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
         }
   }
   __syncthreads();
+  // one CTA has the whole pair, or its part goes to the cluster (through the first ring,
+  // behind its warp's sums), or to the workspace
   const bool whole = pair.kt == 0 && c1 - (int)c0 == pair.nt;
+  const bool shared = a.own > 1;
+  float *const part = rings + MT * D;
   const long long slot = ((long long)blockIdx.y * gridDim.x * kWarps + blockIdx.x * cut.warps) * 2;
   const float vs = S::F8 ? c.v_scale[pair.h] : 1.f;
   const int used = (c1 - (int)c0 + cut.per - 1) / cut.per;  // warps with tiles
-  for (int i = threadIdx.x; i < min(MT, a.G - row0) * (D / 4); i += kThreads) {
+  const int rows_here = min(MT, a.G - row0);
+  const long long hq0 = (long long)pair.b * a.Hq + (long long)pair.h * a.G + row0;
+  for (int i = threadIdx.x; i < rows_here * (D / 4); i += kThreads) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
     float M = -INFINITY, sum = 0.f;
     for (int k = 0; k < used; ++k) M = fmaxf(M, jml[k][row].x);
@@ -667,20 +690,57 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::THREADS, 1) split_kernel(const
       y.z += x.z * f;
       y.w += x.w * f;
     }
-    const long long hq = (long long)pair.b * a.Hq + (long long)pair.h * a.G + row0 + row;
-    const float f = whole ? vs / sum : 1.f;
-    float *dst = whole ? a.O + hq * D : a.part_o + (slot * MT + row) * D;
+    const float f = whole && !shared ? vs / sum : 1.f;
+    float *dst = shared ? part + row * D : whole ? a.O + (hq0 + row) * D : a.part_o + (slot * MT + row) * D;
     *reinterpret_cast<float4 *>(dst + col) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
     if (col == 0) {
-      if (whole) {
+      if (shared) {
+        cml[row] = make_float2(M, sum);
+      } else if (whole) {
         const float x = M + log2f(sum);
-        if (a.lse) a.lse[hq] = x * kLn2;
-        a.lse2[hq] = x;
+        if (a.lse) a.lse[hq0 + row] = x * kLn2;
+        a.lse2[hq0 + row] = x;
       } else {
         a.part_ml[slot * MT + row] = make_float2(M, sum);
       }
     }
   }
+  if (!shared) return;
+  // the cluster's CTAs join the parts, each some of the columns
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int i = cluster.block_rank() * kThreads + threadIdx.x; i < rows_here * (D / 4); i += a.own * kThreads) {
+    const int row = i / (D / 4), col = i % (D / 4) * 4;
+    float2 ml[kMaxOwn];
+    float4 x[kMaxOwn];
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxOwn; ++k) {
+      if (k >= a.own) break;
+      ml[k] = *cluster.map_shared_rank(&cml[row], k);
+      x[k] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part + row * D + col, k));
+      M = fmaxf(M, ml[k].x);
+    }
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMaxOwn; ++k) {
+      if (k >= a.own) break;
+      const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+      sum += ml[k].y * f;
+      y.x += x[k].x * f;
+      y.y += x[k].y * f;
+      y.z += x[k].z * f;
+      y.w += x[k].w * f;
+    }
+    const float f = vs / sum;
+    *reinterpret_cast<float4 *>(a.O + (hq0 + row) * D + col) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    if (col == 0) {
+      const float z = M + log2f(sum);
+      if (a.lse) a.lse[hq0 + row] = z * kLn2;
+      a.lse2[hq0 + row] = z;
+    }
+  }
+  cluster.sync();  // no CTA leaves while its part may still be read
 }
 
 // The parts of pair (b, h), in order.  A CTA whose range lies in the pair
@@ -857,25 +917,41 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   }
 }
 
-// A pair's bytes up to which one CTA per pair is used (where all fit on the SMs).
+// A CTA's share of a pair's bytes up to which clusters own pairs.  Measured
+// with 32 pairs, 4 CTAs each (bf16, d = 128; a call in a graph): see the rule's comment.
 constexpr long long kOwnBytes = 256 * 1024;
+// Cache bytes from which 12 warps of two stages each beat 8 of three: large
+// reads are bound by HBM and gain from more warps, short ranges from more
+// tiles in flight at their start.
+constexpr long long kManyBytes = 256ll << 20;
 
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
 struct Plan {
-  int MT, row_tiles, grid;  // grid: CTAs per row tile
-  bool own;
+  int MT, warps, row_tiles, grid;  // grid: CTAs per row tile
+  int own;
   size_t ml_off, lse_off, plan_off, s_off, total;
 };
 
 Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   Plan p;
   const int G = Hq / c.Hkv;
+  const long long pairs = (long long)c.B * c.Hkv, bytes = (long long)c.cap * c.row_bytes * 2;  // of a pair
   p.MT = G <= 8 ? 8 : 16;
   p.row_tiles = (G + p.MT - 1) / p.MT;
-  const long long most = (long long)c.B * c.Hkv * ((c.cap + kMinRows - 1) / kMinRows);  // ranges worth a warp
+  p.warps = p.MT == 8 && pairs * bytes >= kManyBytes ? 12 : 8;
+  const long long most = pairs * ((c.cap + kMinRows - 1) / kMinRows);  // ranges worth a warp
   p.grid = (int)std::max<long long>(1, std::min<long long>(tr_sm_count() / p.row_tiles, most));
-  p.own = (long long)c.B * c.Hkv * p.row_tiles <= tr_sm_count() && (long long)c.cap * c.row_bytes * 2 <= kOwnBytes;
-  if (p.own) p.grid = c.B * c.Hkv;
+  // clusters as large as fit on the SMs and leave each warp a tile
+  p.own = 0;
+  if (pairs * p.row_tiles <= tr_sm_count()) {
+    int cs = 1;
+    while (cs < kMaxOwn && pairs * p.row_tiles * cs * 2 <= tr_sm_count() && c.cap > cs * 128) cs *= 2;
+    if (bytes <= kOwnBytes * cs) p.own = cs;
+  }
+  if (p.own) {
+    p.warps = 8;
+    p.grid = (int)pairs * p.own;
+  }
   const size_t rows = (size_t)p.row_tiles * p.grid * kMaxWarps * 2 * p.MT;
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
@@ -885,25 +961,26 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   return p;
 }
 
-template <int TYPE, int D, int MT>
-int launch_split(dim3 grid, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
+template <int TYPE, int D, int MT, int NW>
+int launch_split(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
   static std::atomic<bool> set[64];  // per device
   int dev = 0;
   TR_TRY_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
+    TR_TRY_CUDA(cudaFuncSetAttribute(split_kernel<TYPE, D, MT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings));
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  return tr_launch_next(split_kernel<TYPE, D, MT>, {grid, Shape<TYPE, D>::THREADS, kRings}, s, c, a);
+  return tr_launch_next(split_kernel<TYPE, D, MT, NW>, {dim3(p.grid, p.row_tiles), NW * 32, kRings, p.own > 1 ? p.own : 1},
+                        s, c, a);
 }
 
 template <int TYPE, int D>
 int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
-  const dim3 grid(p.grid, p.row_tiles);
-  int rc = p.MT == 8 ? launch_split<TYPE, D, 8>(grid, s, c, a) : launch_split<TYPE, D, 16>(grid, s, c, a);
+  int rc = p.MT == 16     ? launch_split<TYPE, D, 16, 8>(p, s, c, a)
+           : p.warps == 8 ? launch_split<TYPE, D, 8, 8>(p, s, c, a)
+                          : launch_split<TYPE, D, 8, 12>(p, s, c, a);
   if (rc != TR_OK) return rc;
-  if (!p.own)
-    rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * Shape<TYPE, D>::WARPS, p.MT);
+  if (!p.own) rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * p.warps, p.MT);
   if (rc != TR_OK || !a.accumulate) return rc;
   return a.G > 8 ? tr_launch_next(score_kernel<true>, {dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads}, s, c, a)
                  : tr_launch_next(score_kernel<false>, {dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads}, s, c, a);
