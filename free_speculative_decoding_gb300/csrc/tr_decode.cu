@@ -23,9 +23,9 @@
 // its own: a lane's 16-byte piece of a row of K is used as the B fragments of
 // two (8-bit: four) instructions, and Q is loaded in the same order, so that K needs no
 // transposing load.  The accumulators of S are laid out as the A fragments of
-// P V.  V's B fragments pair two rows: a lane reads the same 16-byte piece of
-// four rows and interleaves them with byte permutes; the columns of O come
-// out in runs of 8 or 16 per lane.
+// P V.  V's B fragments pair two rows: transposing loads bring 16-bit ones; of 8-bit
+// rows a lane reads the same 16-byte piece of four rows, interleaves them with byte
+// permutes and widens the pairs.
 //
 // Precision.  The output is fp32, so P must not be rounded to the cache's type:
 // p is split exactly into three bf16 parts (8 + 8 + 8 bits), or into two fp16 parts
@@ -92,8 +92,6 @@ struct Shape {
   static constexpr int THREADS = WARPS * 32;
   static constexpr int RING = kRings / WARPS;           // bytes of a warp's ring
   static constexpr int STAGES = RING / STAGE;
-  static constexpr int VW = F8 && D == 128 ? 16 : 8;    // columns of a lane's piece of V
-  static constexpr int VS = D / (8 * VW);               // pieces of V per lane and row
   static constexpr int NT = D / 8;                      // column blocks of O
   static constexpr int QR = D / 8;                      // registers of one query row's fragments
 };
@@ -134,6 +132,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
+}
+// Four 8 x 8 blocks of 16-bit values, transposed; lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void ldsm_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
 }
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
@@ -199,10 +203,14 @@ template <int CPR>
 __device__ __forceinline__ int swz_k(int r, int ch) {
   return CPR >= 8 ? ch ^ ((r & 1) << 2) : ch;
 }
-template <int CPR>
+template <int CPR, bool F8>
 __device__ __forceinline__ int swz_v(int r, int ch) {
-  return CPR >= 8 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3);
+  return !F8 ? ch ^ (r & 7) : CPR >= 8 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3);
 }
+
+// 8-bit V: columns of a lane's piece of a row, and its pieces per row.
+__host__ __device__ constexpr int piece_cols(int D) { return D == 128 ? 16 : 8; }
+__host__ __device__ constexpr int pieces(int D) { return D / (8 * piece_cols(D)); }
 
 // The warps that a range of pairs is cut for, from the tiles' number alone.
 struct Cut {
@@ -329,21 +337,23 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
         if (whole_tile) {
           const long long at = (long long)__shfl_sync(~0u, page, 0) * c.block_stride + head + kv_row(c, p0 + r0);
           const char *k = c.K + at, *v = c.V + at;
+          auto copy = [&](long long next) {
 #pragma unroll
-          for (int i = 0; i < kCopies; ++i) {
-            const int r = r0 + i * kStep;
-            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, k);
-            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, v);
-            k += kStep * c.row_stride;
-            v += kStep * c.row_stride;
-          }
+            for (int i = 0; i < kCopies; ++i) {
+              const int r = r0 + i * kStep;
+              copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, k + i * next);
+              copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, v + i * next);
+            }
+          };
+          if (c.row_stride == S::ROW) copy(kStep * S::ROW);  // the offsets are part of the instructions
+          else copy(kStep * c.row_stride);
         } else {
 #pragma unroll
           for (int i = 0; i < kCopies; ++i) {
             const int r = r0 + i * kStep;
             const long long at = (long long)__shfl_sync(~0u, page, r) * c.block_stride + head + kv_row(c, p0 + r);
             copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at);
-            copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at);
+            copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at);
           }
         }
       } else {  // a pair's last tile, or a page that is not there: row by row
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
           const bool valid = r < left && (unsigned)pg < (unsigned)blocks;
           const long long at = valid ? (long long)pg * c.block_stride + head + kv_row(c, p0 + r) : 0;
           copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
-          copy16(dv + r * S::ROW + swz_v<S::CPR>(r, ch) * 16, c.V + at, valid);
+          copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at, valid);
         }
       }
       step<kTile>(ld, Ls, c.B, c.Hkv);
@@ -377,6 +387,27 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
     l[r] = 0.f;
     logits[r] = nullptr;
   }
+
+  // a lane's columns of query row g + 8 r, times f
+  auto store_row = [&](float *dst, int r, float f) {
+    if constexpr (!S::F8) {
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n)
+        *reinterpret_cast<float2 *>(dst + n * 8 + 2 * t) = make_float2(o[n][2 * r] * f, o[n][2 * r + 1] * f);
+    } else {
+#pragma unroll
+      for (int v = 0; v < pieces(D); ++v)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < piece_cols(D); e += 4) {
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = o[v * piece_cols(D) + e + k][2 * r + n] * f;
+            *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * piece_cols(D) + e) = make_float4(y[0], y[1], y[2], y[3]);
+          }
+    }
+  };
 
   for (int i = t0; i < t1; ++i) {
     const int stage = (i - t0) % S::STAGES;
@@ -543,7 +574,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
             pt[kb][1][r][j] = pack_half2(x - __low2float(h), y - __high2float(h));
           }
         }
-    // O += P V of 16 rows: column block n = VW * v + e holds columns (lane / 4 + 8 v) * VW + e
+    // O += P V of 16 rows and one column block
     auto pv = [&](float(&to)[2 * R], int kb, uint32_t b0, uint32_t b1) {
       const uint32_t(&p)[kParts][R][2] = pt[kb];
       float acc[4] = {};
@@ -560,43 +591,51 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
       }
     };
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int kb = 0; kb < KB; ++kb) {
+      if constexpr (!S::F8) {
+        // column block n holds columns 8 n ..: transposing loads bring two blocks' fragments
+        const int r = kb * 16 + (lane & 15);
 #pragma unroll
-      for (int v = 0; v < S::VS; ++v) {
-        constexpr int kWords = S::F8 ? S::VW / 4 : S::VW / 2;  // of a piece
-        uint32_t x[4][kWords];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = kb * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
-          if constexpr (kWords == 4) {
-            const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR>(r, g + 8 * v) * 16);
-            x[k][0] = y.x;
-            x[k][1] = y.y;
-            x[k][2] = y.z;
-            x[k][3] = y.w;
-          } else {
-            const uint2 y = lds8(sv + r * S::ROW + swz_v<S::CPR>(r, g >> 1) * 16 + (g & 1) * 8);
-            x[k][0] = y.x;
-            x[k][1] = y.y;
-          }
+        for (int n = 0; n < S::NT; n += 2) {
+          uint32_t x[4];
+          ldsm_trans(x, sv + r * S::ROW + swz_v<S::CPR, false>(r, n + (lane >> 4)) * 16);
+          pv(o[n], kb, x[0], x[1]);
+          pv(o[n + 1], kb, x[2], x[3]);
         }
+      } else {
+        // a lane reads the same piece of four rows and interleaves them: block n = VW * v + e
+        // holds columns (lane / 4 + 8 v) * VW + e
 #pragma unroll
-        for (int e = 0; e < kWords; ++e) {
-          if constexpr (S::F8) {
+        for (int v = 0; v < pieces(D); ++v) {
+          constexpr int kWords = piece_cols(D) / 4;  // of a piece
+          uint32_t x[4][kWords];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = kb * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+            if constexpr (kWords == 4) {
+              const uint4 y = lds16(sv + r * S::ROW + swz_v<S::CPR, true>(r, g + 8 * v) * 16);
+              x[k][0] = y.x;
+              x[k][1] = y.y;
+              x[k][2] = y.z;
+              x[k][3] = y.w;
+            } else {
+              const uint2 y = lds8(sv + r * S::ROW + swz_v<S::CPR, true>(r, g >> 1) * 16 + (g & 1) * 8);
+              x[k][0] = y.x;
+              x[k][1] = y.y;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < kWords; ++e)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
               const uint32_t sel = f ? 0x7362 : 0x5140;
               const uint32_t lo = __byte_perm(x[0][e], x[1][e], sel), hi = __byte_perm(x[2][e], x[3][e], sel);
-              pv(o[v * S::VW + e * 4 + f * 2], kb, widen_lo(lo), widen_lo(hi));
-              pv(o[v * S::VW + e * 4 + f * 2 + 1], kb, widen_hi(lo), widen_hi(hi));
+              pv(o[v * piece_cols(D) + e * 4 + f * 2], kb, widen_lo(lo), widen_lo(hi));
+              pv(o[v * piece_cols(D) + e * 4 + f * 2 + 1], kb, widen_hi(lo), widen_hi(hi));
             }
-          } else {
-            pv(o[v * S::VW + e * 2], kb, __byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x5410));
-            pv(o[v * S::VW + e * 2 + 1], kb, __byte_perm(x[0][e], x[1][e], 0x7632),
-               __byte_perm(x[2][e], x[3][e], 0x7632));
-          }
         }
       }
+    }
 
     if (!joined && (cur.kt == cur.nt - 1 || i == t1 - 1)) {
       // the range leaves this pair: the result, or a partial
@@ -621,19 +660,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
             a.part_ml[slot * MT + row] = make_float2(m[r], l[r]);
           }
         }
-#pragma unroll
-        for (int v = 0; v < S::VS; ++v)
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < S::VW; e += 4) {
-              float y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                y[k] = o[v * S::VW + e + k][2 * r + n] * f;
-              }
-              *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
-            }
+        store_row(dst, r, f);
       }
     }
     step<kTile>(cur, Ls, c.B, c.Hkv);
@@ -651,19 +678,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
     if (t == 0) jml[warp][g + r * 8] = make_float2(m[r], l[r]);
     if (t0 >= t1 || row0 + g + r * 8 >= a.G) continue;
     float *dst = rings + warp * (S::RING / 4) + (g + r * 8) * D;
-#pragma unroll
-    for (int v = 0; v < S::VS; ++v)
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < S::VW; e += 4) {
-          float y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[k] = o[v * S::VW + e + k][2 * r + n];
-          }
-          *reinterpret_cast<float4 *>(dst + (2 * t + n + 8 * v) * S::VW + e) = make_float4(y[0], y[1], y[2], y[3]);
-        }
+    store_row(dst, r, 1.f);
   }
   __syncthreads();
   // one CTA has the whole pair, or its part goes to the cluster (through the first ring,
@@ -917,13 +932,18 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   }
 }
 
-// A CTA's share of a pair's bytes up to which clusters own pairs.  Measured
-// with 32 pairs, 4 CTAs each (bf16, d = 128; a call in a graph): see the rule's comment.
+// A CTA's share of a pair's bytes up to which clusters own pairs.  Measured (bf16,
+// d = 128, calls in a graph; clusters against ranges over all pairs): 32 pairs,
+// 512 rows 5.7 / 7.6 us, 2048 rows 9.2 / 9.9 us; 8 pairs of 4 heads, 4096 rows
+// 9.5 / 9.9 us; one pair of 32 heads, 2048 rows 9.4 / 11.9 us, 4096 rows
+// 12.1 / 20.5 us.  With larger shares the SMs that no cluster uses are missed.
 constexpr long long kOwnBytes = 256 * 1024;
-// Cache bytes from which 12 warps of two stages each beat 8 of three: large
-// reads are bound by HBM and gain from more warps, short ranges from more
-// tiles in flight at their start.
-constexpr long long kManyBytes = 256ll << 20;
+// Cache bytes from which 12 warps of two stages each are launched instead of 8
+// of three.  Large reads gain from more warps (16 x 4k rows of 32 heads: 112
+// against 116 us; 8-bit, 64 sequences: 115 against 121 us), short ranges from more
+// tiles in flight at their start (24 sequences of up to 2k rows, d = 64: 14.2
+// against 12.8 us; 8 x 4k rows of 8 heads, 134 MB: 36.9 against 35.5 us).
+constexpr long long kManyBytes = 512ll << 20;
 
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
 struct Plan {
