@@ -209,6 +209,28 @@ def test_decode_edge_lengths(tr, type, d, layout, Hkv, G):
     c.check(Q, d ** -0.5, O, lse, before)
 
 
+@pytest.mark.parametrize("type", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hkv,G", [(3, 4), (1, 8), (2, 9), (1, 40)])
+@pytest.mark.parametrize("reach", [1 << 14, 1 << 18])
+def test_decode_edge_lengths_in_large_tables(tr, type, d, Hkv, G, reach):
+    """The same lengths in caches that could hold far more: what is launched goes by the table's reach (ranges over
+    all pairs, of 8 and of 12 warps, instead of one cluster for each)."""
+    c = Made(tr, np.random.default_rng(d + G + 1), type, 16, EDGES, Hkv, d, scores=False)
+    wide = torch.full((len(EDGES), reach // 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.pt.shape[1]] = c.pt
+    c.scores = torch.rand(len(EDGES), Hkv, reach, device="cuda")
+    c.cache = tr.KVCache(c.K, c.V, c.L, page_table=wide, scores=c.scores, k_scale=c.ks, v_scale=c.vs)
+    Q = c.queries(Hkv * G, 2.0)
+    before = c.scores.clone()
+    O, lse = c.attend(Q, d ** -0.5, accumulate=True)
+    c.check(Q, d ** -0.5, O, lse, before)
+    first = c.scores.clone()
+    c.scores.copy_(before)
+    O2, lse2 = c.attend(Q, d ** -0.5, accumulate=True)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(c.scores, first)
+
+
 @pytest.mark.parametrize("layout", ["dense_nhd", "wide", 1, 2, 8, 32, 256, 1024, "nhd4", "nhd16", "nhd64"])
 @pytest.mark.parametrize("type", ["bf16", "e4m3"])
 def test_decode_layouts(tr, layout, type):
