@@ -3,29 +3,33 @@
 // For query head hq with KV head g, O = sum_p w_p V[g, p] with w the softmax of
 // scale * Q[hq] . K[g, p] over the cached rows p < L[b].  Every cached row is
 // needed once and used for the few query heads of its group, so the cache's
-// bytes bound the work (1 flop per byte for one head per group, 2 G in general).
+// bytes bound the work: 4 G d flops for 4 d bytes of a 16-bit row, G flops a byte.
+// The 5th-generation tensor cores' 128-row tile would be empty but for G rows, so
+// the products run on the warp-level matrix instructions, which keep up with
+// HBM here (tensor pipe 28% active while DRAM delivers 6.5 TB/s).
 //
 // Split.  A pair is (sequence, KV head) with ceil(L / kTile) tiles.  All pairs'
 // tiles are laid end to end and cut into equal ranges, one per WARP of a
 // one-CTA-per-SM grid.  A warp streams its own tiles through its own ring in
 // shared memory (cp.async) and meets no barrier on the way, whatever the mix of
-// lengths.  Where all pairs of a small cache fit on the SMs at once each is the
-// work of one CTA, or of a cluster whose CTAs join their parts through distributed
-// shared memory, and nothing is left for a second kernel.  With little work only as many warps of each CTA take part as leave
+// lengths.  With little work only as many warps of each CTA take part as leave
 // each about kMinRows rows, so that it spreads over every SM.  A pair that lies
 // inside one range is finished by its warp.  When a CTA's whole range lies in
-// one pair its warps' sums are joined in shared memory first.  What
-// remains are (m, l, O) partials, which join_kernel joins in a fixed order.
+// one pair its warps' sums are joined in shared memory first.  What remains are
+// (m, l, O) partials, which join_kernel joins in a fixed order.  Where all pairs
+// of a small cache fit on the SMs at once each is the work of a cluster of one
+// to eight CTAs that join their parts through distributed shared memory, and
+// nothing is left for a second kernel.
 //
-// Tile.  S = Q K^T with m16n8k16 matrix instructions: the group's query heads
-// are the 16 rows (8 of them empty when the group has at most 8 heads), cached
-// rows are the columns.  The contraction runs over d in an order of
-// its own: a lane's 16-byte piece of a row of K is used as the B fragments of
-// two (8-bit: four) instructions, and Q is loaded in the same order, so that K needs no
+// Tile.  S = Q K^T with m16n8k16 instructions: the group's query heads are the 16
+// rows (8 of them empty when the group has at most 8 heads), cached rows are
+// the columns.  The contraction runs over d in an order of its own: a lane's
+// 16-byte piece of a row of K is used as the B fragments of two (8-bit: four)
+// instructions, and Q is loaded in the same order, so that K needs no
 // transposing load.  The accumulators of S are laid out as the A fragments of
-// P V.  V's B fragments pair two rows: transposing loads bring 16-bit ones; of 8-bit
-// rows a lane reads the same 16-byte piece of four rows, interleaves them with byte
-// permutes and widens the pairs.
+// P V.  V's B fragments pair two rows: transposing loads bring 16-bit ones; of
+// 8-bit rows a lane reads the same 16-byte piece of four rows, interleaves them
+// with byte permutes and widens the pairs.
 //
 // Precision.  The output is fp32, so P must not be rounded to the cache's type:
 // p is split exactly into three bf16 parts (8 + 8 + 8 bits), or into two fp16 parts
@@ -35,9 +39,20 @@
 // unit's own adds cut off what does not fit, always towards zero, so its sums
 // last 16 rows only and are added to O with rounded adds (kept in the unit over a
 // whole range, the loss grew with the range: 7e-6 of the result's norm at 3400
-// rows a warp against 1e-6 for fp32 products and sums).
+// rows a warp against 1e-6 for fp32 products and sums; now 5e-7).
 // An 8-bit row is widened to fp16 (exact); Q is scaled by a power of two per
 // head so that narrowing bf16 to fp16 is exact for all but negligible elements.
+//
+// Measured (one GB300, whole calls in a graph, fractions of the 6675 GB/s of a
+// copy): 4 x 32768 rows of 32 heads, bf16, 308 us = 104%; 16 x 1k-4k rows of 32
+// heads in pages of 64, 112 us = 96%; 64 sequences of 1-8191 rows, 8 heads of
+// groups of 4, 8-bit, weights gathered, 115 us = 75% (split_kernel alone 97 us;
+// bound by instructions: each 8-bit pair is widened); 8 x 4096 rows of 8 heads,
+// weights gathered, 36 us = 57%, 24 x 17-2011 rows, d = 64, 12.5 us = 37%, and
+// one sequence of 512 rows of 32 heads, 6.0 us, are bound by latency: 2 us of
+// launch, 2 us until a first tile is through, 1.1 us for each further tile of a
+// warp (some 400 instructions in chains, two or three warps a scheduler), 2-3 us for
+// each of join_kernel and score_kernel.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -55,7 +70,6 @@ using sm100::ex2;
 using sm100::smem_u32;
 
 constexpr int kMaxB = 1024;
-constexpr int kMaxWarps = 12;            // of any split kernel's CTA
 constexpr int kMaxOwn = 8;               // CTAs of a cluster that share a pair
 constexpr int kRings = 192 * 1024;       // bytes of a CTA's rings
 constexpr int kMinRows = 32;            // cached rows of a warp's range, about, at least
@@ -972,7 +986,7 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
     p.warps = 8;
     p.grid = (int)pairs * p.own;
   }
-  const size_t rows = (size_t)p.row_tiles * p.grid * kMaxWarps * 2 * p.MT;
+  const size_t rows = p.own ? 0 : (size_t)p.row_tiles * p.grid * p.warps * 2 * p.MT;  // clusters leave no partials
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
   p.plan_off = p.lse_off + tr_align_up((size_t)c.B * Hq * 4, 256);

@@ -1,5 +1,14 @@
 // Appending rows to a KV cache and evicting rows from it by accumulated
 // attention weight.
+//
+// Both move bytes and are bound by HBM where there are enough of them.  Measured
+// (one GB300, in a graph, fractions of the 6675 GB/s of a copy over the bytes
+// that the call cannot do without): 8 prompts of up to 4096 rows into an 8-bit
+// cache 28 us = 66% (its floor 18.6 us; the kernel is bound by the instructions of the
+// division: 22.6 M of them with one IEEE division per value took 49 us); one new
+// row for each of 16 sequences 3.3 us, a launch; 16 x 32 heads of 4096 rows cut to
+// 1024, 97 us = 84% (choosing 16 us, moving 81 us = 98%); one sequence of 131072
+// rows x 8 heads cut to 32768, 76 us = 54% (choosing 20 us; moving 11 + 13 + 33 us).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -232,8 +241,8 @@ __device__ __forceinline__ unsigned block_sum(unsigned v, unsigned *wsum) {
 // registers (a slice that is longer is read again in every pass).  The key is
 // found by a radix select, BITS a pass: the CTAs' histograms are added through
 // distributed shared memory and every CTA walks the sum alike.  11 bits (three
-// passes) suit one CTA, 8 bits (four) a cluster, whose exchange is an eighth.  A
-// row's place in keep is the number of rows above the edge before it plus the
+// passes) suit one CTA, 8 bits (four) a cluster, whose exchange is an eighth (131072
+// rows, clusters of 8: 38 us with 11 bits, 20 us with 8).  A row's place in keep is the number of rows above the edge before it plus the
 // number of edge rows taken before it.  split[pair], where asked for, gets the
 // number of kept rows at positions below the budget.
 template <int KPT, int BITS>
@@ -663,9 +672,15 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   const long long pairs = (long long)c.B * c.Hkv;
   int cs = 1;
   while (cs < 8 && c.cap / (2 * cs) >= 4096 && pairs * 2 * cs <= 4 * tr_sm_count()) cs *= 2;
-  // whole rows where the pairs alone give every SM two CTAs; else narrow columns,
-  // many CTAs, for the rows that move within the budget and the others apart
-  const bool few = pairs * 2 < 2LL * tr_sm_count();
+  // Whole rows, one CTA for K and one for V of each pair, or, with few pairs of
+  // many rows, narrow columns for the rows that move within the budget and the others
+  // apart.  Whole rows take 9 ns a row of 256 bytes and CTA until HBM is full, the
+  // other way 1.3 of HBM's time and 15 us.  Measured (bf16, d = 128; whole / apart):
+  // 8 pairs, 2048 rows kept 27 / 25 us, 16384 155 / 46 us, 32768 300 / 85 us;
+  // 32 pairs, 2048 rows 32 / 43 us; 128 pairs, 2048 rows 59 / 70 us; 1 pair, 1024
+  // rows 15 / 18 us.
+  const int row = c.row_bytes;
+  const bool few = pairs < 45 && (double)budget * row * (45 - pairs) > 19e6;
   int32_t *split = few ? (int32_t *)((char *)old_len + tr_align_up((size_t)c.B * 4, 256)) : nullptr;
   // with a budget that the cache cannot exceed this still reports bad lengths
   const dim3 select(c.Hkv * cs, c.B);
@@ -677,7 +692,6 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   rc = cs == 1 ? (small ? pick(evict_select_kernel<8, 11>) : pick(evict_select_kernel<kSelMost, 11>))
                : (small ? pick(evict_select_kernel<8, 8>) : pick(evict_select_kernel<kSelMost, 8>));
   if (rc != TR_OK || budget >= c.cap) return rc;
-  const int row = c.row_bytes;
   int part = row;
   while (few && part > 32 && pairs * 2 * (row / part) < 2LL * tr_sm_count()) part /= 2;
   const dim3 move(2 * (row / part) + 1, c.Hkv, c.B);

@@ -656,6 +656,17 @@ def test_evict_many_pairs(tr, type, d, layout, budget, recent):
     check_evict(c, budget, recent)
 
 
+@pytest.mark.parametrize("type,d,n,budget", [("bf16", 128, 6000, 4700), ("bf16", 128, 20000, 4700),
+                                             ("f16", 64, 14000, 4700), ("e4m3", 128, 6000, 4700),
+                                             ("e4m3", 64, 19000, 8000)])
+@pytest.mark.parametrize("layout", ["wide", 1, 16, "nhd64"])
+@pytest.mark.parametrize("recent", [0, 700, 4700])
+def test_evict_few_pairs_of_many_rows(tr, type, d, n, budget, layout, recent):
+    """Few pairs that keep many rows: those from behind the budget move apart, in two stretches, after the others."""
+    c = Made(tr, np.random.default_rng(38), type, layout, [n, budget + 1], 2, d)
+    check_evict(c, budget, recent)
+
+
 @pytest.mark.parametrize("budget,recent", [(2000, 10), (6000, 5000), (7900, 100), (4096, 0), (8191, 0)])
 def test_evict_around_the_halfway_mark(tr, budget, recent):
     """Few pairs: rows from behind the budget move apart from the others, whatever part of the kept ones they are."""
