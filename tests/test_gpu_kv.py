@@ -814,6 +814,60 @@ def test_first_calls_of_a_process_inside_a_capture(tr):
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
 
 
+def test_calls_behind_a_join_of_two_streams(tr):
+    """Inputs made on a second stream and joined by an event right before each call, eagerly and in a capture (where
+    each call's first kernel then has two predecessors), two graphs of the same operators among them."""
+    c = Made(tr, np.random.default_rng(42), "bf16", 16, [700, 30, 1500], 2, 128, extra=400)
+    a, o = tr.workspace(tr.tr_kv_append_workspace_bytes(c.cache)), tr.workspace(
+        tr.tr_decode_attn_workspace_bytes(c.cache, 8, True))
+    e = tr.workspace(tr.tr_kv_evict_workspace_bytes(c.cache, 500))
+    src = [torch.randn(3, 70, 2, 128, generator=c.g).bfloat16().cuda(), c.queries(8, 2.0).cuda()]
+    n, Q = torch.zeros_like(src[0]), torch.zeros_like(src[1])
+    O = torch.zeros(3, 8, 128, device="cuda")
+    busy = torch.randn(4 << 20, device="cuda")
+    side = torch.cuda.Stream()
+
+    def both(f):
+        """f on the side stream while this one works; then joined."""
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            torch.sin(busy)
+            f()
+        torch.cos(busy)
+        now.wait_stream(side)
+
+    def step():
+        both(lambda: n.copy_(src[0] * 2))
+        tr.tr_kv_append(n, n, c.cache, a)
+        both(lambda: Q.copy_(src[1] * 0.5))
+        tr.tr_decode_attn(Q, c.cache, O, 0.09, o, accumulate=True)
+        both(lambda: torch.cos(busy))
+        tr.tr_kv_evict(c.cache, 500, 60, e)
+
+    state = [raw(c.K), raw(c.V), c.scores, c.L]
+    start = [x.clone() for x in state]
+    outs = []
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for way in (None, 0, 1, 0):
+        for x, y in zip(state, start):
+            x.copy_(y)
+        n.zero_(), Q.zero_(), O.zero_()
+        torch.cuda.synchronize()
+        if way is None:
+            step()
+        else:
+            if not outs[way + 1:]:
+                with torch.cuda.graph(graphs[way]):
+                    step()
+            graphs[way].replay()
+        torch.cuda.synchronize()
+        outs.append([O.clone()] + [x.clone() for x in state])
+    for got in outs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(outs[0], got))
+    assert c.L.tolist() == [500, 100, 500]
+
+
 @pytest.mark.parametrize("layout", ["dense", 16])
 def test_back_to_back_calls_see_each_other(tr, layout):
     """Append, attention and eviction queued without a pause between them (each may be set up while the one before it
