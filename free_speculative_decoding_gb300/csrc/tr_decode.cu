@@ -1025,9 +1025,9 @@ int launch(int d, const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArg
   return d == 64 ? launch<TYPE, 64>(p, s, c, a) : launch<TYPE, 128>(p, s, c, a);
 }
 
-// Launch grids hold B * Hq in 31 bits and the KV heads in 16.
+// Launch grids hold B * Hq in 31 bits, the KV heads and the row tiles in 16.
 bool fits(const KvDev &c, int Hq) {
-  return (long long)c.B * Hq < (1LL << 31) && c.Hkv <= 65535 && Hq / c.Hkv <= 65535 * 8;
+  return (long long)c.B * Hq < (1LL << 31) && Hq < (1 << 24) && c.Hkv <= 65535 && Hq / c.Hkv <= 65535 * 8;
 }
 
 }  // namespace
@@ -1043,7 +1043,7 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   KvDev c;
   int rc = kv_check(cache, &c);
   if (rc != TR_OK) return rc;
-  if (!Q || !O || Hq < 1 || Hq % c.Hkv || !(scale > 0.f) || !(scale < INFINITY)) return TR_E_INVAL;
+  if (!Q || !O || Hq < 1 || Hq % c.Hkv || !(scale > 0.f) || !(scale < 0x1p127f)) return TR_E_INVAL;
   if ((((uintptr_t)Q | (uintptr_t)O) & 15) || ((uintptr_t)lse & 3)) return TR_E_INVAL;
   if (accumulate && !c.scores) return TR_E_INVAL;
   if (!fits(c, Hq)) return TR_E_UNSUPPORTED;

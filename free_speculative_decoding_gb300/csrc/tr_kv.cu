@@ -241,10 +241,11 @@ __device__ __forceinline__ unsigned block_sum(unsigned v, unsigned *wsum) {
 // registers (a slice that is longer is read again in every pass).  The key is
 // found by a radix select, BITS a pass: the CTAs' histograms are added through
 // distributed shared memory and every CTA walks the sum alike.  11 bits (three
-// passes) suit one CTA, 8 bits (four) a cluster, whose exchange is an eighth (131072
-// rows, clusters of 8: 38 us with 11 bits, 20 us with 8).  A row's place in keep is the number of rows above the edge before it plus the
-// number of edge rows taken before it.  split[pair], where asked for, gets the
-// number of kept rows at positions below the budget.
+// passes) suit one CTA, 8 bits (four) a cluster, whose exchange is an eighth
+// (131072 rows, clusters of 8: 38 us with 11 bits, 20 us with 8).  A row's place
+// in keep is the number of rows above the edge before it plus the number of edge
+// rows taken before it.  split[pair], where asked for, gets the number of kept rows
+// at positions below the budget.
 template <int KPT, int BITS>
 __global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
     evict_select_kernel(const KvDev c, int budget, int recent, int32_t *keep, int32_t *old_len, int32_t *split,

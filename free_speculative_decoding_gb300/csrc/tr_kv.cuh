@@ -89,7 +89,7 @@ static inline int kv_check(const tr_kv_cache *c, KvDev *out) {
     span += st[at] * (n[at] - 1);
   }
   if (c->scores && (c->scores_ld < cap || ((uintptr_t)c->scores & 3))) return TR_E_INVAL;
-  if (c->B > 1024 || cap >= (1LL << 31) || (long long)c->B * c->Hkv * cap >= (1LL << 31)) return TR_E_UNSUPPORTED;
+  if (c->B > 1024 || cap > (1LL << 30) || (long long)c->B * c->Hkv * cap >= (1LL << 31)) return TR_E_UNSUPPORTED;
   v.K = (char *)c->K;
   v.V = (char *)c->V;
   v.B = c->B;

@@ -338,8 +338,8 @@ typedef enum { TR_KV_BF16 = 0, TR_KV_F16 = 1, TR_KV_E4M3 = 2 } tr_kvtype;
  * write (append: those that receive rows; evict: all of the sequence's) to
  * belong to one sequence.
  * K, V and all strides are 16-byte aligned, rows do not overlap, d is 64 or
- * 128, page_size a power of two, B <= 1024 and B * Hkv * (positions a sequence
- * can hold) < 2^31. */
+ * 128, page_size a power of two, B <= 1024, the positions a sequence can hold
+ * at most 2^30 and B * Hkv times as many below 2^31. */
 typedef struct tr_kv_cache {
   void *K, *V;
   tr_kvtype type;
@@ -370,7 +370,8 @@ typedef struct tr_kv_cache {
  * accumulate != 0: also scores[b, g, p] += sum over the Hq / Hkv query heads of
  * group g of w_p, for p < L[b]; the sums' order is fixed, so equal calls give
  * equal bits.
- * Hq a multiple of Hkv (any group size), scale positive and finite.  A length
+ * Hq a multiple of Hkv (any group of up to 524280 heads, Hq < 2^24), scale
+ * positive and below 2^127.  A length
  * outside the cache sets TR_DEV_BAD_LENGTH and counts as 0; an entry of the
  * page table outside [0, num_pages) sets TR_DEV_BAD_PAGE, is not followed, and
  * leaves that sequence's results undefined.

@@ -40,7 +40,9 @@ BAD_CACHES = [  # (fields, refused as)
     (dict(scores_ld=63), "INVAL"), (dict(scores=P + 2), "INVAL"), (dict(B=1025), "UNSUPPORTED"),
     (dict(PAGED, page_size=24), "UNSUPPORTED"), (dict(PAGED, page_size=0), "INVAL"),
     (dict(PAGED, max_pages=0), "INVAL"), (dict(PAGED, num_pages=0), "INVAL"),
-    (dict(PAGED, max_pages=1 << 28, scores=None), "UNSUPPORTED"), (dict(PAGED, scores_ld=63), "INVAL"),
+    (dict(PAGED, max_pages=1 << 28, scores=None), "UNSUPPORTED"),
+    (dict(PAGED, B=1, Hkv=1, max_pages=(1 << 26) + 1, scores=None), "UNSUPPORTED"),   # 2^30 + 16 positions
+    (dict(B=1, Hkv=1, cap=(1 << 30) + 1, scores=None), "UNSUPPORTED"), (dict(PAGED, scores_ld=63), "INVAL"),
 ]
 
 
@@ -80,10 +82,11 @@ def test_decode_arguments(tr):
         def call(Q=P, Hq=8, scale=0.1, O=P, lse=P, acc=0, ws=P, nb=BIG):
             return lib.tr_decode_attn(Q, r, Hq, scale, O, lse, acc, ws, nb, None)
         for kw in (dict(Q=None), dict(O=None), dict(Q=P + 8), dict(O=P + 4), dict(lse=P + 2), dict(Hq=0),
-                   dict(Hq=6), dict(Hq=-4), dict(scale=0.0), dict(scale=-1.0), dict(scale=inf), dict(scale=nan),
+                   dict(Hq=6), dict(Hq=-4), dict(scale=0.0), dict(scale=-1.0), dict(scale=inf), dict(scale=nan), dict(scale=3e38),
                    dict(ws=None), dict(ws=P + 8), dict(nb=0), dict(acc=1, nb=need - 1)):
             assert call(**kw) == tr.TR_E_INVAL, kw
         assert lib.tr_decode_attn_workspace_bytes(r, 6, 0) == 0
+        assert call(Hq=1 << 24) == tr.TR_E_UNSUPPORTED and lib.tr_decode_attn_workspace_bytes(r, 1 << 24, 0) == 0
     c = cache(tr, scores=None)
     assert lib.tr_decode_attn(P, ctypes.byref(c), 8, 0.1, P, P, 1, P, BIG, None) == tr.TR_E_INVAL
 
