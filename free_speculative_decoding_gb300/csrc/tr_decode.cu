@@ -142,6 +142,14 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 16 bytes from global memory where valid, else zero; not moved behind the copies that follow.
+__device__ __forceinline__ uint4 ldg16(const uint4 *p, bool valid) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (valid)
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -250,65 +258,79 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
   tr_let_next_start();
   tr_wait_for_previous();
 
-  // lengths and, for one head, the tiles before each sequence
-  int mine[kOwn], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int b = threadIdx.x * kOwn + i;
-    int L = b < c.B ? c.L[b] : 0;
-    if (L < 0 || L > c.cap) {
-      if (blockIdx.x == 0 && blockIdx.y == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
-      L = 0;
-    }
-    if (b < kMaxB) Ls[b] = L;
-    mine[i] = sum;
-    sum += (L + kTile - 1) / kTile;
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  int before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += wsum[w];
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i)
-    if (threadIdx.x * kOwn + i <= kMaxB) tp[threadIdx.x * kOwn + i] = before + mine[i];
-  if (threadIdx.x == kThreads - 1 && kThreads * kOwn == kMaxB) tp[kMaxB] = before + sum;
-  __syncthreads();
-  const int T = tp[c.B] * c.Hkv;
-  Cut cut = cut_of(T, gridDim.x, kTile, kWarps);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i <= c.B + 2; i += kThreads) a.plan[i] = i == 0 ? cut.per : i == 1 ? cut.warps : tp[i - 2];
-  // sequences without rows belong to no warp's range
-  if (blockIdx.y == 0)
-    for (int b = blockIdx.x; b < c.B; b += gridDim.x)
-      if (Ls[b] == 0)
-        for (int i = threadIdx.x; i < a.Hq * D; i += kThreads) {
-          a.O[(long long)b * a.Hq * D + i] = 0.f;
-          if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
-        }
-
-  // the CTA's range of tiles, and its first pair
-  long long c0 = (long long)blockIdx.x * cut.warps * cut.per;
-  Cursor cur, ld;
+  // the CTA's range of tiles, [c0, c1) in the order of all pairs' tiles, and its first pair
+  long long c0;
   int c1;
+  Cursor cur, ld;
+  Cut cut;
   if (a.own) {
+    // of one pair alone: counted from the pair's first tile
     const int pair_id = blockIdx.x / a.own, part = blockIdx.x % a.own;
     cur.b = pair_id / c.Hkv;
-    cur.h = pair_id % c.Hkv;
-    cur.L = Ls[cur.b];
-    cur.nt = tp[cur.b + 1] - tp[cur.b];
-    if (cur.nt == 0) return;  // the whole cluster
+    cur.h = pair_id - cur.b * c.Hkv;
+    cur.L = c.L[cur.b];
+    const bool bad = cur.L < 0 || cur.L > c.cap;
+    if (bad && part == 0 && cur.h == 0 && blockIdx.y == 0 && threadIdx.x == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
+    if (bad || cur.L == 0) {  // the whole cluster
+      const int m0 = blockIdx.y * MT;
+      const long long hq = (long long)cur.b * a.Hq + (long long)cur.h * a.G + m0;
+      if (part == 0)
+        for (int i = threadIdx.x; i < min(MT, a.G - m0) * D; i += kThreads) {
+          a.O[hq * D + i] = 0.f;
+          if (a.lse && i < min(MT, a.G - m0)) a.lse[hq + i] = -INFINITY;
+        }
+      return;
+    }
+    cur.nt = (cur.L + kTile - 1) / kTile;
     cut.warps = kWarps;
     cut.per = (cur.nt + a.own * kWarps - 1) / (a.own * kWarps);
     cur.kt = min(cur.nt, part * kWarps * cut.per);
-    c0 = (long long)tp[cur.b] * c.Hkv + cur.h * cur.nt + cur.kt;
-    c1 = (int)c0 + min(cur.nt - cur.kt, kWarps * cut.per);
+    c0 = cur.kt;
+    c1 = cur.kt + min(cur.nt - cur.kt, kWarps * cut.per);
   } else {
+    // lengths and, for one head, the tiles before each sequence
+    int mine[kOwn], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int b = threadIdx.x * kOwn + i;
+      int L = b < c.B ? c.L[b] : 0;
+      if (L < 0 || L > c.cap) {
+        if (blockIdx.x == 0 && blockIdx.y == 0) tr_flag(a.status, TR_DEV_BAD_LENGTH);
+        L = 0;
+      }
+      if (b < kMaxB) Ls[b] = L;
+      mine[i] = sum;
+      sum += (L + kTile - 1) / kTile;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (threadIdx.x * kOwn + i <= kMaxB) tp[threadIdx.x * kOwn + i] = before + mine[i];
+    if (threadIdx.x == kThreads - 1 && kThreads * kOwn == kMaxB) tp[kMaxB] = before + sum;
+    __syncthreads();
+    const int T = tp[c.B] * c.Hkv;
+    cut = cut_of(T, gridDim.x, kTile, kWarps);
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+      for (int i = threadIdx.x; i <= c.B + 2; i += kThreads)
+        a.plan[i] = i == 0 ? cut.per : i == 1 ? cut.warps : tp[i - 2];
+    // sequences without rows belong to no warp's range
+    if (blockIdx.y == 0)
+      for (int b = blockIdx.x; b < c.B; b += gridDim.x)
+        if (Ls[b] == 0)
+          for (int i = threadIdx.x; i < a.Hq * D; i += kThreads) {
+            a.O[(long long)b * a.Hq * D + i] = 0.f;
+            if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+          }
+    c0 = (long long)blockIdx.x * cut.warps * cut.per;
     if (c0 >= T) return;
     c1 = (int)min((long long)T, c0 + (long long)cut.warps * cut.per);
     seek(cur, tp, Ls, c.B, c.Hkv, (int)c0);
@@ -330,68 +352,116 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
   ld = cur;
   int t_ld = t0;
 
-  // the page of row `lane` of the next tile to load, looked up a tile ahead of its use
-  auto page_of = [&]() {
-    const int p = ld.kt * kTile + lane;
-    return !c.page_table ? ld.b
-           : t_ld < t1 && lane < kTile && p < ld.L ? c.page_table[(long long)ld.b * c.max_pages + (p >> c.page_log2)]
-                                                   : 0;
+  // Queries of a pair, raw: requested before the rows, which would keep them waiting.
+  constexpr int R = MT / 8;                           // query rows of a lane: g, g + 8
+  uint32_t q[R][S::QR];
+  auto fetch_q = [&](const Cursor &u) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int m_row = row0 + g + r * 8;
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.Q) +
+                         ((long long)u.b * a.Hq + (long long)u.h * a.G + m_row) * (D / 8);
+#pragma unroll
+      for (int s = 0; s < S::QR / 4; ++s) {
+        // 16-bit rows: a lane's pieces are 8 elements apart by four; 8-bit ones: 16
+        const uint4 x = ldg16(src + (S::F8 ? (4 * (s / 2) + t) * 2 + s % 2 : 4 * s + t), m_row < a.G);
+        q[r][s * 4] = x.x;
+        q[r][s * 4 + 1] = x.y;
+        q[r][s * 4 + 2] = x.z;
+        q[r][s * 4 + 3] = x.w;
+      }
+    }
   };
-  int page = page_of();
+  if (t0 < t1) fetch_q(cur);
+
+  // The loader.  `run` whole tiles lie right behind the last one in the same page (or
+  // dense sequence): they take two pointer steps each.  Any other tile is looked up
+  // by its rows' pages; lane l holds that of row l, read ahead of its use.
   const int blocks = c.page_table ? c.num_pages : c.B;
   const bool whole_tile = !c.page_table || (1 << c.page_log2) >= kTile;  // a tile lies in one page
+  constexpr int kCopies = KB * S::CPR / 2, kStep = 32 / S::CPR;  // per lane and tensor; rows apart
+  const int ch = lane % S::CPR, r0 = lane / S::CPR;
+  const char *kp = nullptr, *vp = nullptr;
+  int run = 0, page = 0;
+  auto page_of = [&](Cursor u, int ahead) {
+    u.kt += ahead;
+    if (u.kt >= u.nt) {  // behind the pair's last tile: the next one's first
+      u.kt = u.nt - 1;
+      step<kTile>(u, Ls, c.B, c.Hkv);
+    }
+    const int p = u.kt * kTile + lane;
+    page = !c.page_table ? u.b
+           : lane < kTile && p < u.L ? c.page_table[(long long)u.b * c.max_pages + (p >> c.page_log2)]
+                                     : 0;
+  };
+  if (t0 < t1) page_of(ld, 0);
   auto issue = [&](int stage) {
     if (t_ld < t1) {
       const uint32_t dk = ring + stage * S::STAGE, dv = dk + kTile * S::ROW;
-      const int p0 = ld.kt * kTile, ch = lane % S::CPR, r0 = lane / S::CPR, left = ld.L - p0;
-      const long long head = (long long)ld.h * c.head_stride + ch * 16;
-      constexpr int kCopies = KB * S::CPR / 2, kStep = 32 / S::CPR;  // per lane and tensor; rows apart
-      const bool bad = lane < min(kTile, left) && (unsigned)page >= (unsigned)blocks;
-      if (left >= kTile && !__any_sync(~0u, bad)) {
-        if (whole_tile) {
+      bool whole = run > 0;
+      if (!whole) {
+        const int p0 = ld.kt * kTile, left = ld.L - p0;
+        const long long head = (long long)ld.h * c.head_stride + ch * 16;
+        const bool bad = lane < min(kTile, left) && (unsigned)page >= (unsigned)blocks;
+        if (whole_tile && left >= kTile && !__any_sync(~0u, bad)) {
           const long long at = (long long)__shfl_sync(~0u, page, 0) * c.block_stride + head + kv_row(c, p0 + r0);
-          const char *k = c.K + at, *v = c.V + at;
-          auto copy = [&](long long next) {
+          kp = c.K + at;
+          vp = c.V + at;
+          whole = true;
+          // whole tiles of the pair and tiles of the page behind this one
+          run = left / kTile - 1;
+          if (c.page_table) {
+            const int per_page = (1 << c.page_log2) / kTile;
+            run = min(run, per_page - 1 - (ld.kt & (per_page - 1)));
+          }
+          run = min(run, t1 - 1 - t_ld) + 1;
+        } else {  // small pages, a pair's last tile, or a page that is not there: row by row
+          if (bad) tr_flag(a.status, TR_DEV_BAD_PAGE);
+          if (left >= kTile && !__any_sync(~0u, bad)) {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
               const int r = r0 + i * kStep;
-              copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, k + i * next);
-              copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, v + i * next);
+              const long long at = (long long)__shfl_sync(~0u, page, r) * c.block_stride + head + kv_row(c, p0 + r);
+              copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at);
+              copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at);
             }
-          };
-          if (c.row_stride == S::ROW) copy(kStep * S::ROW);  // the offsets are part of the instructions
-          else copy(kStep * c.row_stride);
-        } else {
+          } else {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+              const int r = r0 + i * kStep, pg = __shfl_sync(~0u, page, r);
+              const bool valid = r < left && (unsigned)pg < (unsigned)blocks;
+              const long long at = valid ? (long long)pg * c.block_stride + head + kv_row(c, p0 + r) : 0;
+              copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
+              copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at, valid);
+            }
+          }
+          run = 1;
+        }
+        if (t_ld + run < t1) page_of(ld, run);
+      }
+      if (whole) {
+        auto copy = [&](long long next) {
 #pragma unroll
           for (int i = 0; i < kCopies; ++i) {
             const int r = r0 + i * kStep;
-            const long long at = (long long)__shfl_sync(~0u, page, r) * c.block_stride + head + kv_row(c, p0 + r);
-            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at);
-            copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at);
+            copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, kp + i * next);
+            copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, vp + i * next);
           }
-        }
-      } else {  // a pair's last tile, or a page that is not there: row by row
-        if (bad) tr_flag(a.status, TR_DEV_BAD_PAGE);
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          const int r = r0 + i * kStep, pg = __shfl_sync(~0u, page, r);
-          const bool valid = r < left && (unsigned)pg < (unsigned)blocks;
-          const long long at = valid ? (long long)pg * c.block_stride + head + kv_row(c, p0 + r) : 0;
-          copy16(dk + r * S::ROW + swz_k<S::CPR>(r, ch) * 16, c.K + at, valid);
-          copy16(dv + r * S::ROW + swz_v<S::CPR, S::F8>(r, ch) * 16, c.V + at, valid);
-        }
+        };
+        if (c.row_stride == S::ROW) copy(kStep * S::ROW);  // the offsets are part of the instructions
+        else copy(kStep * c.row_stride);
+        kp += kTile * c.row_stride;
+        vp += kTile * c.row_stride;
       }
-      step<kTile>(ld, Ls, c.B, c.Hkv);
+      --run;
       ++t_ld;
-      page = page_of();
+      if (t_ld < t1) step<kTile>(ld, Ls, c.B, c.Hkv);
     }
     copy_commit();
   };
   for (int i = 0; i < S::STAGES - 1; ++i) issue(i);
 
-  constexpr int R = MT / 8;                           // query rows of a lane: g, g + 8
   constexpr float kOff = S::BF ? 0.f : 7.f;           // fp16 weights run up to 2^15
-  uint32_t q[R][S::QR];
   float mul[R], m[R], l[R], o[S::NT][2 * R];
   float *logits[R];  // where a lane's logits of the next tile go
   int kt0 = 0;
@@ -428,29 +498,18 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
     if (i == t0 || cur.kt == 0) {
       // a new pair: its queries, empty sums
       kt0 = cur.kt;
+      if (i > t0) fetch_q(cur);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int m_row = row0 + g + r * 8;
-        const bool valid = m_row < a.G;
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.Q) +
-                           ((long long)cur.b * a.Hq + (long long)cur.h * a.G + m_row) * (D / 8);
         mul[r] = a.scale_log2;
-        logits[r] = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + m_row) * a.s_ld + cur.kt * kTile + 2 * t;
+        logits[r] = a.s + ((long long)cur.b * a.Hq + (long long)cur.h * a.G + row0 + g + r * 8) * a.s_ld +
+                    cur.kt * kTile + 2 * t;
         if constexpr (S::F8) {
-          // a lane's pieces are 16 elements; narrowed to fp16 after scaling the head's largest to 2^14
+          // narrowed to fp16 after scaling the head's largest to 2^14
           float amax = 0.f;
 #pragma unroll
-          for (int s = 0; s < D / 64; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint4 x = valid ? src[(4 * s + t) * 2 + j] : make_uint4(0, 0, 0, 0);
-              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                q[r][s * 8 + j * 4 + e] = y[e];
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(y[e] << 16)), fabsf(__uint_as_float(y[e] & 0xFFFF0000u))));
-              }
-            }
+          for (int e = 0; e < S::QR; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[r][e] << 16)), fabsf(__uint_as_float(q[r][e] & 0xFFFF0000u))));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
           const int up = amax > 0.f ? 14 - ilogbf(amax) : 0;
@@ -459,15 +518,6 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
             q[r][e] = pack_half2(scalbnf(__uint_as_float(q[r][e] << 16), up),
                                  scalbnf(__uint_as_float(q[r][e] & 0xFFFF0000u), up));
           mul[r] = scalbnf(a.scale_log2 * c.k_scale[cur.h], -up);
-        } else {
-#pragma unroll
-          for (int s = 0; s < D / 32; ++s) {
-            const uint4 x = valid ? src[4 * s + t] : make_uint4(0, 0, 0, 0);
-            q[r][s * 4] = x.x;
-            q[r][s * 4 + 1] = x.y;
-            q[r][s * 4 + 2] = x.z;
-            q[r][s * 4 + 3] = x.w;
-          }
         }
         m[r] = -INFINITY;
         l[r] = 0.f;
@@ -677,7 +727,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
         store_row(dst, r, f);
       }
     }
-    step<kTile>(cur, Ls, c.B, c.Hkv);
+    if (i + 1 < t1) step<kTile>(cur, Ls, c.B, c.Hkv);
   }
   if (!joined) return;
 
