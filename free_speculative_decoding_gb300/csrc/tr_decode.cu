@@ -33,8 +33,9 @@
 //
 // Precision.  The output is fp32, so P must not be rounded to the cache's type:
 // p is split exactly into three bf16 parts (8 + 8 + 8 bits), or into two fp16 parts
-// (22 bits, p scaled up to 2^15 so that small weights stay normal numbers), and
-// each part is multiplied with V.  With at most 8 heads the empty half of the
+// (22 bits; p is scaled up to between 2^7 and 2^15 at the largest, so that what
+// fp16 cannot hold is below 2^-32 of the weights' sum), and each part is
+// multiplied with V.  With at most 8 heads the empty half of the
 // instruction's rows carries the second part at no extra cost.  The matrix
 // unit's own adds cut off what does not fit, always towards zero, so its sums
 // last 16 rows only and are added to O with rounded adds (kept in the unit over a

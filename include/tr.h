@@ -369,7 +369,8 @@ typedef struct tr_kv_cache {
  *   O   [B, Hq, d] fp32 output         lse [B, Hq] fp32 output, may be NULL
  * accumulate != 0: also scores[b, g, p] += sum over the Hq / Hkv query heads of
  * group g of w_p, for p < L[b]; the sums' order is fixed, so equal calls give
- * equal bits.
+ * equal bits.  Products and sums are fp32 (of fp16 and e4m3 caches, weights below
+ * 2^-32 of the largest do not reach O).
  * Hq a multiple of Hkv (any group of up to 524280 heads, Hq < 2^24), scale
  * positive and below 2^127.  A length
  * outside the cache sets TR_DEV_BAD_LENGTH and counts as 0; an entry of the
