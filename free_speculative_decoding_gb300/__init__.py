@@ -418,7 +418,7 @@ class KVCache:
         self._index = K.get_device()
 
     def _stream(self):
-        if self._index != torch.cuda.current_device():
+        if self._index != torch._C._cuda_getDevice():
             raise ValueError("the cache must live on the current CUDA device")
         return torch._C._cuda_getCurrentRawStream(self._index)
 
@@ -441,16 +441,19 @@ def tr_decode_attn(Q, cache, O, scale, ws, lse=None, accumulate=False):
     """Attention of one new token per sequence: Q [B, Hq, d] over the cache's first
     L[b] rows into O [B, Hq, d] float32 (and lse [B, Hq] float32); ``accumulate``
     adds each row's weights to cache.scores."""
-    if Q.dim() != 3 or Q.shape[0] != cache.B or Q.shape[2] != cache.d:
+    shape = Q.shape
+    if len(shape) != 3 or shape[0] != cache.B or shape[2] != cache.d:
         raise ValueError("Q must be [B, Hq, d]")
-    if O.shape != Q.shape:
+    if O.shape != shape:
         raise ValueError("O must be [B, Hq, d]")
-    if lse is not None and lse.shape != Q.shape[:2]:
+    if lse is not None and lse.shape != shape[:2]:
         raise ValueError("lse must be [B, Hq]")
-    _check("tr_decode_attn", lib().tr_decode_attn(
-        cache._arg(Q, "Q", cache.row_dtype), cache._ref, Q.shape[1], scale, cache._arg(O, "O", torch.float32),
-        None if lse is None else cache._arg(lse, "lse", torch.float32), int(accumulate),
-        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream()))
+    rc = lib().tr_decode_attn(
+        cache._arg(Q, "Q", cache.row_dtype), cache._ref, shape[1], scale, cache._arg(O, "O", torch.float32),
+        None if lse is None else cache._arg(lse, "lse", torch.float32), accumulate,
+        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream())
+    if rc:
+        _check("tr_decode_attn", rc)
 
 
 def tr_kv_append_workspace_bytes(cache):
@@ -460,14 +463,17 @@ def tr_kv_append_workspace_bytes(cache):
 def tr_kv_append(Kn, Vn, cache, ws, count=None):
     """Appends the first count[b] (all T without ``count``) rows of Kn, Vn [B, T, Hkv, d]
     to each sequence, converting them to the cache's type, and advances L."""
-    if Kn.dim() != 4 or Kn.shape[0] != cache.B or Kn.shape[2:] != (cache.Hkv, cache.d) or Vn.shape != Kn.shape:
+    shape = Kn.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[2] != cache.Hkv or shape[3] != cache.d or Vn.shape != shape:
         raise ValueError("Kn and Vn must be [B, T, Hkv, d]")
-    if count is not None and tuple(count.shape) != (cache.B,):
+    if count is not None and (count.dim() != 1 or count.shape[0] != cache.B):
         raise ValueError("count must be [B]")
-    _check("tr_kv_append", lib().tr_kv_append(
-        cache._arg(Kn, "Kn", cache.row_dtype), cache._arg(Vn, "Vn", cache.row_dtype), Kn.shape[1],
+    rc = lib().tr_kv_append(
+        cache._arg(Kn, "Kn", cache.row_dtype), cache._arg(Vn, "Vn", cache.row_dtype), shape[1],
         None if count is None else cache._arg(count, "count", torch.int32), cache._ref,
-        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream()))
+        cache._arg(ws, "ws", torch.uint8), ws.numel(), cache._stream())
+    if rc:
+        _check("tr_kv_append", rc)
 
 
 def tr_kv_evict_workspace_bytes(cache, budget):
