@@ -45,15 +45,15 @@
 // head so that narrowing bf16 to fp16 is exact for all but negligible elements.
 //
 // Measured (one GB300, whole calls in a graph, fractions of the 6675 GB/s of a
-// copy): 4 x 32768 rows of 32 heads, bf16, 308 us = 104%; 16 x 1k-4k rows of 32
+// copy): 4 x 32768 rows of 32 heads, bf16, 308 us = 105%; 16 x 1k-4k rows of 32
 // heads in pages of 64, 112 us = 96%; 64 sequences of 1-8191 rows, 8 heads of
-// groups of 4, 8-bit, weights gathered, 115 us = 75% (split_kernel alone 97 us;
+// groups of 4, 8-bit, weights gathered, 116 us = 74% (split_kernel alone 97 us;
 // bound by instructions: each 8-bit pair is widened); 8 x 4096 rows of 8 heads,
-// weights gathered, 36 us = 57%, 24 x 17-2011 rows, d = 64, 12.5 us = 37%, and
-// one sequence of 512 rows of 32 heads, 6.0 us, are bound by latency: 2 us of
-// launch, 2 us until a first tile is through, 1.1 us for each further tile of a
-// warp (some 400 instructions in chains, two or three warps a scheduler), 2-3 us for
-// each of join_kernel and score_kernel.
+// weights gathered, 33 us = 61%, 24 x 17-2011 rows, d = 64, 13 us = 36%, and one
+// sequence of 512 rows of 32 heads, 5.6 us, are bound by latency: 2 us of launch,
+// 1 to 2 us until the first rows are there, then 0.7 us for a tile of a warp by itself
+// and about 1 us beside the SM's others (350 to 400 instructions in chains), 2 to 3 us
+// for each kernel behind this one.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -871,15 +871,13 @@ __device__ __forceinline__ long long part_slot(const Parts &u, int i) {
 constexpr int kFinThreads = 128;
 constexpr int kFinWarps = kFinThreads / 32;
 
-// Joins the partials of one query head per CTA, in the order of the warps.
+// Joins the partials of one query head (a row of O), in the order of the parts.
 template <int D>
-__global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const DecodeArgs a, int W, int MT) {
+__device__ __forceinline__ void join(const KvDev &c, const DecodeArgs &a, int W, int MT, int id) {
   __shared__ float sm[kFinWarps], sl[kFinWarps];
   __shared__ float4 acc[kFinWarps][D / 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq, h = hq / a.G, m = hq % a.G;
-  tr_let_next_start();
-  tr_wait_for_previous();
+  const int hq = id % a.Hq, b = id / a.Hq, h = hq / a.G, m = hq % a.G;
   Parts u;
   const int parts = parts_of(c, a, b, h, u);
   if (parts <= 1) return;  // empty, or finished by one warp or CTA
@@ -940,14 +938,21 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
       y.w += acc[i][threadIdx.x].w * f4[i];
     }
     const float f = (c.v_scale ? c.v_scale[h] : 1.f) / l;
-    *reinterpret_cast<float4 *>(a.O + (long long)blockIdx.x * D + threadIdx.x * 4) =
+    *reinterpret_cast<float4 *>(a.O + (long long)id * D + threadIdx.x * 4) =
         make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
   }
   if (threadIdx.x == 0) {
     const float lse2 = M + log2f(l);
-    a.lse2[blockIdx.x] = lse2;
-    if (a.lse) a.lse[blockIdx.x] = lse2 * kLn2;
+    a.lse2[id] = lse2;
+    if (a.lse) a.lse[id] = lse2 * kLn2;
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const DecodeArgs a, int W, int MT) {
+  tr_let_next_start();
+  tr_wait_for_previous();
+  join<D>(c, a, W, MT, blockIdx.x);
 }
 
 // Adds the weights of a pair's rows, summed over its query heads, to the
@@ -955,22 +960,19 @@ __global__ void __launch_bounds__(kFinThreads) join_kernel(const KvDev c, const 
 // takes 128 rows, each warp every fourth head; else 512 rows and every thread all
 // heads of four rows.  With 4 heads and 262 k rows the split form took 20 us
 // and the other 12 us; with 40 heads and 50 k rows 8 us and 19 us.
-template <bool SPLIT>
-__global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const DecodeArgs a) {
-  constexpr int kRows = SPLIT ? 128 : 512;
+// lse2_of(m): the log2 of query head m's softmax denominator.
+template <bool SPLIT, typename Lse2>
+__device__ __forceinline__ void add_scores(const KvDev &c, const DecodeArgs &a, int b, int h, int L, int p0,
+                                           Lse2 lse2_of) {
   __shared__ float4 sums[SPLIT ? kFinWarps : 1][32];
-  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tr_wait_for_previous();
-  const int L = c.L[b];
-  if (L < 0 || L > c.cap || (int)blockIdx.x * kRows >= L) return;
-  const int p = blockIdx.x * kRows + (SPLIT ? lane : threadIdx.x) * 4;
-  const long long hq = (long long)b * a.Hq + (long long)h * a.G;
-  const float *src = a.s + hq * a.s_ld + p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p = p0 + (SPLIT ? lane : threadIdx.x) * 4;
+  const float *src = a.s + ((long long)b * a.Hq + (long long)h * a.G) * a.s_ld + p;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   if (p < L) {
 #pragma unroll 4
     for (int m = SPLIT ? warp : 0; m < a.G; m += SPLIT ? kFinWarps : 1) {
-      const float lse2 = __ldcg(a.lse2 + hq + m);
+      const float lse2 = lse2_of(m);
       const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + m * a.s_ld));  // behind the last row: not used
       w.x += ex2(x.x - lse2);
       w.y += ex2(x.y - lse2);
@@ -982,12 +984,12 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
   if constexpr (SPLIT) {
     sums[warp][lane] = w;
     __syncthreads();
-    const int r = blockIdx.x * kRows + threadIdx.x;
+    const int r = p0 + threadIdx.x;
     if (r >= L) return;
     const float *all = reinterpret_cast<const float *>(sums);
     float x = all[threadIdx.x];
 #pragma unroll
-    for (int i = 1; i < kFinWarps; ++i) x += all[i * kRows + threadIdx.x];
+    for (int i = 1; i < kFinWarps; ++i) x += all[i * 128 + threadIdx.x];
     dst[r] += x;
   } else {
     const float x[4] = {w.x, w.y, w.z, w.w};
@@ -995,6 +997,65 @@ __global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const
     for (int i = 0; i < 4; ++i)
       if (p + i < L) dst[p + i] += x[i];
   }
+}
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(kFinThreads) score_kernel(const KvDev c, const DecodeArgs a) {
+  const int h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * (SPLIT ? 128 : 512);
+  tr_wait_for_previous();
+  const int L = c.L[b];
+  if (L < 0 || L > c.cap || p0 >= L) return;
+  const float *lse2 = a.lse2 + (long long)b * a.Hq + (long long)h * a.G;
+  add_scores<SPLIT>(c, a, b, h, L, p0, [&](int m) { return __ldcg(lse2 + m); });
+}
+
+// Joins and scores in one kernel: the first B * Hq CTAs join a query head each,
+// those behind them (`chunks` for each pair, at most 8 heads a group) take their
+// denominators from the parts' (m, l) themselves, a warp for each head.  It saves
+// waiting for the joins and costs every one of these CTAs the denominators:
+// 8 sequences of 4096 rows of 8 heads (512 of them) 35.5 us with two kernels, 33.1
+// with one; 64 of up to 8191 (8192 of them) 113.6 and 117.1 us.
+constexpr long long kOneFinish = 1024;
+template <int D>
+__global__ void __launch_bounds__(kFinThreads) finish_kernel(const KvDev c, const DecodeArgs a, int W, int MT,
+                                                             unsigned joins, unsigned chunks) {
+  __shared__ float lse2[8];
+  tr_wait_for_previous();
+  if (blockIdx.x < joins) {
+    join<D>(c, a, W, MT, blockIdx.x);
+    return;
+  }
+  const unsigned k = blockIdx.x - joins, pair = k / chunks;
+  const int b = pair / c.Hkv, h = pair % c.Hkv, p0 = (k % chunks) * 512, L = c.L[b];
+  if (L < 0 || L > c.cap || p0 >= L) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Parts u;
+  const int parts = parts_of(c, a, b, h, u);
+  const long long hq = (long long)b * a.Hq + (long long)h * a.G;
+  for (int m = warp; m < a.G; m += kFinWarps) {
+    float x;
+    if (parts <= 1) {
+      x = __ldcg(a.lse2 + hq + m);
+    } else {
+      float M = -INFINITY, l = 0.f;
+      for (int i = lane; i < parts; i += 32) {
+        const float2 y = __ldcg(a.part_ml + part_slot(u, i) * MT + m);
+        const float mn = fmaxf(M, y.x), base = mn == -INFINITY ? 0.f : mn;
+        l = l * ex2(M - base) + y.y * ex2(y.x - base);
+        M = mn;
+      }
+      const float own = M;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+      l *= ex2(own - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+      x = M + log2f(l);
+    }
+    if (lane == 0) lse2[m] = x;
+  }
+  __syncthreads();
+  add_scores<false>(c, a, b, h, L, p0, [&](int m) { return lse2[m]; });
 }
 
 // A CTA's share of a pair's bytes up to which clusters own pairs.  Measured (bf16,
@@ -1065,10 +1126,16 @@ int launch(const Plan &p, cudaStream_t s, const KvDev &c, const DecodeArgs &a) {
            : p.warps == 8 ? launch_split<TYPE, D, 8, 8>(p, s, c, a)
                           : launch_split<TYPE, D, 8, 12>(p, s, c, a);
   if (rc != TR_OK) return rc;
+  const long long chunks = (c.cap + 511) / 512, pairs = (long long)c.B * c.Hkv;
+  if (!p.own && a.accumulate && a.G <= 8 && pairs * chunks <= kOneFinish) {
+    const unsigned joins = c.B * a.Hq;
+    return tr_launch_next(finish_kernel<D>, {dim3(joins + (unsigned)(pairs * chunks)), kFinThreads}, s, c, a,
+                          p.grid * p.warps, p.MT, joins, (unsigned)chunks);
+  }
   if (!p.own) rc = tr_launch_next(join_kernel<D>, {dim3(c.B * a.Hq), kFinThreads}, s, c, a, p.grid * p.warps, p.MT);
   if (rc != TR_OK || !a.accumulate) return rc;
   return a.G > 8 ? tr_launch_next(score_kernel<true>, {dim3((c.cap + 127) / 128, c.Hkv, c.B), kFinThreads}, s, c, a)
-                 : tr_launch_next(score_kernel<false>, {dim3((c.cap + 511) / 512, c.Hkv, c.B), kFinThreads}, s, c, a);
+                 : tr_launch_next(score_kernel<false>, {dim3((unsigned)chunks, c.Hkv, c.B), kFinThreads}, s, c, a);
 }
 
 template <int TYPE>
