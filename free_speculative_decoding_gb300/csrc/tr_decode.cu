@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
     if (blockIdx.y == 0)
       for (int b = blockIdx.x; b < c.B; b += gridDim.x)
         if (Ls[b] == 0)
-          for (int i = threadIdx.x; i < a.Hq * D; i += kThreads) {
+          for (unsigned i = threadIdx.x; i < (unsigned)a.Hq * D; i += kThreads) {  // up to 2^31 - 128
             a.O[(long long)b * a.Hq * D + i] = 0.f;
-            if (a.lse && i < a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+            if (a.lse && i < (unsigned)a.Hq) a.lse[(long long)b * a.Hq + i] = -INFINITY;
           }
     c0 = (long long)blockIdx.x * cut.warps * cut.per;
     if (c0 >= T) return;

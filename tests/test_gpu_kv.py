@@ -462,6 +462,24 @@ def test_offsets_past_32_bits(tr):
     attend(keep)
 
 
+@pytest.mark.parametrize("n", [0, 1])
+def test_decode_most_query_heads(tr, n):
+    """The most query heads that the call takes (groups of 65793): O's elements come within 128 of 2^31."""
+    Hkv, Hq, d = 255, (1 << 24) - 1, 128
+    K = torch.randn(1, Hkv, 16, d, device="cuda").bfloat16()
+    V = torch.randn(1, Hkv, 16, d, device="cuda").bfloat16()
+    cache = tr.KVCache(K, V, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    Q = torch.zeros(1, Hq, d, dtype=torch.bfloat16, device="cuda")
+    O = torch.full((1, Hq, d), float("nan"), device="cuda")
+    lse = torch.full((1, Hq), float("nan"), device="cuda")
+    ws = torch.empty(tr.tr_decode_attn_workspace_bytes(cache, Hq), dtype=torch.uint8, device="cuda")
+    tr.tr_decode_attn(Q, cache, O, d ** -0.5, ws, lse)
+    # one row has the weight 1, logits of 0 a logarithm of 0
+    want = V[0, :, :1].float() * n
+    assert bool((O.view(Hkv, Hq // Hkv, d) == want).all())
+    assert bool((lse == (0.0 if n else -float("inf"))).all())
+
+
 def test_tensors_of_the_binding(tr):
     """What the Python layer refuses beyond the host checks of the library."""
     K = torch.zeros(2, 4, 64, 128, dtype=torch.bfloat16, device="cuda")
