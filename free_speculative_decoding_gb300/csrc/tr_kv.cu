@@ -628,7 +628,7 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
   KvDev c;
   int rc = kv_check(cache, &c);
   if (rc != TR_OK) return rc;
-  if (!Kn || !Vn || T < 1 || (((uintptr_t)Kn | (uintptr_t)Vn) & 15)) return TR_E_INVAL;
+  if (!Kn || !Vn || T < 1 || (((uintptr_t)Kn | (uintptr_t)Vn) & 15) || ((uintptr_t)count & 3)) return TR_E_INVAL;
   const bool e4m3 = cache->type == TR_KV_E4M3;
   const long long pieces = (long long)T * c.Hkv * (cache->d / 8);
   const long long per = kAppendThreads * kAppendUnroll;

@@ -68,6 +68,8 @@ static inline int kv_check(const tr_kv_cache *c, KvDev *out) {
   }
   const long long esz = e4m3 ? 1 : 2;
   if (((uintptr_t)c->K | (uintptr_t)c->V) & 15) return TR_E_INVAL;
+  if (((uintptr_t)c->L | (uintptr_t)c->page_table | (uintptr_t)c->k_scale | (uintptr_t)c->v_scale | (uintptr_t)c->scores) & 3)
+    return TR_E_INVAL;
   const long long rows = c->page_table ? c->page_size : cap;
   // strides: 16-byte aligned wherever they are used, and no two rows overlap
   // (sorted by stride, each dimension steps over what the smaller ones span)
@@ -88,7 +90,7 @@ static inline int kv_check(const tr_kv_cache *c, KvDev *out) {
     if (st[at] > (1LL << 60) / n[at]) return TR_E_INVAL;
     span += st[at] * (n[at] - 1);
   }
-  if (c->scores && (c->scores_ld < cap || ((uintptr_t)c->scores & 3))) return TR_E_INVAL;
+  if (c->scores && c->scores_ld < cap) return TR_E_INVAL;
   if (c->B > 1024 || cap > (1LL << 30) || (long long)c->B * c->Hkv * cap >= (1LL << 31)) return TR_E_UNSUPPORTED;
   v.K = (char *)c->K;
   v.V = (char *)c->V;

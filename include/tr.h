@@ -336,10 +336,11 @@ typedef enum { TR_KV_BF16 = 0, TR_KV_F16 = 1, TR_KV_E4M3 = 2 } tr_kvtype;
  * are never read, so they may hold anything.  A page may be shared between
  * sequences for reading; tr_kv_append and tr_kv_evict need the pages that they
  * write (append: those that receive rows; evict: all of the sequence's) to
- * belong to one sequence.
- * K, V and all strides are 16-byte aligned, rows do not overlap, d is 64 or
- * 128, page_size a power of two, B <= 1024, the positions a sequence can hold
- * at most 2^30 and B * Hkv times as many below 2^31. */
+ * belong to one sequence, at one place of its table.
+ * K, V and all strides are 16-byte aligned (the other arrays to their
+ * elements), rows do not overlap, d is 64 or 128, page_size a power of two,
+ * B <= 1024, the positions a sequence can hold at most 2^30 and B * Hkv times as
+ * many below 2^31. */
 typedef struct tr_kv_cache {
   void *K, *V;
   tr_kvtype type;

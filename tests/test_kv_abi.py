@@ -58,6 +58,20 @@ def test_bad_caches_are_refused_by_every_call(tr, fields, code):
     assert lib.tr_kv_evict_workspace_bytes(r, 8) == 0
 
 
+@pytest.mark.parametrize("fields", [dict(L=P + 2), dict(PAGED, page_table=P + 1), dict(E4M3, k_scale=P + 2),
+                                    dict(E4M3, v_scale=P + 1)])
+def test_misaligned_arrays_are_refused(tr, fields):
+    c = cache(tr, **fields)
+    r, lib = ctypes.byref(c), tr.lib()
+    assert lib.tr_decode_attn(P, r, 8, 0.1, P, P, 0, P, BIG, None) == tr.TR_E_INVAL
+    assert lib.tr_kv_append(P, P, 1, None, r, P, BIG, None) == tr.TR_E_INVAL
+    assert lib.tr_kv_evict(r, 8, 2, P, BIG, None) == tr.TR_E_INVAL
+
+
+def test_misaligned_counts_are_refused(tr):
+    assert tr.lib().tr_kv_append(P, P, 1, P + 2, ctypes.byref(cache(tr)), P, BIG, None) == tr.TR_E_INVAL
+
+
 def test_null_cache(tr):
     lib = tr.lib()
     assert lib.tr_decode_attn(P, None, 8, 0.1, P, P, 0, P, BIG, None) == tr.TR_E_INVAL
