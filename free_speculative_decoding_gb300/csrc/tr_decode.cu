@@ -42,7 +42,8 @@
 // whole range, the loss grew with the range: 7e-6 of the result's norm at 3400
 // rows a warp against 1e-6 for fp32 products and sums; now 5e-7).
 // An 8-bit row is widened to fp16 (exact); Q is scaled by a power of two per
-// head so that narrowing bf16 to fp16 is exact for all but negligible elements.
+// head so that narrowing bf16 to fp16 is exact for all elements down to 2^-31 of
+// the head's largest.
 //
 // Measured (one GB300, whole calls in a graph, fractions of the 6675 GB/s of a
 // copy): 4 x 32768 rows of 32 heads, bf16, 308 us = 105%; 16 x 1k-4k rows of 32
@@ -58,6 +59,8 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 
 #include <cooperative_groups.h>
 
@@ -89,6 +92,8 @@ struct DecodeArgs {
   int Hq, G, accumulate;
   int own;           // CTAs (a cluster) that share one pair and row tile; 0: ranges over all pairs
   float scale_log2;
+  float scale_man;   // scale_log2 = scale_man * 2^scale_exp, scale_man in [1, 2)
+  int scale_exp;
   unsigned *status;
 };
 
@@ -229,6 +234,19 @@ __device__ __forceinline__ int swz_k(int r, int ch) {
 template <int CPR, bool F8>
 __device__ __forceinline__ int swz_v(int r, int ch) {
   return !F8 ? ch ^ (r & 7) : CPR >= 8 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3);
+}
+
+// What a product of the scaled query (2^up) and an 8-bit row is multiplied with:
+// scale * ks * 2^-up in log2 units.  The softmax below takes the largest product
+// for the largest logit and masks rows with a product of -inf, so the factor must
+// be a positive number.  2^-126 stands for everything below it, a scale of 0
+// included: products are below 2^31, so all such weights are equal as they should be.
+// Mantissas and exponents apart: no intermediate leaves the range that the factor is in.
+__device__ __forceinline__ float logit_factor(const DecodeArgs &a, float ks, int up) {
+  if (!(ks < INFINITY)) return ks * 0.f;  // NaN: so is every logit
+  const int e = ks > 0.f ? ilogbf(ks) : 0;
+  const float f = scalbnf(a.scale_man * scalbnf(ks, -e), a.scale_exp + e - up);
+  return fminf(fmaxf(f, 0x1p-126f), FLT_MAX);
 }
 
 // 8-bit V: columns of a lane's piece of a row, and its pieces per row.
@@ -513,12 +531,16 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const 
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[r][e] << 16)), fabsf(__uint_as_float(q[r][e] & 0xFFFF0000u))));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-          const int up = amax > 0.f ? 14 - ilogbf(amax) : 0;
+          const int up = amax > 0.f ? max(14 - ilogbf(amax), -114) : 0;  // -114: infinite
+          const float ks = c.k_scale[cur.h];
+          const uint32_t flip = ks < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to the query
+          // 2^up, up to 2^147, in two factors; neither product rounds what fp16 can hold
+          const float f0 = __int_as_float((127 + (up >> 1)) << 23), f1 = __int_as_float((127 + up - (up >> 1)) << 23);
 #pragma unroll
           for (int e = 0; e < S::QR; ++e)
-            q[r][e] = pack_half2(scalbnf(__uint_as_float(q[r][e] << 16), up),
-                                 scalbnf(__uint_as_float(q[r][e] & 0xFFFF0000u), up));
-          mul[r] = scalbnf(a.scale_log2 * c.k_scale[cur.h], -up);
+            q[r][e] = pack_half2(__uint_as_float(q[r][e] << 16) * f0 * f1,
+                                 __uint_as_float(q[r][e] & 0xFFFF0000u) * f0 * f1) ^ flip;
+          mul[r] = logit_factor(a, fabsf(ks), up);
         }
         m[r] = -INFINITY;
         l[r] = 0.f;
@@ -1184,6 +1206,8 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   a.accumulate = accumulate != 0;
   a.own = p.own;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_man = 2.f * std::frexp(a.scale_log2, &a.scale_exp);
+  --a.scale_exp;
   a.status = tr_status_dev();
   cudaStream_t s = (cudaStream_t)stream;
   if (cache->type == TR_KV_BF16) return launch<TR_KV_BF16>(cache->d, p, s, c, a);

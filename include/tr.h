@@ -324,7 +324,8 @@ size_t tr_kv_commit_workspace_bytes(int B);
 
 /* Element type of the cached rows.  bf16 and fp16 caches take queries and new
  * rows of their own type; an e4m3 cache (8-bit, no infinities) takes bf16 ones
- * and holds K = k_scale[h] * e4m3, V = v_scale[h] * e4m3. */
+ * and holds K = k_scale[h] * e4m3, V = v_scale[h] * e4m3; scales are any finite
+ * numbers, 0 and negative ones among them. */
 typedef enum { TR_KV_BF16 = 0, TR_KV_F16 = 1, TR_KV_E4M3 = 2 } tr_kvtype;
 
 /* A batch's KV cache.  Position p of sequence b, KV head h, starts at element

@@ -351,6 +351,49 @@ def test_decode_small_magnitudes_e4m3(tr):
         c.check(Q, scale, O, lse)
 
 
+def widened(tr, c, reach):
+    """The same cache under a page table that could hold `reach` rows a sequence (pages of 16)."""
+    wide = torch.full((len(c.lengths), reach // 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.pt.shape[1]] = c.pt
+    c.scores = torch.rand(len(c.lengths), c.Hkv, reach, device="cuda")
+    c.cache = tr.KVCache(c.K, c.V, c.L, page_table=wide, scores=c.scores, k_scale=c.ks, v_scale=c.vs)
+
+
+@pytest.mark.parametrize("reach", [0, 1 << 14, 1 << 18])   # one cluster for each pair, ranges of 8 and 12 warps
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 8), (128, 12)])
+def test_decode_e4m3_scales_at_and_below_zero(tr, reach, d, G):
+    """A head whose scale is 0 (or so small that its logits vanish) weighs all rows alike; a negative scale turns its
+    logits around.  Lengths on and off the tile edges."""
+    c = Made(tr, np.random.default_rng(50 + G), "e4m3", 16, [17, 33, 100, 64, 0, 1, 700], 6, d)
+    c.ks.copy_(torch.tensor([0.0, -0.02, 0.015, 1e-42, -0.0, -0.5]))
+    if reach:
+        widened(tr, c, reach)
+    Q = c.queries(6 * G, 4.0)
+    before = c.scores.clone()
+    O, lse = c.attend(Q, d ** -0.5, accumulate=True)
+    c.check(Q, d ** -0.5, O, lse, before)
+    n = 33
+    flat = torch.tensor(float(np.log(n)), device="cuda")
+    assert torch.allclose(lse[1, :G], flat) and torch.allclose(lse[1, 3 * G:5 * G], flat)
+
+
+@pytest.mark.parametrize("reach", [0, 1 << 18])
+@pytest.mark.parametrize("factor", [2.0 ** -133, 2.0 ** -127, 2.0 ** -120, 1e-30, 2.0 ** 60])
+def test_decode_e4m3_tiny_queries(tr, reach, factor):
+    """Queries so small that every weight is the same, under an ordinary scale (what they are multiplied with inside
+    goes below the smallest number), and large ones with a tiny scale of the head."""
+    c = Made(tr, np.random.default_rng(51), "e4m3", 16, [17, 33, 100], 2, 128)
+    c.ks.copy_(torch.tensor([0.01, 1e-10]) if factor < 1 else torch.tensor([2.0 ** -60, -2.0 ** -130]))
+    if reach:
+        widened(tr, c, reach)
+    Q = c.queries(8, 1.0).float().sign().mul(factor).to(c.cache.row_dtype)
+    Q[:, 1] = 0.0
+    assert Q[:, 0].float().abs().min() > 0
+    before = c.scores.clone()
+    O, lse = c.attend(Q, 0.088, accumulate=True)
+    c.check(Q, 0.088, O, lse, before)
+
+
 def test_decode_repeats_bit_for_bit_and_shares_pages(tr):
     """Equal calls give equal bits, alone and on two streams at once with a workspace each; sequences may share pages."""
     c = Made(tr, np.random.default_rng(9), "bf16", 16, [3000, 3000, 100, 0], 2, 128)
