@@ -29,8 +29,9 @@ constexpr int kAppendUnroll = 4;  // 16-byte pieces of K and of V per thread
 // multiply-adds the last step rounds correctly).  For s in [2^-60, 2^60]: x is
 // first held to +-most, a bf16 number between 1024 s and 1033 s (the quotient is
 // past 448 either way, and nothing overflows; NaN stays), and where the remainder
-// underflows the quotient is below 2^-40, which rounds to 0 either way.  Other
-// scales (r = 0) take the division itself, which costs two to three times as much.
+// underflows the quotient is below 2^-40, which rounds to 0 either way.  The remainder
+// is exact and a zero one is made -0, which takes no sign from q0: -0 / s stays -0.
+// Other scales (r = 0) take the division itself, which costs two to three times as much.
 struct Scale {
   float s, r;
   uint32_t most;  // twice
@@ -49,6 +50,14 @@ __device__ __forceinline__ void mul2(float &x, float &y, float a, float b, float
 __device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float m, float c, float d) {
   asm("{ .reg .b64 p, q, r; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %4}; mov.b64 r, {%5, %6};"
       " fma.rn.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(m), "f"(c), "f"(d));
+}
+// The same rounded down: where the sum is exact only the sign of a zero differs, which is -0
+// unless both terms are +0.
+__device__ __forceinline__ void fma2_down(float &x, float &y, float a, float b, float m, float c, float d) {
+  asm("{ .reg .b64 p, q, r; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %4}; mov.b64 r, {%5, %6};"
+      " fma.rm.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }"
       : "=f"(x), "=f"(y)
       : "f"(a), "f"(b), "f"(m), "f"(c), "f"(d));
 }
@@ -73,7 +82,7 @@ __device__ __forceinline__ uint2 e4m3_of(const uint4 &x, const Scale &sc) {
       const float lo = __uint_as_float(h << 16), hi = __uint_as_float(h & 0xFFFF0000u);
       float p, q, u, v;
       mul2(p, q, lo, hi, sc.r);
-      fma2(u, v, p, q, -sc.s, lo, hi);
+      fma2_down(u, v, p, q, -sc.s, lo, hi);
       fma2(p, q, u, v, sc.r, p, q);
       r[i] = __nv_cvt_float2_to_fp8x2(make_float2(p, q), __NV_SATFINITE, __NV_E4M3);
     }

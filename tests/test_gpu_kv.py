@@ -793,6 +793,27 @@ def test_append_divides_exactly(tr, scale):
         assert np.array_equal(got[0, 0, :T].double().cpu().numpy(), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 2.0 ** -59, 2.0 ** 59, 3e-19, 1e-25, 2e30, -0.5])
+def test_append_keeps_the_sign_of_zero(tr, scale):
+    """-0, and what is too small to be held, keep their signs: bytes as the division and one rounding give them, with
+    scales of both ways that the division is done."""
+    d, T = 64, 8
+    K = torch.zeros(1, 1, 16, d, device="cuda").to(TYPES["e4m3"])
+    V, L = K.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = torch.tensor([scale], device="cuda")
+    cache = tr.KVCache(K, V, L, k_scale=s, v_scale=s)
+    x = torch.tensor([0.0, -0.0, 1e-20, -1e-20, 2.0 ** -133, -2.0 ** -133, 1e-38, -1e-38], dtype=torch.float64)
+    y = torch.tensor([1.0, -1.0, 2.0 ** -11, -2.0 ** -11, 2.0 ** -10, -2.0 ** -10, 2.0 ** -9, -2.0 ** -9, 448.0, -448.0,
+                      1e6, -1e6], dtype=torch.float64) * abs(scale)
+    x = torch.cat([x, y, -x, -y])
+    x = torch.cat([x] * 13)[:T * d].bfloat16().view(1, T, 1, d)
+    tr.tr_kv_append(x.cuda(), (-x).cuda(), cache, tr.workspace(tr.tr_kv_append_workspace_bytes(cache)))
+    for got, rows in ((K, x), (V, -x)):
+        q = oracle.e4m3_round((rows[0, :, 0].float() / s.cpu()).numpy())
+        want = torch.from_numpy(q).float().to(TYPES["e4m3"])
+        assert torch.equal(raw(got[0, 0, :T]).cpu(), raw(want))
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "few", "special", "negative", "sorted", "reversed", "tiny"])
 def test_evict_ties_and_special_scores(tr, kind):
     """Ties go to the lower position; NaN ranks below -inf; -0 equals +0; order is that of the values."""
