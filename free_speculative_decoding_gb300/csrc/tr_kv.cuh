@@ -90,8 +90,9 @@ static inline int kv_check(const tr_kv_cache *c, KvDev *out) {
     if (st[at] > (1LL << 60) / n[at]) return TR_E_INVAL;
     span += st[at] * (n[at] - 1);
   }
-  if (c->scores && c->scores_ld < cap) return TR_E_INVAL;
-  if (c->B > 1024 || cap > (1LL << 30) || (long long)c->B * c->Hkv * cap >= (1LL << 31)) return TR_E_UNSUPPORTED;
+  const long long pairs = (long long)c->B * c->Hkv;
+  if (c->scores && (c->scores_ld < cap || c->scores_ld > (1LL << 60) / pairs)) return TR_E_INVAL;
+  if (c->B > 1024 || cap > (1LL << 30) || pairs > ((1LL << 31) - 1) / cap) return TR_E_UNSUPPORTED;
   v.K = (char *)c->K;
   v.V = (char *)c->V;
   v.B = c->B;

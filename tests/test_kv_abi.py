@@ -68,6 +68,20 @@ def test_misaligned_arrays_are_refused(tr, fields):
     assert lib.tr_kv_evict(r, 8, 2, P, BIG, None) == tr.TR_E_INVAL
 
 
+@pytest.mark.parametrize("fields,code", [
+    # B * Hkv * positions is 2^64; strides of the scores whose products pass 2^63
+    (dict(PAGED, B=1024, Hkv=1 << 24, max_pages=1 << 10, page_size=1 << 20, num_pages=1, head_stride=1 << 27), "UNSUPPORTED"),
+    (dict(scores=P, scores_ld=1 << 62), "INVAL"), (dict(scores=P, scores_ld=(1 << 63) - 1), "INVAL")])
+def test_sizes_whose_products_pass_64_bits_are_refused(tr, fields, code):
+    c = cache(tr, **{**dict(scores=None), **fields})
+    code = getattr(tr, "TR_E_" + code)
+    r, lib = ctypes.byref(c), tr.lib()
+    assert lib.tr_kv_evict_workspace_bytes(r, 8) == 0
+    assert lib.tr_decode_attn_workspace_bytes(r, c.Hkv, 0) == 0
+    assert lib.tr_decode_attn(P, r, c.Hkv, 0.1, P, P, 0, P, BIG, None) == code
+    assert lib.tr_kv_append(P, P, 1, None, r, P, BIG, None) == code
+
+
 def test_misaligned_counts_are_refused(tr):
     assert tr.lib().tr_kv_append(P, P, 1, P + 2, ctypes.byref(cache(tr)), P, BIG, None) == tr.TR_E_INVAL
 
