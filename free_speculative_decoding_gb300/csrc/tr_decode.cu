@@ -184,6 +184,11 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
   asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -1080,6 +1085,26 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(const KvDev c, cons
   add_scores<false>(c, a, b, h, L, p0, [&](int m) { return lse2[m]; });
 }
 
+// bf16 products can pass fp32's range where the scaled logits do not.  Below a scale
+// of 2^-64 half of its exponent is multiplied into a copy of the queries first, so
+// logits below 2^64 are right with any scale.  What that rounds is queries below 2^-51,
+// by 2^-134 at most, which moves a logit by less than 2^-30 whatever the rows hold.  A
+// kernel of its own: the multiplication inside split_kernel took every call of one
+// sequence of 512 rows from 5.37 to 5.47 us.
+constexpr int kPlainScale = -64;
+constexpr int kScaleThreads = 256;
+__global__ void __launch_bounds__(kScaleThreads) scale_queries_kernel(const uint4 *Q, uint4 *to, long long pieces,
+                                                                      uint32_t factor) {
+  tr_let_next_start();
+  tr_wait_for_previous();
+  for (long long i = (long long)blockIdx.x * kScaleThreads + threadIdx.x; i < pieces;
+       i += (long long)gridDim.x * kScaleThreads) {
+    const uint4 x = Q[i];
+    to[i] = make_uint4(mul_bf16x2(x.x, factor), mul_bf16x2(x.y, factor), mul_bf16x2(x.z, factor),
+                       mul_bf16x2(x.w, factor));
+  }
+}
+
 // A CTA's share of a pair's bytes up to which clusters own pairs.  Measured (bf16,
 // d = 128, calls in a graph; clusters against ranges over all pairs): 32 pairs,
 // 512 rows 5.7 / 7.6 us, 2048 rows 9.2 / 9.9 us; 8 pairs of 4 heads, 4096 rows
@@ -1093,14 +1118,14 @@ constexpr long long kOwnBytes = 256 * 1024;
 // against 12.8 us; 8 x 4k rows of 8 heads, 134 MB: 36.9 against 35.5 us).
 constexpr long long kManyBytes = 512ll << 20;
 
-// Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | logits]
+// Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | scaled queries (bf16) | logits]
 struct Plan {
   int MT, warps, row_tiles, grid;  // grid: CTAs per row tile
   int own;
-  size_t ml_off, lse_off, plan_off, s_off, total;
+  size_t ml_off, lse_off, plan_off, q_off, s_off, total;
 };
 
-Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
+Plan make_plan(const KvDev &c, tr_kvtype type, int Hq, int d, int accumulate) {
   Plan p;
   const int G = Hq / c.Hkv;
   const long long pairs = (long long)c.B * c.Hkv, bytes = (long long)c.cap * c.row_bytes * 2;  // of a pair
@@ -1124,7 +1149,8 @@ Plan make_plan(const KvDev &c, int Hq, int d, int accumulate) {
   p.ml_off = tr_align_up(rows * d * 4, 256);
   p.lse_off = p.ml_off + tr_align_up(rows * 8, 256);
   p.plan_off = p.lse_off + tr_align_up((size_t)c.B * Hq * 4, 256);
-  p.s_off = p.plan_off + tr_align_up((size_t)(c.B + 3) * 4, 256);
+  p.q_off = p.plan_off + tr_align_up((size_t)(c.B + 3) * 4, 256);
+  p.s_off = p.q_off + (type == TR_KV_BF16 ? tr_align_up((size_t)c.B * Hq * d * 2, 256) : 0);
   p.total = p.s_off + (accumulate ? (size_t)c.B * Hq * tr_align_up(c.cap, 32) * 4 : 0);
   return p;
 }
@@ -1175,7 +1201,7 @@ bool fits(const KvDev &c, int Hq) {
 extern "C" size_t tr_decode_attn_workspace_bytes(const tr_kv_cache *cache, int Hq, int accumulate) {
   KvDev c;
   if (kv_check(cache, &c) != TR_OK || Hq < 1 || Hq % c.Hkv || !fits(c, Hq)) return 0;
-  return make_plan(c, Hq, cache->d, accumulate).total;
+  return make_plan(c, cache->type, Hq, cache->d, accumulate).total;
 }
 
 extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, float scale, float *O, float *lse,
@@ -1187,7 +1213,7 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   if ((((uintptr_t)Q | (uintptr_t)O) & 15) || ((uintptr_t)lse & 3)) return TR_E_INVAL;
   if (accumulate && !c.scores) return TR_E_INVAL;
   if (!fits(c, Hq)) return TR_E_UNSUPPORTED;
-  const Plan p = make_plan(c, Hq, cache->d, accumulate);
+  const Plan p = make_plan(c, cache->type, Hq, cache->d, accumulate);
   if (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.total) return TR_E_INVAL;
   rc = tr_check_device();
   if (rc != TR_OK) return rc;
@@ -1205,11 +1231,24 @@ extern "C" int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, f
   a.G = Hq / c.Hkv;
   a.accumulate = accumulate != 0;
   a.own = p.own;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.scale_man = 2.f * std::frexp(a.scale_log2, &a.scale_exp);
+  const double scale_log2 = (double)scale * 1.4426950408889634f;  // exact: the smallest scales keep their bits
+  a.scale_log2 = (float)scale_log2;
+  a.scale_man = 2.f * (float)std::frexp(scale_log2, &a.scale_exp);
   --a.scale_exp;
   a.status = tr_status_dev();
   cudaStream_t s = (cudaStream_t)stream;
+  if (cache->type == TR_KV_BF16 && a.scale_exp < kPlainScale) {
+    const int half = a.scale_exp / 2;
+    const uint32_t f = (uint32_t)(127 + half) << 7;
+    const long long pieces = (long long)cache->B * Hq * cache->d / 8;
+    const long long ctas = std::min<long long>((pieces + kScaleThreads - 1) / kScaleThreads, 8LL * tr_sm_count());
+    uint4 *const to = (uint4 *)((char *)ws + p.q_off);
+    rc = tr_launch_next(scale_queries_kernel, {dim3((unsigned)ctas), kScaleThreads}, s, (const uint4 *)Q, to, pieces,
+                        f | f << 16);
+    if (rc != TR_OK) return rc;
+    a.Q = to;
+    a.scale_log2 = (float)std::ldexp(scale_log2, -half);
+  }
   if (cache->type == TR_KV_BF16) return launch<TR_KV_BF16>(cache->d, p, s, c, a);
   if (cache->type == TR_KV_F16) return launch<TR_KV_F16>(cache->d, p, s, c, a);
   return launch<TR_KV_E4M3>(cache->d, p, s, c, a);

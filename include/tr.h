@@ -373,6 +373,9 @@ typedef struct tr_kv_cache {
  * group g of w_p, for p < L[b]; the sums' order is fixed, so equal calls give
  * equal bits.  Products and sums are fp32 (of fp16 and e4m3 caches, weights below
  * 2^-32 of the largest do not reach O).
+ * Numbers' range: scale * sum_i |Q_i K_i| below 2^64, elements of V below 2^90 in
+ * magnitude (weights are summed relative to a running maximum, before they are
+ * divided by their sum); an infinite element of V makes its column infinite or NaN.
  * Hq a multiple of Hkv (any group of up to 524280 heads, Hq < 2^24), scale
  * positive and below 2^127.  A length
  * outside the cache sets TR_DEV_BAD_LENGTH and counts as 0; an entry of the

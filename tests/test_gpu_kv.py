@@ -394,6 +394,27 @@ def test_decode_e4m3_tiny_queries(tr, reach, factor):
     c.check(Q, 0.088, O, lse, before)
 
 
+@pytest.mark.parametrize("reach", [0, 1 << 14, 1 << 18])
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("q2,k2,scale2", [(66, 62, -126), (98, 28, -125), (126, 0, -125), (-126, 120, 5),
+                                          (10, 116, -125), (-8, 126, -119), (0, 126, -126),
+                                          (70, 62, -131), (90, 60, -145)])
+def test_decode_products_beyond_fp32(tr, reach, G, q2, k2, scale2):
+    """bf16 rows whose products with the queries pass fp32's range, or come near it, while the scaled logits are
+    ordinary ones."""
+    c = Made(tr, np.random.default_rng(52), "bf16", 16, [17, 40, 300], 2, 128)
+    for b in range(3):
+        c.rows_k[b] = (c.rows_k[b].double() * 2.0 ** k2).clamp(-3e38, 3e38).bfloat16()
+        c.put(c.K, b, c.rows_k[b])
+    if reach:
+        widened(tr, c, reach)
+    Q = (c.queries(2 * G, 1.0).double() * 2.0 ** q2).clamp(-3e38, 3e38).bfloat16()
+    scale = 1.5 * 2.0 ** scale2
+    before = c.scores.clone()
+    O, lse = c.attend(Q, scale, accumulate=True)
+    c.check(Q, scale, O, lse, before)
+
+
 def test_decode_repeats_bit_for_bit_and_shares_pages(tr):
     """Equal calls give equal bits, alone and on two streams at once with a workspace each; sequences may share pages."""
     c = Made(tr, np.random.default_rng(9), "bf16", 16, [3000, 3000, 100, 0], 2, 128)
