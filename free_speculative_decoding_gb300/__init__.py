@@ -483,7 +483,8 @@ def tr_kv_evict_workspace_bytes(cache, budget):
 
 def tr_kv_evict(cache, budget, recent, ws):
     """Cuts every sequence longer than ``budget`` down to it: the last ``recent`` rows
-    and the best-scored others stay, per KV head, moved up in their old order."""
+    and the best-scored others stay, per KV head, moved up in their old order.  Scores
+    behind the budget are left: set them to 0 before tr_kv_commit or tr_step adds rows."""
     _i31(budget, "budget")
     _i31(recent, "recent")
     _check("tr_kv_evict", lib().tr_kv_evict(cache._ref, budget, recent, cache._arg(ws, "ws", torch.uint8),

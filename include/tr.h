@@ -358,7 +358,8 @@ typedef struct tr_kv_cache {
   const float *k_scale;      /* [Hkv] (device), e4m3 only (else NULL) */
   const float *v_scale;
   float *scores;             /* [B, Hkv, scores_ld] (device), or NULL: the attention weight
-                              * gathered by each row, scores[b, h, p] */
+                              * gathered by each row, scores[b, h, p]; only the three calls
+                              * below keep them (see tr_kv_evict) */
   int64_t scores_ld;         /* >= positions a sequence can hold */
 } tr_kv_cache;
 
@@ -408,8 +409,11 @@ size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache);
  * of the rows before them, the budget - recent with the largest scores (equal
  * scores: the lower position stays; -0 equals +0; NaN ranks below -inf).  The
  * kept rows of K, V and scores move to positions 0 .. budget-1 in their old
- * order and L[b] becomes budget; what lies behind is left as it is.  Sequences
- * within the budget are left alone.  cache->scores must be present.
+ * order and L[b] becomes budget; what lies behind is left as it is, scores too:
+ * tr_kv_append sets those of its rows to 0, but tr_kv_commit and tr_step know no
+ * scores, so a program that adds rows with them sets scores behind L[b] to 0 first,
+ * or the new rows go on from the weights of evicted ones.  Sequences within the
+ * budget are left alone.  cache->scores must be present.
  *   1 <= budget, 0 <= recent <= budget
  * A length outside the cache (TR_DEV_BAD_LENGTH) or a bad page in use
  * (TR_DEV_BAD_PAGE) leaves that sequence untouched.

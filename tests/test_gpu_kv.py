@@ -1049,6 +1049,31 @@ def test_decoding_steps_with_eviction(tr, type, layout):
             check_evict(c, 32, 8)
 
 
+def test_scores_behind_an_eviction_and_commits_of_tree_steps(tr):
+    """An eviction leaves scores behind the budget as they are and a tree step's commit does not touch them: set to 0
+    in between, as the header asks, the committed rows start from nothing."""
+    B, Hkv, cap, d, budget = 2, 2, 96, 128, 24
+    c = Made(tr, np.random.default_rng(55), "bf16", "dense", [60, 41], Hkv, d, extra=36)
+    assert c.cap == cap
+    tr.tr_kv_evict(c.cache, budget, 4, tr.workspace(tr.tr_kv_evict_workspace_bytes(c.cache, budget)))
+    left = c.scores.clone()
+    assert bool((left[0, :, budget:60] > 0).all())
+    c.scores[:, :, budget:].zero_()
+    tree = tr.Tree((2, 1, 0, 0), 4)
+    kt = torch.randn(B, tree.N, Hkv, d, generator=c.g).bfloat16().cuda()
+    path = torch.tensor([[0, 1, 3], [0, 2, 0]], dtype=torch.int32, device="cuda")
+    acc = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    tr.tr_kv_commit(kt, kt, c.K, c.V, c.L, tree, path, acc, tr.workspace(tr.tr_kv_commit_workspace_bytes(B)))
+    assert c.L.tolist() == [27, 26]
+    before = c.scores.clone()
+    assert torch.equal(before[:, :, :budget], left[:, :, :budget]) and not before[:, :, budget:].any()
+    c.lengths = [27, 26]
+    c.rows_k, c.rows_v = [[c.get(x, b, n) for b, n in enumerate(c.lengths)] for x in (c.K, c.V)]
+    Q = c.queries(4, 2.0)
+    O, lse = c.attend(Q, 0.09, accumulate=True)
+    c.check(Q, 0.09, O, lse, before)
+
+
 @pytest.mark.parametrize("budget", [0, 100])
 def test_engine_alternates_tree_and_single_token_steps(tr, budget):
     """TRState: tree steps and steps without a draft on one state, evictions between them, against the oracle's loop
