@@ -791,6 +791,25 @@ def test_evict_very_long(tr, n, budget, recent):
     check_evict(c, budget, recent)
 
 
+@pytest.mark.parametrize("n", [131071, 131072, 131073, 131105])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_where_a_cluster_stops_holding_the_scores(tr, n, ties):
+    """One pair, a cluster of eight CTAs: 16384 scores of each are held in its registers, of more they are read again."""
+    c = Made(tr, np.random.default_rng(53), "e4m3", 256, [n], 1, 64)
+    if ties:
+        c.scores.copy_((c.scores * 50).round() / 50)
+    check_evict(c, 40_000, 0)
+
+
+@pytest.mark.parametrize("n", [16384, 16385, 20011])
+def test_evict_many_pairs_of_long_sequences(tr, n):
+    """So many pairs that one CTA chooses the rows of each, of which it holds 16384: more are read again in every pass."""
+    lengths = [0, n + 37, 3, 700, n] + [0] * 35
+    c = Made(tr, np.random.default_rng(54), "e4m3", 64, lengths, 8, 64)
+    c.scores.copy_((c.scores * 200).round() / 200)
+    check_evict(c, 600, 37)
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.0123, 1e-3, 3e-19, 1e-25, 7e18, 2e30])
 def test_append_divides_exactly(tr, scale):
     """Every quotient that decides between two 8-bit values: the rows lie on and next to the rounding borders."""
