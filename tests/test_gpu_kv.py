@@ -646,6 +646,20 @@ def test_append(tr, type, d, layout):
     check_append(c, 4, None)
 
 
+@pytest.mark.parametrize("Hkv", [256, 257, 300])
+def test_append_many_heads_e4m3(tr, Hkv):
+    """Up to 256 heads' scales are kept by a CTA, of more each thread takes its own."""
+    c = Made(tr, np.random.default_rng(56), "e4m3", 16, [5, 0, 17], Hkv, 64, extra=20)
+    check_append(c, 1, None)
+    check_append(c, 9, [9, 3, 0])
+
+
+def test_append_and_evict_most_sequences(tr):
+    c = Made(tr, np.random.default_rng(57), "bf16", 16, [(7 * b) % 40 for b in range(1024)], 1, 64, extra=8)
+    check_append(c, 3, [b % 4 for b in range(1024)])
+    check_evict(c, 11, 3)
+
+
 def test_append_exactly_full_and_over(tr):
     """Rows up to the last place; one more is refused for that sequence alone."""
     c = Made(tr, np.random.default_rng(21), "bf16", "dense", [60, 50, 64], 2, 128)
