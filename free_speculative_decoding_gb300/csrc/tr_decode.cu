@@ -48,10 +48,11 @@
 // Measured (one GB300, whole calls in a graph, fractions of the 6675 GB/s of a
 // copy): 4 x 32768 rows of 32 heads, bf16, 308 us = 105%; 16 x 1k-4k rows of 32
 // heads in pages of 64, 112 us = 96%; 64 sequences of 1-8191 rows, 8 heads of
-// groups of 4, 8-bit, weights gathered, 116 us = 74% (split_kernel alone 97 us;
+// groups of 4, 8-bit, weights gathered, 116 us = 74% (98 us without weights;
 // bound by instructions: each 8-bit pair is widened); 8 x 4096 rows of 8 heads,
 // weights gathered, 33 us = 61%, 24 x 17-2011 rows, d = 64, 13 us = 36%, and one
-// sequence of 512 rows of 32 heads, 5.6 us, are bound by latency: 2 us of launch,
+// sequence of 512 rows of 32 heads, 5.4 us (6.5 where L2 does not hold its rows), are
+// bound by latency: 2 us of launch,
 // 1 to 2 us until the first rows are there, then 0.7 us for a tile of a warp by itself
 // and about 1 us beside the SM's others (350 to 400 instructions in chains), 2 to 3 us
 // for each kernel behind this one.
@@ -270,6 +271,8 @@ __device__ __forceinline__ Cut cut_of(int T, int ctas, int kTile, int most) {
   return c;
 }
 
+// Registers of a thread: 168 with 12 warps, up to 246 with 8; with 16 query rows 255,
+// and at d = 128 12 (bf16) or 20 (8-bit) bytes spilled.
 template <int TYPE, int D, int MT, int NW>
 __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const KvDev c, const DecodeArgs a) {
   using S = Shape<TYPE, D, NW>;
@@ -1110,12 +1113,18 @@ __global__ void __launch_bounds__(kScaleThreads) scale_queries_kernel(const uint
 // 512 rows 5.7 / 7.6 us, 2048 rows 9.2 / 9.9 us; 8 pairs of 4 heads, 4096 rows
 // 9.5 / 9.9 us; one pair of 32 heads, 2048 rows 9.4 / 11.9 us, 4096 rows
 // 12.1 / 20.5 us.  With larger shares the SMs that no cluster uses are missed.
+// The host knows no lengths, so this and the rule below go by the positions that a
+// sequence can hold; the figures are of caches that are full.  With room the same
+// rows take the way of longer ones (rows not in L2): 32 pairs of 512 rows 6.6 us in a
+// full cache, 8.9 with 8192 positions, 11.0 with 32768; 128 pairs of 4 heads 9.9 us,
+// 17.3 with 8192.
 constexpr long long kOwnBytes = 256 * 1024;
 // Cache bytes from which 12 warps of two stages each are launched instead of 8
 // of three.  Large reads gain from more warps (16 x 4k rows of 32 heads: 112
 // against 116 us; 8-bit, 64 sequences: 115 against 121 us), short ranges from more
 // tiles in flight at their start (24 sequences of up to 2k rows, d = 64: 14.2
-// against 12.8 us; 8 x 4k rows of 8 heads, 134 MB: 36.9 against 35.5 us).
+// against 12.8 us; 8 x 4k rows of 8 heads, 134 MB: 36.9 against 35.5 us).  With room
+// for 32768 rows the latter take 31.8 us without weights, 29.1 in a full cache.
 constexpr long long kManyBytes = 512ll << 20;
 
 // Launch shape and workspace: [partial O | partial (m, l) | lse2 | plan | scaled queries (bf16) | logits]

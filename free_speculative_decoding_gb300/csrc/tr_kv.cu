@@ -5,10 +5,12 @@
 // (one GB300, in a graph, fractions of the 6675 GB/s of a copy over the bytes
 // that the call cannot do without): 8 prompts of up to 4096 rows into an 8-bit
 // cache 28 us = 66% (its floor 18.6 us; the kernel is bound by the instructions of the
-// division: 22.6 M of them with one IEEE division per value took 49 us); one new
-// row for each of 16 sequences 3.3 us, a launch; 16 x 32 heads of 4096 rows cut to
-// 1024, 97 us = 84% (choosing 16 us, moving 81 us = 98%); one sequence of 131072
-// rows x 8 heads cut to 32768, 76 us = 54% (choosing 20 us; moving 11 + 13 + 33 us).
+// division: 22.6 M of them with one IEEE division per value took 49 us), into a 16-bit
+// one 29 us = 86%; one new row for each of 16 sequences 2.2 us behind another kernel, a
+// launch (8-bit 2.7); 16 x 32 heads of 4096 rows cut to 1024, 100 us = 82% (choosing
+// 16 us, moving 81 us = 98%; of 128-byte rows 68 us = 62%, of 64-byte ones 50 us =
+// 43%); one sequence of 131072 rows x 8 heads cut to 32768, 76 us = 54% (choosing
+// 20 us; moving 11 + 13 + 33 us; of 128-byte rows 57 us = 37%, of 64-byte ones 50 us = 22%).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -255,6 +257,7 @@ __device__ __forceinline__ unsigned block_sum(unsigned v, unsigned *wsum) {
 // in keep is the number of rows above the edge before it plus the number of edge
 // rows taken before it.  split[pair], where asked for, gets the number of kept rows
 // at positions below the budget.
+// Four CTAs of the short form share an SM, for which it spills 36 to 44 bytes.
 template <int KPT, int BITS>
 __global__ void __launch_bounds__(kSelThreads, KPT <= 8 ? 4 : 2)
     evict_select_kernel(const KvDev c, int budget, int recent, int32_t *keep, int32_t *old_len, int32_t *split,
@@ -688,7 +691,10 @@ extern "C" int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, voi
   // other way 1.3 of HBM's time and 15 us.  Measured (bf16, d = 128; whole / apart):
   // 8 pairs, 2048 rows kept 27 / 25 us, 16384 155 / 46 us, 32768 300 / 85 us;
   // 32 pairs, 2048 rows 32 / 43 us; 128 pairs, 2048 rows 59 / 70 us; 1 pair, 1024
-  // rows 15 / 18 us.
+  // rows 15 / 18 us.  The host knows no lengths: pairs within the budget count too, so
+  // one sequence of 131072 rows among eight short ones goes as whole rows (8 heads cut
+  // to 32768: 430 us, alone 76).  Shorter rows follow by their bytes; that rule was
+  // measured with rows of 256 bytes only.
   const int row = c.row_bytes;
   const bool few = pairs < 45 && (double)budget * row * (45 - pairs) > 19e6;
   int32_t *split = few ? (int32_t *)((char *)old_len + tr_align_up((size_t)c.B * 4, 256)) : nullptr;

@@ -324,8 +324,8 @@ size_t tr_kv_commit_workspace_bytes(int B);
 
 /* Element type of the cached rows.  bf16 and fp16 caches take queries and new
  * rows of their own type; an e4m3 cache (8-bit, no infinities) takes bf16 ones
- * and holds K = k_scale[h] * e4m3, V = v_scale[h] * e4m3; scales are any finite
- * numbers, 0 and negative ones among them. */
+ * and holds K = k_scale[h] * e4m3, V = v_scale[h] * e4m3; scales are finite, 0
+ * and negative ones among them (a v_scale below 2^-80 in magnitude costs O bits). */
 typedef enum { TR_KV_BF16 = 0, TR_KV_F16 = 1, TR_KV_E4M3 = 2 } tr_kvtype;
 
 /* A batch's KV cache.  Position p of sequence b, KV head h, starts at element
@@ -373,7 +373,8 @@ typedef struct tr_kv_cache {
  * accumulate != 0: also scores[b, g, p] += sum over the Hq / Hkv query heads of
  * group g of w_p, for p < L[b]; the sums' order is fixed, so equal calls give
  * equal bits.  Products and sums are fp32 (of fp16 and e4m3 caches, weights below
- * 2^-32 of the largest do not reach O).
+ * 2^-32 of the largest do not reach O; with an e4m3 cache elements of Q below 2^-31
+ * of their head's largest are rounded).
  * Numbers' range: scale * sum_i |Q_i K_i| below 2^64, elements of V below 2^90 in
  * magnitude (weights are summed relative to a running maximum, before they are
  * divided by their sum); an infinite element of V makes its column infinite or NaN.
@@ -382,6 +383,11 @@ typedef struct tr_kv_cache {
  * outside the cache sets TR_DEV_BAD_LENGTH and counts as 0; an entry of the
  * page table outside [0, num_pages) sets TR_DEV_BAD_PAGE, is not followed, and
  * leaves that sequence's results undefined.
+ * What is launched, and the workspace, go by the positions that a sequence can
+ * hold (dense: cap, paged: max_pages * page_size), not by L: with room for far more
+ * rows than there are short calls take longer, and accumulate needs 4 bytes for each
+ * of B * Hq times these positions.  Pass no wider a page table than the longest
+ * sequence may need.
  * ws: tr_decode_attn_workspace_bytes bytes, 16-byte aligned; its contents do
  * not matter and nothing is kept in it between calls. */
 int tr_decode_attn(const void *Q, const tr_kv_cache *cache, int Hq, float scale, float *O, float *lse,
