@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -61,6 +62,15 @@ class tr_kv_cache(ctypes.Structure):
     ]
 
 
+class tr_rope(ctypes.Structure):
+    _fields_ = [("d", _i), ("rot", _i), ("pairs", _i), ("inv_freq", _p), ("q_norm", _p), ("k_norm", _p), ("eps", _f)]
+
+
+class tr_qkv(ctypes.Structure):
+    _fields_ = [("Q", _p), ("K", _p), ("V", _p), ("type", _i), ("B", _i), ("T", _i), ("Hq", _i), ("Hkv", _i),
+                ("q_stride", _i64 * 3), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3)]
+
+
 # name -> (restype, argtypes)
 _SIGS = {
     "tr_tree_create": (_i, [_p, _i, _i, ctypes.POINTER(_p)]),
@@ -89,6 +99,9 @@ _SIGS = {
     "tr_kv_append_workspace_bytes": (_sz, [ctypes.POINTER(tr_kv_cache)]),
     "tr_kv_evict": (_i, [ctypes.POINTER(tr_kv_cache), _i, _i, _p, _sz, _p]),
     "tr_kv_evict_workspace_bytes": (_sz, [ctypes.POINTER(tr_kv_cache), _i]),
+    "tr_qkv_rope": (_i, [_p, ctypes.POINTER(tr_rope), _p, _p, _p, _p, _p, _p]),
+    "tr_kv_append_rope": (_i, [_p, ctypes.POINTER(tr_rope), _p, _p, ctypes.POINTER(tr_kv_cache), _p, _p, _sz, _p]),
+    "tr_sample": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p]),
     "tr_step": (_i, [ctypes.POINTER(tr_step_args), _p]),
     "tr_step_workspace_bytes": (_sz, [ctypes.POINTER(tr_step_args)]),
     "tr_get_status": (_i, [ctypes.POINTER(ctypes.c_int32), _p]),
@@ -489,6 +502,165 @@ def tr_kv_evict(cache, budget, recent, ws):
     _i31(recent, "recent")
     _check("tr_kv_evict", lib().tr_kv_evict(cache._ref, budget, recent, cache._arg(ws, "ws", torch.uint8),
                                             ws.numel(), cache._stream()))
+
+
+class Rope:
+    """What tr_qkv_rope and tr_kv_append_rope do to a head's row (``tr_rope``): a view of
+    the caller's tensors, which it keeps alive.
+
+    d: elements of a row, 64 or 128.  inv_freq [rot / 2] float32: radians a position of
+    each pair (rot a multiple of 16, at most d; the elements behind are not rotated), or
+    None: no rotation.  pairs: neighbouring elements make a pair, else those rot / 2
+    apart.  q_norm, k_norm [d] float32: weights of the RMS norm of queries and of keys,
+    None: no norm."""
+
+    def __init__(self, d, inv_freq=None, pairs=False, q_norm=None, k_norm=None, eps=1e-6):
+        if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.numel() == 0):
+            raise ValueError("inv_freq must be float32 [rot / 2]")
+        for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (d,)):
+                raise ValueError("%s must be float32 [d]" % name)
+        self.rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+        if d not in (64, 128) or self.rot > d or self.rot % 16:
+            raise ValueError("d must be 64 or 128, rot a multiple of 16 and at most d")
+        if not 0.0 <= eps < float("inf"):
+            raise ValueError("eps must be >= 0 and finite")
+        self.d, self.inv_freq, self.q_norm, self.k_norm = d, inv_freq, q_norm, k_norm
+        self._devices = [t.get_device() for t in (inv_freq, q_norm, k_norm) if t is not None]
+        c = tr_rope()
+        c.d, c.rot, c.pairs, c.eps = d, self.rot, int(pairs), eps
+        c.inv_freq, c.q_norm, c.k_norm = _ptr(inv_freq), _ptr(q_norm), _ptr(k_norm)
+        if len(set(self._devices)) > 1:
+            raise ValueError("inv_freq, q_norm and k_norm must live on one device")
+        self._index = self._devices[0] if self._devices else -1
+        self.struct = c
+        self._ref = ctypes.byref(c)
+
+
+_ROW_TYPES = {torch.bfloat16: TR_KV_BF16, torch.float16: TR_KV_F16}
+_QKV = struct.Struct("@PPPiiiii9q")  # tr_qkv
+assert _QKV.size == ctypes.sizeof(tr_qkv)
+_NO_STRIDE = (0, 0, 0)
+
+
+def _rows_of(Q, K, V, rope, index):
+    """A tr_qkv of the three (Q or K and V may be None), as bytes: a step is a few
+    microseconds on the device, so no ctypes fields are set here."""
+    x = K if Q is None else Q
+    if x is None:
+        x = V
+    B, T, _, d = x.shape
+    if d != rope.d:
+        raise ValueError("Q, K and V must be [B, T, heads, d]")
+    dtype, at, heads, strides = x.dtype, [], [], []
+    for t, name in ((Q, "Q"), (K, "K"), (V, "V")):
+        if t is None:
+            at.append(0)
+            heads.append(0)
+            strides += _NO_STRIDE
+            continue
+        shape, st = t.shape, t.stride()
+        if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d:
+            raise ValueError("Q, K and V must be [B, T, heads, d]")
+        if t.dtype != dtype:
+            raise ValueError("Q, K and V must have the same dtype")
+        if t.get_device() != index:
+            raise ValueError("%s must live on the current CUDA device" % name)
+        if st[3] != 1:
+            raise ValueError("%s must be contiguous along the last axis" % name)
+        at.append(t.data_ptr())
+        heads.append(shape[2])
+        strides += st[:3]
+    if heads[1] and heads[2] and heads[1] != heads[2]:
+        raise ValueError("K and V must have the same heads")
+    if dtype not in _ROW_TYPES:
+        raise ValueError("Q, K and V must be bfloat16 or float16")
+    if rope._index != index and rope._index != -1:
+        raise ValueError("the rope's tensors must live on the current CUDA device")
+    return _QKV.pack(at[0], at[1], at[2], _ROW_TYPES[dtype], B, T, heads[0], heads[1] or heads[2], *strides), B, T
+
+
+def _dense(t, name, dtype, index, shape=None):
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    if t.get_device() != index:
+        raise ValueError("%s must live on the current CUDA device" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return t.data_ptr()
+
+
+def tr_qkv_rope(Q, K, V, rope, pos, Qo, Ko, Vo, tree=None):
+    """Norms and rotates Q [B, T, Hq, d] and K [B, T, Hkv, d] into the dense Qo and Ko
+    and copies V to Vo; the inputs may be strided views, None leaves one (and its
+    output) out.  Row i of sequence b stands at position pos[b] + i, with ``tree``
+    (T = its nodes) at pos[b] + depth of node i."""
+    index = torch._C._cuda_getDevice()
+    if Q is None and K is None and V is None:
+        raise ValueError("Q, K and V are all None")
+    rows, B, T = _rows_of(Q, K, V, rope, index)
+    if tree is not None and tree.N != T:
+        raise ValueError("T must be the tree's nodes")
+    out = []
+    for x, y, name in ((Q, Qo, "Qo"), (K, Ko, "Ko"), (V, Vo, "Vo")):
+        if (x is None) != (y is None):
+            raise ValueError("%s belongs to its input" % name)
+        out.append(None if x is None else _dense(y, name, x.dtype, index, x.shape))
+    rc = lib().tr_qkv_rope(rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, (B,)),
+                           None if tree is None else tree.handle, out[0], out[1], out[2],
+                           torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check("tr_qkv_rope", rc)
+
+
+def tr_kv_append_rope(Q, Kn, Vn, rope, cache, Qo, ws, pos=None, count=None):
+    """tr_kv_append of Kn, Vn [B, T, Hkv, d] with the keys normed and rotated on the way,
+    and Q [B, T, Hq, d] into the dense Qo (both may be None).  The inputs may be
+    strided views.  Row i of sequence b stands at position pos[b] + i, without ``pos`` at
+    its place in the cache, L[b] + i."""
+    stream, index = cache._stream(), cache._index
+    if Kn is None or Vn is None or (Q is None) != (Qo is None):
+        raise ValueError("Kn and Vn are needed, Qo belongs to Q")
+    rows, B, T = _rows_of(Q, Kn, Vn, rope, index)
+    if B != cache.B or Kn.shape[2] != cache.Hkv or rope.d != cache.d:
+        raise ValueError("Kn and Vn must be [B, T, Hkv, d]")
+    if Kn.dtype != cache.row_dtype:
+        raise ValueError("Kn must be %s" % cache.row_dtype)
+    rc = lib().tr_kv_append_rope(
+        rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, (B,)),
+        None if count is None else _dense(count, "count", torch.int32, index, (B,)), cache._ref,
+        None if Qo is None else _dense(Qo, "Qo", Q.dtype, index, Q.shape), cache._arg(ws, "ws", torch.uint8),
+        ws.numel(), stream)
+    if rc:
+        _check("tr_kv_append_rope", rc)
+
+
+def tr_sample(logits, U, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, V=None):
+    """Draws one token from each row of logits [rows, ld] (columns [0, V)) into token [rows]
+    int32, by the uniforms U [rows]; temperature, top_p and min_p [rows] float32 and top_k [rows]
+    int32 are each row's own rules (None: 1, and off).  logprob [rows] float32 gets the
+    logarithm of the drawn token's probability among those that the rules left."""
+    index = torch._C._cuda_getDevice()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, ld]")
+    rows, ld = logits.shape
+    V = ld if V is None else V
+    _i31(V, "V")
+    at = _dense(logits, "logits", logits.dtype, index)
+    n = (rows,)
+    rc = lib().tr_sample(
+        at, _ftype(logits), rows, V, ld,
+        None if temperature is None else _dense(temperature, "temperature", torch.float32, index, n),
+        None if top_k is None else _dense(top_k, "top_k", torch.int32, index, n),
+        None if top_p is None else _dense(top_p, "top_p", torch.float32, index, n),
+        None if min_p is None else _dense(min_p, "min_p", torch.float32, index, n),
+        _dense(U, "U", torch.float32, index, n), _dense(token, "token", torch.int32, index, n),
+        None if logprob is None else _dense(logprob, "logprob", torch.float32, index, n),
+        torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check("tr_sample", rc)
 
 
 def make_step_args(tree, M, tree_tok, ids, vals, acc_len, path, committed, root, L, logits=None, H=None, Wt=None,

@@ -631,6 +631,10 @@ size_t evict_bytes(const KvDev &c, int budget) {
 // ABI
 // ---------------------------------------------------------------------------
 
+int kv_append_plan(const KvDev &c, int T, const int32_t *count, int2 *todo, cudaStream_t s) {
+  return tr_launch_next(append_plan_kernel, {dim3(c.B), kAppendThreads}, s, c, T, count, todo, tr_status_dev());
+}
+
 extern "C" size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache) {
   return cache && cache->B > 0 ? tr_align_up((size_t)cache->B * sizeof(int2), 256) : 0;
 }
@@ -653,7 +657,7 @@ extern "C" int tr_kv_append(const void *Kn, const void *Vn, int T, const int32_t
   cudaStream_t s = (cudaStream_t)stream;
   int2 *todo = grid > 1 ? (int2 *)ws : nullptr;
   if (todo) {
-    rc = tr_launch_next(append_plan_kernel, {dim3(c.B), kAppendThreads}, s, c, T, count, todo, tr_status_dev());
+    rc = kv_append_plan(c, T, count, todo, s);
     if (rc != TR_OK) return rc;
   }
   auto run = [&](auto kernel) {

@@ -113,3 +113,7 @@ static inline int kv_check(const tr_kv_cache *c, KvDev *out) {
   *out = v;
   return TR_OK;
 }
+
+// The first kernel of an append (tr_kv.cu): the checks of all sequences and their new
+// lengths; the rows that each takes go to todo[b] = (old length, rows).
+int kv_append_plan(const KvDev &c, int T, const int32_t *count, int2 *todo, cudaStream_t s);

@@ -38,7 +38,7 @@
  *    status word and may run concurrently on different streams as long as
  *    they do not share output buffers or workspace.
  *  - Limits: tree nodes N <= 128, K <= 32, head dim d == 128 (the single-token
- *    calls on a tr_kv_cache also take d == 64).
+ *    calls on a tr_kv_cache and the position rotation also take d == 64).
  */
 #ifndef TR_H
 #define TR_H
@@ -427,6 +427,107 @@ size_t tr_kv_append_workspace_bytes(const tr_kv_cache *cache);
  * matter and nothing is kept in it between calls. */
 int tr_kv_evict(const tr_kv_cache *cache, int budget, int recent, void *ws, size_t ws_bytes, tr_stream_t stream);
 size_t tr_kv_evict_workspace_bytes(const tr_kv_cache *cache, int budget);
+
+/* ------------------------------------------------------------------------ */
+/* Norms and position rotation                                                */
+/* ------------------------------------------------------------------------ */
+
+/* What a target model does to a layer's queries and keys between the projection
+ * and attention, in one pass: an RMS norm of every head's row and the rotation of
+ * its elements by the row's position.  tr_qkv_rope prepares what tr_verify_attn
+ * and tr_kv_commit take (a tree's rows), tr_kv_append_rope does it on the way into
+ * a cache (a prompt, a step without a draft). */
+
+/* A row x of d elements at position p becomes
+ *   y = x * w / sqrt(sum_i x_i^2 / d + eps)        (w = q_norm or k_norm; NULL: y = x)
+ *   z_i = y_i cos(p f_i) - y_j sin(p f_i),  z_j = y_j cos(p f_i) + y_i sin(p f_i)
+ * for 0 <= i < rot / 2, with j = i + rot / 2, or with pairs != 0 the elements 2 i and
+ * 2 i + 1 in their place; the elements from rot on are those of y.  fp32 throughout
+ * (the angle's turns are exact to 2^-54 of p f), rounded once to the output's type.
+ * The sum of a row's squares must stay in fp32's range. */
+typedef struct tr_rope {
+  int d;                 /* 64 or 128 */
+  int rot;               /* elements that are rotated: a multiple of 16, 0 (none) .. d */
+  int pairs;             /* which elements make a pair: 0 halves of the rotated part, else neighbours */
+  const float *inv_freq; /* [rot / 2] (device) f, in radians a position; ignored where rot == 0 */
+  const float *q_norm;   /* [d] (device), or NULL: queries have no norm */
+  const float *k_norm;
+  float eps;             /* >= 0 and finite */
+} tr_rope;
+
+/* New rows of a batch as a projection leaves them: [B, T, heads, d] with free
+ * strides, the d elements of a head contiguous (all three may be views of one
+ * [B, T, Hq + 2 Hkv, d]). */
+typedef struct tr_qkv {
+  const void *Q, *K, *V; /* Q may be NULL, in tr_qkv_rope K and V too */
+  tr_kvtype type;        /* TR_KV_BF16 or TR_KV_F16 */
+  int B, T, Hq, Hkv;
+  int64_t q_stride[3];   /* elements between sequences, rows, heads: multiples of 8, >= 0 */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+} tr_qkv;
+
+/* Norms and rotates a batch's queries and keys and copies its values: Qo [B, T, Hq, d],
+ * Ko, Vo [B, T, Hkv, d], dense, of the rows' type (NULL where the input is).  Row i of
+ * sequence b stands at position pos[b] + depth of node i (T = the tree's nodes; the root's
+ * position is the number of tokens before it: L[b] unless rows were evicted), or without a
+ * tree (NULL) at pos[b] + i.
+ *   pos [B] int32 (device); NULL only where rot == 0
+ * An output may be its (dense) input itself; no other overlap.  All pointers 16-byte
+ * aligned but inv_freq, norms and pos (4).  TR_E_UNSUPPORTED for other d, rot no multiple
+ * of 16, B * T past 2^31 - 1 or Hq + 2 Hkv past 2^20. */
+int tr_qkv_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *pos, const struct tr_tree *tree, void *Qo,
+                void *Ko, void *Vo, tr_stream_t stream);
+
+/* tr_kv_append of normed and rotated keys, and the queries with them: for i < n, with
+ * n = count[b] (T where count is NULL), row i of sequence b stands at position
+ * pos[b] + i (pos NULL: L[b] + i, its place in the cache);
+ *   K[b, h, L[b] + i] = the key normed and rotated, V[b, h, L[b] + i] = the value,
+ *   Qo[b, i] = the query normed and rotated (Q and Qo NULL: no queries),
+ * then L[b] += n (pos is left as it is).  The cache takes each number in one rounding from
+ * fp32 (an e4m3 cache: e4m3(x / k_scale[h]) as tr_kv_append); scores, if present, are set to
+ * 0 at the new rows.  Qo [B, T, Hq, d] dense, may be Q itself; its rows from n on are left as
+ * they are.  Sequences that tr_kv_append would leave untouched are, in Qo too, and
+ * set the same status bits.
+ * rows->type is the type of the cache's new rows (TR_KV_F16 for an fp16 cache, else
+ * TR_KV_BF16), rows->B, Hkv and rope->d are the cache's.
+ * ws: tr_kv_append_workspace_bytes bytes, 16-byte aligned; its contents do not matter and
+ * nothing is kept in it between calls. */
+int tr_kv_append_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *pos, const int32_t *count,
+                      const tr_kv_cache *cache, void *Qo, void *ws, size_t ws_bytes, tr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sampling                                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* Draws one token from each row of logits [rows, ld] (columns [0, V) used), the next
+ * token of a step without a draft under sampling.  With T = temperature[r] and
+ * w_v = exp((x_v - max x) / T), three rules leave fewer and fewer tokens; each is off
+ * where its array is NULL or the row's number says so:
+ *   top_k  the k tokens of the largest logits (equal ones: the lower ID); off: k <= 0
+ *   top_p  of these, in that order, the fewest whose weights sum to at least top_p times
+ *          the sum of all of these (at least one); off: top_p >= 1 or NaN
+ *   min_p  of these, the ones with w_v >= min_p (the largest is always left); off: min_p <= 0
+ *          or NaN
+ * With W the sum of the weights that are left, token[r] is the lowest ID y for which the
+ * weights left of IDs up to y sum to more than U[r] W (the inverse of the distribution function
+ * over ascending IDs, as in tr_accept_sampled), logprob[r] = ln(w_y / W).
+ *   logits of ftype TR_F32 or TR_BF16, aligned to their elements.  -inf marks a token that is never
+ *   drawn, and so does NaN; where the largest is +inf, the tokens that have it share the draw.
+ *   A row in which nothing else is left gets token -1 and logprob -inf.
+ *   temperature [rows] fp32 or NULL (1); 0, anything below 2^-126 or NaN: the largest
+ *   logit's token (lowest ID), logprob 0
+ *   top_k [rows] int32, top_p and min_p [rows] fp32, each may be NULL
+ *   U [rows] fp32 uniforms in [0, 1) (the random numbers are inputs; others are
+ *   moved to the nearest end, NaN to 0)
+ *   token [rows] int32 out; logprob [rows] fp32 out, may be NULL
+ * Weights are good to about 2^-29 (relative) and summed exactly as integers, so a draw or an
+ * edge of the rules differs from exact arithmetic only within about 4e-9 + V^2 / 2^61 of a
+ * border.  No workspace; equal calls give equal bits.  rows == 0 does nothing; TR_E_UNSUPPORTED for
+ * rows past 2^24 or V past 2^30. */
+int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64_t V, int64_t ld, const float *temperature,
+              const int32_t *top_k, const float *top_p, const float *min_p, const float *U, int32_t *token,
+              float *logprob, tr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Fused step                                                                 */
