@@ -16,8 +16,14 @@ or, without a draft (one token per sequence, the root's),
 
 and the two may alternate (``single_token=True``).  With ``budget`` the attention weights that the
 cached rows gather in decode are kept, and evict() cuts every sequence longer
-than the budget down to it.  L then no longer is a token's position: a program
-that needs positions (rotary embeddings) keeps count of them itself.
+than the budget down to it.  L then no longer is a token's position.
+
+With ``rope`` (a Rope) the state norms and rotates queries and keys itself and keeps
+count of the positions (``pos``, the roots').  Its rows come straight from the projection:
+
+    state.verify(*state.rotate(Q, K, V))       # the tree's rows, at pos + depth
+    ... state.finish(logits=..., Kt=state.Kt, Vt=state.Vt) ...
+    state.decode(Q, Kn, Vn)                    # the roots' rows, at pos
 
 Every call is asynchronous and allocation-free after construction, so whole
 loops can be captured in a CUDA graph.
@@ -26,16 +32,17 @@ from __future__ import annotations
 
 import torch
 
-from . import (TR_INIT_INHERIT, TR_UPD_ALL, KVCache, Tree, make_step_args, tr_accept, tr_decode_attn,
-               tr_decode_attn_workspace_bytes, tr_get_status, tr_init_matrix, tr_kv_append,
-               tr_kv_append_workspace_bytes, tr_kv_evict, tr_kv_evict_workspace_bytes, tr_retrieve, tr_step,
-               tr_step_sampled, tr_step_workspace_bytes, tr_topk, tr_topk_workspace_bytes, tr_update, tr_verify_attn,
-               tr_verify_attn_workspace_bytes, workspace)
+from . import (TR_INIT_INHERIT, TR_UPD_ALL, KVCache, Rope, Tree, make_step_args, tr_accept, tr_decode_attn,
+               tr_decode_attn_workspace_bytes, tr_get_status, tr_init_matrix, tr_kv_append, tr_kv_append_rope,
+               tr_kv_append_workspace_bytes, tr_kv_evict, tr_kv_evict_workspace_bytes, tr_qkv_rope, tr_retrieve,
+               tr_sample, tr_step, tr_step_sampled, tr_step_workspace_bytes, tr_topk, tr_topk_workspace_bytes, tr_update,
+               tr_verify_attn, tr_verify_attn_workspace_bytes, workspace)
 
 
 class TRState:
     def __init__(self, tree: Tree, B: int, V: int, m_dtype=torch.int64, Hq=0, Hkv=0, d=128, cap=0,
-                 logits_dtype=torch.float32, D=0, device="cuda", single_token=False, budget=0, recent=0):
+                 logits_dtype=torch.float32, D=0, device="cuda", single_token=False, budget=0, recent=0,
+                 rope: Rope | None = None):
         self.tree = tree
         self.B, self.V, self.K, self.N = B, V, tree.K, tree.N
         self.Dmax = tree.max_depth
@@ -60,6 +67,14 @@ class TRState:
             self.O = torch.zeros(B, self.N, Hq, d, dtype=torch.float32, **dev)
             self.ws_attn = workspace(tr_verify_attn_workspace_bytes(B, Hq, Hkv, d, cap, tree), device)
             self.scale = d ** -0.5
+        self.rope = rope
+        if rope is not None:
+            if not self.attention or rope.d != d:
+                raise ValueError("a rope needs a cache (Hq > 0) with heads of its d")
+            self.pos = torch.zeros(B, dtype=torch.int32, **dev)  # tokens before the root, evicted ones too
+            self.Q = torch.zeros(B, self.N, Hq, d, dtype=torch.bfloat16, **dev)
+            self.Kt = torch.zeros(B, self.N, Hkv, d, dtype=torch.bfloat16, **dev)
+            self.Vt = torch.zeros_like(self.Kt)
         self.budget, self.recent, self.scores = budget, recent, None
         if single_token or budget:
             if not self.attention:
@@ -82,6 +97,8 @@ class TRState:
             self.scores = torch.zeros(B, self.Hkv, self.cap, dtype=torch.float32, **dev)
         self.cache = KVCache(self.Kc, self.Vc, self.L, scores=self.scores)
         self.O1 = torch.zeros(B, Hq, self.d, dtype=torch.float32, **dev)
+        if self.rope is not None:
+            self.Q1 = torch.zeros(B, Hq, self.d, dtype=torch.bfloat16, **dev)
         self.ws_decode = workspace(tr_decode_attn_workspace_bytes(self.cache, Hq, bool(budget)), self.device)
         self.ws_append = workspace(tr_kv_append_workspace_bytes(self.cache), self.device)
         if budget:
@@ -101,6 +118,8 @@ class TRState:
         already is."""
         self.root.copy_(torch.as_tensor(root, dtype=torch.int32))
         self.L.copy_(torch.as_tensor(L, dtype=torch.int32))
+        if self.rope is not None:
+            self.pos.copy_(self.L)
         if self.scores is not None:
             self.scores.zero_()
         if M_src is not None and M_src.dim() == 3:
@@ -108,6 +127,14 @@ class TRState:
         elif mode is not None:
             tr_init_matrix(self.M, mode, M_src, seed)
         tr_retrieve(self.M, self.tree, self.root, self.tree_tok)
+
+    def rotate(self, Q, K, V):
+        """The tree's rows Q [B, N, Hq, d], K, V [B, N, Hkv, d] (views of the projection's
+        output), normed and rotated: what verify takes, and finish as Kt and Vt."""
+        if self.rope is None:
+            raise ValueError("rotate needs a rope")
+        tr_qkv_rope(Q, K, V, self.rope, self.pos, self.Q, self.Kt, self.Vt, tree=self.tree)
+        return self.Q, self.Kt, self.Vt
 
     def verify(self, Q, Kt, Vt):
         tr_verify_attn(Q, Kt, Vt, self.Kc, self.Vc, self.L, self.tree, self.O, self.scale, self.ws_attn)
@@ -125,22 +152,40 @@ class TRState:
             tr_step(a)
         else:
             tr_step_sampled(a, temperature, U)
+        if self.rope is not None:
+            self.pos.add_(self.acc_len).add_(1)
 
     def decode(self, Q, Kn, Vn):
         """A step without a draft: appends the root's Kn, Vn [B, Hkv, d] to the cache
         and attends with Q [B, Hq, d] over all its rows (the root's own among
-        them); with a budget the rows' weights are gathered."""
-        tr_kv_append(Kn.unsqueeze(1), Vn.unsqueeze(1), self.cache, self.ws_append)
+        them); with a budget the rows' weights are gathered.  With a rope Q and Kn are
+        normed and rotated first."""
+        if self.rope is not None:
+            tr_kv_append_rope(Q.unsqueeze(1), Kn.unsqueeze(1), Vn.unsqueeze(1), self.rope, self.cache,
+                              self.Q1.unsqueeze(1), self.ws_append, pos=self.pos)
+            Q = self.Q1
+        else:
+            tr_kv_append(Kn.unsqueeze(1), Vn.unsqueeze(1), self.cache, self.ws_append)
         tr_decode_attn(Q, self.cache, self.O1, self.scale, self.ws_decode, accumulate=self.scores is not None)
         return self.O1
 
-    def finish_decode(self, logits):
+    def finish_decode(self, logits, U=None, temperature=None, top_k=None, top_p=None, min_p=None):
         """The end of a step without a draft, from the roots' logits [B, V]: the root's
-        row of M becomes its top-K, its first token the next root (committed1)."""
+        row of M becomes its top-K, its first token the next root (committed1).  With the
+        uniforms U [B] the next root is drawn by tr_sample instead, with every
+        sequence's own rules [B]."""
         tr_topk(logits, self.K, self.ids1, None, self.ws_topk1, V=self.V)
         tok = self.root.unsqueeze(1)
         tr_update(self.M, self.tree1, tok, self.ids1)
-        tr_accept(self.tree1, tok, self.ids1, self.acc_len, self.path1, self.committed1, self.root)
+        if U is None:
+            tr_accept(self.tree1, tok, self.ids1, self.acc_len, self.path1, self.committed1, self.root)
+        else:
+            tr_sample(logits, U, self.root, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, V=self.V)
+            self.committed1.copy_(tok)   # the root is the drawn token now
+            self.acc_len.zero_()
+            self.path1.zero_()
+        if self.rope is not None:
+            self.pos.add_(1)
         tr_retrieve(self.M, self.tree, self.root, self.tree_tok)
 
     def evict(self):
