@@ -16,14 +16,19 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "tr_append.cuh"
 
 namespace {
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 8;
+constexpr int kCtas = 2;    // of rope_kernel on an SM
+constexpr int kStages = 8;  // groups in a warp's ring
+constexpr int kShort = 2;   // groups of a task in append_rope_kernel
 
 struct RopeArgs {
   const char *x[3];               // queries, keys, values
@@ -36,8 +41,8 @@ struct RopeArgs {
   const int32_t *pos, *count;
   const int2 *todo;               // cache: (old length, rows) of each sequence, or NULL: found here
   unsigned *status;
-  int batches[3], all_batches;    // tasks of a token, of each kind
-  int per;                        // tasks of a warp
+  int groups[3], all_groups;      // of heads: of a kind, of a token
+  int parts, per;                 // shares of a token, groups of a share
 };
 
 // Depths of a tree's nodes; without nodes the positions follow the rows.
@@ -59,6 +64,15 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi, bool bf) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const char *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
 // Turns a position as a fraction of 2^64: a multiplication by the position wraps around
 // with the whole turns, so far positions lose nothing.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
@@ -73,15 +87,40 @@ __device__ __forceinline__ float2 turn(long long p, unsigned long long f) {
   return r;
 }
 
-// What a warp keeps of a token and a kind.
+// Two fp32 values in one register pair, and one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {  // a b + c
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+__device__ __forceinline__ F2 operator-(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
+
+// What a warp keeps of a token and a kind: z0 = x0 a0 - x1 b0, z1 = x1 a1 + x0 b1 with the
+// angles' cosines in a and sines in b, each times the weight of its element of x; two
+// pairs of elements to a register pair.
 struct Held {
-  float2 cs[8];       // cosines and sines of the lane's pairs
-  float w[16];        // norm weights of the lane's elements
+  F2 a0[4], b0[4], a1[4], b1[4];  // b0 negated
 };
 
 enum { kDense, kCache, kCache8 };  // where keys and values go
 
-template <bool BF, int D, bool PAIRS, int DST, int U>
+template <bool BF, int D, bool PAIRS, int DST>
 struct Rows {
   static constexpr int LPH = D / 16, HPG = 32 / LPH;  // lanes of a head, heads of a group
   const RopeArgs &a;
@@ -90,6 +129,8 @@ struct Rows {
   int lane, sub, head, pa, pb;  // lane of its head, head of the group, the lane's pieces
   bool turned;
   unsigned long long f[D / 64];
+  Held k;
+  int held;           // the kind that k is of
 
   __device__ __forceinline__ Rows(const RopeArgs &a_, const KvDev &c_, float2 *t) : a(a_), c(c_), table(t) {
     lane = threadIdx.x & 31;
@@ -99,219 +140,364 @@ struct Rows {
     const bool apart = turned && !PAIRS;
     pa = apart ? sub : 2 * sub;
     pb = apart ? sub + a.rot / 16 : 2 * sub + 1;
+    held = -1;
+  }
+
+  __device__ __forceinline__ void frequencies() {
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) f[e] = lane + 32 * e < a.rot / 2 ? turns_of(a.inv_freq[lane + 32 * e]) : 0;
   }
 
-  __device__ __forceinline__ void angles(long long p, Held &k) {
+  // Cosines and sines of the token at position p into the table.
+  __device__ __forceinline__ void angles(long long p) {
+    held = -1;
     if (a.rot == 0) return;
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < D / 64; ++e)
       if (lane + 32 * e < a.rot / 2) table[lane + 32 * e] = turn(p, f[e]);
     __syncwarp();
-    if (!turned) return;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 x = reinterpret_cast<const float4 *>(table + sub * 8)[e];
-      k.cs[2 * e] = make_float2(x.x, x.y);
-      k.cs[2 * e + 1] = make_float2(x.z, x.w);
-    }
   }
 
-  __device__ __forceinline__ void weights(int kind, Held &k) {
-    const float *w = kind < 2 ? a.norm[kind] : nullptr;
-    if (!w) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      k.w[e] = w[pa * 8 + e];
-      k.w[8 + e] = w[pb * 8 + e];
-    }
-  }
-
-  __device__ __forceinline__ void load(int kind, int b, int i, int h0, uint4 (&x)[U][2]) {
-    const char *src = a.x[kind] + b * a.stride[kind][0] + i * a.stride[kind][1];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * HPG + head;
-      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-      if (h < a.heads[kind]) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(src + h * a.stride[kind][2]);
-        x[u][0] = p[pa];
-        x[u][1] = p[pb];
-      }
-    }
-  }
-
-  // The task's rows of token i of sequence b, whose place in the cache is p.
-  __device__ __forceinline__ void finish(int kind, int b, int i, int p, int h0, const uint4 (&x)[U][2], const Held &k) {
-    const bool dense = DST == kDense || kind == 0;
-    const long long block = dense ? 0 : kv_block(c, b, p) + kv_row(c, p);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * HPG + head;
-      if (h0 + u * HPG >= a.heads[kind]) break;
-      float y[16];
-      uint4 out[2] = {x[u][0], x[u][1]};
-      if (kind < 2 || DST == kCache8) {
+  // The lane's factors for a kind: eight pairs of elements, (x0, x1) = elements e of
+  // its two pieces, or neighbours.
+  __device__ __forceinline__ void factors(int kind) {
+    if (held == kind) return;
+    held = kind;
+    const float *w = a.norm[kind];
+    float wa[8], wb[8];
+    if (w) {
+      // one 16-byte load for four where the array's address allows it
+      if (((uintptr_t)w & 15) == 0) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint32_t w[4] = {x[u][q].x, x[u][q].y, x[u][q].z, x[u][q].w};
+          const float4 x = reinterpret_cast<const float4 *>(w + pa * 8)[q], y = reinterpret_cast<const float4 *>(w + pb * 8)[q];
+          wa[4 * q] = x.x, wa[4 * q + 1] = x.y, wa[4 * q + 2] = x.z, wa[4 * q + 3] = x.w;
+          wb[4 * q] = y.x, wb[4 * q + 1] = y.y, wb[4 * q + 2] = y.z, wb[4 * q + 3] = y.w;
+        }
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = widen(w[e], BF);
-            y[8 * q + 2 * e] = v.x;
-            y[8 * q + 2 * e + 1] = v.y;
-          }
+        for (int e = 0; e < 8; ++e) {
+          wa[e] = w[pa * 8 + e];
+          wb[e] = w[pb * 8 + e];
         }
       }
-      if (kind < 2) {
-        if (a.norm[kind]) {
-          float s0 = 0.f, s1 = 0.f;
+    }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            s0 = fmaf(y[e], y[e], s0);
-            s1 = fmaf(y[8 + e], y[8 + e], s1);
-          }
-          float s = s0 + s1;
+    for (int q = 0; q < 4; ++q) {
+      float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (turned) cs = reinterpret_cast<const float4 *>(table + sub * 8)[q];
+      F2 c2 = f2(cs.x, cs.z), s2 = f2(cs.y, cs.w);
+      if (w) {
+        // PAIRS: pairs 2q, 2q + 1 are elements 4q .. 4q + 3 of the 16
+        const F2 w0 = PAIRS ? (q < 2 ? f2(wa[(4 * q) & 7], wa[(4 * q + 2) & 7]) : f2(wb[(4 * q) & 7], wb[(4 * q + 2) & 7]))
+                            : f2(wa[2 * q], wa[2 * q + 1]);
+        const F2 w1 = PAIRS ? (q < 2 ? f2(wa[(4 * q + 1) & 7], wa[(4 * q + 3) & 7]) : f2(wb[(4 * q + 1) & 7], wb[(4 * q + 3) & 7]))
+                            : f2(wb[2 * q], wb[2 * q + 1]);
+        k.a0[q] = c2 * w0;
+        k.b0[q] = -(s2 * w1);
+        k.a1[q] = c2 * w1;
+        k.b1[q] = s2 * w0;
+      } else {
+        k.a0[q] = k.a1[q] = c2;
+        k.b0[q] = -s2;
+        k.b1[q] = s2;
+      }
+    }
+  }
+
+  // Whether a kind's rows go to dense rows, and whether they are narrowed to 8 bits.
+  static constexpr bool to_rows(int kind) { return DST == kDense || kind == 0; }
+  static constexpr bool to_8(int kind) { return !to_rows(kind) && DST == kCache8; }
+
+  // Where head h of token i of sequence b goes, p being its place in the cache, and bytes between heads there.
+  template <int KIND>
+  __device__ __forceinline__ char *target(int b, int i, int p, int h) const {
+    if (to_rows(KIND)) return a.out[KIND] + (((long long)b * a.T + i) * a.heads[KIND] + h) * (D * 2);
+    return (KIND == 1 ? c.K : c.V) + kv_block(c, b, p) + kv_row(c, p) + h * c.head_stride;
+  }
+  template <int KIND>
+  __device__ __forceinline__ long long pitch() const {
+    return to_rows(KIND) ? D * 2 : c.head_stride;
+  }
+
+  // Norms and turns the lane's pieces x of head h and stores them, where the head is there
+  // (else they may be anything).
+  template <int KIND>
+  __device__ __forceinline__ void store(char *dst, int h, bool there, const uint4 (&x)[2]) {
+    constexpr bool kNarrow = to_8(KIND);
+    uint4 out[2] = {x[0], x[1]};
+    F2 x0[4], x1[4];  // the two elements of pairs 2q and 2q + 1
+    if (KIND < 2 || kNarrow) {
+      const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
 #pragma unroll
-          for (int o = LPH / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-          const float r = rsqrtf(fmaf(s, 1.f / D, a.eps));
+      for (int q = 0; q < 4; ++q) {
+        const float2 m = widen(PAIRS ? w[2 * q] : w[q], BF), n = widen(PAIRS ? w[2 * q + 1] : w[4 + q], BF);
+        x0[q] = PAIRS ? f2(m.x, n.x) : f2(m.x, m.y);
+        x1[q] = PAIRS ? f2(m.y, n.y) : f2(n.x, n.y);
+      }
+    }
+    if (KIND < 2) {
+      const bool norm = a.norm[KIND < 2 ? KIND : 0] != nullptr;
+      F2 r2;
+      if (norm) {
+        F2 s0 = x0[0] * x0[0], s1 = x1[0] * x1[0];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] *= r * k.w[e];
+        for (int q = 1; q < 4; ++q) {
+          s0 = fma(x0[q], x0[q], s0);
+          s1 = fma(x1[q], x1[q], s1);
         }
-        if (turned) {
+        const float2 y0 = split(s0), y1 = split(s1);
+        float s = (y0.x + y0.y) + (y1.x + y1.y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float &p0 = y[PAIRS ? 2 * e : e], &p1 = y[PAIRS ? 2 * e + 1 : 8 + e];
-            const float z0 = fmaf(p0, k.cs[e].x, -(p1 * k.cs[e].y)), z1 = fmaf(p1, k.cs[e].x, p0 * k.cs[e].y);
-            p0 = z0;
-            p1 = z1;
-          }
+        for (int o = LPH / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        const float r = rsqrtf(fmaf(s, 1.f / D, a.eps));
+        r2 = f2(r, r);
+      }
+      if (turned) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const F2 z0 = fma(x1[q], k.b0[q], x0[q] * k.a0[q]), z1 = fma(x0[q], k.b1[q], x1[q] * k.a1[q]);
+          x0[q] = z0;
+          x1[q] = z1;
         }
+      } else if (norm) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x0[q] = x0[q] * k.a0[q];
+          x1[q] = x1[q] * k.a1[q];
+        }
+      }
+      if (norm) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x0[q] = x0[q] * r2;
+          x1[q] = x1[q] * r2;
+        }
+      }
+    }
+    float y[16];  // in the order of the pieces
+    if (KIND < 2 || kNarrow) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 z0 = split(x0[q]), z1 = split(x1[q]);
+        y[PAIRS ? 4 * q : 2 * q] = z0.x;
+        y[PAIRS ? 4 * q + 2 : 2 * q + 1] = z0.y;
+        y[PAIRS ? 4 * q + 1 : 8 + 2 * q] = z1.x;
+        y[PAIRS ? 4 * q + 3 : 8 + 2 * q + 1] = z1.y;
+      }
+    }
+    if (!there) return;
+    if constexpr (kNarrow) {
+      const Scale s = make_scale((KIND == 1 ? c.k_scale : c.v_scale)[h]);
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = y[e];
+        hi[e] = y[8 + e];
+      }
+      reinterpret_cast<uint2 *>(dst)[pa] = e4m3_of(lo, s);
+      reinterpret_cast<uint2 *>(dst)[pb] = e4m3_of(hi, s);
+    } else {
+      if (KIND < 2) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           out[q] = make_uint4(narrow(y[8 * q], y[8 * q + 1], BF), narrow(y[8 * q + 2], y[8 * q + 3], BF),
                               narrow(y[8 * q + 4], y[8 * q + 5], BF), narrow(y[8 * q + 6], y[8 * q + 7], BF));
       }
-      if (h >= a.heads[kind]) continue;
-      if (dense) {
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out[kind] + (((long long)b * a.T + i) * a.heads[kind] + h) * (D * 2));
-        dst[pa] = out[0];
-        dst[pb] = out[1];
-      } else {
-        char *dst = (kind == 1 ? c.K : c.V) + block + (long long)h * c.head_stride;
-        if constexpr (DST == kCache8) {
-          const Scale s = make_scale((kind == 1 ? c.k_scale : c.v_scale)[h]);
-          float lo[8], hi[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            lo[e] = y[e];
-            hi[e] = y[8 + e];
-          }
-          reinterpret_cast<uint2 *>(dst)[pa] = e4m3_of(lo, s);
-          reinterpret_cast<uint2 *>(dst)[pb] = e4m3_of(hi, s);
-        } else {
-          reinterpret_cast<uint4 *>(dst)[pa] = out[0];
-          reinterpret_cast<uint4 *>(dst)[pb] = out[1];
-        }
-        if (kind == 1 && c.scores && sub == 0) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + p] = 0.f;
-      }
+      reinterpret_cast<uint4 *>(dst)[pa] = out[0];
+      reinterpret_cast<uint4 *>(dst)[pb] = out[1];
     }
   }
 
-  // Kind and first head of a token's task.
-  __device__ __forceinline__ int place(int t, int &h0) const {
+  // Kind and first head of a token's group; the address of its rows.
+  __device__ __forceinline__ int place(int g, int &h0) const {
     int kind = 0;
-    while (t >= a.batches[kind]) t -= a.batches[kind++];
-    h0 = t * U * HPG;
+    if (g >= a.groups[0]) g -= a.groups[0], kind = 1;
+    if (kind == 1 && g >= a.groups[1]) g -= a.groups[1], kind = 2;
+    h0 = g * HPG;
     return kind;
+  }
+  __device__ __forceinline__ const uint4 *source(int kind, int b, int i, int h) const {
+    return reinterpret_cast<const uint4 *>(a.x[kind] + b * a.stride[kind][0] + i * a.stride[kind][1] +
+                                           h * a.stride[kind][2]);
   }
 };
 
-// Tasks of all tokens in order, a.per consecutive ones to a warp.  CACHE: with the lengths
-// that the plan kernel has left in todo.
-template <bool BF, int D, bool PAIRS, int DST, int U>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, const KvDev c, const __grid_constant__ Depths tree) {
-  __shared__ __align__(16) float2 tables[8][D / 2];
+// All tokens: an item is a token, or one of a.parts shares of its groups, and a warp takes every
+// gridDim * 8-th item.  Groups come through the warp's ring in shared memory (cp.async), kStages - 1
+// ahead of the one in work and across items, so that the bytes under way need no
+// registers.  With a cache the lengths are what the plan kernel has left in todo.
+template <bool BF, int D, bool PAIRS, int DST>
+__global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, const KvDev c,
+                                                          const __grid_constant__ Depths tree) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5;
+  using R = Rows<BF, D, PAIRS, DST>;
+  R r(a, c, reinterpret_cast<float2 *>(smem) + warp * (D / 2));
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + 8 * (D / 2) * 8 + warp * (kStages * 1024);
+  // a group's heads lie one behind the other in a stage: copied in order, read by pieces
+  const uint32_t copy_at = ring + r.head * (D * 2) + r.sub * 16;
+  const uint32_t read_a = ring + r.head * (D * 2) + r.pa * 16, read_b = ring + r.head * (D * 2) + r.pb * 16;
   tr_let_next_start();
   tr_wait_for_previous();
-  const int warp = threadIdx.x >> 5;
-  const long long tasks = (long long)a.B * a.T * a.all_batches;
-  long long t = ((long long)blockIdx.x * 8 + warp) * a.per;
-  const long long t1 = min(tasks, t + a.per);
-  if (t >= t1) return;
-  Rows<BF, D, PAIRS, DST, U> r(a, c, tables[warp]);
-  long long row = t / a.all_batches;
-  int at = (int)(t - row * a.all_batches), b = (int)(row / a.T), i = (int)(row - (long long)b * a.T);
-  int angle_of = -1, weights_of = -1, p = 0;
-  bool there = true;
-  Held k;
-  for (; t < t1; ++t) {
+  const unsigned items = (unsigned)a.B * a.T * a.parts, stride = gridDim.x * 8;
+  struct Cursor {
+    unsigned it;
+    int g, b, i, len;  // g: first group
+  };
+  auto enter = [&](Cursor &u) {  // item u.it, or the next one that there is
+    for (; u.it < items; u.it += stride) {
+      const unsigned row = a.parts == 1 ? u.it : u.it / a.parts;
+      u.b = row / a.T;
+      u.i = row - u.b * a.T;
+      u.g = (u.it - row * a.parts) * a.per;
+      if (DST == kDense) return;
+      const int2 todo = a.todo[u.b];
+      u.len = todo.x;
+      if (u.i < todo.y) return;
+    }
+  };
+  Cursor u, ld;
+  u.it = blockIdx.x * 8 + warp;
+  enter(u);
+  ld = u;
+  // the loader's place: `run` groups of one kind from src on, the lane's head among the kind's `left` ones
+  const char *src = nullptr;
+  long long src_step = 0;
+  int run = 0, left = 0;
+  auto find = [&] {
     int h0;
-    const int kind = r.place(at, h0);
-    if (angle_of != i) {
-      if (DST != kDense) {
-        const int2 todo = a.todo[b];
-        there = i < todo.y;
-        p = todo.x + i;
-      }
+    const int kind = r.place(ld.g, h0);
+    src_step = a.stride[kind][2] * R::HPG;
+    src = reinterpret_cast<const char *>(r.source(kind, ld.b, ld.i, h0 + r.head)) + r.sub * 16;
+    left = a.heads[kind] - h0 - r.head;
+    const int end = min(a.all_groups, (ld.g / a.per + 1) * a.per);
+    run = min((a.heads[kind] - h0 + R::HPG - 1) / R::HPG, end - ld.g);
+    ld.g += run;
+    if (ld.g == end) {
+      ld.it += stride;
+      enter(ld);
     }
-    if (there) {
-      uint4 x[U][2];
-      r.load(kind, b, i, h0, x);
-      if (angle_of != i && kind < 2) {
-        r.angles(a.pos ? (long long)a.pos[b] + (tree.nodes ? tree.of[i] : i) : p, k);
-        angle_of = i;
+  };
+  auto issue = [&](uint32_t stage) {
+    if (run == 0 && ld.it < items) find();
+    if (run > 0) {
+      if (left > 0) {
+        copy16(copy_at + stage, src);
+        copy16(copy_at + stage + R::LPH * 16, src + R::LPH * 16);
       }
-      if (weights_of != kind) r.weights(weights_of = kind, k);
-      r.finish(kind, b, i, p, h0, x, k);
+      src += src_step;
+      left -= R::HPG;
+      --run;
     }
-    if (++at == a.all_batches) {
-      at = 0;
-      angle_of = -1;
-      if (++i == a.T) {
-        i = 0;
-        ++b;
-      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) issue(k * 1024);
+  r.frequencies();
+  uint32_t stage = 0;
+  // groups [g0, g1) of a kind, counted from its first
+  auto groups = [&](auto K, int g0, int g1, int p) {
+    constexpr int KIND = decltype(K)::value;
+    if (g0 >= g1) return;
+    if (KIND < 2) r.factors(KIND);
+    int h = g0 * R::HPG + r.head;
+    char *dst = r.template target<KIND>(u.b, u.i, p, h);
+    const long long step = r.template pitch<KIND>() * R::HPG;
+    if (!R::to_rows(KIND) && KIND == 1 && c.scores)  // of all the groups' heads
+      for (int k = g0 * R::HPG + r.lane; k < min(a.heads[1], g1 * R::HPG); k += 32)
+        c.scores[((long long)u.b * c.Hkv + k) * c.scores_ld + p] = 0.f;
+    for (int g = g0; g < g1; ++g) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // every lane's copies are there, and the stage before this one is free
+      const uint4 x[2] = {lds16(read_a + stage), lds16(read_b + stage)};
+      issue((stage + (kStages - 1) * 1024) % (kStages * 1024));
+      r.template store<KIND>(dst, h, h < a.heads[KIND], x);
+      dst += step;
+      h += R::HPG;
+      stage = (stage + 1024) % (kStages * 1024);
     }
+  };
+  for (; u.it < items; u.it += stride, enter(u)) {
+    const int g0 = u.g, g1 = min(a.all_groups, g0 + a.per), p = u.len + u.i;
+    const int k1 = a.groups[0], k2 = k1 + a.groups[1];
+    if (g0 < k2) r.angles(a.pos ? (long long)a.pos[u.b] + (tree.nodes ? tree.of[u.i] : u.i) : p);
+    groups(std::integral_constant<int, 0>{}, g0, min(g1, k1), p);
+    groups(std::integral_constant<int, 1>{}, max(g0, k1) - k1, min(g1, k2) - k1, p);
+    groups(std::integral_constant<int, 2>{}, max(g0, k2) - k2, g1 - k2, p);
   }
 }
 
 // Few rows: a cluster takes a sequence, checks it, copies its rows and advances its length,
-// so that no kernel is needed before this one.
-template <bool BF, int D, bool PAIRS, int DST, int U>
-__global__ void __launch_bounds__(kMaxWarps * 32) append_rope_kernel(const RopeArgs a, const KvDev c) {
+// so that no kernel is needed before this one.  A task is the next U groups of a token, a warp
+// takes every (gridDim * warps)-th.
+template <bool BF, int D, bool PAIRS, int DST>
+__global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const RopeArgs a, const KvDev c) {
+  constexpr int U = kShort;
   __shared__ __align__(16) float2 tables[kMaxWarps][D / 2];
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  Rows<BF, D, PAIRS, DST> r(a, c, tables[warp]);
   tr_let_next_start();
   tr_wait_for_previous();
-  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int b = blockIdx.y, Lb = c.L[b], n0 = a.count ? a.count[b] : a.T;
-  const int step = gridDim.x * warps;
-  Rows<BF, D, PAIRS, DST, U> r(a, c, tables[warp]);
-  int t = blockIdx.x * warps + warp, i = t / a.all_batches, at = t - i * a.all_batches, h0;
-  int kind = r.place(at, h0);
-  // the first task's rows are requested before the checks (they are read even if these fail)
+  const int step = gridDim.x * warps, tasks = (a.all_groups + U - 1) / U;
   uint4 x[U][2];
-  if (i < a.T) r.load(kind, b, i, h0, x);
+  int i, g;
+  auto load = [&](int t) {
+    i = t / tasks;
+    g = (t - i * tasks) * U;
+    if (i >= a.T) return;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      int h0;
+      const int kind = r.place(g + k, h0);
+      x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+      if (g + k >= a.all_groups || h0 + r.head >= a.heads[kind]) continue;
+      const uint4 *src = r.source(kind, b, i, h0 + r.head);
+      x[k][0] = src[r.pa];
+      x[k][1] = src[r.pb];
+    }
+  };
+  int t = blockIdx.x * warps + warp;
+  load(t);  // before the checks (the rows are read even if these fail)
+  r.frequencies();
   const long long base = a.pos ? (long long)a.pos[b] : Lb;
   const int n = append_rows(c, b, Lb, n0, a.T, a.status);
-  int angle_of = -1, weights_of = -1;
-  Held k;
+  int angle_of = -1;
   while (i < n) {
-    if (angle_of != i && kind < 2) r.angles(base + (angle_of = i), k);
-    if (weights_of != kind) r.weights(weights_of = kind, k);
-    r.finish(kind, b, i, Lb + i, h0, x, k);
-    t += step;
-    i = t / a.all_batches;
-    at = t - i * a.all_batches;
-    kind = r.place(at, h0);
-    if (i < n) r.load(kind, b, i, h0, x);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      int h0;
+      const int kind = r.place(g + k, h0);
+      if (g + k >= a.all_groups) break;
+      if (kind < 2) {
+        if (angle_of != i) r.angles(base + (angle_of = i));
+        r.factors(kind);
+      }
+      const int h = h0 + r.head;
+      const bool there = h < a.heads[kind];
+      if (kind == 0) {
+        r.template store<0>(r.template target<0>(b, i, Lb + i, h), h, there, x[k]);
+      } else if (kind == 1) {
+        r.template store<1>(r.template target<1>(b, i, Lb + i, h), h, there, x[k]);
+        if (c.scores && r.sub == 0 && there) c.scores[((long long)b * c.Hkv + h) * c.scores_ld + Lb + i] = 0.f;
+      } else {
+        r.template store<2>(r.template target<2>(b, i, Lb + i, h), h, there, x[k]);
+      }
+    }
+    load(t += step);
   }
   if (gridDim.x > 1) {  // the sequence's other CTAs have read the old length
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && n > 0) c.L[b] = Lb + n;
+}
+
+void count_groups(RopeArgs *a, int d) {
+  const int heads = 32 / (d / 16);
+  a->all_groups = 0;
+  for (int i = 0; i < 3; ++i) a->all_groups += a->groups[i] = (a->heads[i] + heads - 1) / heads;
 }
 
 // Checks the rows and the rotation on the host and fills what the kernel needs of them.
@@ -350,49 +536,44 @@ int fill(const tr_qkv *x, const tr_rope *r, const int32_t *pos, RopeArgs *out) {
   a.norm[0] = r->q_norm;
   a.norm[1] = r->k_norm;
   a.eps = r->eps;
+  count_groups(&a, r->d);
   a.pos = pos;
   *out = a;
   return TR_OK;
 }
 
-// Groups of a task in a large call, and in a small one.
-constexpr int kWide = 4, kShort = 2;
-
-// Tasks of a token; returns their number.
-int plan(RopeArgs *a, int d, int U) {
-  const int heads = 32 / (d / 16) * U;
-  a->all_batches = 0;
-  for (int i = 0; i < 3; ++i) a->all_batches += a->batches[i] = (a->heads[i] + heads - 1) / heads;
-  return a->all_batches;
-}
-
 template <bool BF, int D, bool PAIRS, int DST>
 int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
-  auto go = [&](auto kernel, int U) {
-    const long long tasks = (long long)a.B * a.T * plan(&a, D, U);
-    a.per = tasks >= 64LL * tr_sm_count() ? a.all_batches : 1;
-    const long long ctas = (tasks + 8LL * a.per - 1) / (8LL * a.per);
-    if (ctas >= (1LL << 31)) return (int)TR_E_UNSUPPORTED;
-    return tr_launch_next(kernel, {dim3((unsigned)ctas), 256}, s, a, c, tree);
-  };
-  const long long wide = (long long)a.B * a.T * plan(&a, D, kWide);
-  if (wide >= 16LL * tr_sm_count()) return go(rope_kernel<BF, D, PAIRS, DST, kWide>, kWide);
-  return go(rope_kernel<BF, D, PAIRS, DST, kShort>, kShort);
+  constexpr int kSmem = 8 * (kStages * 1024 + D / 2 * 8);
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  TR_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    TR_TRY_CUDA(cudaFuncSetAttribute(rope_kernel<BF, D, PAIRS, DST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
+  const long long rows = (long long)a.B * a.T, most = (long long)kCtas * tr_sm_count();
+  // shares of a token, where there are too few to go round
+  a.parts = (int)std::max<long long>(1, std::min<long long>(a.all_groups, most * 8 / rows));
+  a.per = (a.all_groups + a.parts - 1) / a.parts;
+  a.parts = (a.all_groups + a.per - 1) / a.per;
+  const long long ctas = (rows * a.parts + 7) / 8;
+  return tr_launch_next(rope_kernel<BF, D, PAIRS, DST>, {dim3((unsigned)std::min(ctas, most)), 256, kSmem}, s, a, c, tree);
 }
 
 // One kernel for a sequence's rows up to this many tasks of a warp.
-constexpr int kRounds = 4, kMostCluster = 8;
+constexpr int kRounds = 8, kMostCluster = 8;
 
 template <bool BF, int D, bool PAIRS, int DST>
 int launch_append(RopeArgs a, const KvDev &c, const int32_t *count, void *ws, cudaStream_t s) {
-  const long long tasks = (long long)a.T * plan(&a, D, kShort);
+  const long long tasks = (long long)a.T * ((a.all_groups + kShort - 1) / kShort);
   if (tasks <= (long long)kMostCluster * kMaxWarps * kRounds) {
     int cs = 1;
     while (cs < kMostCluster && tasks > (long long)cs * kMaxWarps) cs *= 2;
     const int warps = (int)std::min<long long>(kMaxWarps, (tasks + cs - 1) / cs);
     a.count = count;
     a.status = tr_status_dev();
-    return tr_launch_next(append_rope_kernel<BF, D, PAIRS, DST, kShort>, {dim3(cs, a.B), warps * 32, 0, cs}, s, a, c);
+    return tr_launch_next(append_rope_kernel<BF, D, PAIRS, DST>, {dim3(cs, a.B), warps * 32, 0, cs}, s, a, c);
   }
   a.todo = (const int2 *)ws;
   const int rc = kv_append_plan(c, a.T, count, (int2 *)ws, s);
