@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const Ro
     load(t += step);
   }
   if (gridDim.x > 1) {  // the sequence's other CTAs have read the old length
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && n > 0) c.L[b] = Lb + n;
 }

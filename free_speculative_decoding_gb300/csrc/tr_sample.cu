@@ -5,15 +5,26 @@
 // 2^-S, so their sums are exact and do not depend on the order: top-p's edge is found
 // from sums over any grouping, and equal calls give equal bits.  A token is left when its key
 // (the order of its logit) is above the row's edge, or at it with an ID up to the edge's.
+//
+// A cluster of up to eight CTAs holds a row in shared memory, which is read from DRAM once.
+// An edge is found in two steps.  A histogram over a linear scale of the logits
+// (counts for top-k; for top-p weights of 16 bits, whose error is bounded) gives the bins
+// that the edge must lie in; their tokens, few hundred at most, are gathered in the first
+// CTA, sorted, and the edge read off exact sums.  Where they are more than the list holds
+// (long runs of equal logits) the key is narrowed down by eight bits a pass instead.
+// A last pass sums the weights that are left over ascending IDs and finds the uniform's place.
 #include <cfloat>
 #include <cmath>
+
+#include <atomic>
+
+#include <cooperative_groups.h>
 
 #include "tr_internal.cuh"
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
 struct SampleArgs {
@@ -24,65 +35,59 @@ struct SampleArgs {
   const int32_t *top_k;
   int32_t *token;
   float *logprob;
+  int granules;  // of a CTA's slice
 };
 
 // The order of a logit; NaN and -inf (never drawn) are 0x007FFFFF, below every other.
 constexpr uint32_t kNever = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float x) { return x == x ? tr_ord(x) : kNever; }
 
-// Weights of a row.  The exponent (m - x) log2(e) / T is carried in two fp32 numbers, its
-// fraction's power of two comes from a table of 2^(-j / 64) and a polynomial in the rest.
+// Weights of a row: 2^S 2^(x c - K), c = log2(e) / T and K the whole number at or above m c, rounded
+// down.  x c is split into a multiple of 1 / 64 (adding and taking away 1.5 2^17 rounds to it) and a
+// rest whose error is below 2^-31; the multiple's power of two comes from a table, the rest's from a
+// polynomial.  Where |m c| passes 2^15, x is taken relative to m first: what has weight then
+// lies so near to m that the difference is exact.
 struct Weight {
-  float m, c_hi, c_lo;
-  int S;
-  const float2 *table;  // 2^(-j / 64): as a float, and (as bits) 2^31 times it
-  // 2^S w, rounded down
+  float m, base, c_hi, c_lo;
+  int K, S;
+  const float2 *table;  // 2^(j / 64): 2^31 times it as a float, and as an integer (in its bits)
+  __device__ __forceinline__ void set(float m_, float temp, int S_, const float2 *t) {
+    const double c = 1.4426950408889634 / (double)temp;
+    m = m_;
+    S = S_;
+    table = t;
+    c_hi = (float)c;
+    c_lo = (float)(c - (double)c_hi);
+    const bool far = !(fabs((double)m * c) < 32768.0);  // infinite too
+    base = far ? m : 0.f;
+    K = far ? 0 : (int)ceil((double)m * c);
+  }
   __device__ __forceinline__ u64 operator()(float x) const {
-    if (x == m) return 1ull << S;
-    // d = m - x exactly, as d + e
-    const float d = m - x, z = d - m, e = (m - (d - z)) - (x + z);
-    const float t = d * c_hi;
-    if (!(t < 63.f)) return 0;  // below every S, or not a number: x is -inf
-    const float lo = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);
-    const float n = rintf(t * 64.f);
-    const float r = fmaf(n, -1.f / 64.f, t) + lo;  // |r| <= 1 / 128 and a little
-    // 2^-r - 1
-    float y = fmaf(r, 9.618129107628477e-3f, -5.550410866482158e-2f);  // ln2^4 / 24, -ln2^3 / 6
-    y = fmaf(r, y, 2.402265069591007e-1f);
-    y = fmaf(r, y, -6.931471805599453e-1f);
-    y *= r;
-    const int j = (int)n;
-    const float2 p = table[j & 63];
-    const unsigned mant = __float_as_uint(p.y) + (unsigned)__float2int_rn(y * p.x * 0x1p31f);
-    const int shift = (j >> 6) + 31 - S;  // the weight is mant 2^-31 2^-(j >> 6)
-    return shift >= 0 ? (u64)mant >> min(shift, 63) : (u64)mant << -shift;
+    const float t = (m - x) * c_hi;
+    if (!(t < 62.f)) return x == m ? 1ull << S : 0;  // below every S, or not a number: infinite logits
+    const float y = x - base, p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
+    const float r = fmaf(y, c_lo, fmaf(y, c_hi, -q));  // |r| <= 1 / 128 and a little
+    float e = fmaf(r, 5.550410866482158e-2f, 2.402265069591007e-1f);  // 2^r - 1: ln2^3 / 6, ln2^2 / 2, ln2
+    e = fmaf(r, e, 6.931471805599453e-1f);
+    e *= r;
+    const int n = __float_as_int(p) - 0x48400000;  // 64 q
+    const float2 f = table[n & 63];
+    const unsigned mant = __float_as_uint(f.y) + (unsigned)__float2int_rn(e * f.x);
+    return ((u64)mant << (S - 31)) >> (K - (n >> 6));
   }
 };
 
-struct Smem {
-  float2 table[64];
-  u64 hist[256];
-  u64 wsum[kWarps];
-  u64 best;
-  u64 base;      // of the keys above
-  uint32_t prefix;
-  int id;
-};
+__device__ __forceinline__ void fill_table(float2 *table) {
+  if (threadIdx.x < 64) {
+    const double p = exp2((double)threadIdx.x / 64.0) * 0x1p31;
+    table[threadIdx.x] = make_float2((float)p, __uint_as_float((unsigned)__double2ull_rn(p)));
+  }
+}
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
-}
-// Sum over the block, in every thread (two barriers).
-__device__ __forceinline__ u64 block_sum(u64 v, u64 *wsum) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
-  for (int i = 0; i < kWarps; ++i) s += wsum[i];
-  __syncthreads();
-  return s;
 }
 
 // floor(f * n) and whether it is exact, for a float f in [0, 1) and n < 2^63.
@@ -104,11 +109,13 @@ __device__ __forceinline__ u64 part_of(float f, u64 n, bool *exact) {
   *exact = (lo << (64 - shift)) == 0;
   return (lo >> shift) | (hi << (64 - shift));
 }
-
-// The range of IDs of a warp: consecutive ones.
-struct Range {
-  int lo, hi;
-};
+// The sum that top-p asks for: the least whole number that is at least p times `all`, at least 1.
+__device__ __forceinline__ u64 share_of(float p, u64 all) {
+  bool exact;
+  u64 n = part_of(p, all, &exact);
+  n += !exact;
+  return n > 0 ? n : 1;
+}
 
 template <typename T>
 __device__ __forceinline__ float get(const T *x, int v) {
@@ -119,10 +126,681 @@ __device__ __forceinline__ float get(const __nv_bfloat16 *x, int v) {
   return __bfloat162float(x[v]);
 }
 
+// Of the tokens with the edge's key those with an ID up to the edge's are left, and all above.
+struct Edge {
+  uint32_t key;
+  int id;
+  __device__ __forceinline__ bool leaves(uint32_t k, int v) const { return k > key || (k == key && v <= id); }
+};
+
+// min_p's edge: the least logit whose weight is at least min_p of the largest one's.
+__device__ __forceinline__ Edge with_min_p(Edge e, float mp, float m, float temp) {
+  if (mp > 0.f && temp < INFINITY) {  // with an infinite temperature all weights are 1
+    const uint32_t k = key_of(__double2float_ru((double)m + (double)temp * log(fmin((double)mp, 1.0))));
+    if (k > e.key) e = {k, INT_MAX};
+  }
+  return e;
+}
+
+__device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f), 1.f - 0x1p-24f); }  // NaN: 0
+
+// ---------------------------------------------------------------------------
+// rows that a cluster's shared memory holds
+// ---------------------------------------------------------------------------
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;       // 64 to a power of two, where they are weighted
+constexpr int kList = 1024;
+
+struct Smem {
+  float2 table[64];
+  u64 box[2][kMaxCluster][2];     // what the cluster's CTAs have told this one, of two exchanges
+  u64 wsum[kWarps];
+  unsigned listed;                // tokens that were to go to the list
+  unsigned found[3];
+  int id;
+  u64 cum;
+  union {
+    unsigned hist[kBins];
+    u64 wide[256];
+    u64 list[kList];              // key << 32 | ~ID
+  };
+};
+
+// Granules of a warp, of a slice's.
+__device__ __forceinline__ int warp_granules(int granules) { return (granules + kWarps * 32 - 1) / (kWarps * 32) * 32; }
+
+template <typename T>
+struct Row {
+  static constexpr int VEC = 16 / sizeof(T);
+  const SampleArgs &a;
+  Smem &s;
+  const uint4 *data;   // the CTA's slice, 16-byte granules; what is no token is -inf
+  int CS, rank, parity = 0;
+  int warp, lane;
+  int id0;             // ID of the slice's first element (below 0: no token)
+  int g0, g1;          // the warp's granules
+  Weight w;
+
+  __device__ __forceinline__ Row(const SampleArgs &a_, Smem &s_) : a(a_), s(s_) {
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+  }
+
+  __device__ __forceinline__ void sync() {
+    if (CS == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
+  }
+
+  // f(x, ID) for every element of the warp's granules, 32 * VEC consecutive ones at a time; all lanes
+  // call f alike (with -inf behind the last granule).
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int g = g0 + lane; g - lane < g1; g += 32) {
+      constexpr uint32_t kNone = VEC == 4 ? 0xFF800000u : 0xFF80FF80u;
+      const uint4 v = g < g1 ? data[g] : make_uint4(kNone, kNone, kNone, kNone);
+      const int id = id0 + g * VEC;
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      if constexpr (VEC == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(__uint_as_float(u[e]), id + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f(__uint_as_float(u[e] << 16), id + 2 * e);
+          f(__uint_as_float(u[e] & 0xFFFF0000u), id + 2 * e + 1);
+        }
+      }
+    }
+  }
+
+  // Sum of v over the CTA, in every thread (two barriers).
+  __device__ __forceinline__ u64 block_sum(u64 v) {
+    v = warp_sum(v);
+    if (lane == 0) s.wsum[warp] = v;
+    __syncthreads();
+    u64 r = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) r += s.wsum[i];
+    __syncthreads();
+    return r;
+  }
+
+  // Tells every CTA of the cluster two numbers of this one (the same in all threads) and waits for
+  // theirs: heard(r, i).
+  __device__ __forceinline__ void tell(u64 x, u64 y) {
+    if ((int)threadIdx.x < CS) {
+      u64 *to = &s.box[parity][rank][0];
+      if (CS > 1) to = cg::this_cluster().map_shared_rank(to, threadIdx.x);
+      to[0] = x;
+      to[1] = y;
+    }
+    sync();
+    parity ^= 1;
+  }
+  __device__ __forceinline__ u64 heard(int r, int i) const { return s.box[parity ^ 1][r][i]; }
+
+  // Inclusive sum over the CTA's threads (two barriers).
+  __device__ __forceinline__ u64 block_scan(u64 v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) s.wsum[warp] = v;
+    __syncthreads();
+    u64 before = 0;
+    for (int i = 0; i < warp; ++i) before += s.wsum[i];
+    __syncthreads();
+    return before + v;
+  }
+
+  // The lowest ID at which the running sum of amount(x, ID) over ascending IDs passes `target`, and
+  // the whole sum before it is known: target_of(sum).  In the one CTA that holds it; -1 in the others.
+  template <typename F, typename G>
+  __device__ __forceinline__ int first_past(F amount, G target_of, u64 *all) {
+    u64 mine = 0;
+    each([&](float x, int v) { mine += amount(x, v); });
+    mine = warp_sum(mine);
+    if (lane == 0) s.wsum[warp] = mine;
+    __syncthreads();
+    u64 cta = 0, before = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) cta += s.wsum[i];
+    tell(cta, 0);
+    for (int r = 0; r < CS; ++r) {
+      if (r < rank) before += heard(r, 0);
+      sum += heard(r, 0);
+    }
+    *all = sum;
+    const u64 target = target_of(sum);
+    if (!(before <= target && before + cta > target)) return -1;
+    // the warp's range that holds it, then an eighth of that range by each warp
+    int q = 0;
+    while (before + s.wsum[q] <= target) before += s.wsum[q++];
+    const int seg = warp_granules(a.granules), lo = min(a.granules, q * seg), hi = min(a.granules, lo + seg);
+    const int part = ((hi - lo + kWarps - 1) / kWarps + 31) & ~31;
+    const int p0 = min(hi, lo + warp * part), p1 = min(hi, p0 + part);
+    const int keep0 = g0, keep1 = g1;
+    g0 = p0;
+    g1 = p1;
+    mine = 0;
+    each([&](float x, int v) { mine += amount(x, v); });
+    mine = warp_sum(mine);
+    __syncthreads();
+    if (lane == 0) s.wsum[warp] = mine;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) before += s.wsum[i];
+    if (before <= target && before + mine > target) {  // one warp
+      for (int g = p0; g < p1; g += 32) {
+        g0 = g;
+        g1 = min(p1, g + 32);
+        u64 c = 0;
+        each([&](float x, int v) { c += amount(x, v); });
+        const u64 own = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 y = __shfl_up_sync(~0u, c, o);
+          if (lane >= o) c += y;
+        }
+        const unsigned past = __ballot_sync(~0u, before + c > target);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            u64 run = before + c - own;
+            int id = -1;
+            each([&](float x, int v) {
+              run += amount(x, v);
+              if (id < 0 && run > target) id = v;
+            });
+            s.id = id;
+          }
+          break;
+        }
+        before += __shfl_sync(~0u, c, 31);
+      }
+    }
+    g0 = keep0;
+    g1 = keep1;
+    __syncthreads();
+    return s.id;
+  }
+
+  // A token's place on the histogram's scale: falling logits, rising bins.
+  static __device__ __forceinline__ int bin_of(float m, float x, float scale) {
+    return (int)fminf((m - x) * scale, (float)(kBins - 1));
+  }
+
+  // Adds up the CTAs' histograms; the first bins at which the running sum reaches `lo_of(all)` and
+  // `hi_of(all)` (kBins where it does not), the sum before the first of them, and its own entry in 32 bits.
+  template <typename F, typename G, typename H>
+  __device__ __forceinline__ void crossing(F value, G lo_of, H hi_of, int *b0, int *b1, u64 *base, unsigned *own) {
+    sync();  // the histograms are whole
+    const int mine = kBins / CS, per = mine / kThreads;  // bins of a CTA, of a thread
+    u64 v[kBins / kThreads], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kBins / kThreads; ++j) {
+      if (j >= per) break;
+      const int b = rank * mine + threadIdx.x * per + j;
+      u64 n = 0;
+      for (int r = 0; r < CS; ++r) n += CS > 1 ? *cg::this_cluster().map_shared_rank(&s.hist[b], r) : s.hist[b];
+      v[j] = value(b, n);
+      sum += v[j];
+    }
+    const u64 incl = block_scan(sum);
+    if (threadIdx.x == kThreads - 1) s.cum = incl;
+    if (threadIdx.x < 2) s.found[threadIdx.x] = kBins;
+    __syncthreads();
+    tell(s.cum, 0);
+    u64 before = 0, all = 0;
+    for (int r = 0; r < CS; ++r) {
+      if (r < rank) before += heard(r, 0);
+      all += heard(r, 0);
+    }
+    u64 run = before + incl - sum;
+    const u64 lo = lo_of(all), hi = hi_of(all);
+#pragma unroll
+    for (int j = 0; j < kBins / kThreads; ++j) {
+      if (j >= per) break;
+      const unsigned b = rank * mine + threadIdx.x * per + j;
+      if (run < lo && run + v[j] >= lo) {
+        s.found[0] = b;
+        s.found[2] = (unsigned)v[j];
+        s.cum = run;
+      }
+      if (run < hi && run + v[j] >= hi) s.found[1] = b;
+      run += v[j];
+    }
+    __syncthreads();
+    tell((u64)s.found[2] << 32 | s.found[1] << 16 | s.found[0], s.cum);
+    *b0 = *b1 = kBins;
+    *base = 0;
+    *own = 0;
+    for (int r = 0; r < CS; ++r) {
+      const u64 x = heard(r, 0);
+      if ((x & 0xFFFF) < kBins) {
+        *b0 = (int)(x & 0xFFFF);
+        *own = (unsigned)(x >> 32);
+        *base = heard(r, 1);
+      }
+      if ((x >> 16 & 0xFFFF) < kBins) *b1 = (int)(x >> 16 & 0xFFFF);
+    }
+  }
+
+  // Clears the histogram (list) of every CTA, before anybody adds to it.
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
+    if (threadIdx.x == 0) s.listed = 0;
+    __syncthreads();
+  }
+
+  // Puts tokens on the first CTA's list; all lanes of the warp call it.
+  __device__ __forceinline__ void gather(bool take, float x, int v) {
+    const unsigned m = __ballot_sync(~0u, take);
+    if (m == 0) return;
+    Smem *first = CS > 1 ? cg::this_cluster().map_shared_rank(&s, 0) : &s;
+    unsigned at = 0;
+    if (lane == 0) at = atomicAdd(&first->listed, __popc(m));
+    at = __shfl_sync(~0u, at, 0) + __popc(m & ((1u << lane) - 1));
+    if (take && at < kList) first->list[at] = (u64)key_of(x) << 32 | (0xFFFFFFFFu - (unsigned)v);
+  }
+
+  // Sorts the list's n <= kList entries, the largest first.
+  __device__ __forceinline__ void sort_list(int n) {
+    int N = 32;
+    while (N < n) N *= 2;
+    for (int i = n + threadIdx.x; i < N; i += kThreads) s.list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= N; k *= 2)
+      for (int j = k / 2; j; j /= 2) {
+        for (int i = threadIdx.x; i < N / 2; i += kThreads) {
+          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+          const u64 x = s.list[lo], y = s.list[hi];
+          if ((x < y) == ((lo & k) == 0)) {
+            s.list[lo] = y;
+            s.list[hi] = x;
+          }
+        }
+        __syncthreads();
+      }
+  }
+
+  // In the first CTA: the place in the sorted list of n entries at which the running sum of the weights,
+  // from `base` on, reaches target_of(base + their sum); n where it does not.
+  template <typename G>
+  __device__ __forceinline__ int place(int n, u64 base, G target_of) {
+    u64 v[kList / kThreads], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      const int i = threadIdx.x * (kList / kThreads) + j;
+      v[j] = i < n ? w(tr_unord((uint32_t)(s.list[i] >> 32))) : 0;
+      sum += v[j];
+    }
+    const u64 incl = block_scan(sum);
+    if (threadIdx.x == kThreads - 1) s.cum = incl;
+    if (threadIdx.x == 0) s.id = n;
+    __syncthreads();
+    const u64 target = target_of(base + s.cum);
+    u64 run = base + incl - sum;
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      if (run < target && run + v[j] >= target) s.id = threadIdx.x * (kList / kThreads) + j;
+      run += v[j];
+    }
+    __syncthreads();
+    const int at = s.id;
+    __syncthreads();
+    return at;
+  }
+
+  __device__ __forceinline__ Edge edge_at(int i) const {
+    const u64 e = s.list[i];
+    return {(uint32_t)(e >> 32), (int)(0xFFFFFFFFu - (uint32_t)e)};
+  }
+
+  // The edge that leaves, of the tokens that `old` leaves, the first ones in falling order whose
+  // amounts sum to at least `target`: the key is narrowed down by eight bits a pass, then the
+  // lowest IDs among equal keys.
+  template <typename F>
+  __device__ __forceinline__ Edge narrow_down(u64 target, Edge old, F amount) {
+    uint32_t prefix = 0;
+    u64 base = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      sync();  // the first CTA has read the last pass's sums
+      for (int i = threadIdx.x; i < 256; i += kThreads) s.wide[i] = 0;
+      __syncthreads();
+      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      each([&](float x, int v) {
+        const uint32_t k = key_of(x);
+        const u64 n = (k & mask) == prefix && k > kNever && old.leaves(k, v) ? amount(x) : 0;
+        const unsigned m = __ballot_sync(~0u, n != 0), b = (k >> shift) & 255;
+        if (m == 0) return;
+        int same;  // a warp whose tokens all share a bin adds once
+        __match_all_sync(~0u, b, &same);
+        if (same) {
+          const u64 t = warp_sum(n);
+          if (lane == 0) atomicAdd(&s.wide[b], t);
+        } else if (n) {
+          atomicAdd(&s.wide[b], n);
+        }
+      });
+      sync();
+      if (rank == 0) {
+        // thread t has the bin that is t-th from above
+        const int b = 255 - (int)threadIdx.x;
+        u64 n = 0;
+        for (int r = 0; r < CS; ++r) n += CS > 1 ? *cg::this_cluster().map_shared_rank(&s.wide[b], r) : s.wide[b];
+        const u64 incl = base + block_scan(n);
+        if (incl >= target && incl - n < target) {
+          s.found[0] = b;
+          s.cum = incl - n;
+        }
+        __syncthreads();
+      }
+      tell(s.found[0], s.cum);
+      prefix |= (uint32_t)(heard(0, 0) & 255) << shift;
+      base = heard(0, 1);
+    }
+    const u64 each_ = amount(tr_unord(prefix));
+    const u64 take = each_ ? (target - base + each_ - 1) / each_ : 0;
+    u64 n;
+    const int id = first_past([&](float x, int v) -> u64 { return key_of(x) == prefix && old.leaves(prefix, v); },
+                              [&](u64) -> u64 { return take - 1; }, &n);
+    tell(id >= 0, (u64)(unsigned)id);
+    Edge e = {prefix, INT_MAX};
+    for (int r = 0; r < CS; ++r)
+      if (heard(r, 0)) e.id = (int)(unsigned)heard(r, 1);
+    return e;
+  }
+
+  __device__ __forceinline__ Edge hear_edge(bool *ok) const {
+    const u64 x = heard(0, 0);
+    *ok = heard(0, 1) & 1;
+    return {(uint32_t)(x >> 32), (int)(uint32_t)x};
+  }
+
+  // top-k, and top-p with it where all of the k tokens fit the list (*p_done).
+  // lowest: the least of the threads' maxima; at least CS * kThreads tokens lie at or above it.
+  __device__ __forceinline__ Edge top_k(int k, float p, float lowest, bool *p_done) {
+    const Edge none = {kNever, -1};
+    *p_done = false;
+    // bins over the logits that matter
+    float least = lowest;
+    const bool sure = k <= CS * kThreads && lowest > -INFINITY;
+    if (!sure) {  // over all logits
+      least = INFINITY;
+      each([&](float x, int) { least = x > -INFINITY ? fminf(least, x) : least; });
+#pragma unroll
+      for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+      if (lane == 0) s.wsum[warp] = __float_as_uint(least);
+      __syncthreads();
+      for (int i = 0; i < kWarps; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
+      tell(__float_as_uint(least), 0);
+      for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
+    }
+    const float m = w.m, span = m - least;
+    if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
+    const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
+    clear();
+    each([&](float x, int) {
+      if (x >= least) atomicAdd(&s.hist[bin_of(m, x, scale)], 1u);
+    });
+    int b0, b1;
+    u64 above;
+    unsigned at_edge;
+    crossing([](int, u64 n) { return n; }, [&](u64) -> u64 { return (u64)k; }, [&](u64) -> u64 { return (u64)k; }, &b0, &b1,
+             &above, &at_edge);
+    if (b0 >= kBins) return none;  // fewer than k tokens: all are left
+    const bool whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
+    each([&](float x, int v) {
+      const int b = x >= least ? bin_of(m, x, scale) : kBins;
+      gather(whole ? b <= b0 : b == b0, x, v);
+    });
+    sync();
+    if (rank == 0) {
+      const int n = (int)s.listed, need = whole ? k : k - (int)above;
+      bool ok = n <= kList;
+      Edge e = none;
+      if (ok) {
+        sort_list(n);
+        e = edge_at(need - 1);
+        if (whole && p < 1.f) {
+          const int at = place(k, 0, [&](u64 all) { return share_of(p, all); });
+          e = edge_at(min(at, k - 1));
+        }
+      }
+      tell((u64)e.key << 32 | (uint32_t)e.id, ok);
+    } else {
+      tell(0, 0);
+    }
+    bool ok;
+    const Edge e = hear_edge(&ok);
+    if (!ok) return narrow_down_k(k);
+    *p_done = whole;
+    return e;
+  }
+  __device__ __noinline__ Edge narrow_down_k(int k) {
+    u64 n = 0;
+    each([&](float x, int) { n += x > -INFINITY; });
+    n = block_sum(n);
+    tell(n, 0);
+    n = 0;
+    for (int r = 0; r < CS; ++r) n += heard(r, 0);
+    const Edge none = {kNever, -1};
+    return n <= (u64)k ? none : narrow_down((u64)k, none, [](float) -> u64 { return 1; });
+  }
+
+  // top-p among the tokens that `old` leaves.
+  __device__ __forceinline__ Edge top_p(float p, Edge old) {
+    // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
+    // (2^16 of them: the sum of a slice stays below 2^32).  A token beyond the last bin but one has a weight below
+    // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
+    const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
+    clear();
+    each([&](float x, int v) {
+      const float t = (m - x) * scale;
+      if (!(t < (float)(kBins - 1)) || !old.leaves(key_of(x), v)) return;
+      const int b = (int)t;
+      float f;  // within its power of two
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(((float)(b & ~63) - t) * (1.f / 64.f)));
+      atomicAdd(&s.hist[b], (unsigned)(f * 65535.f));
+    });
+    int b0, b1;
+    u64 base;
+    unsigned own;
+    // in units of 2^-43
+    crossing([](int b, u64 n) { return (n << 27) >> (b >> 6); },
+             [&](u64 all) -> u64 { return share_of(p, all - (all >> 14)); },
+             [&](u64 all) -> u64 { return share_of(p, all + (all >> 14) + ((u64)a.V << 12)); }, &b0, &b1, &base, &own);
+    // the exact sums, of all and of what lies above the bins that hold the edge
+    u64 all = 0, above = 0;
+    each([&](float x, int v) {
+      const float t = (m - x) * scale;
+      const bool left = x > -INFINITY && old.leaves(key_of(x), v);
+      const int b = (int)fminf(t, (float)kBins);
+      const u64 q = left ? w(x) : 0;
+      all += q;
+      above += b < b0 ? q : 0;
+      gather(left && b >= b0 && b <= b1, x, v);
+    });
+    all = block_sum(all);
+    above = block_sum(above);
+    tell(all, above);
+    all = above = 0;
+    for (int r = 0; r < CS; ++r) {
+      all += heard(r, 0);
+      above += heard(r, 1);
+    }
+    const u64 target = share_of(p, all);
+    if (rank == 0) {
+      const int n = (int)s.listed;
+      Edge e = {kNever, -1};
+      bool ok = n <= kList && above < target;
+      if (ok) {
+        sort_list(n);
+        const int at = place(n, above, [&](u64) { return target; });
+        ok = at < n;
+        if (ok) e = edge_at(at);
+      }
+      tell((u64)e.key << 32 | (uint32_t)e.id, ok);
+    } else {
+      tell(0, 0);
+    }
+    bool ok;
+    const Edge e = hear_edge(&ok);
+    return ok ? e : narrow_down_p(target, old);
+  }
+  __device__ __noinline__ Edge narrow_down_p(u64 target, Edge old) { return narrow_down(target, old, w); }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  Smem &s = *reinterpret_cast<Smem *>(smem);
+  Row<T> r(a, s);
+  constexpr int VEC = Row<T>::VEC;
+  const long long row = blockIdx.x / CS;
+  r.CS = CS;
+  r.rank = blockIdx.x - (int)row * CS;
+  uint4 *const data = reinterpret_cast<uint4 *>(smem + sizeof(Smem));
+  r.data = data;
+  const int seg = warp_granules(a.granules);
+  r.g0 = min(a.granules, r.warp * seg);
+  r.g1 = min(a.granules, r.g0 + seg);
+  fill_table(s.table);
+  tr_let_next_start();
+  tr_wait_for_previous();
+  // the slice, in granules that start on 16-byte boundaries; each lane copies what it reads
+  const T *const x = reinterpret_cast<const T *>(a.x) + row * a.ld;
+  const int off = (int)(((uintptr_t)x & 15) / sizeof(T));
+  r.id0 = (int)((long long)r.rank * a.granules * VEC) - off;
+  for (int g = r.g0 + r.lane; g < r.g1; g += 32) {
+    const int id = r.id0 + g * VEC;
+    if (id >= 0 && id <= a.V - VEC) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(data + g)),
+                   "l"(x + id)
+                   : "memory");
+    } else {
+      T *to = reinterpret_cast<T *>(data + g);
+      for (int e = 0; e < VEC; ++e) to[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
+    }
+  }
+  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+
+  // the largest logit, and the least of the threads' largest
+  float most = -INFINITY;
+  r.each([&](float y, int) { most = fmaxf(most, y); });
+  float least = most;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    least = fminf(least, __shfl_xor_sync(~0u, least, o));
+  }
+  if (r.lane == 0) s.wsum[r.warp] = (u64)key_of(most) << 32 | key_of(least);
+  __syncthreads();
+  uint32_t top = 0, low = ~0u;
+  for (int i = 0; i < kWarps; ++i) {
+    top = max(top, (uint32_t)(s.wsum[i] >> 32));
+    low = min(low, (uint32_t)s.wsum[i]);
+  }
+  const uint32_t own_top = top;
+  r.tell(top, low);
+  int owner = 0;  // the first CTA that has the largest
+  for (int k = CS - 1; k >= 0; --k) {
+    const uint32_t t = (uint32_t)r.heard(k, 0);
+    if (t >= top) {
+      top = t;
+      owner = k;
+    }
+    low = min(low, (uint32_t)r.heard(k, 1));
+  }
+  const float temp = a.temperature ? a.temperature[row] : 1.f;
+  const int k = a.top_k ? a.top_k[row] : 0;
+  if (top <= kNever || !(temp >= FLT_MIN) || k == 1) {
+    if (top <= kNever) {
+      if (r.rank == 0 && threadIdx.x == 0) {
+        a.token[row] = -1;
+        if (a.logprob) a.logprob[row] = -INFINITY;
+      }
+    } else if (r.rank == owner && own_top == top) {
+      if (threadIdx.x == 0) s.id = INT_MAX;
+      __syncthreads();
+      int first = INT_MAX;
+      r.each([&](float y, int v) { first = min(first, key_of(y) == top ? v : INT_MAX); });
+      atomicMin(&s.id, first);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        a.token[row] = s.id;
+        if (a.logprob) a.logprob[row] = 0.f;
+      }
+    }
+    return;
+  }
+  r.w.set(tr_unord(top), temp, a.S, s.table);
+
+  Edge edge = {kNever, -1};
+  const float p = a.top_p ? a.top_p[row] : 1.f;
+  bool p_done = !(p < 1.f);
+  if (k > 0 && k < a.V) {
+    bool done;
+    edge = r.top_k(k, p, low > kNever ? tr_unord(low) : -INFINITY, &done);
+    p_done |= done;
+  }
+  if (!p_done) edge = r.top_p(p, edge);
+  edge = with_min_p(edge, a.min_p ? a.min_p[row] : 0.f, r.w.m, temp);
+  const float u = uniform_of(a.U[row]);
+  u64 all;
+  const int id = r.first_past([&](float y, int v) -> u64 { return edge.leaves(key_of(y), v) ? r.w(y) : 0; },
+                              [&](u64 sum) {
+                                bool exact;
+                                return part_of(u, sum, &exact);
+                              },
+                              &all);
+  if (id >= 0 && threadIdx.x == 0) {
+    a.token[row] = id;
+    const float y = get(reinterpret_cast<const T *>(data), id - r.id0);
+    if (a.logprob) a.logprob[row] = (float)log((double)r.w(y) / (double)all);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// longer rows: one CTA reads the row from global memory (L2) in every pass
+// ---------------------------------------------------------------------------
+
+constexpr int kBigThreads = 512;
+constexpr int kBigWarps = kBigThreads / 32;
+
+struct BigSmem {
+  float2 table[64];
+  u64 hist[256];
+  u64 wsum[kBigWarps];
+  u64 best;
+  u64 base;      // of the keys above
+  uint32_t prefix;
+  int id;
+};
+
+// Sum over the block, in every thread (two barriers).
+__device__ __forceinline__ u64 block_sum(u64 v, u64 *wsum) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 s = 0;
+  for (int i = 0; i < kBigWarps; ++i) s += wsum[i];
+  __syncthreads();
+  return s;
+}
+
+// The range of IDs of a warp: consecutive ones.
+struct Range {
+  int lo, hi;
+};
+
 // The lowest ID at which the running sum of weight_of(id) over ascending IDs passes
 // `target` (V if it never does).  Every thread gets it.
 template <typename F>
-__device__ __forceinline__ int first_past(u64 target, Range r, Smem &s, F weight_of) {
+__device__ __forceinline__ int first_past(u64 target, Range r, BigSmem &s, F weight_of) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   u64 sum = 0;
   for (int v = r.lo + lane; v < r.hi; v += 32) sum += weight_of(v);
@@ -157,19 +835,15 @@ __device__ __forceinline__ int first_past(u64 target, Range r, Smem &s, F weight
 // The edge that leaves, of the tokens whose key is above `never`, the first ones in
 // falling order whose amounts sum to at least `target` (>= 1): the key is narrowed down by
 // eight bits a pass.  amount(x) of equal keys is equal.
-struct Edge {
-  uint32_t key;
-  int id;  // of the tokens with that key the ones up to this ID are left
-};
 template <typename T, typename F>
-__device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, Edge old, Smem &s, F amount) {
+__device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, Edge old, BigSmem &s, F amount) {
   uint32_t prefix = 0;
   u64 base = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += kBigThreads) s.hist[i] = 0;
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int v = threadIdx.x; v < V; v += kThreads) {
+    for (int v = threadIdx.x; v < V; v += kBigThreads) {
       const float y = get(x, v);
       const uint32_t k = key_of(y);
       if ((k & mask) != prefix || !(k > old.key || (k == old.key && v <= old.id))) continue;
@@ -204,25 +878,22 @@ __device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, E
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
-  __shared__ Smem s;
+__global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a) {
+  __shared__ BigSmem s;
   tr_let_next_start();
   tr_wait_for_previous();
   const long long row = blockIdx.x;
   const T *x = reinterpret_cast<const T *>(a.x) + row * a.ld;
   const int V = a.V, warp = threadIdx.x >> 5;
-  const int seg = (int)(((long long)V + kWarps - 1) / kWarps);
+  const int seg = (int)(((long long)V + kBigWarps - 1) / kBigWarps);
   const Range r = {(int)min((long long)V, (long long)warp * seg), (int)min((long long)V, (long long)(warp + 1) * seg)};
-  if (threadIdx.x < 64) {
-    const double p = exp2(-(double)threadIdx.x / 64.0);
-    s.table[threadIdx.x] = make_float2((float)p, __uint_as_float((unsigned)__double2ll_rn(p * 0x1p31)));
-  }
+  fill_table(s.table);
   if (threadIdx.x == 0) s.best = 0;
   __syncthreads();
 
   // the largest logit and its lowest ID
   u64 best = 0;
-  for (int v = threadIdx.x; v < V; v += kThreads) {
+  for (int v = threadIdx.x; v < V; v += kBigThreads) {
     const u64 k = (u64)key_of(get(x, v)) << 32 | (0xFFFFFFFFu - (uint32_t)v);
     best = k > best ? k : best;
   }
@@ -239,56 +910,73 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     return;
   }
   Weight w;
-  w.m = tr_unord(top);
-  w.S = a.S;
-  w.table = s.table;
-  const double c = 1.4426950408889634 / (double)temp;
-  w.c_hi = (float)c;
-  w.c_lo = (float)(c - (double)w.c_hi);
+  w.set(tr_unord(top), temp, a.S, s.table);
 
   Edge edge = {kNever, -1};
   const int k = a.top_k ? a.top_k[row] : 0;
   if (k > 0 && k < V) {
     // fewer than k tokens in all: the edge stays below them
     u64 n = 0;
-    for (int v = threadIdx.x; v < V; v += kThreads) n += key_of(get(x, v)) > kNever;
+    for (int v = threadIdx.x; v < V; v += kBigThreads) n += key_of(get(x, v)) > kNever;
     n = block_sum(n, s.wsum);
     if (n > (u64)k) edge = select(x, V, r, (u64)k, edge, s, [](float) -> u64 { return 1; });
   }
-  auto left = [&](uint32_t key, int v) { return key > edge.key || (key == edge.key && v <= edge.id); };
+  auto left = [&](uint32_t key, int v) { return edge.leaves(key, v); };
   const float p = a.top_p ? a.top_p[row] : 1.f;
   if (p < 1.f) {
     u64 all = 0;
-    for (int v = threadIdx.x; v < V; v += kThreads) {
+    for (int v = threadIdx.x; v < V; v += kBigThreads) {
       const float y = get(x, v);
       if (left(key_of(y), v)) all += w(y);
     }
     all = block_sum(all, s.wsum);
-    bool exact;
-    u64 need = part_of(p, all, &exact);
-    need += !exact;
-    edge = select(x, V, r, need > 0 ? need : 1, edge, s, w);
+    edge = select(x, V, r, share_of(p, all), edge, s, w);
   }
-  const float mp = a.min_p ? a.min_p[row] : 0.f;
-  if (mp > 0.f && temp < INFINITY) {  // with an infinite temperature all weights are 1
-    const float f = __double2float_ru((double)w.m + (double)temp * log(fmin((double)mp, 1.0)));
-    const uint32_t lk = key_of(f);
-    if (lk > edge.key) edge = {lk, INT_MAX};
-  }
+  edge = with_min_p(edge, a.min_p ? a.min_p[row] : 0.f, w.m, temp);
   auto weight_of = [&](int v) -> u64 {
     const float y = get(x, v);
     return left(key_of(y), v) ? w(y) : 0;
   };
   u64 all = 0;
-  for (int v = threadIdx.x; v < V; v += kThreads) all += weight_of(v);
+  for (int v = threadIdx.x; v < V; v += kBigThreads) all += weight_of(v);
   all = block_sum(all, s.wsum);
-  const float u = fminf(fmaxf(a.U[row], 0.f), 1.f - 0x1p-24f);  // NaN: 0
+  const float u = uniform_of(a.U[row]);
   bool exact;
   const int id = first_past(part_of(u, all, &exact), r, s, weight_of);
   if (threadIdx.x == 0) {
     a.token[row] = id;
     if (a.logprob) a.logprob[row] = (float)log((double)w(get(x, id)) / (double)all);
   }
+}
+
+// A slice's bytes: three CTAs share an SM up to the first, one has it up to the second; its tokens, so
+// that top-p's sums of 16-bit weights stay below 2^32.
+constexpr long long kSlice = 64 * 1024, kMostSlice = 208 * 1024, kMostTokens = 65536;
+
+template <typename T>
+int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
+  auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first granule
+    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC;
+    return (all + cs - 1) / cs;
+  };
+  int cs = 1;
+  while (cs < kMaxCluster && granules(cs) * 16 > kSlice) cs *= 2;
+  if (granules(cs) * 16 > kMostSlice || granules(cs) * VEC > kMostTokens)
+    return tr_launch_next(big_row_kernel<T>, {dim3((unsigned)rows), kBigThreads}, s, a);
+  // few rows: more SMs for each, down to slices of 4 KB
+  while (cs < kMaxCluster && rows * cs * 2 <= 3LL * tr_sm_count() && granules(cs) * 16 > 8192) cs *= 2;
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  TR_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(sizeof(Smem) + kMostSlice)));
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
+  a.granules = (int)granules(cs);
+  return tr_launch_next(sample_kernel<T>,
+                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs);
 }
 
 }  // namespace
@@ -309,8 +997,6 @@ extern "C" int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64
   if (rc != TR_OK) return rc;
   SampleArgs a = {logits, ld, (int)V, 62, temperature, top_p, min_p, U, top_k, token, logprob};
   while (a.S > 30 && (V >> (62 - a.S)) > 1) --a.S;  // V weights of 2^S and less stay below 2^63
-  auto go = [&](auto kernel) {
-    return tr_launch_next(kernel, {dim3((unsigned)rows), kThreads}, (cudaStream_t)stream, a);
-  };
-  return ftype == TR_F32 ? go(sample_kernel<float>) : go(sample_kernel<__nv_bfloat16>);
+  cudaStream_t s = (cudaStream_t)stream;
+  return ftype == TR_F32 ? launch<float>(a, rows, s) : launch<__nv_bfloat16>(a, rows, s);
 }
