@@ -15,6 +15,7 @@
 // A last pass sums the weights that are left over ascending IDs and finds the uniform's place.
 #include <cfloat>
 #include <cmath>
+#include <cstring>
 
 #include <atomic>
 
@@ -42,30 +43,33 @@ struct SampleArgs {
 constexpr uint32_t kNever = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float x) { return x == x ? tr_ord(x) : kNever; }
 
-// Weights of a row: 2^S 2^(x c - K), c = log2(e) / T and K the whole number at or above m c, rounded
+// Weights of a row: 2^S 2^(x c - K), c = log2(e) / T and K a whole number above m c by 1.02 at most, rounded
 // down.  x c is split into a multiple of 1 / 64 (adding and taking away 1.5 2^17 rounds to it) and a
 // rest whose error is below 2^-31; the multiple's power of two comes from a table, the rest's from a
 // polynomial.  Where |m c| passes 2^15, x is taken relative to m first: what has weight then
-// lies so near to m that the difference is exact.
+// lies so near to m that the difference is exact.  A weight below 2^-62 is 0.
 struct Weight {
-  float m, base, c_hi, c_lo;
+  float m, base, least, c_hi, c_lo;  // least: below it (as y) there is no weight
   int K, S;
+  bool infinite;        // the largest logit is +inf
   const float2 *table;  // 2^(j / 64): 2^31 times it as a float, and as an integer (in its bits)
-  __device__ __forceinline__ void set(float m_, float temp, int S_, const float2 *t) {
-    const double c = 1.4426950408889634 / (double)temp;
+  __device__ __forceinline__ void set(float m_, float2 c, int S_, const float2 *t) {
     m = m_;
     S = S_;
     table = t;
-    c_hi = (float)c;
-    c_lo = (float)(c - (double)c_hi);
-    const bool far = !(fabs((double)m * c) < 32768.0);  // infinite too
+    c_hi = c.x;
+    c_lo = c.y;
+    infinite = m == INFINITY;
+    const float mc = m * c_hi;
+    const bool far = !(fabsf(mc) < 32700.f);  // infinite too
     base = far ? m : 0.f;
-    K = far ? 0 : (int)ceil((double)m * c);
+    K = far ? 1 : (int)ceilf(mc + 0.01f);  // m c is off by 2^-9 at most
+    least = fmaxf((far ? 0.f : m) - 62.f / c_hi, -FLT_MAX);
   }
+  // of a logit above -inf
   __device__ __forceinline__ u64 operator()(float x) const {
-    const float t = (m - x) * c_hi;
-    if (!(t < 62.f)) return x == m ? 1ull << S : 0;  // below every S, or not a number: infinite logits
-    const float y = x - base, p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
+    if (infinite) return x == m ? 1ull << S : 0;
+    const float y = fmaxf(x - base, least), p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
     const float r = fmaf(y, c_lo, fmaf(y, c_hi, -q));  // |r| <= 1 / 128 and a little
     float e = fmaf(r, 5.550410866482158e-2f, 2.402265069591007e-1f);  // 2^r - 1: ln2^3 / 6, ln2^2 / 2, ln2
     e = fmaf(r, e, 6.931471805599453e-1f);
@@ -73,15 +77,22 @@ struct Weight {
     const int n = __float_as_int(p) - 0x48400000;  // 64 q
     const float2 f = table[n & 63];
     const unsigned mant = __float_as_uint(f.y) + (unsigned)__float2int_rn(e * f.x);
-    return ((u64)mant << (S - 31)) >> (K - (n >> 6));
+    return ((u64)mant << (S - 31)) >> min(K - (n >> 6), 63);
   }
 };
+// c of a temperature, in two numbers.
+__device__ __forceinline__ float2 log2e_over(float temp) {
+  const double c = 1.4426950408889634 / (double)temp;
+  const float hi = (float)c;
+  return make_float2(hi, (float)(c - (double)hi));
+}
 
-__device__ __forceinline__ void fill_table(float2 *table) {
-  if (threadIdx.x < 64) {
-    const double p = exp2((double)threadIdx.x / 64.0) * 0x1p31;
-    table[threadIdx.x] = make_float2((float)p, __uint_as_float((unsigned)__double2ull_rn(p)));
-  }
+// 2^(j / 64) 2^31, j = 0 .. 63, as a number and as an integer: worked out once on the host.
+struct Table {
+  float2 of[64];
+};
+__device__ __forceinline__ void fill_table(float2 *table, const Table &t) {
+  if (threadIdx.x < 64) table[threadIdx.x] = t.of[threadIdx.x];
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -130,13 +141,24 @@ __device__ __forceinline__ float get(const __nv_bfloat16 *x, int v) {
 struct Edge {
   uint32_t key;
   int id;
-  __device__ __forceinline__ bool leaves(uint32_t k, int v) const { return k > key || (k == key && v <= id); }
+};
+// The same on logits: NaN and -inf are never left.
+struct Left {
+  float at;
+  int id;
+  __device__ __forceinline__ Left(Edge e) : at(e.key <= kNever ? -INFINITY : tr_unord(e.key)), id(e.key <= kNever ? -1 : e.id) {}
+  __device__ __forceinline__ bool operator()(float x, int v) const { return x > at || (x == at && v <= id); }
 };
 
 // min_p's edge: the least logit whose weight is at least min_p of the largest one's.
-__device__ __forceinline__ Edge with_min_p(Edge e, float mp, float m, float temp) {
-  if (mp > 0.f && temp < INFINITY) {  // with an infinite temperature all weights are 1
-    const uint32_t k = key_of(__double2float_ru((double)m + (double)temp * log(fmin((double)mp, 1.0))));
+// below: T ln(min(min_p, 1)), how far that is below the largest logit; NaN: off.
+__device__ __forceinline__ double min_p_below(float mp, float temp) {
+  // with an infinite temperature all weights are 1
+  return mp > 0.f && temp < INFINITY ? (double)temp * log(fmin((double)mp, 1.0)) : __longlong_as_double(~0ll);
+}
+__device__ __forceinline__ Edge with_min_p(Edge e, double below, float m) {
+  if (below == below) {
+    const uint32_t k = key_of(__double2float_ru((double)m + below));
     if (k > e.key) e = {k, INT_MAX};
   }
   return e;
@@ -159,6 +181,10 @@ struct Smem {
   u64 box[2][kMaxCluster][2];     // what the cluster's CTAs have told this one, of two exchanges
   u64 wsum[kWarps];
   unsigned listed;                // tokens that were to go to the list
+  float temp, p, u;               // the row's rules
+  int k;
+  float2 c;
+  double below;
   unsigned found[3];
   int id;
   u64 cum;
@@ -463,7 +489,7 @@ struct Row {
   // amounts sum to at least `target`: the key is narrowed down by eight bits a pass, then the
   // lowest IDs among equal keys.
   template <typename F>
-  __device__ __forceinline__ Edge narrow_down(u64 target, Edge old, F amount) {
+  __device__ __forceinline__ Edge narrow_down(u64 target, Left old, F amount) {
     uint32_t prefix = 0;
     u64 base = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
@@ -473,7 +499,7 @@ struct Row {
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
       each([&](float x, int v) {
         const uint32_t k = key_of(x);
-        const u64 n = (k & mask) == prefix && k > kNever && old.leaves(k, v) ? amount(x) : 0;
+        const u64 n = (k & mask) == prefix && old(x, v) ? amount(x) : 0;
         const unsigned m = __ballot_sync(~0u, n != 0), b = (k >> shift) & 255;
         if (m == 0) return;
         int same;  // a warp whose tokens all share a bin adds once
@@ -505,7 +531,7 @@ struct Row {
     const u64 each_ = amount(tr_unord(prefix));
     const u64 take = each_ ? (target - base + each_ - 1) / each_ : 0;
     u64 n;
-    const int id = first_past([&](float x, int v) -> u64 { return key_of(x) == prefix && old.leaves(prefix, v); },
+    const int id = first_past([&](float x, int v) -> u64 { return key_of(x) == prefix && old(x, v); },
                               [&](u64) -> u64 { return take - 1; }, &n);
     tell(id >= 0, (u64)(unsigned)id);
     Edge e = {prefix, INT_MAX};
@@ -588,11 +614,11 @@ struct Row {
     n = 0;
     for (int r = 0; r < CS; ++r) n += heard(r, 0);
     const Edge none = {kNever, -1};
-    return n <= (u64)k ? none : narrow_down((u64)k, none, [](float) -> u64 { return 1; });
+    return n <= (u64)k ? none : narrow_down((u64)k, Left(none), [](float) -> u64 { return 1; });
   }
 
   // top-p among the tokens that `old` leaves.
-  __device__ __forceinline__ Edge top_p(float p, Edge old) {
+  __device__ __forceinline__ Edge top_p(float p, Left old) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
     // (2^16 of them: the sum of a slice stays below 2^32).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
@@ -600,7 +626,7 @@ struct Row {
     clear();
     each([&](float x, int v) {
       const float t = (m - x) * scale;
-      if (!(t < (float)(kBins - 1)) || !old.leaves(key_of(x), v)) return;
+      if (!(t < (float)(kBins - 1)) || !old(x, v)) return;
       const int b = (int)t;
       float f;  // within its power of two
       asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(((float)(b & ~63) - t) * (1.f / 64.f)));
@@ -617,7 +643,7 @@ struct Row {
     u64 all = 0, above = 0;
     each([&](float x, int v) {
       const float t = (m - x) * scale;
-      const bool left = x > -INFINITY && old.leaves(key_of(x), v);
+      const bool left = old(x, v);
       const int b = (int)fminf(t, (float)kBins);
       const u64 q = left ? w(x) : 0;
       all += q;
@@ -651,11 +677,12 @@ struct Row {
     const Edge e = hear_edge(&ok);
     return ok ? e : narrow_down_p(target, old);
   }
-  __device__ __noinline__ Edge narrow_down_p(u64 target, Edge old) { return narrow_down(target, old, w); }
+  __device__ __noinline__ Edge narrow_down_p(u64 target, Left old) { return narrow_down(target, old, w); }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS) {
+__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS,
+                                                             const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
   Row<T> r(a, s);
@@ -668,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   const int seg = warp_granules(a.granules);
   r.g0 = min(a.granules, r.warp * seg);
   r.g1 = min(a.granules, r.g0 + seg);
-  fill_table(s.table);
+  fill_table(s.table, table);
   tr_let_next_start();
   tr_wait_for_previous();
   // the slice, in granules that start on 16-byte boundaries; each lane copies what it reads
@@ -686,7 +713,17 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       for (int e = 0; e < VEC; ++e) to[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
     }
   }
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (threadIdx.x == kThreads - 1) {  // the rules, while the slice is under way; 64-bit arithmetic once
+    const float temp = a.temperature ? a.temperature[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
+    s.temp = temp;
+    s.k = a.top_k ? a.top_k[row] : 0;
+    s.p = a.top_p ? a.top_p[row] : 1.f;
+    s.u = uniform_of(a.U[row]);
+    s.c = log2e_over(temp);
+    s.below = min_p_below(mp, temp);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 
   // the largest logit, and the least of the threads' largest
   float most = -INFINITY;
@@ -715,9 +752,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     }
     low = min(low, (uint32_t)r.heard(k, 1));
   }
-  const float temp = a.temperature ? a.temperature[row] : 1.f;
-  const int k = a.top_k ? a.top_k[row] : 0;
-  if (top <= kNever || !(temp >= FLT_MIN) || k == 1) {
+  const int k = s.k;
+  if (top <= kNever || !(s.temp >= FLT_MIN) || k == 1) {
     if (top <= kNever) {
       if (r.rank == 0 && threadIdx.x == 0) {
         a.token[row] = -1;
@@ -737,21 +773,21 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     }
     return;
   }
-  r.w.set(tr_unord(top), temp, a.S, s.table);
+  r.w.set(tr_unord(top), s.c, a.S, s.table);
 
   Edge edge = {kNever, -1};
-  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const float p = s.p;
   bool p_done = !(p < 1.f);
   if (k > 0 && k < a.V) {
     bool done;
     edge = r.top_k(k, p, low > kNever ? tr_unord(low) : -INFINITY, &done);
     p_done |= done;
   }
-  if (!p_done) edge = r.top_p(p, edge);
-  edge = with_min_p(edge, a.min_p ? a.min_p[row] : 0.f, r.w.m, temp);
-  const float u = uniform_of(a.U[row]);
+  if (!p_done) edge = r.top_p(p, Left(edge));
+  const Left left(with_min_p(edge, s.below, r.w.m));
+  const float u = s.u;
   u64 all;
-  const int id = r.first_past([&](float y, int v) -> u64 { return edge.leaves(key_of(y), v) ? r.w(y) : 0; },
+  const int id = r.first_past([&](float y, int v) -> u64 { return left(y, v) ? r.w(y) : 0; },
                               [&](u64 sum) {
                                 bool exact;
                                 return part_of(u, sum, &exact);
@@ -836,7 +872,7 @@ __device__ __forceinline__ int first_past(u64 target, Range r, BigSmem &s, F wei
 // falling order whose amounts sum to at least `target` (>= 1): the key is narrowed down by
 // eight bits a pass.  amount(x) of equal keys is equal.
 template <typename T, typename F>
-__device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, Edge old, BigSmem &s, F amount) {
+__device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, Left old, BigSmem &s, F amount) {
   uint32_t prefix = 0;
   u64 base = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
@@ -846,7 +882,7 @@ __device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, E
     for (int v = threadIdx.x; v < V; v += kBigThreads) {
       const float y = get(x, v);
       const uint32_t k = key_of(y);
-      if ((k & mask) != prefix || !(k > old.key || (k == old.key && v <= old.id))) continue;
+      if ((k & mask) != prefix || !old(y, v)) continue;
       const u64 a = amount(y);
       if (a) atomicAdd(&s.hist[(k >> shift) & 255], a);
     }
@@ -872,13 +908,14 @@ __device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, E
   Edge e = {prefix, INT_MAX};
   if (take)
     e.id = first_past(take - 1, r, s, [&](int v) -> u64 {
-      return key_of(get(x, v)) == prefix && !(prefix == old.key && v > old.id);
+      const float y = get(x, v);
+      return key_of(y) == prefix && old(y, v);
     });
   return e;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a, const __grid_constant__ Table table) {
   __shared__ BigSmem s;
   tr_let_next_start();
   tr_wait_for_previous();
@@ -887,7 +924,7 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
   const int V = a.V, warp = threadIdx.x >> 5;
   const int seg = (int)(((long long)V + kBigWarps - 1) / kBigWarps);
   const Range r = {(int)min((long long)V, (long long)warp * seg), (int)min((long long)V, (long long)(warp + 1) * seg)};
-  fill_table(s.table);
+  fill_table(s.table, table);
   if (threadIdx.x == 0) s.best = 0;
   __syncthreads();
 
@@ -910,7 +947,7 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
     return;
   }
   Weight w;
-  w.set(tr_unord(top), temp, a.S, s.table);
+  w.set(tr_unord(top), log2e_over(temp), a.S, s.table);
 
   Edge edge = {kNever, -1};
   const int k = a.top_k ? a.top_k[row] : 0;
@@ -919,23 +956,22 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
     u64 n = 0;
     for (int v = threadIdx.x; v < V; v += kBigThreads) n += key_of(get(x, v)) > kNever;
     n = block_sum(n, s.wsum);
-    if (n > (u64)k) edge = select(x, V, r, (u64)k, edge, s, [](float) -> u64 { return 1; });
+    if (n > (u64)k) edge = select(x, V, r, (u64)k, Left(edge), s, [](float) -> u64 { return 1; });
   }
-  auto left = [&](uint32_t key, int v) { return edge.leaves(key, v); };
   const float p = a.top_p ? a.top_p[row] : 1.f;
   if (p < 1.f) {
     u64 all = 0;
     for (int v = threadIdx.x; v < V; v += kBigThreads) {
       const float y = get(x, v);
-      if (left(key_of(y), v)) all += w(y);
+      if (Left(edge)(y, v)) all += w(y);
     }
     all = block_sum(all, s.wsum);
-    edge = select(x, V, r, share_of(p, all), edge, s, w);
+    edge = select(x, V, r, share_of(p, all), Left(edge), s, w);
   }
-  edge = with_min_p(edge, a.min_p ? a.min_p[row] : 0.f, w.m, temp);
+  const Left left(with_min_p(edge, min_p_below(a.min_p ? a.min_p[row] : 0.f, temp), w.m));
   auto weight_of = [&](int v) -> u64 {
     const float y = get(x, v);
-    return left(key_of(y), v) ? w(y) : 0;
+    return left(y, v) ? w(y) : 0;
   };
   u64 all = 0;
   for (int v = threadIdx.x; v < V; v += kBigThreads) all += weight_of(v);
@@ -953,6 +989,20 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
 // that top-p's sums of 16-bit weights stay below 2^32.
 constexpr long long kSlice = 64 * 1024, kMostSlice = 208 * 1024, kMostTokens = 65536;
 
+const Table &table() {
+  static const Table t = [] {
+    Table x;
+    for (int j = 0; j < 64; ++j) {
+      const double p = std::exp2(j / 64.0) * 0x1p31;
+      const uint32_t bits = (uint32_t)std::llround(p);
+      x.of[j].x = (float)p;
+      memcpy(&x.of[j].y, &bits, 4);
+    }
+    return x;
+  }();
+  return t;
+}
+
 template <typename T>
 int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
@@ -963,7 +1013,7 @@ int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
   int cs = 1;
   while (cs < kMaxCluster && granules(cs) * 16 > kSlice) cs *= 2;
   if (granules(cs) * 16 > kMostSlice || granules(cs) * VEC > kMostTokens)
-    return tr_launch_next(big_row_kernel<T>, {dim3((unsigned)rows), kBigThreads}, s, a);
+    return tr_launch_next(big_row_kernel<T>, {dim3((unsigned)rows), kBigThreads}, s, a, table());
   // few rows: more SMs for each, down to slices of 4 KB
   while (cs < kMaxCluster && rows * cs * 2 <= 3LL * tr_sm_count() && granules(cs) * 16 > 8192) cs *= 2;
   static std::atomic<bool> set[64];  // per device
@@ -976,7 +1026,7 @@ int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
   }
   a.granules = (int)granules(cs);
   return tr_launch_next(sample_kernel<T>,
-                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs);
+                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs, table());
 }
 
 }  // namespace
