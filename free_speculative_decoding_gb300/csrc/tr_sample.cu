@@ -30,24 +30,48 @@ typedef unsigned long long u64;
 
 struct SampleArgs {
   const void *x;
-  long long ld;
+  long long ld, rows;
   int V, S;  // weights are in units of 2^-S
   const float *temperature, *top_p, *min_p, *U;
   const int32_t *top_k;
   int32_t *token;
   float *logprob;
-  int granules;  // of a CTA's slice
+  int granules;  // of a CTA's slice, kWarps * 32 or a multiple
 };
 
 // The order of a logit; NaN and -inf (never drawn) are 0x007FFFFF, below every other.
 constexpr uint32_t kNever = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float x) { return x == x ? tr_ord(x) : kNever; }
 
+// Two fp32 values in one register pair, and one instruction.
+struct F2 {
+  u64 v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {  // a b + c
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+
 // Weights of a row: 2^S 2^(x c - K), c = log2(e) / T and K a whole number above m c by 1.02 at most, rounded
 // down.  x c is split into a multiple of 1 / 64 (adding and taking away 1.5 2^17 rounds to it) and a
 // rest whose error is below 2^-31; the multiple's power of two comes from a table, the rest's from a
 // polynomial.  Where |m c| passes 2^15, x is taken relative to m first: what has weight then
 // lies so near to m that the difference is exact.  A weight below 2^-62 is 0.
+constexpr float kL1 = 6.931471805599453e-1f, kL2 = 2.402265069591007e-1f, kL3 = 5.550410866482158e-2f;  // ln2^i / i!
 struct Weight {
   float m, base, least, c_hi, c_lo;  // least: below it (as y) there is no weight
   int K, S;
@@ -66,19 +90,44 @@ struct Weight {
     K = far ? 1 : (int)ceilf(mc + 0.01f);  // m c is off by 2^-9 at most
     least = fmaxf((far ? 0.f : m) - 62.f / c_hi, -FLT_MAX);
   }
-  // of a logit above -inf
-  __device__ __forceinline__ u64 operator()(float x) const {
-    if (infinite) return x == m ? 1ull << S : 0;
-    const float y = fmaxf(x - base, least), p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
-    const float r = fmaf(y, c_lo, fmaf(y, c_hi, -q));  // |r| <= 1 / 128 and a little
-    float e = fmaf(r, 5.550410866482158e-2f, 2.402265069591007e-1f);  // 2^r - 1: ln2^3 / 6, ln2^2 / 2, ln2
-    e = fmaf(r, e, 6.931471805599453e-1f);
-    e *= r;
+  __device__ __forceinline__ u64 whole(float p, float e) const {
     const int n = __float_as_int(p) - 0x48400000;  // 64 q
     const float2 f = table[n & 63];
     const unsigned mant = __float_as_uint(f.y) + (unsigned)__float2int_rn(e * f.x);
     return ((u64)mant << (S - 31)) >> min(K - (n >> 6), 63);
   }
+  // Of logits above -inf.
+  __device__ __forceinline__ u64 operator()(float x) const {
+    if (infinite) return x == m ? 1ull << S : 0;
+    const float y = fmaxf(x - base, least), p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
+    const float r = fmaf(y, c_lo, fmaf(y, c_hi, -q));  // |r| <= 1 / 128 and a little
+    float e = fmaf(r, kL3, kL2);               // 2^r - 1
+    e = fmaf(r, e, kL1);
+    return whole(p, e * r);
+  }
+  // The weights of N logits, of those that are -inf or NaN 0: the same arithmetic, two to an instruction.
+  template <int N>
+  __device__ __forceinline__ void of(const float (&x)[N], u64 (&w)[N]) const {
+    if (infinite) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = x[i] == m ? 1ull << S : 0;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const F2 c = f2(c_hi, c_hi), magic = f2(0x1.8p17f, 0x1.8p17f);
+      const F2 y = f2(fmaxf(x[i] - base, least), fmaxf(x[i + 1] - base, least));
+      const F2 p = fma(y, c, magic), q = fma(p, f2(-1.f, -1.f), magic);
+      const F2 r = fma(y, f2(c_lo, c_lo), fma(y, c, q));
+      F2 e = fma(r, f2(kL3, kL3), f2(kL2, kL2));
+      e = fma(r, e, f2(kL1, kL1)) * r;
+      const float2 p1 = split(p), e1 = split(e);
+      w[i] = x[i] > -INFINITY ? whole(p1.x, e1.x) : 0;
+      w[i + 1] = x[i + 1] > -INFINITY ? whole(p1.y, e1.y) : 0;
+    }
+  }
+  // The logit from which on there are weights, about: those below have none.
+  __device__ __forceinline__ float floor() const { return infinite ? m : fmaxf(base + least, -FLT_MAX); }
 };
 // c of a temperature, in two numbers.
 __device__ __forceinline__ float2 log2e_over(float temp) {
@@ -150,19 +199,16 @@ struct Left {
   __device__ __forceinline__ bool operator()(float x, int v) const { return x > at || (x == at && v <= id); }
 };
 
-// min_p's edge: the least logit whose weight is at least min_p of the largest one's.
+// min_p's edge: the key of the least logit whose weight is at least min_p of the largest one's (0: off).
 // below: T ln(min(min_p, 1)), how far that is below the largest logit; NaN: off.
 __device__ __forceinline__ double min_p_below(float mp, float temp) {
   // with an infinite temperature all weights are 1
   return mp > 0.f && temp < INFINITY ? (double)temp * log(fmin((double)mp, 1.0)) : __longlong_as_double(~0ll);
 }
-__device__ __forceinline__ Edge with_min_p(Edge e, double below, float m) {
-  if (below == below) {
-    const uint32_t k = key_of(__double2float_ru((double)m + below));
-    if (k > e.key) e = {k, INT_MAX};
-  }
-  return e;
+__device__ __forceinline__ uint32_t min_p_key(double below, float m) {
+  return below == below ? key_of(__double2float_ru((double)m + below)) : 0;
 }
+__device__ __forceinline__ Edge with_min_p(Edge e, uint32_t key) { return key > e.key ? Edge{key, INT_MAX} : e; }
 
 __device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f), 1.f - 0x1p-24f); }  // NaN: 0
 
@@ -176,13 +222,13 @@ constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;       // 64 to a power of two, where they are weighted
 constexpr int kList = 1024;
 
-struct Smem {
+struct alignas(128) Smem {  // the slice lies behind it
   float2 table[64];
   u64 box[2][kMaxCluster][2];     // what the cluster's CTAs have told this one, of two exchanges
   u64 wsum[kWarps];
+  u64 kept[kWarps];               // the weights that are left in the warps' ranges, where they are known
   unsigned listed;                // tokens that were to go to the list
   float temp, p, u;               // the row's rules
-  int k;
   float2 c;
   double below;
   unsigned found[3];
@@ -195,8 +241,7 @@ struct Smem {
   };
 };
 
-// Granules of a warp, of a slice's.
-__device__ __forceinline__ int warp_granules(int granules) { return (granules + kWarps * 32 - 1) / (kWarps * 32) * 32; }
+static_assert(sizeof(Smem) % 16 == 0);
 
 template <typename T>
 struct Row {
@@ -220,25 +265,38 @@ struct Row {
     else asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
   }
 
-  // f(x, ID) for every element of the warp's granules, 32 * VEC consecutive ones at a time; all lanes
-  // call f alike (with -inf behind the last granule).
+  // f(x[VEC], first ID) for the warp's granules, 32 * VEC consecutive elements at a time, where any of these is
+  // at or above `floor`; all lanes call f alike.
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int g = g0 + lane; g - lane < g1; g += 32) {
-      constexpr uint32_t kNone = VEC == 4 ? 0xFF800000u : 0xFF80FF80u;
-      const uint4 v = g < g1 ? data[g] : make_uint4(kNone, kNone, kNone, kNone);
-      const int id = id0 + g * VEC;
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  __device__ __forceinline__ void each(float floor, F f) const {
+#pragma unroll 2
+    for (int g = g0 + lane; g < g1; g += 32) {  // a multiple of 32
+      float x[VEC];
+      if (!__any_sync(~0u, unpack(data[g], x) >= floor)) continue;
+      f(x, id0 + g * VEC);
+    }
+  }
+  // A granule's elements; the largest.
+  static __device__ __forceinline__ float unpack(const uint4 &v, float (&x)[VEC]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
       if constexpr (VEC == 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f(__uint_as_float(u[e]), id + e);
+        x[e] = __uint_as_float(u[e]);
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f(__uint_as_float(u[e] << 16), id + 2 * e);
-          f(__uint_as_float(u[e] & 0xFFFF0000u), id + 2 * e + 1);
-        }
+        x[2 * e] = __uint_as_float(u[e] << 16);
+        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
       }
+    }
+    return most(v);
+  }
+  static __device__ __forceinline__ float most(const uint4 &v) {
+    if constexpr (VEC == 4) {
+      return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+      auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(b(v.x), b(v.y)), __hmax2(b(v.z), b(v.w)));
+      return fmaxf(__low2float(m), __high2float(m));
     }
   }
 
@@ -283,14 +341,17 @@ struct Row {
     return before + v;
   }
 
-  // The lowest ID at which the running sum of amount(x, ID) over ascending IDs passes `target`, and
-  // the whole sum before it is known: target_of(sum).  In the one CTA that holds it; -1 in the others.
+  // The lowest ID at which the running sum over ascending IDs passes target_of(whole sum), in the one CTA that
+  // holds it; -1 in the others.  amounts(x, first ID) is the sum of a granule's, none of which lies below `floor`.
+  // known: the sums of the warps' ranges are in s.kept.
   template <typename F, typename G>
-  __device__ __forceinline__ int first_past(F amount, G target_of, u64 *all) {
+  __device__ __forceinline__ int first_past(float floor, F amounts, G target_of, u64 *all, bool known = false) {
     u64 mine = 0;
-    each([&](float x, int v) { mine += amount(x, v); });
-    mine = warp_sum(mine);
-    if (lane == 0) s.wsum[warp] = mine;
+    if (!known) {
+      each(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
+      mine = warp_sum(mine);
+    }
+    if (lane == 0) s.wsum[warp] = known ? s.kept[warp] : mine;
     __syncthreads();
     u64 cta = 0, before = 0, sum = 0;
 #pragma unroll
@@ -303,29 +364,30 @@ struct Row {
     *all = sum;
     const u64 target = target_of(sum);
     if (!(before <= target && before + cta > target)) return -1;
-    // the warp's range that holds it, then an eighth of that range by each warp
+    // the warp's range that holds it, a part of that range by each warp, 32 granules, a granule
     int q = 0;
-    while (before + s.wsum[q] <= target) before += s.wsum[q++];
-    const int seg = warp_granules(a.granules), lo = min(a.granules, q * seg), hi = min(a.granules, lo + seg);
-    const int part = ((hi - lo + kWarps - 1) / kWarps + 31) & ~31;
+    while (q < kWarps - 1 && before + s.wsum[q] <= target) before += s.wsum[q++];
+    const int seg = a.granules / kWarps, lo = q * seg, hi = lo + seg;
+    const int part = ((seg + kWarps - 1) / kWarps + 31) & ~31;
     const int p0 = min(hi, lo + warp * part), p1 = min(hi, p0 + part);
     const int keep0 = g0, keep1 = g1;
     g0 = p0;
     g1 = p1;
     mine = 0;
-    each([&](float x, int v) { mine += amount(x, v); });
+    each(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
     mine = warp_sum(mine);
     __syncthreads();
     if (lane == 0) s.wsum[warp] = mine;
+    if (threadIdx.x == 0) s.id = max(id0, 0);
     __syncthreads();
     for (int i = 0; i < warp; ++i) before += s.wsum[i];
     if (before <= target && before + mine > target) {  // one warp
       for (int g = p0; g < p1; g += 32) {
-        g0 = g;
-        g1 = min(p1, g + 32);
-        u64 c = 0;
-        each([&](float x, int v) { c += amount(x, v); });
-        const u64 own = c;
+        float x[VEC];
+        unpack(data[g + lane], x);
+        const int id = id0 + (g + lane) * VEC;
+        const u64 own = amounts(x, id, ~0u);
+        u64 c = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const u64 y = __shfl_up_sync(~0u, c, o);
@@ -334,13 +396,10 @@ struct Row {
         const unsigned past = __ballot_sync(~0u, before + c > target);
         if (past) {
           if (lane == __ffs(past) - 1) {
-            u64 run = before + c - own;
-            int id = -1;
-            each([&](float x, int v) {
-              run += amount(x, v);
-              if (id < 0 && run > target) id = v;
-            });
-            s.id = id;
+            const u64 run = before + c - own;
+            int e = 0;
+            while (e < VEC - 1 && run + amounts(x, id, (2u << e) - 1) <= target) ++e;
+            s.id = id + e;
           }
           break;
         }
@@ -481,7 +540,7 @@ struct Row {
   }
 
   __device__ __forceinline__ Edge edge_at(int i) const {
-    const u64 e = s.list[i];
+    const u64 e = s.list[min(max(i, 0), kList - 1)];
     return {(uint32_t)(e >> 32), (int)(0xFFFFFFFFu - (uint32_t)e)};
   }
 
@@ -497,18 +556,21 @@ struct Row {
       for (int i = threadIdx.x; i < 256; i += kThreads) s.wide[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      each([&](float x, int v) {
-        const uint32_t k = key_of(x);
-        const u64 n = (k & mask) == prefix && old(x, v) ? amount(x) : 0;
-        const unsigned m = __ballot_sync(~0u, n != 0), b = (k >> shift) & 255;
-        if (m == 0) return;
-        int same;  // a warp whose tokens all share a bin adds once
-        __match_all_sync(~0u, b, &same);
-        if (same) {
-          const u64 t = warp_sum(n);
-          if (lane == 0) atomicAdd(&s.wide[b], t);
-        } else if (n) {
-          atomicAdd(&s.wide[b], n);
+      each(-FLT_MAX, [&](const float (&x)[VEC], int v) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const uint32_t k = key_of(x[e]);
+          const u64 n = (k & mask) == prefix && old(x[e], v + e) ? amount(x[e]) : 0;
+          const unsigned m = __ballot_sync(~0u, n != 0), b = (k >> shift) & 255;
+          if (m == 0) continue;
+          int same;  // a warp whose tokens all share a bin adds once
+          __match_all_sync(~0u, b, &same);
+          if (same) {
+            const u64 t = warp_sum(n);
+            if (lane == 0) atomicAdd(&s.wide[b], t);
+          } else if (n) {
+            atomicAdd(&s.wide[b], n);
+          }
         }
       });
       sync();
@@ -531,7 +593,14 @@ struct Row {
     const u64 each_ = amount(tr_unord(prefix));
     const u64 take = each_ ? (target - base + each_ - 1) / each_ : 0;
     u64 n;
-    const int id = first_past([&](float x, int v) -> u64 { return key_of(x) == prefix && old(x, v); },
+    const float at = tr_unord(prefix);
+    const int id = first_past(at,
+                              [&](const float (&x)[VEC], int v, unsigned which) -> u64 {
+                                unsigned t = 0;
+#pragma unroll
+                                for (int e = 0; e < VEC; ++e) t += (which >> e & 1) && x[e] == at && old(x[e], v + e);
+                                return t;
+                              },
                               [&](u64) -> u64 { return take - 1; }, &n);
     tell(id >= 0, (u64)(unsigned)id);
     Edge e = {prefix, INT_MAX};
@@ -540,75 +609,136 @@ struct Row {
     return e;
   }
 
-  __device__ __forceinline__ Edge hear_edge(bool *ok) const {
-    const u64 x = heard(0, 0);
-    *ok = heard(0, 1) & 1;
-    return {(uint32_t)(x >> 32), (int)(uint32_t)x};
+  // What the first CTA found in its sorted list: the edge, and how many entries are left.
+  struct Found {
+    Edge edge;
+    bool ok;
+    int left;  // entries of the list; -1: not those alone and what lies above the list
+  };
+  __device__ __forceinline__ Found hear_found() const {
+    const u64 x = heard(0, 0), y = heard(0, 1);
+    return {{(uint32_t)(x >> 32), (int)(uint32_t)x}, (y & 1) != 0, (int)(y >> 1) - 1};
+  }
+  __device__ __forceinline__ void tell_found(Edge e, bool ok, int left) {
+    tell((u64)e.key << 32 | (uint32_t)e.id, (u64)(left + 1) << 1 | ok);
   }
 
-  // top-k, and top-p with it where all of the k tokens fit the list (*p_done).
-  // lowest: the least of the threads' maxima; at least CS * kThreads tokens lie at or above it.
-  __device__ __forceinline__ Edge top_k(int k, float p, float lowest, bool *p_done) {
+  // Adds the weights of the first n entries of the first CTA's list to s.kept of the warps in whose ranges they lie.
+  __device__ __forceinline__ void add_listed(int n) {
+    const Smem *first = CS > 1 ? cg::this_cluster().map_shared_rank(&s, 0) : &s;
+    const int seg = a.granules / kWarps * VEC;  // a warp's range
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const u64 e = first->list[i];
+      const unsigned at = (0xFFFFFFFFu - (uint32_t)e) - (unsigned)id0;
+      if (at < (unsigned)(kWarps * seg)) atomicAdd(&s.kept[at / seg], w(tr_unord((uint32_t)(e >> 32))));
+    }
+    __syncthreads();
+  }
+
+  // top-k, and the other rules with it where the list takes all tokens at or above the edge: then *left is the number of
+  // its entries that are left (else -1).
+  // low: at least k tokens lie at or above it, or -inf.
+  __device__ __forceinline__ Edge top_k(int k, float p, uint32_t min_p_key, float low, int *left) {
     const Edge none = {kNever, -1};
-    *p_done = false;
-    // bins over the logits that matter
-    float least = lowest;
-    const bool sure = k <= CS * kThreads && lowest > -INFINITY;
-    if (!sure) {  // over all logits
-      least = INFINITY;
-      each([&](float x, int) { least = x > -INFINITY ? fminf(least, x) : least; });
-#pragma unroll
-      for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
-      if (lane == 0) s.wsum[warp] = __float_as_uint(least);
-      __syncthreads();
-      for (int i = 0; i < kWarps; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
-      tell(__float_as_uint(least), 0);
-      for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
-    }
-    const float m = w.m, span = m - least;
-    if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
-    const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
-    clear();
-    each([&](float x, int) {
-      if (x >= least) atomicAdd(&s.hist[bin_of(m, x, scale)], 1u);
-    });
-    int b0, b1;
-    u64 above;
-    unsigned at_edge;
-    crossing([](int, u64 n) { return n; }, [&](u64) -> u64 { return (u64)k; }, [&](u64) -> u64 { return (u64)k; }, &b0, &b1,
-             &above, &at_edge);
-    if (b0 >= kBins) return none;  // fewer than k tokens: all are left
-    const bool whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
-    each([&](float x, int v) {
-      const int b = x >= least ? bin_of(m, x, scale) : kBins;
-      gather(whole ? b <= b0 : b == b0, x, v);
-    });
-    sync();
-    if (rank == 0) {
-      const int n = (int)s.listed, need = whole ? k : k - (int)above;
-      bool ok = n <= kList;
-      Edge e = none;
-      if (ok) {
-        sort_list(n);
-        e = edge_at(need - 1);
-        if (whole && p < 1.f) {
-          const int at = place(k, 0, [&](u64 all) { return share_of(p, all); });
-          e = edge_at(min(at, k - 1));
+    *left = -1;
+    bool whole = low > -INFINITY;
+    int need = k;
+    auto found = [&]() -> Found {  // of the gathered tokens
+      sync();
+      if (rank == 0) {
+        const int n = (int)s.listed;
+        Edge e = none;
+        int keep = -1;
+        if (n <= kList) {
+          sort_list(n);
+          if (whole) {
+            keep = min(k, n);
+            if (p < 1.f) keep = min(keep, place(keep, 0, [&](u64 all) { return share_of(p, all); }) + 1);
+            keep = at_least(keep, min_p_key);
+            e = edge_at(keep - 1);
+          } else {
+            e = edge_at(need - 1);
+          }
         }
+        tell_found(e, n <= kList, keep);
+      } else {
+        tell(0, 0);
       }
-      tell((u64)e.key << 32 | (uint32_t)e.id, ok);
-    } else {
-      tell(0, 0);
+      return hear_found();
+    };
+    Found f = {none, false, -1};
+    if (whole) {
+      // often the list takes all tokens from `low` on
+      each(low, [&](const float (&x)[VEC], int v) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) gather(x[e] >= low, x[e], v + e);
+      });
+      f = found();
     }
-    bool ok;
-    const Edge e = hear_edge(&ok);
-    if (!ok) return narrow_down_k(k);
-    *p_done = whole;
-    return e;
+    if (!f.ok) {
+      float least = low;
+      if (!(low > -INFINITY)) {  // bins over all logits
+        least = INFINITY;
+        each(-FLT_MAX, [&](const float (&x)[VEC], int) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
+        });
+#pragma unroll
+        for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+        if (lane == 0) s.wsum[warp] = __float_as_uint(least);
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
+        tell(__float_as_uint(least), 0);
+        for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
+      }
+      const float m = w.m, span = m - least;
+      if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
+      const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
+      clear();
+      each(least, [&](const float (&x)[VEC], int) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] >= least) atomicAdd(&s.hist[bin_of(m, x[e], scale)], 1u);
+      });
+      int b0, b1;
+      u64 above;
+      unsigned at_edge;
+      crossing([](int, u64 n) { return n; }, [&](u64) -> u64 { return (u64)k; }, [&](u64) -> u64 { return (u64)k; }, &b0,
+               &b1, &above, &at_edge);
+      if (b0 >= kBins) return none;         // fewer than k tokens: all are left
+      whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
+      if (!whole) need = k - (int)above;
+      // (a logit of bin b lies at or above m - (b + 1) / scale, but for the roundings: half a bin covers them)
+      each(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[VEC], int v) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int b = x[e] >= least ? bin_of(m, x[e], scale) : kBins;
+          gather(whole ? b <= b0 : b == b0, x[e], v + e);
+        }
+      });
+      f = found();
+    }
+    if (!f.ok) return narrow_down_k(k);
+    if (whole) {
+      *left = f.left;
+      if (threadIdx.x < kWarps) s.kept[threadIdx.x] = 0;
+      __syncthreads();
+      add_listed(f.left);
+    }
+    return f.edge;
+  }
+  // How many of the sorted list's first n entries have at least this key (the first one has).
+  __device__ __forceinline__ int at_least(int n, uint32_t key) {
+    int c = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) c += (uint32_t)(s.list[i] >> 32) >= key;
+    return (int)block_sum(c);
   }
   __device__ __noinline__ Edge narrow_down_k(int k) {
     u64 n = 0;
-    each([&](float x, int) { n += x > -INFINITY; });
+    each(-FLT_MAX, [&](const float (&x)[VEC], int) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) n += x[e] > -INFINITY;
+    });
     n = block_sum(n);
     tell(n, 0);
     n = 0;
@@ -617,20 +747,24 @@ struct Row {
     return n <= (u64)k ? none : narrow_down((u64)k, Left(none), [](float) -> u64 { return 1; });
   }
 
-  // top-p among the tokens that `old` leaves.
-  __device__ __forceinline__ Edge top_p(float p, Left old) {
+  // top-p among the tokens that `old` leaves; *known: the weights that are left, by warps, are in s.kept (unless min_p
+  // takes more).
+  __device__ __forceinline__ Edge top_p(float p, Left old, uint32_t min_p_key, bool *known) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
     // (2^16 of them: the sum of a slice stays below 2^32).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
-    const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
+    const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX), floor = fmaxf(old.at, w.floor());
     clear();
-    each([&](float x, int v) {
-      const float t = (m - x) * scale;
-      if (!(t < (float)(kBins - 1)) || !old(x, v)) return;
-      const int b = (int)t;
-      float f;  // within its power of two
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(((float)(b & ~63) - t) * (1.f / 64.f)));
-      atomicAdd(&s.hist[b], (unsigned)(f * 65535.f));
+    each(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[VEC], int v) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float t = (m - x[e]) * scale;
+        if (!(t < (float)(kBins - 1)) || !old(x[e], v + e)) continue;
+        const int b = (int)t;
+        float f;  // within its power of two
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(((float)(b & ~63) - t) * (1.f / 64.f)));
+        atomicAdd(&s.hist[b], (unsigned)(f * 65535.f));
+      }
     });
     int b0, b1;
     u64 base;
@@ -641,17 +775,31 @@ struct Row {
              [&](u64 all) -> u64 { return share_of(p, all + (all >> 14) + ((u64)a.V << 12)); }, &b0, &b1, &base, &own);
     // the exact sums, of all and of what lies above the bins that hold the edge
     u64 all = 0, above = 0;
-    each([&](float x, int v) {
-      const float t = (m - x) * scale;
-      const bool left = old(x, v);
-      const int b = (int)fminf(t, (float)kBins);
-      const u64 q = left ? w(x) : 0;
-      all += q;
-      above += b < b0 ? q : 0;
-      gather(left && b >= b0 && b <= b1, x, v);
+    each(floor, [&](const float (&x)[VEC], int v) {
+      u64 q[VEC];
+      w.of(x, q);
+      bool any = false;
+      unsigned in = 0;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int b = (int)fminf((m - x[e]) * scale, (float)kBins);
+        if (!old(x[e], v + e)) continue;
+        all += q[e];
+        if (b < b0) above += q[e];
+        else if (b <= b1) in |= 1u << e;
+      }
+      any = in != 0;
+      if (__any_sync(~0u, any)) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) gather(in >> e & 1, x[e], v + e);
+      }
     });
-    all = block_sum(all);
-    above = block_sum(above);
+    above = warp_sum(above);
+    if (lane == 0) s.kept[warp] = above;
+    all = block_sum(all);  // (its barrier makes s.kept known)
+    above = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) above += s.kept[i];
     tell(all, above);
     all = above = 0;
     for (int r = 0; r < CS; ++r) {
@@ -663,25 +811,32 @@ struct Row {
       const int n = (int)s.listed;
       Edge e = {kNever, -1};
       bool ok = n <= kList && above < target;
+      int keep = -1;
       if (ok) {
         sort_list(n);
         const int at = place(n, above, [&](u64) { return target; });
         ok = at < n;
-        if (ok) e = edge_at(at);
+        if (ok) {
+          e = edge_at(at);
+          keep = at + 1;
+        }
       }
-      tell((u64)e.key << 32 | (uint32_t)e.id, ok);
+      tell_found(e, ok, keep);
     } else {
       tell(0, 0);
     }
-    bool ok;
-    const Edge e = hear_edge(&ok);
-    return ok ? e : narrow_down_p(target, old);
+    const Found f = hear_found();
+    *known = false;
+    if (!f.ok) return narrow_down_p(target, old);
+    *known = f.edge.key >= min_p_key;
+    if (*known) add_listed(f.left);
+    return f.edge;
   }
   __device__ __noinline__ Edge narrow_down_p(u64 target, Left old) { return narrow_down(target, old, w); }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS,
+__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS, long long ahead,
                                                              const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
@@ -692,32 +847,45 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   r.rank = blockIdx.x - (int)row * CS;
   uint4 *const data = reinterpret_cast<uint4 *>(smem + sizeof(Smem));
   r.data = data;
-  const int seg = warp_granules(a.granules);
-  r.g0 = min(a.granules, r.warp * seg);
-  r.g1 = min(a.granules, r.g0 + seg);
+  r.g0 = r.warp * (a.granules / kWarps);
+  r.g1 = r.g0 + a.granules / kWarps;
   fill_table(s.table, table);
+  if (threadIdx.x == 0) s.listed = 0;
   tr_let_next_start();
   tr_wait_for_previous();
   // the slice, in granules that start on 16-byte boundaries; each lane copies what it reads
   const T *const x = reinterpret_cast<const T *>(a.x) + row * a.ld;
   const int off = (int)(((uintptr_t)x & 15) / sizeof(T));
   r.id0 = (int)((long long)r.rank * a.granules * VEC) - off;
-  for (int g = r.g0 + r.lane; g < r.g1; g += 32) {
-    const int id = r.id0 + g * VEC;
-    if (id >= 0 && id <= a.V - VEC) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(data + g)),
-                   "l"(x + id)
-                   : "memory");
-    } else {
-      T *to = reinterpret_cast<T *>(data + g);
-      for (int e = 0; e < VEC; ++e) to[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
+  {
+    // granules whose elements are all tokens: [whole0, whole1) of the slice
+    const int whole0 = r.id0 < 0 ? 1 : 0;
+    const int whole1 = r.id0 >= a.V ? 0 : (int)min((long long)a.granules, ((long long)a.V - r.id0) / VEC);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(data);
+    const T *from = x + r.id0;
+#pragma unroll 4
+    for (int g = r.g0 + r.lane; g < r.g1; g += 32) {
+      if (g >= whole0 && g < whole1) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + g * 16), "l"(from + g * VEC) : "memory");
+      } else {
+        T *edge = reinterpret_cast<T *>(data + g);
+        const int id = r.id0 + g * VEC;
+        for (int e = 0; e < VEC; ++e) edge[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
+      }
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
+  if (threadIdx.x == 0 && ahead > 0 && row + ahead < a.rows) {
+    // the slice that the CTA behind this one will want, into L2: memory works on while this one computes
+    const uintptr_t to = ((uintptr_t)(x + ahead * a.ld + r.id0 + off) + 15) & ~(uintptr_t)15;
+    const long long n = min((long long)a.granules * 16, (long long)((uintptr_t)(x + ahead * a.ld + a.V) - to)) & ~15ll;
+    if (n > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(to), "r"((int)n) : "memory");
+  }
+  int k = a.top_k ? a.top_k[row] : 0;
+  if (k >= a.V) k = 0;
   if (threadIdx.x == kThreads - 1) {  // the rules, while the slice is under way; 64-bit arithmetic once
     const float temp = a.temperature ? a.temperature[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
     s.temp = temp;
-    s.k = a.top_k ? a.top_k[row] : 0;
     s.p = a.top_p ? a.top_p[row] : 1.f;
     s.u = uniform_of(a.U[row]);
     s.c = log2e_over(temp);
@@ -725,14 +893,28 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-  // the largest logit, and the least of the threads' largest
+  // The largest logit; and, for top-k, one that at least k lie at or above: with N warps in the cluster, at least
+  // ceil(k / N) lanes of each have a largest logit there.
   float most = -INFINITY;
-  r.each([&](float y, int) { most = fmaxf(most, y); });
-  float least = most;
+#pragma unroll 4
+  for (int g = r.g0 + r.lane; g < r.g1; g += 32) most = fmaxf(most, Row<T>::most(data[g]));
+  const int lanes = k > 0 ? (int)(((long long)k + kWarps * CS - 1) / (kWarps * CS)) : 33;
+  float least = -INFINITY;
+  if (lanes <= 32) {
+    // the lanes' in falling order, the `lanes`-th of them
+    float v = most;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-    least = fminf(least, __shfl_xor_sync(~0u, least, o));
+    for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+      for (int j = n / 2; j; j /= 2) {
+        const float o = __shfl_xor_sync(~0u, v, j);
+        v = ((r.lane & n) == 0) == ((r.lane & j) == 0) ? fmaxf(v, o) : fminf(v, o);
+      }
+    least = __shfl_sync(~0u, v, lanes - 1);
+    most = __shfl_sync(~0u, v, 0);
+  } else {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
   }
   if (r.lane == 0) s.wsum[r.warp] = (u64)key_of(most) << 32 | key_of(least);
   __syncthreads();
@@ -752,7 +934,6 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     }
     low = min(low, (uint32_t)r.heard(k, 1));
   }
-  const int k = s.k;
   if (top <= kNever || !(s.temp >= FLT_MIN) || k == 1) {
     if (top <= kNever) {
       if (r.rank == 0 && threadIdx.x == 0) {
@@ -763,7 +944,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       if (threadIdx.x == 0) s.id = INT_MAX;
       __syncthreads();
       int first = INT_MAX;
-      r.each([&](float y, int v) { first = min(first, key_of(y) == top ? v : INT_MAX); });
+      const float m = tr_unord(top);
+      r.each(m, [&](const float (&y)[VEC], int v) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) first = min(first, y[e] == m ? v + e : INT_MAX);
+      });
       atomicMin(&s.id, first);
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -777,22 +962,30 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
 
   Edge edge = {kNever, -1};
   const float p = s.p;
-  bool p_done = !(p < 1.f);
-  if (k > 0 && k < a.V) {
-    bool done;
-    edge = r.top_k(k, p, low > kNever ? tr_unord(low) : -INFINITY, &done);
-    p_done |= done;
+  const uint32_t mp = min_p_key(s.below, r.w.m);
+  bool known = false;  // the weights that are left, by warps
+  int listed = -1;
+  if (k > 0) {
+    edge = r.top_k(k, p, mp, low > kNever ? tr_unord(low) : -INFINITY, &listed);
+    known = listed >= 0;
   }
-  if (!p_done) edge = r.top_p(p, Left(edge));
-  const Left left(with_min_p(edge, s.below, r.w.m));
+  if (p < 1.f && listed < 0) edge = r.top_p(p, Left(edge), mp, &known);
+  const Left left(with_min_p(edge, mp));
   const float u = s.u;
   u64 all;
-  const int id = r.first_past([&](float y, int v) -> u64 { return left(y, v) ? r.w(y) : 0; },
+  const int id = r.first_past(fmaxf(left.at, r.w.floor()),
+                              [&](const float (&y)[VEC], int v, unsigned which) {
+                                u64 q[VEC], sum = 0;
+                                r.w.of(y, q);
+#pragma unroll
+                                for (int e = 0; e < VEC; ++e) sum += (which >> e & 1) && left(y[e], v + e) ? q[e] : 0;
+                                return sum;
+                              },
                               [&](u64 sum) {
                                 bool exact;
                                 return part_of(u, sum, &exact);
                               },
-                              &all);
+                              &all, known);
   if (id >= 0 && threadIdx.x == 0) {
     a.token[row] = id;
     const float y = get(reinterpret_cast<const T *>(data), id - r.id0);
@@ -968,7 +1161,7 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
     all = block_sum(all, s.wsum);
     edge = select(x, V, r, share_of(p, all), Left(edge), s, w);
   }
-  const Left left(with_min_p(edge, min_p_below(a.min_p ? a.min_p[row] : 0.f, temp), w.m));
+  const Left left(with_min_p(edge, min_p_key(min_p_below(a.min_p ? a.min_p[row] : 0.f, temp), w.m)));
   auto weight_of = [&](int v) -> u64 {
     const float y = get(x, v);
     return left(y, v) ? w(y) : 0;
@@ -1006,9 +1199,9 @@ const Table &table() {
 template <typename T>
 int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
-  auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first granule
-    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC;
-    return (all + cs - 1) / cs;
+  auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first one: a multiple of 32 for each warp
+    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs;
+    return (mine + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
   };
   int cs = 1;
   while (cs < kMaxCluster && granules(cs) * 16 > kSlice) cs *= 2;
@@ -1025,8 +1218,11 @@ int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   a.granules = (int)granules(cs);
+  // rows that are in work at a time, about
+  const long long per_sm = std::min<long long>(3, (227 * 1024) / (sizeof(Smem) + a.granules * 16 + 1024));
+  const long long ahead = per_sm * tr_sm_count() / cs;
   return tr_launch_next(sample_kernel<T>,
-                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs, table());
+                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs, ahead, table());
 }
 
 }  // namespace
@@ -1045,7 +1241,7 @@ extern "C" int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64
   if (V > (1LL << 30) || rows > (1LL << 24) || ld > (1LL << 60) / rows) return TR_E_UNSUPPORTED;
   const int rc = tr_check_device();
   if (rc != TR_OK) return rc;
-  SampleArgs a = {logits, ld, (int)V, 62, temperature, top_p, min_p, U, top_k, token, logprob};
+  SampleArgs a = {logits, ld, rows, (int)V, 62, temperature, top_p, min_p, U, top_k, token, logprob};
   while (a.S > 30 && (V >> (62 - a.S)) > 1) --a.S;  // V weights of 2^S and less stay below 2^63
   cudaStream_t s = (cudaStream_t)stream;
   return ftype == TR_F32 ? launch<float>(a, rows, s) : launch<__nv_bfloat16>(a, rows, s);
