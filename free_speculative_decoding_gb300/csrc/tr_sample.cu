@@ -70,11 +70,12 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {  // a b + c
 // down.  x c is split into a multiple of 1 / 64 (adding and taking away 1.5 2^17 rounds to it) and a
 // rest whose error is below 2^-31; the multiple's power of two comes from a table, the rest's from a
 // polynomial.  Where |m c| passes 2^15, x is taken relative to m first: what has weight then
-// lies so near to m that the difference is exact.  A weight below 2^-62 is 0.
+// lies so near to m that the difference is exact.  A weight below 2^-S is 0.
 constexpr float kL1 = 6.931471805599453e-1f, kL2 = 2.402265069591007e-1f, kL3 = 5.550410866482158e-2f;  // ln2^i / i!
 struct Weight {
-  float m, base, least, c_hi, c_lo;  // least: below it (as y) there is no weight
-  int K, S;
+  float m, base, c_hi, c_lo;
+  float floor;          // logits up to this one have no weight
+  int shift, S;         // shift: (K - (bits of 0 + 1.5 2^17) / 64) + 63 - S, see whole()
   bool infinite;        // the largest logit is +inf
   const float2 *table;  // 2^(j / 64): 2^31 times it as a float, and as an integer (in its bits)
   __device__ __forceinline__ void set(float m_, float2 c, int S_, const float2 *t) {
@@ -87,47 +88,50 @@ struct Weight {
     const float mc = m * c_hi;
     const bool far = !(fabsf(mc) < 32700.f);  // infinite too
     base = far ? m : 0.f;
-    K = far ? 1 : (int)ceilf(mc + 0.01f);  // m c is off by 2^-9 at most
-    least = fmaxf((far ? 0.f : m) - 62.f / c_hi, -FLT_MAX);
+    const int K = far ? 1 : (int)ceilf(mc + 0.01f);  // m c is off by 2^-9 at most
+    shift = K + (0x48400000 >> 6) + 63 - S;
+    floor = infinite ? FLT_MAX : m - (float)(S - 2) / c_hi;  // an infinite temperature: -inf
+    if (floor == m) floor = tr_unord(tr_ord(m) - 1);         // the next number already is too far below
   }
+  // From p = q + 1.5 2^17, whose bits are 64 q more than those of 1.5 2^17, and e = 2^r - 1: the
+  // mantissa, times 2^32 and shifted right by less than 64 (for what lies above `floor`).
   __device__ __forceinline__ u64 whole(float p, float e) const {
-    const int n = __float_as_int(p) - 0x48400000;  // 64 q
+    const int n = __float_as_int(p);
     const float2 f = table[n & 63];
     const unsigned mant = __float_as_uint(f.y) + (unsigned)__float2int_rn(e * f.x);
-    return ((u64)mant << (S - 31)) >> min(K - (n >> 6), 63);
+    return ((u64)mant << 32) >> (shift - (n >> 6));
   }
-  // Of logits above -inf.
   __device__ __forceinline__ u64 operator()(float x) const {
     if (infinite) return x == m ? 1ull << S : 0;
-    const float y = fmaxf(x - base, least), p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
+    if (!(x > floor)) return 0;
+    const float y = x - base, p = fmaf(y, c_hi, 0x1.8p17f), q = p - 0x1.8p17f;
     const float r = fmaf(y, c_lo, fmaf(y, c_hi, -q));  // |r| <= 1 / 128 and a little
-    float e = fmaf(r, kL3, kL2);               // 2^r - 1
+    float e = fmaf(r, kL3, kL2);                       // 2^r - 1
     e = fmaf(r, e, kL1);
     return whole(p, e * r);
   }
-  // The weights of N logits, of those that are -inf or NaN 0: the same arithmetic, two to an instruction.
+  // The weights of N logits, the same arithmetic, two to an instruction; what lies up to `floor`, or is NaN, gets any
+  // number.
   template <int N>
   __device__ __forceinline__ void of(const float (&x)[N], u64 (&w)[N]) const {
     if (infinite) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = x[i] == m ? 1ull << S : 0;
+      for (int i = 0; i < N; ++i) w[i] = (*this)(x[i]);
       return;
     }
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       const F2 c = f2(c_hi, c_hi), magic = f2(0x1.8p17f, 0x1.8p17f);
-      const F2 y = f2(fmaxf(x[i] - base, least), fmaxf(x[i + 1] - base, least));
+      const F2 y = f2(x[i] - base, x[i + 1] - base);
       const F2 p = fma(y, c, magic), q = fma(p, f2(-1.f, -1.f), magic);
       const F2 r = fma(y, f2(c_lo, c_lo), fma(y, c, q));
       F2 e = fma(r, f2(kL3, kL3), f2(kL2, kL2));
       e = fma(r, e, f2(kL1, kL1)) * r;
       const float2 p1 = split(p), e1 = split(e);
-      w[i] = x[i] > -INFINITY ? whole(p1.x, e1.x) : 0;
-      w[i + 1] = x[i + 1] > -INFINITY ? whole(p1.y, e1.y) : 0;
+      w[i] = whole(p1.x, e1.x);
+      w[i + 1] = whole(p1.y, e1.y);
     }
   }
-  // The logit from which on there are weights, about: those below have none.
-  __device__ __forceinline__ float floor() const { return infinite ? m : fmaxf(base + least, -FLT_MAX); }
 };
 // c of a temperature, in two numbers.
 __device__ __forceinline__ float2 log2e_over(float temp) {
@@ -197,6 +201,15 @@ struct Left {
   int id;
   __device__ __forceinline__ Left(Edge e) : at(e.key <= kNever ? -INFINITY : tr_unord(e.key)), id(e.key <= kNever ? -1 : e.id) {}
   __device__ __forceinline__ bool operator()(float x, int v) const { return x > at || (x == at && v <= id); }
+  // Of these, the ones above `floor`.
+  __device__ __forceinline__ Left above(float floor) const {
+    Left l = *this;
+    if (floor >= at) {
+      l.at = floor;
+      l.id = -1;
+    }
+    return l;
+  }
 };
 
 // min_p's edge: the key of the least logit whose weight is at least min_p of the largest one's (0: off).
@@ -753,7 +766,8 @@ struct Row {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
     // (2^16 of them: the sum of a slice stays below 2^32).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
-    const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX), floor = fmaxf(old.at, w.floor());
+    const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
+    const Left weighted = old.above(w.floor);
     clear();
     each(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[VEC], int v) {
 #pragma unroll
@@ -761,9 +775,10 @@ struct Row {
         const float t = (m - x[e]) * scale;
         if (!(t < (float)(kBins - 1)) || !old(x[e], v + e)) continue;
         const int b = (int)t;
-        float f;  // within its power of two
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(((float)(b & ~63) - t) * (1.f / 64.f)));
-        atomicAdd(&s.hist[b], (unsigned)(f * 65535.f));
+        float f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(t * (-1.f / 64.f)));
+        // in (2^-(o + 1), 2^-o], o = b / 64: 16 bits of it from the float's own
+        atomicAdd(&s.hist[b], 32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8));
       }
     });
     int b0, b1;
@@ -775,21 +790,21 @@ struct Row {
              [&](u64 all) -> u64 { return share_of(p, all + (all >> 14) + ((u64)a.V << 12)); }, &b0, &b1, &base, &own);
     // the exact sums, of all and of what lies above the bins that hold the edge
     u64 all = 0, above = 0;
-    each(floor, [&](const float (&x)[VEC], int v) {
+    const float first = (float)b0, behind = b1 < kBins ? (float)(b1 + 1) : INFINITY;  // of the bins with the edge
+    each(weighted.at, [&](const float (&x)[VEC], int v) {
       u64 q[VEC];
       w.of(x, q);
-      bool any = false;
       unsigned in = 0;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int b = (int)fminf((m - x[e]) * scale, (float)kBins);
-        if (!old(x[e], v + e)) continue;
-        all += q[e];
-        if (b < b0) above += q[e];
-        else if (b <= b1) in |= 1u << e;
+        const float t = (m - x[e]) * scale;
+        const bool left = weighted(x[e], v + e);
+        const u64 n = left ? q[e] : 0;
+        all += n;
+        above += t < first ? n : 0;
+        in |= t >= first && t < behind && left ? 1u << e : 0;
       }
-      any = in != 0;
-      if (__any_sync(~0u, any)) {
+      if (__any_sync(~0u, in != 0)) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) gather(in >> e & 1, x[e], v + e);
       }
@@ -970,10 +985,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     known = listed >= 0;
   }
   if (p < 1.f && listed < 0) edge = r.top_p(p, Left(edge), mp, &known);
-  const Left left(with_min_p(edge, mp));
+  const Left left = Left(with_min_p(edge, mp)).above(r.w.floor);
   const float u = s.u;
   u64 all;
-  const int id = r.first_past(fmaxf(left.at, r.w.floor()),
+  const int id = r.first_past(left.at,
                               [&](const float (&y)[VEC], int v, unsigned which) {
                                 u64 q[VEC], sum = 0;
                                 r.w.of(y, q);
@@ -1180,7 +1195,7 @@ __global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a
 
 // A slice's bytes: three CTAs share an SM up to the first, one has it up to the second; its tokens, so
 // that top-p's sums of 16-bit weights stay below 2^32.
-constexpr long long kSlice = 64 * 1024, kMostSlice = 208 * 1024, kMostTokens = 65536;
+constexpr long long kSlice = 64 * 1024, kMostSlice = 208 * 1024, kMostTokens = 65535;
 
 const Table &table() {
   static const Table t = [] {
