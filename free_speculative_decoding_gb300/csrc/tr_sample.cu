@@ -37,6 +37,7 @@ struct SampleArgs {
   int32_t *token;
   float *logprob;
   int granules;  // of a CTA's slice, kWarps * 32 or a multiple
+  int drop;      // bits that top-p's histogram gives up
 };
 
 // The order of a logit; NaN and -inf (never drawn) are 0x007FFFFF, below every other.
@@ -256,12 +257,15 @@ struct alignas(128) Smem {  // the slice lies behind it
 
 static_assert(sizeof(Smem) % 16 == 0);
 
-template <typename T>
+// HELD: the CTA's slice is in shared memory; else it is read from global memory (L2) in every pass.
+template <typename T, bool HELD>
 struct Row {
   static constexpr int VEC = 16 / sizeof(T);
   const SampleArgs &a;
   Smem &s;
-  const uint4 *data;   // the CTA's slice, 16-byte granules; what is no token is -inf
+  const uint4 *data;   // held: the slice's 16-byte granules; what is no token is -inf
+  const T *x;          // the row
+  int whole0, whole1;  // granules of the slice whose elements are all tokens
   int CS, rank, parity = 0;
   int warp, lane;
   int id0;             // ID of the slice's first element (below 0: no token)
@@ -278,19 +282,62 @@ struct Row {
     else asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
   }
 
-  // f(x[VEC], first ID) for the warp's granules, 32 * VEC consecutive elements at a time, where any of these is
-  // at or above `floor`; all lanes call f alike.
-  template <typename F>
-  __device__ __forceinline__ void each(float floor, F f) const {
-#pragma unroll 2
-    for (int g = g0 + lane; g < g1; g += 32) {  // a multiple of 32
-      float x[VEC];
-      if (!__any_sync(~0u, unpack(data[g], x) >= floor)) continue;
-      f(x, id0 + g * VEC);
+  // Granule g of the slice, some of whose elements may be no tokens.
+  __device__ __forceinline__ uint4 edge(int g) const {
+    union {
+      uint4 v;
+      T e[VEC];
+    } u;
+    const int id = id0 + g * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) u.e[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
+    return u.v;
+  }
+  __device__ __forceinline__ const uint4 *granules() const {
+    return HELD ? data : reinterpret_cast<const uint4 *>(x + id0);
+  }
+  __device__ __forceinline__ uint4 fetch(int g) const {
+    return HELD || (g >= whole0 && g < whole1) ? granules()[g] : edge(g);
+  }
+  // f(granule, first ID) for the warp's granules, a batch of 32 at a time, N batches under way; all lanes call f
+  // alike.
+  template <int N, typename F>
+  __device__ __forceinline__ void scan(F f) const {
+    const int n = (g1 - g0) / 32;  // batches; those from i0 to i1 hold nothing but tokens
+    const int i0 = HELD || g0 >= whole0 ? 0 : 1, i1 = HELD ? n : min(n, (whole1 - g0) >> 5);
+    const uint4 *p = granules() + g0 + lane;
+    int id = id0 + (g0 + lane) * VEC;
+    for (int i = 0; i < n;) {
+      if (i >= i0 && i + N <= i1) {
+        uint4 v[N];
+#pragma unroll
+        for (int b = 0; b < N; ++b) v[b] = p[b * 32];
+#pragma unroll
+        for (int b = 0; b < N; ++b) f(v[b], id + b * (32 * VEC));
+        i += N;
+        p += N * 32;
+        id += N * 32 * VEC;
+      } else {
+        f(i >= i0 && i < i1 ? *p : fetch(g0 + i * 32 + lane), id);
+        ++i;
+        p += 32;
+        id += 32 * VEC;
+      }
     }
   }
+  // f(x[VEC], first ID), where any of the warp's elements is at or above `floor`.
+  template <int N, typename F>
+  __device__ __forceinline__ void each(float floor, F f) const {
+    scan<N>([&](const uint4 &v, int id) {
+      if (!__any_sync(~0u, most(v) >= floor)) return;
+      float y[VEC];
+      unpack(v, y);
+      f(y, id);
+    });
+  }
+  static constexpr int kLight = 16 / VEC, kHeavy = 8 / VEC;  // batches under way, of passes that do little or much
   // A granule's elements; the largest.
-  static __device__ __forceinline__ float unpack(const uint4 &v, float (&x)[VEC]) {
+  static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[VEC]) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -301,11 +348,12 @@ struct Row {
         x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
       }
     }
-    return most(v);
   }
   static __device__ __forceinline__ float most(const uint4 &v) {
     if constexpr (VEC == 4) {
-      return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+      float m;
+      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
+      return fmaxf(m, __uint_as_float(v.w));
     } else {
       auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
       const __nv_bfloat162 m = __hmax2(__hmax2(b(v.x), b(v.y)), __hmax2(b(v.z), b(v.w)));
@@ -361,7 +409,7 @@ struct Row {
   __device__ __forceinline__ int first_past(float floor, F amounts, G target_of, u64 *all, bool known = false) {
     u64 mine = 0;
     if (!known) {
-      each(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
+      each<kHeavy>(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
       mine = warp_sum(mine);
     }
     if (lane == 0) s.wsum[warp] = known ? s.kept[warp] : mine;
@@ -387,7 +435,7 @@ struct Row {
     g0 = p0;
     g1 = p1;
     mine = 0;
-    each(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
+    each<kHeavy>(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
     mine = warp_sum(mine);
     __syncthreads();
     if (lane == 0) s.wsum[warp] = mine;
@@ -397,7 +445,7 @@ struct Row {
     if (before <= target && before + mine > target) {  // one warp
       for (int g = p0; g < p1; g += 32) {
         float x[VEC];
-        unpack(data[g + lane], x);
+        unpack(fetch(g + lane), x);
         const int id = id0 + (g + lane) * VEC;
         const u64 own = amounts(x, id, ~0u);
         u64 c = own;
@@ -569,7 +617,7 @@ struct Row {
       for (int i = threadIdx.x; i < 256; i += kThreads) s.wide[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      each(-FLT_MAX, [&](const float (&x)[VEC], int v) {
+      each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int v) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const uint32_t k = key_of(x[e]);
@@ -682,7 +730,7 @@ struct Row {
     Found f = {none, false, -1};
     if (whole) {
       // often the list takes all tokens from `low` on
-      each(low, [&](const float (&x)[VEC], int v) {
+      each<kLight>(low, [&](const float (&x)[VEC], int v) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) gather(x[e] >= low, x[e], v + e);
       });
@@ -692,7 +740,7 @@ struct Row {
       float least = low;
       if (!(low > -INFINITY)) {  // bins over all logits
         least = INFINITY;
-        each(-FLT_MAX, [&](const float (&x)[VEC], int) {
+        each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
         });
@@ -708,7 +756,7 @@ struct Row {
       if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
       const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
       clear();
-      each(least, [&](const float (&x)[VEC], int) {
+      each<kHeavy>(least, [&](const float (&x)[VEC], int) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           if (x[e] >= least) atomicAdd(&s.hist[bin_of(m, x[e], scale)], 1u);
@@ -722,7 +770,7 @@ struct Row {
       whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
       if (!whole) need = k - (int)above;
       // (a logit of bin b lies at or above m - (b + 1) / scale, but for the roundings: half a bin covers them)
-      each(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[VEC], int v) {
+      each<kLight>(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[VEC], int v) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int b = x[e] >= least ? bin_of(m, x[e], scale) : kBins;
@@ -748,7 +796,7 @@ struct Row {
   }
   __device__ __noinline__ Edge narrow_down_k(int k) {
     u64 n = 0;
-    each(-FLT_MAX, [&](const float (&x)[VEC], int) {
+    each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) n += x[e] > -INFINITY;
     });
@@ -764,12 +812,12 @@ struct Row {
   // takes more).
   __device__ __forceinline__ Edge top_p(float p, Left old, uint32_t min_p_key, bool *known) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
-    // (2^16 of them: the sum of a slice stays below 2^32).  A token beyond the last bin but one has a weight below
+    // (2^16 of them: the sum of a slice of 65535 tokens stays below 2^32; of longer ones some bits are dropped).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
     const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
     const Left weighted = old.above(w.floor);
     clear();
-    each(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[VEC], int v) {
+    each<kHeavy>(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[VEC], int v) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float t = (m - x[e]) * scale;
@@ -778,20 +826,21 @@ struct Row {
         float f;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(t * (-1.f / 64.f)));
         // in (2^-(o + 1), 2^-o], o = b / 64: 16 bits of it from the float's own
-        atomicAdd(&s.hist[b], 32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8));
+        atomicAdd(&s.hist[b], (32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8)) >> a.drop);
       }
     });
     int b0, b1;
     u64 base;
     unsigned own;
-    // in units of 2^-43
-    crossing([](int b, u64 n) { return (n << 27) >> (b >> 6); },
-             [&](u64 all) -> u64 { return share_of(p, all - (all >> 14)); },
-             [&](u64 all) -> u64 { return share_of(p, all + (all >> 14) + ((u64)a.V << 12)); }, &b0, &b1, &base, &own);
+    // in units of 2^-S
+    const int off = 14 - a.drop;  // sums are off by less than 2^-off
+    crossing([&](int b, u64 n) { return (n << (a.S - 16 + a.drop)) >> (b >> 6); },
+             [&](u64 all) -> u64 { return share_of(p, all - (all >> off)); },
+             [&](u64 all) -> u64 { return share_of(p, all + (all >> off) + ((u64)a.V << max(a.S - 31, 0))); }, &b0, &b1, &base, &own);
     // the exact sums, of all and of what lies above the bins that hold the edge
     u64 all = 0, above = 0;
     const float first = (float)b0, behind = b1 < kBins ? (float)(b1 + 1) : INFINITY;  // of the bins with the edge
-    each(weighted.at, [&](const float (&x)[VEC], int v) {
+    each<kHeavy>(weighted.at, [&](const float (&x)[VEC], int v) {
       u64 q[VEC];
       w.of(x, q);
       unsigned in = 0;
@@ -850,13 +899,14 @@ struct Row {
   __device__ __noinline__ Edge narrow_down_p(u64 target, Left old) { return narrow_down(target, old, w); }
 };
 
-template <typename T>
+template <typename T, bool HELD>
 __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS, long long ahead,
                                                              const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
-  Row<T> r(a, s);
-  constexpr int VEC = Row<T>::VEC;
+  using R = Row<T, HELD>;
+  R r(a, s);
+  constexpr int VEC = R::VEC;
   const long long row = blockIdx.x / CS;
   r.CS = CS;
   r.rank = blockIdx.x - (int)row * CS;
@@ -872,15 +922,15 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   const T *const x = reinterpret_cast<const T *>(a.x) + row * a.ld;
   const int off = (int)(((uintptr_t)x & 15) / sizeof(T));
   r.id0 = (int)((long long)r.rank * a.granules * VEC) - off;
-  {
-    // granules whose elements are all tokens: [whole0, whole1) of the slice
-    const int whole0 = r.id0 < 0 ? 1 : 0;
-    const int whole1 = r.id0 >= a.V ? 0 : (int)min((long long)a.granules, ((long long)a.V - r.id0) / VEC);
+  r.x = x;
+  r.whole0 = r.id0 < 0 ? 1 : 0;
+  r.whole1 = r.id0 >= a.V ? 0 : (int)min((long long)a.granules, ((long long)a.V - r.id0) / VEC);
+  if (HELD) {
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(data);
     const T *from = x + r.id0;
 #pragma unroll 4
     for (int g = r.g0 + r.lane; g < r.g1; g += 32) {
-      if (g >= whole0 && g < whole1) {
+      if (g >= r.whole0 && g < r.whole1) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + g * 16), "l"(from + g * VEC) : "memory");
       } else {
         T *edge = reinterpret_cast<T *>(data + g);
@@ -888,9 +938,9 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
         for (int e = 0; e < VEC; ++e) edge[e] = id + e >= 0 && id + e < a.V ? x[id + e] : (T)-INFINITY;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  if (threadIdx.x == 0 && ahead > 0 && row + ahead < a.rows) {
+  if (HELD && threadIdx.x == 0 && ahead > 0 && row + ahead < a.rows) {
     // the slice that the CTA behind this one will want, into L2: memory works on while this one computes
     const uintptr_t to = ((uintptr_t)(x + ahead * a.ld + r.id0 + off) + 15) & ~(uintptr_t)15;
     const long long n = min((long long)a.granules * 16, (long long)((uintptr_t)(x + ahead * a.ld + a.V) - to)) & ~15ll;
@@ -906,13 +956,12 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     s.c = log2e_over(temp);
     s.below = min_p_below(mp, temp);
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (HELD) asm volatile("cp.async.wait_group 0;" ::: "memory");
 
   // The largest logit; and, for top-k, one that at least k lie at or above: with N warps in the cluster, at least
   // ceil(k / N) lanes of each have a largest logit there.
   float most = -INFINITY;
-#pragma unroll 4
-  for (int g = r.g0 + r.lane; g < r.g1; g += 32) most = fmaxf(most, Row<T>::most(data[g]));
+  r.template scan<R::kLight>([&](const uint4 &v, int) { most = fmaxf(most, R::most(v)); });
   const int lanes = k > 0 ? (int)(((long long)k + kWarps * CS - 1) / (kWarps * CS)) : 33;
   float least = -INFINITY;
   if (lanes <= 32) {
@@ -960,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       __syncthreads();
       int first = INT_MAX;
       const float m = tr_unord(top);
-      r.each(m, [&](const float (&y)[VEC], int v) {
+      r.template each<R::kLight>(m, [&](const float (&y)[VEC], int v) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) first = min(first, y[e] == m ? v + e : INT_MAX);
       });
@@ -1003,199 +1052,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
                               &all, known);
   if (id >= 0 && threadIdx.x == 0) {
     a.token[row] = id;
-    const float y = get(reinterpret_cast<const T *>(data), id - r.id0);
+    const float y = get(x, id);
     if (a.logprob) a.logprob[row] = (float)log((double)r.w(y) / (double)all);
   }
 }
-
-// ---------------------------------------------------------------------------
-// longer rows: one CTA reads the row from global memory (L2) in every pass
-// ---------------------------------------------------------------------------
-
-constexpr int kBigThreads = 512;
-constexpr int kBigWarps = kBigThreads / 32;
-
-struct BigSmem {
-  float2 table[64];
-  u64 hist[256];
-  u64 wsum[kBigWarps];
-  u64 best;
-  u64 base;      // of the keys above
-  uint32_t prefix;
-  int id;
-};
-
-// Sum over the block, in every thread (two barriers).
-__device__ __forceinline__ u64 block_sum(u64 v, u64 *wsum) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
-  for (int i = 0; i < kBigWarps; ++i) s += wsum[i];
-  __syncthreads();
-  return s;
-}
-
-// The range of IDs of a warp: consecutive ones.
-struct Range {
-  int lo, hi;
-};
-
-// The lowest ID at which the running sum of weight_of(id) over ascending IDs passes
-// `target` (V if it never does).  Every thread gets it.
-template <typename F>
-__device__ __forceinline__ int first_past(u64 target, Range r, BigSmem &s, F weight_of) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  u64 sum = 0;
-  for (int v = r.lo + lane; v < r.hi; v += 32) sum += weight_of(v);
-  sum = warp_sum(sum);
-  if (threadIdx.x == 0) s.id = INT_MAX;
-  if (lane == 0) s.wsum[warp] = sum;
-  __syncthreads();
-  u64 before = 0;
-  for (int i = 0; i < warp; ++i) before += s.wsum[i];
-  if (before <= target && before + sum > target) {  // one warp at most
-    for (int v0 = r.lo; v0 < r.hi; v0 += 32) {
-      u64 c = v0 + lane < r.hi ? weight_of(v0 + lane) : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(~0u, c, o);
-        if (lane >= o) c += y;
-      }
-      const unsigned past = __ballot_sync(~0u, before + c > target);
-      if (past) {
-        if (lane == 0) s.id = v0 + __ffs(past) - 1;
-        break;
-      }
-      before += __shfl_sync(~0u, c, 31);
-    }
-  }
-  __syncthreads();
-  const int id = s.id;
-  __syncthreads();
-  return id;
-}
-
-// The edge that leaves, of the tokens whose key is above `never`, the first ones in
-// falling order whose amounts sum to at least `target` (>= 1): the key is narrowed down by
-// eight bits a pass.  amount(x) of equal keys is equal.
-template <typename T, typename F>
-__device__ __forceinline__ Edge select(const T *x, int V, Range r, u64 target, Left old, BigSmem &s, F amount) {
-  uint32_t prefix = 0;
-  u64 base = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kBigThreads) s.hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int v = threadIdx.x; v < V; v += kBigThreads) {
-      const float y = get(x, v);
-      const uint32_t k = key_of(y);
-      if ((k & mask) != prefix || !old(y, v)) continue;
-      const u64 a = amount(y);
-      if (a) atomicAdd(&s.hist[(k >> shift) & 255], a);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 sum = base;
-      int b = 255;
-      for (; b > 0; --b) {
-        if (sum + s.hist[b] >= target) break;
-        sum += s.hist[b];
-      }
-      s.base = sum;
-      s.prefix = prefix | (uint32_t)b << shift;
-    }
-    __syncthreads();
-    base = s.base;
-    prefix = s.prefix;
-    __syncthreads();
-  }
-  // of the tokens at the edge the lowest IDs, as many as are needed
-  const u64 each = amount(tr_unord(prefix));
-  const u64 take = each ? (target - base + each - 1) / each : 0;
-  Edge e = {prefix, INT_MAX};
-  if (take)
-    e.id = first_past(take - 1, r, s, [&](int v) -> u64 {
-      const float y = get(x, v);
-      return key_of(y) == prefix && old(y, v);
-    });
-  return e;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kBigThreads) big_row_kernel(const SampleArgs a, const __grid_constant__ Table table) {
-  __shared__ BigSmem s;
-  tr_let_next_start();
-  tr_wait_for_previous();
-  const long long row = blockIdx.x;
-  const T *x = reinterpret_cast<const T *>(a.x) + row * a.ld;
-  const int V = a.V, warp = threadIdx.x >> 5;
-  const int seg = (int)(((long long)V + kBigWarps - 1) / kBigWarps);
-  const Range r = {(int)min((long long)V, (long long)warp * seg), (int)min((long long)V, (long long)(warp + 1) * seg)};
-  fill_table(s.table, table);
-  if (threadIdx.x == 0) s.best = 0;
-  __syncthreads();
-
-  // the largest logit and its lowest ID
-  u64 best = 0;
-  for (int v = threadIdx.x; v < V; v += kBigThreads) {
-    const u64 k = (u64)key_of(get(x, v)) << 32 | (0xFFFFFFFFu - (uint32_t)v);
-    best = k > best ? k : best;
-  }
-  atomicMax(&s.best, best);
-  __syncthreads();
-  best = s.best;
-  const uint32_t top = (uint32_t)(best >> 32);
-  const float temp = a.temperature ? a.temperature[row] : 1.f;
-  if (top <= kNever || !(temp >= FLT_MIN)) {
-    if (threadIdx.x == 0) {
-      a.token[row] = top <= kNever ? -1 : (int)(0xFFFFFFFFu - (uint32_t)best);
-      if (a.logprob) a.logprob[row] = top <= kNever ? -INFINITY : 0.f;
-    }
-    return;
-  }
-  Weight w;
-  w.set(tr_unord(top), log2e_over(temp), a.S, s.table);
-
-  Edge edge = {kNever, -1};
-  const int k = a.top_k ? a.top_k[row] : 0;
-  if (k > 0 && k < V) {
-    // fewer than k tokens in all: the edge stays below them
-    u64 n = 0;
-    for (int v = threadIdx.x; v < V; v += kBigThreads) n += key_of(get(x, v)) > kNever;
-    n = block_sum(n, s.wsum);
-    if (n > (u64)k) edge = select(x, V, r, (u64)k, Left(edge), s, [](float) -> u64 { return 1; });
-  }
-  const float p = a.top_p ? a.top_p[row] : 1.f;
-  if (p < 1.f) {
-    u64 all = 0;
-    for (int v = threadIdx.x; v < V; v += kBigThreads) {
-      const float y = get(x, v);
-      if (Left(edge)(y, v)) all += w(y);
-    }
-    all = block_sum(all, s.wsum);
-    edge = select(x, V, r, share_of(p, all), Left(edge), s, w);
-  }
-  const Left left(with_min_p(edge, min_p_key(min_p_below(a.min_p ? a.min_p[row] : 0.f, temp), w.m)));
-  auto weight_of = [&](int v) -> u64 {
-    const float y = get(x, v);
-    return left(y, v) ? w(y) : 0;
-  };
-  u64 all = 0;
-  for (int v = threadIdx.x; v < V; v += kBigThreads) all += weight_of(v);
-  all = block_sum(all, s.wsum);
-  const float u = uniform_of(a.U[row]);
-  bool exact;
-  const int id = first_past(part_of(u, all, &exact), r, s, weight_of);
-  if (threadIdx.x == 0) {
-    a.token[row] = id;
-    if (a.logprob) a.logprob[row] = (float)log((double)w(get(x, id)) / (double)all);
-  }
-}
-
-// A slice's bytes: three CTAs share an SM up to the first, one has it up to the second; its tokens, so
-// that top-p's sums of 16-bit weights stay below 2^32.
-constexpr long long kSlice = 64 * 1024, kMostSlice = 208 * 1024, kMostTokens = 65535;
 
 const Table &table() {
   static const Table t = [] {
@@ -1211,33 +1071,46 @@ const Table &table() {
   return t;
 }
 
+// Many rows: a CTA each (three on an SM), which reads it from L2 in every pass after the first.  Few: a cluster
+// each, in whose shared memory it lies, 64 KB to a CTA.
+constexpr long long kSlice = 64 * 1024;
+constexpr int kMostTokens = 65535;  // of a slice, see top_p
+
+template <typename T, bool HELD>
+int launch(SampleArgs a, int cs, size_t smem, long long ahead, cudaStream_t s) {
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  TR_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(sizeof(Smem) + kSlice)));
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
+  return tr_launch_next(sample_kernel<T, HELD>, {dim3((unsigned)(a.rows * cs)), kThreads, smem, cs}, s, a, cs, ahead, table());
+}
+
 template <typename T>
-int launch(SampleArgs a, int64_t rows, cudaStream_t s) {
+int launch(SampleArgs a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
   auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first one: a multiple of 32 for each warp
     const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs;
     return (mine + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
   };
+  const long long slots = 3LL * tr_sm_count();
   int cs = 1;
-  while (cs < kMaxCluster && granules(cs) * 16 > kSlice) cs *= 2;
-  if (granules(cs) * 16 > kMostSlice || granules(cs) * VEC > kMostTokens)
-    return tr_launch_next(big_row_kernel<T>, {dim3((unsigned)rows), kBigThreads}, s, a, table());
-  // few rows: more SMs for each, down to slices of 4 KB
-  while (cs < kMaxCluster && rows * cs * 2 <= 3LL * tr_sm_count() && granules(cs) * 16 > 8192) cs *= 2;
-  static std::atomic<bool> set[64];  // per device
-  int dev = 0;
-  TR_TRY_CUDA(cudaGetDevice(&dev));
-  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)(sizeof(Smem) + kMostSlice)));
-    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
-  }
+  while (cs < kMaxCluster && a.rows * cs * 2 <= slots) cs *= 2;
+  bool held = granules(cs) * 16 <= kSlice;
+  if (!held && cs == kMaxCluster / 2 && granules(kMaxCluster) * 16 <= kSlice && a.rows <= slots / 4) held = true, cs = kMaxCluster;
+  while (cs > 1 && held && granules(cs) * 16 <= 4096) cs /= 2;
+  while (cs < kMaxCluster && granules(cs) * VEC > kMostTokens) cs *= 2;
   a.granules = (int)granules(cs);
+  a.drop = 0;
+  while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
+  const size_t slice = held ? (size_t)a.granules * 16 : 0;
   // rows that are in work at a time, about
-  const long long per_sm = std::min<long long>(3, (227 * 1024) / (sizeof(Smem) + a.granules * 16 + 1024));
-  const long long ahead = per_sm * tr_sm_count() / cs;
-  return tr_launch_next(sample_kernel<T>,
-                        {dim3((unsigned)(rows * cs)), kThreads, sizeof(Smem) + (size_t)a.granules * 16, cs}, s, a, cs, ahead, table());
+  const long long per_sm = std::min<long long>(3, (227 * 1024) / (long long)(sizeof(Smem) + slice + 1024));
+  return held ? launch<T, true>(a, cs, sizeof(Smem) + slice, per_sm * tr_sm_count() / cs, s)
+              : launch<T, false>(a, cs, sizeof(Smem), 0, s);
 }
 
 }  // namespace
@@ -1259,5 +1132,5 @@ extern "C" int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64
   SampleArgs a = {logits, ld, rows, (int)V, 62, temperature, top_p, min_p, U, top_k, token, logprob};
   while (a.S > 30 && (V >> (62 - a.S)) > 1) --a.S;  // V weights of 2^S and less stay below 2^63
   cudaStream_t s = (cudaStream_t)stream;
-  return ftype == TR_F32 ? launch<float>(a, rows, s) : launch<__nv_bfloat16>(a, rows, s);
+  return ftype == TR_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
 }
