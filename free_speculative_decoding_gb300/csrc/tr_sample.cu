@@ -15,6 +15,7 @@
 // A last pass sums the weights that are left over ascending IDs and finds the uniform's place.
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 #include <cstring>
 
 #include <atomic>
@@ -238,10 +239,10 @@ constexpr int kList = 1024;
 
 struct alignas(128) Smem {  // the slice lies behind it
   float2 table[64];
-  u64 box[2][kMaxCluster][2];     // what the cluster's CTAs have told this one, of two exchanges
+  u64 box[2][kMaxCluster][3];     // what the cluster's CTAs have told this one, of two exchanges
   u64 wsum[kWarps];
   u64 kept[kWarps];               // the weights that are left in the warps' ranges, where they are known
-  unsigned listed;                // tokens that were to go to the list
+  unsigned listed;                // tokens that were to go to this CTA's list
   float temp, p, u;               // the row's rules
   float2 c;
   double below;
@@ -249,13 +250,14 @@ struct alignas(128) Smem {  // the slice lies behind it
   int id;
   u64 cum;
   union {
-    unsigned hist[kBins];
+    alignas(16) unsigned hist[kBins];
     u64 wide[256];
-    u64 list[kList];              // key << 32 | ~ID
+    u64 list[kList];              // key << 32 | ~ID, of all the cluster's CTAs
   };
+  u64 own[kList];                 // the same, gathered by this one
 };
 
-static_assert(sizeof(Smem) % 16 == 0);
+static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, hist) % 16 == 0);
 
 // HELD: the CTA's slice is in shared memory; else it is read from global memory (L2) in every pass.
 template <typename T, bool HELD>
@@ -325,30 +327,30 @@ struct Row {
       }
     }
   }
-  // f(x[VEC], first ID), where any of the warp's elements is at or above `floor`.
+  // f(x[4], first ID), where any of the warp's elements is at or above `floor`.
   template <int N, typename F>
   __device__ __forceinline__ void each(float floor, F f) const {
     scan<N>([&](const uint4 &v, int id) {
-      if (!__any_sync(~0u, most(v) >= floor)) return;
-      float y[VEC];
-      unpack(v, y);
-      f(y, id);
+      if (__any_sync(~0u, most(v) >= floor)) by_four(v, id, f);
     });
   }
-  static constexpr int kLight = 16 / VEC, kHeavy = 8 / VEC;  // batches under way, of passes that do little or much
-  // A granule's elements; the largest.
-  static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[VEC]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  template <typename F>
+  static __device__ __forceinline__ void by_four(const uint4 &v, int id, F f) {
+    if constexpr (VEC == 4) {
+      const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+      f(x, id);
+    } else {
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (VEC == 4) {
-        x[e] = __uint_as_float(u[e]);
-      } else {
-        x[2 * e] = __uint_as_float(u[e] << 16);
-        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      for (int h = 0; h < 2; ++h) {
+        const float x[4] = {__uint_as_float(u[2 * h] << 16), __uint_as_float(u[2 * h] & 0xFFFF0000u),
+                            __uint_as_float(u[2 * h + 1] << 16), __uint_as_float(u[2 * h + 1] & 0xFFFF0000u)};
+        f(x, id + 4 * h);
       }
     }
   }
+  static constexpr int kLight = 16 / VEC, kHeavy = 8 / VEC;  // batches under way, of passes that do little or much
+  // A granule's largest element.
   static __device__ __forceinline__ float most(const uint4 &v) {
     if constexpr (VEC == 4) {
       float m;
@@ -373,14 +375,15 @@ struct Row {
     return r;
   }
 
-  // Tells every CTA of the cluster two numbers of this one (the same in all threads) and waits for
+  // Tells every CTA of the cluster up to three numbers of this one (the same in all threads) and waits for
   // theirs: heard(r, i).
-  __device__ __forceinline__ void tell(u64 x, u64 y) {
+  __device__ __forceinline__ void tell(u64 x, u64 y = 0, u64 z = 0) {
     if ((int)threadIdx.x < CS) {
       u64 *to = &s.box[parity][rank][0];
       if (CS > 1) to = cg::this_cluster().map_shared_rank(to, threadIdx.x);
       to[0] = x;
       to[1] = y;
+      to[2] = z;
     }
     sync();
     parity ^= 1;
@@ -409,7 +412,7 @@ struct Row {
   __device__ __forceinline__ int first_past(float floor, F amounts, G target_of, u64 *all, bool known = false) {
     u64 mine = 0;
     if (!known) {
-      each<kHeavy>(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
+      each<kHeavy>(floor, [&](const float (&x)[4], int v) { mine += amounts(x, v, ~0u); });
       mine = warp_sum(mine);
     }
     if (lane == 0) s.wsum[warp] = known ? s.kept[warp] : mine;
@@ -417,7 +420,7 @@ struct Row {
     u64 cta = 0, before = 0, sum = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) cta += s.wsum[i];
-    tell(cta, 0);
+    tell(cta);
     for (int r = 0; r < CS; ++r) {
       if (r < rank) before += heard(r, 0);
       sum += heard(r, 0);
@@ -435,7 +438,7 @@ struct Row {
     g0 = p0;
     g1 = p1;
     mine = 0;
-    each<kHeavy>(floor, [&](const float (&x)[VEC], int v) { mine += amounts(x, v, ~0u); });
+    each<kHeavy>(floor, [&](const float (&x)[4], int v) { mine += amounts(x, v, ~0u); });
     mine = warp_sum(mine);
     __syncthreads();
     if (lane == 0) s.wsum[warp] = mine;
@@ -443,28 +446,42 @@ struct Row {
     __syncthreads();
     for (int i = 0; i < warp; ++i) before += s.wsum[i];
     if (before <= target && before + mine > target) {  // one warp
-      for (int g = p0; g < p1; g += 32) {
-        float x[VEC];
-        unpack(fetch(g + lane), x);
-        const int id = id0 + (g + lane) * VEC;
-        const u64 own = amounts(x, id, ~0u);
-        u64 c = own;
+      bool done = false;
+      for (int g = p0; g < p1 && !done; g += 128) {
+        uint4 v[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 y = __shfl_up_sync(~0u, c, o);
-          if (lane >= o) c += y;
-        }
-        const unsigned past = __ballot_sync(~0u, before + c > target);
-        if (past) {
-          if (lane == __ffs(past) - 1) {
-            const u64 run = before + c - own;
-            int e = 0;
-            while (e < VEC - 1 && run + amounts(x, id, (2u << e) - 1) <= target) ++e;
-            s.id = id + e;
+        for (int b = 0; b < 4; ++b)
+          if (g + b * 32 < p1) v[b] = fetch(g + b * 32 + lane);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (done || g + b * 32 >= p1) break;
+          const int id = id0 + (g + b * 32 + lane) * VEC;
+          u64 own = 0;
+          by_four(v[b], id, [&](const float (&x)[4], int i) { own += amounts(x, i, ~0u); });
+          u64 c = own;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(~0u, c, o);
+            if (lane >= o) c += y;
           }
-          break;
+          const unsigned past = __ballot_sync(~0u, before + c > target);
+          if (past) {
+            if (lane == __ffs(past) - 1) {
+              u64 run = before + c - own;
+              int at = -1;
+              by_four(v[b], id, [&](const float (&x)[4], int i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  run += amounts(x, i, 1u << e);
+                  if (at < 0 && run > target) at = i + e;
+                }
+              });
+              if (at >= 0) s.id = at;
+            }
+            done = true;
+          }
+          before += __shfl_sync(~0u, c, 31);
         }
-        before += __shfl_sync(~0u, c, 31);
       }
     }
     g0 = keep0;
@@ -478,38 +495,42 @@ struct Row {
     return (int)fminf((m - x) * scale, (float)(kBins - 1));
   }
 
-  // Adds up the CTAs' histograms; the first bins at which the running sum reaches `lo_of(all)` and
-  // `hi_of(all)` (kBins where it does not), the sum before the first of them, and its own entry in 32 bits.
+  // Adds up the CTAs' histograms (each CTA all of them: one wait for the cluster instead of three); the first bins at
+  // which the running sum reaches lo_of(all) and hi_of(all) (kBins where it does not), the sum before the first of
+  // them, and its own entry in 32 bits.
   template <typename F, typename G, typename H>
   __device__ __forceinline__ void crossing(F value, G lo_of, H hi_of, int *b0, int *b1, u64 *base, unsigned *own) {
+    constexpr int kPer = kBins / kThreads;  // consecutive bins of a thread
+    if (threadIdx.x < 3) s.found[threadIdx.x] = kBins;
     sync();  // the histograms are whole
-    const int mine = kBins / CS, per = mine / kThreads;  // bins of a CTA, of a thread
-    u64 v[kBins / kThreads], sum = 0;
+    u64 v[kPer] = {}, sum = 0;
+#pragma unroll 4
+    for (int r = 0; r < CS; ++r) {
+      const unsigned *h = s.hist + threadIdx.x * kPer;
+      if (CS > 1) h = cg::this_cluster().map_shared_rank(h, r);
 #pragma unroll
-    for (int j = 0; j < kBins / kThreads; ++j) {
-      if (j >= per) break;
-      const int b = rank * mine + threadIdx.x * per + j;
-      u64 n = 0;
-      for (int r = 0; r < CS; ++r) n += CS > 1 ? *cg::this_cluster().map_shared_rank(&s.hist[b], r) : s.hist[b];
-      v[j] = value(b, n);
+      for (int j = 0; j < kPer; j += 4) {
+        const uint4 n = *reinterpret_cast<const uint4 *>(h + j);
+        v[j] += n.x;
+        v[j + 1] += n.y;
+        v[j + 2] += n.z;
+        v[j + 3] += n.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      v[j] = value(threadIdx.x * kPer + j, v[j]);
       sum += v[j];
     }
     const u64 incl = block_scan(sum);
     if (threadIdx.x == kThreads - 1) s.cum = incl;
-    if (threadIdx.x < 2) s.found[threadIdx.x] = kBins;
     __syncthreads();
-    tell(s.cum, 0);
-    u64 before = 0, all = 0;
-    for (int r = 0; r < CS; ++r) {
-      if (r < rank) before += heard(r, 0);
-      all += heard(r, 0);
-    }
-    u64 run = before + incl - sum;
-    const u64 lo = lo_of(all), hi = hi_of(all);
+    const u64 all = s.cum, lo = lo_of(all), hi = hi_of(all);
+    __syncthreads();
+    u64 run = incl - sum;
 #pragma unroll
-    for (int j = 0; j < kBins / kThreads; ++j) {
-      if (j >= per) break;
-      const unsigned b = rank * mine + threadIdx.x * per + j;
+    for (int j = 0; j < kPer; ++j) {
+      const unsigned b = threadIdx.x * kPer + j;
       if (run < lo && run + v[j] >= lo) {
         s.found[0] = b;
         s.found[2] = (unsigned)v[j];
@@ -519,48 +540,75 @@ struct Row {
       run += v[j];
     }
     __syncthreads();
-    tell((u64)s.found[2] << 32 | s.found[1] << 16 | s.found[0], s.cum);
-    *b0 = *b1 = kBins;
-    *base = 0;
-    *own = 0;
-    for (int r = 0; r < CS; ++r) {
-      const u64 x = heard(r, 0);
-      if ((x & 0xFFFF) < kBins) {
-        *b0 = (int)(x & 0xFFFF);
-        *own = (unsigned)(x >> 32);
-        *base = heard(r, 1);
-      }
-      if ((x >> 16 & 0xFFFF) < kBins) *b1 = (int)(x >> 16 & 0xFFFF);
-    }
+    *b0 = s.found[0];
+    *b1 = s.found[1];
+    *own = s.found[2];
+    *base = s.cum;
   }
 
-  // Clears the histogram (list) of every CTA, before anybody adds to it.
+  // Clears the histogram and the list before anybody adds to them.
   __device__ __forceinline__ void clear() {
+    __syncthreads();  // the last list has been read
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
   }
 
-  // Puts tokens on the first CTA's list; all lanes of the warp call it.
+  // Puts tokens on the CTA's list; all lanes of the warp call it.
   __device__ __forceinline__ void gather(bool take, float x, int v) {
     const unsigned m = __ballot_sync(~0u, take);
     if (m == 0) return;
-    Smem *first = CS > 1 ? cg::this_cluster().map_shared_rank(&s, 0) : &s;
     unsigned at = 0;
-    if (lane == 0) at = atomicAdd(&first->listed, __popc(m));
+    if (lane == 0) at = atomicAdd(&s.listed, __popc(m));
     at = __shfl_sync(~0u, at, 0) + __popc(m & ((1u << lane) - 1));
-    if (take && at < kList) first->list[at] = (u64)key_of(x) << 32 | (0xFFFFFFFFu - (unsigned)v);
+    if (take && at < kList) s.own[at] = (u64)key_of(x) << 32 | (0xFFFFFFFFu - (unsigned)v);
   }
 
-  // Sorts the list's n <= kList entries, the largest first.
-  __device__ __forceinline__ void sort_list(int n) {
-    int N = 32;
-    while (N < n) N *= 2;
-    for (int i = n + threadIdx.x; i < N; i += kThreads) s.list[i] = 0;
+  // The cluster's lists, the largest entry first: every CTA makes its own copy.  The CTAs have told each other
+  // how long theirs are: heard(r, 0).  Their number, more than kList where they do not fit.
+  __device__ __forceinline__ int merge_lists() {
+    u64 n = 0, before = 0;
+    for (int r = 0; r < CS; ++r) {
+      if (r < warp) before += heard(r, 0);
+      n += heard(r, 0);
+    }
+    if (n > kList) return kList + 1;
+    if (warp < CS) {  // warp r takes CTA r's
+      const int mine = (int)heard(warp, 0);
+      const u64 *from = CS > 1 ? cg::this_cluster().map_shared_rank(s.own, warp) : s.own;
+      for (int i = lane; i < mine; i += 32) s.list[before + i] = from[i];
+    }
     __syncthreads();
-    for (int k = 2; k <= N; k *= 2)
+    sort_list((int)n);
+    return (int)n;
+  }
+
+  // Sorts the list's n <= kList entries, the largest first: short ones by counting the larger entries of each (no
+  // barrier between steps: 128 entries 0.4 us, by exchanges 1.0), longer ones by exchanges.
+  __device__ __forceinline__ void sort_list(int n) {
+    if (n <= 2 * kThreads) {
+      const u64 e0 = (int)threadIdx.x < n ? s.list[threadIdx.x] : 0;
+      const u64 e1 = (int)threadIdx.x + kThreads < n ? s.list[threadIdx.x + kThreads] : 0;
+      int r0 = 0, r1 = 0;
+      if ((int)threadIdx.x - lane < n) {
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const u64 v = s.list[i];
+          r0 += v > e0;
+          r1 += v > e1;
+        }
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < n) s.list[r0] = e0;
+      if ((int)threadIdx.x + kThreads < n) s.list[r1] = e1;
+      __syncthreads();
+      return;
+    }
+    for (int i = n + threadIdx.x; i < kList; i += kThreads) s.list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= kList; k *= 2)
       for (int j = k / 2; j; j /= 2) {
-        for (int i = threadIdx.x; i < N / 2; i += kThreads) {
+        for (int i = threadIdx.x; i < kList / 2; i += kThreads) {
           const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
           const u64 x = s.list[lo], y = s.list[hi];
           if ((x < y) == ((lo & k) == 0)) {
@@ -572,7 +620,7 @@ struct Row {
       }
   }
 
-  // In the first CTA: the place in the sorted list of n entries at which the running sum of the weights,
+  // The place in the sorted list of n entries at which the running sum of the weights,
   // from `base` on, reaches target_of(base + their sum); n where it does not.
   template <typename G>
   __device__ __forceinline__ int place(int n, u64 base, G target_of) {
@@ -617,9 +665,9 @@ struct Row {
       for (int i = threadIdx.x; i < 256; i += kThreads) s.wide[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int v) {
+      each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int v) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const uint32_t k = key_of(x[e]);
           const u64 n = (k & mask) == prefix && old(x[e], v + e) ? amount(x[e]) : 0;
           const unsigned m = __ballot_sync(~0u, n != 0), b = (k >> shift) & 255;
@@ -656,10 +704,10 @@ struct Row {
     u64 n;
     const float at = tr_unord(prefix);
     const int id = first_past(at,
-                              [&](const float (&x)[VEC], int v, unsigned which) -> u64 {
+                              [&](const float (&x)[4], int v, unsigned which) -> u64 {
                                 unsigned t = 0;
 #pragma unroll
-                                for (int e = 0; e < VEC; ++e) t += (which >> e & 1) && x[e] == at && old(x[e], v + e);
+                                for (int e = 0; e < 4; ++e) t += (which >> e & 1) && x[e] == at && old(x[e], v + e);
                                 return t;
                               },
                               [&](u64) -> u64 { return take - 1; }, &n);
@@ -670,26 +718,11 @@ struct Row {
     return e;
   }
 
-  // What the first CTA found in its sorted list: the edge, and how many entries are left.
-  struct Found {
-    Edge edge;
-    bool ok;
-    int left;  // entries of the list; -1: not those alone and what lies above the list
-  };
-  __device__ __forceinline__ Found hear_found() const {
-    const u64 x = heard(0, 0), y = heard(0, 1);
-    return {{(uint32_t)(x >> 32), (int)(uint32_t)x}, (y & 1) != 0, (int)(y >> 1) - 1};
-  }
-  __device__ __forceinline__ void tell_found(Edge e, bool ok, int left) {
-    tell((u64)e.key << 32 | (uint32_t)e.id, (u64)(left + 1) << 1 | ok);
-  }
-
-  // Adds the weights of the first n entries of the first CTA's list to s.kept of the warps in whose ranges they lie.
+  // Adds the weights of the sorted list's first n entries to s.kept of the warps in whose ranges they lie.
   __device__ __forceinline__ void add_listed(int n) {
-    const Smem *first = CS > 1 ? cg::this_cluster().map_shared_rank(&s, 0) : &s;
     const int seg = a.granules / kWarps * VEC;  // a warp's range
     for (int i = threadIdx.x; i < n; i += kThreads) {
-      const u64 e = first->list[i];
+      const u64 e = s.list[i];
       const unsigned at = (0xFFFFFFFFu - (uint32_t)e) - (unsigned)id0;
       if (at < (unsigned)(kWarps * seg)) atomicAdd(&s.kept[at / seg], w(tr_unord((uint32_t)(e >> 32))));
     }
@@ -704,61 +737,54 @@ struct Row {
     *left = -1;
     bool whole = low > -INFINITY;
     int need = k;
-    auto found = [&]() -> Found {  // of the gathered tokens
-      sync();
-      if (rank == 0) {
-        const int n = (int)s.listed;
-        Edge e = none;
-        int keep = -1;
-        if (n <= kList) {
-          sort_list(n);
-          if (whole) {
-            keep = min(k, n);
-            if (p < 1.f) keep = min(keep, place(keep, 0, [&](u64 all) { return share_of(p, all); }) + 1);
-            keep = at_least(keep, min_p_key);
-            e = edge_at(keep - 1);
-          } else {
-            e = edge_at(need - 1);
-          }
-        }
-        tell_found(e, n <= kList, keep);
+    Edge edge = none;
+    auto found = [&] {  // from the gathered tokens
+      __syncthreads();
+      tell(s.listed);
+      const int n = merge_lists();
+      if (n > kList) return false;
+      if (whole) {
+        int keep = min(k, n);
+        if (p < 1.f) keep = min(keep, place(keep, 0, [&](u64 all) { return share_of(p, all); }) + 1);
+        *left = keep = at_least(keep, min_p_key);
+        edge = edge_at(keep - 1);
       } else {
-        tell(0, 0);
+        edge = edge_at(need - 1);
       }
-      return hear_found();
+      return true;
     };
-    Found f = {none, false, -1};
+    bool ok = false;
     if (whole) {
       // often the list takes all tokens from `low` on
-      each<kLight>(low, [&](const float (&x)[VEC], int v) {
+      each<kLight>(low, [&](const float (&x)[4], int v) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) gather(x[e] >= low, x[e], v + e);
+        for (int e = 0; e < 4; ++e) gather(x[e] >= low, x[e], v + e);
       });
-      f = found();
+      ok = found();
     }
-    if (!f.ok) {
+    if (!ok) {
       float least = low;
       if (!(low > -INFINITY)) {  // bins over all logits
         least = INFINITY;
-        each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int) {
+        each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
+          for (int e = 0; e < 4; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
         });
 #pragma unroll
         for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
         if (lane == 0) s.wsum[warp] = __float_as_uint(least);
         __syncthreads();
         for (int i = 0; i < kWarps; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
-        tell(__float_as_uint(least), 0);
+        tell(__float_as_uint(least));
         for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
       }
       const float m = w.m, span = m - least;
       if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
       const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
       clear();
-      each<kHeavy>(least, [&](const float (&x)[VEC], int) {
+      each<kHeavy>(least, [&](const float (&x)[4], int) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
+        for (int e = 0; e < 4; ++e)
           if (x[e] >= least) atomicAdd(&s.hist[bin_of(m, x[e], scale)], 1u);
       });
       int b0, b1;
@@ -770,23 +796,22 @@ struct Row {
       whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
       if (!whole) need = k - (int)above;
       // (a logit of bin b lies at or above m - (b + 1) / scale, but for the roundings: half a bin covers them)
-      each<kLight>(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[VEC], int v) {
+      each<kLight>(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[4], int v) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const int b = x[e] >= least ? bin_of(m, x[e], scale) : kBins;
           gather(whole ? b <= b0 : b == b0, x[e], v + e);
         }
       });
-      f = found();
+      ok = found();
     }
-    if (!f.ok) return narrow_down_k(k);
+    if (!ok) return narrow_down_k(k);
     if (whole) {
-      *left = f.left;
       if (threadIdx.x < kWarps) s.kept[threadIdx.x] = 0;
       __syncthreads();
-      add_listed(f.left);
+      add_listed(*left);
     }
-    return f.edge;
+    return edge;
   }
   // How many of the sorted list's first n entries have at least this key (the first one has).
   __device__ __forceinline__ int at_least(int n, uint32_t key) {
@@ -796,12 +821,12 @@ struct Row {
   }
   __device__ __noinline__ Edge narrow_down_k(int k) {
     u64 n = 0;
-    each<kHeavy>(-FLT_MAX, [&](const float (&x)[VEC], int) {
+    each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) n += x[e] > -INFINITY;
+      for (int e = 0; e < 4; ++e) n += x[e] > -INFINITY;
     });
     n = block_sum(n);
-    tell(n, 0);
+    tell(n);
     n = 0;
     for (int r = 0; r < CS; ++r) n += heard(r, 0);
     const Edge none = {kNever, -1};
@@ -817,9 +842,9 @@ struct Row {
     const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
     const Left weighted = old.above(w.floor);
     clear();
-    each<kHeavy>(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[VEC], int v) {
+    each<kHeavy>(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[4], int v) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const float t = (m - x[e]) * scale;
         if (!(t < (float)(kBins - 1)) || !old(x[e], v + e)) continue;
         const int b = (int)t;
@@ -840,12 +865,12 @@ struct Row {
     // the exact sums, of all and of what lies above the bins that hold the edge
     u64 all = 0, above = 0;
     const float first = (float)b0, behind = b1 < kBins ? (float)(b1 + 1) : INFINITY;  // of the bins with the edge
-    each<kHeavy>(weighted.at, [&](const float (&x)[VEC], int v) {
-      u64 q[VEC];
+    each<kHeavy>(weighted.at, [&](const float (&x)[4], int v) {
+      u64 q[4];
       w.of(x, q);
       unsigned in = 0;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const float t = (m - x[e]) * scale;
         const bool left = weighted(x[e], v + e);
         const u64 n = left ? q[e] : 0;
@@ -855,7 +880,7 @@ struct Row {
       }
       if (__any_sync(~0u, in != 0)) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) gather(in >> e & 1, x[e], v + e);
+        for (int e = 0; e < 4; ++e) gather(in >> e & 1, x[e], v + e);
       }
     });
     above = warp_sum(above);
@@ -864,43 +889,28 @@ struct Row {
     above = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) above += s.kept[i];
-    tell(all, above);
+    tell(s.listed, all, above);
     all = above = 0;
     for (int r = 0; r < CS; ++r) {
-      all += heard(r, 0);
-      above += heard(r, 1);
+      all += heard(r, 1);
+      above += heard(r, 2);
     }
     const u64 target = share_of(p, all);
-    if (rank == 0) {
-      const int n = (int)s.listed;
-      Edge e = {kNever, -1};
-      bool ok = n <= kList && above < target;
-      int keep = -1;
-      if (ok) {
-        sort_list(n);
-        const int at = place(n, above, [&](u64) { return target; });
-        ok = at < n;
-        if (ok) {
-          e = edge_at(at);
-          keep = at + 1;
-        }
-      }
-      tell_found(e, ok, keep);
-    } else {
-      tell(0, 0);
-    }
-    const Found f = hear_found();
     *known = false;
-    if (!f.ok) return narrow_down_p(target, old);
-    *known = f.edge.key >= min_p_key;
-    if (*known) add_listed(f.left);
-    return f.edge;
+    const int n = above < target ? merge_lists() : kList + 1;
+    if (n > kList) return narrow_down_p(target, old);
+    const int at = place(n, above, [&](u64) { return target; });
+    if (at >= n) return narrow_down_p(target, old);
+    const Edge edge = edge_at(at);
+    *known = edge.key >= min_p_key;
+    if (*known) add_listed(at + 1);
+    return edge;
   }
   __device__ __noinline__ Edge narrow_down_p(u64 target, Left old) { return narrow_down(target, old, w); }
 };
 
 template <typename T, bool HELD>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, int CS, long long ahead,
+__global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const SampleArgs a, int CS, long long ahead,
                                                              const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
@@ -1009,9 +1019,9 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       __syncthreads();
       int first = INT_MAX;
       const float m = tr_unord(top);
-      r.template each<R::kLight>(m, [&](const float (&y)[VEC], int v) {
+      r.template each<R::kLight>(m, [&](const float (&y)[4], int v) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) first = min(first, y[e] == m ? v + e : INT_MAX);
+        for (int e = 0; e < 4; ++e) first = min(first, y[e] == m ? v + e : INT_MAX);
       });
       atomicMin(&s.id, first);
       __syncthreads();
@@ -1038,11 +1048,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   const float u = s.u;
   u64 all;
   const int id = r.first_past(left.at,
-                              [&](const float (&y)[VEC], int v, unsigned which) {
-                                u64 q[VEC], sum = 0;
+                              [&](const float (&y)[4], int v, unsigned which) {
+                                u64 q[4], sum = 0;
                                 r.w.of(y, q);
 #pragma unroll
-                                for (int e = 0; e < VEC; ++e) sum += (which >> e & 1) && left(y[e], v + e) ? q[e] : 0;
+                                for (int e = 0; e < 4; ++e) sum += (which >> e & 1) && left(y[e], v + e) ? q[e] : 0;
                                 return sum;
                               },
                               [&](u64 sum) {
@@ -1096,7 +1106,7 @@ int launch(SampleArgs a, cudaStream_t s) {
     const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs;
     return (mine + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
   };
-  const long long slots = 3LL * tr_sm_count();
+  const long long slots = 2LL * tr_sm_count();
   int cs = 1;
   while (cs < kMaxCluster && a.rows * cs * 2 <= slots) cs *= 2;
   bool held = granules(cs) * 16 <= kSlice;
