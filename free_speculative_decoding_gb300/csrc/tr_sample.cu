@@ -349,7 +349,9 @@ struct Row {
       }
     }
   }
-  static constexpr int kLight = 16 / VEC, kHeavy = 8 / VEC;  // batches under way, of passes that do little or much
+  // Batches under way, of passes that do little or much.  From shared memory one: more copies of a pass's code, each of
+  // which a short row runs through once, cost more in fetching instructions (gathering from 4096 logits a CTA took 9 us with four).
+  static constexpr int kLight = HELD ? 1 : 16 / VEC, kHeavy = HELD ? 1 : 8 / VEC;
   // A granule's largest element.
   static __device__ __forceinline__ float most(const uint4 &v) {
     if constexpr (VEC == 4) {
@@ -406,58 +408,51 @@ struct Row {
   }
 
   // The lowest ID at which the running sum over ascending IDs passes target_of(whole sum), in the one CTA that
-  // holds it; -1 in the others.  amounts(x, first ID) is the sum of a granule's, none of which lies below `floor`.
-  // known: the sums of the warps' ranges are in s.kept.
-  template <typename F, typename G>
-  __device__ __forceinline__ int first_past(float floor, F amounts, G target_of, u64 *all, bool known = false) {
-    u64 mine = 0;
-    if (!known) {
-      each<kHeavy>(floor, [&](const float (&x)[4], int v) { mine += amounts(x, v, ~0u); });
+  // holds it; -1 in the others.  amounts(x[4], first ID) is the sum of four tokens, none of which lies below `floor`,
+  // amount(x, ID) one's.  known: the sums of the warps' ranges are in s.kept.
+  template <typename F, typename A, typename G>
+  __device__ __forceinline__ int first_past(float floor, F amounts, A amount, G target_of, u64 *all, bool known = false) {
+    const int keep0 = g0, keep1 = g1, seg = a.granules / kWarps;
+    u64 before = 0, target = 0, mine;
+    bool here = true;
+    // the sums of the warps' ranges; then, in the CTA that holds the place, of an eighth of the range that does
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+      mine = 0;
+      if (round || !known) each<kHeavy>(floor, [&](const float (&x)[4], int v) { mine += amounts(x, v); });
       mine = warp_sum(mine);
+      if (round == 0 && known) mine = s.kept[warp];
+      __syncthreads();
+      if (lane == 0) s.wsum[warp] = mine;
+      if (threadIdx.x == 0) s.id = max(id0, 0);
+      __syncthreads();
+      if (round) break;
+      u64 cta = 0, sum = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) cta += s.wsum[i];
+      tell(cta);
+      for (int r = 0; r < CS; ++r) {
+        if (r < rank) before += heard(r, 0);
+        sum += heard(r, 0);
+      }
+      *all = sum;
+      target = target_of(sum);
+      here = before <= target && before + cta > target;
+      if (!here) break;
+      int q = 0;
+      while (q < kWarps - 1 && before + s.wsum[q] <= target) before += s.wsum[q++];
+      const int part = ((seg + kWarps - 1) / kWarps + 31) & ~31, hi = (q + 1) * seg;
+      g0 = min(hi, q * seg + warp * part);
+      g1 = min(hi, g0 + part);
     }
-    if (lane == 0) s.wsum[warp] = known ? s.kept[warp] : mine;
-    __syncthreads();
-    u64 cta = 0, before = 0, sum = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) cta += s.wsum[i];
-    tell(cta);
-    for (int r = 0; r < CS; ++r) {
-      if (r < rank) before += heard(r, 0);
-      sum += heard(r, 0);
-    }
-    *all = sum;
-    const u64 target = target_of(sum);
-    if (!(before <= target && before + cta > target)) return -1;
-    // the warp's range that holds it, a part of that range by each warp, 32 granules, a granule
-    int q = 0;
-    while (q < kWarps - 1 && before + s.wsum[q] <= target) before += s.wsum[q++];
-    const int seg = a.granules / kWarps, lo = q * seg, hi = lo + seg;
-    const int part = ((seg + kWarps - 1) / kWarps + 31) & ~31;
-    const int p0 = min(hi, lo + warp * part), p1 = min(hi, p0 + part);
-    const int keep0 = g0, keep1 = g1;
-    g0 = p0;
-    g1 = p1;
-    mine = 0;
-    each<kHeavy>(floor, [&](const float (&x)[4], int v) { mine += amounts(x, v, ~0u); });
-    mine = warp_sum(mine);
-    __syncthreads();
-    if (lane == 0) s.wsum[warp] = mine;
-    if (threadIdx.x == 0) s.id = max(id0, 0);
-    __syncthreads();
-    for (int i = 0; i < warp; ++i) before += s.wsum[i];
-    if (before <= target && before + mine > target) {  // one warp
-      bool done = false;
-      for (int g = p0; g < p1 && !done; g += 128) {
-        uint4 v[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (g + b * 32 < p1) v[b] = fetch(g + b * 32 + lane);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (done || g + b * 32 >= p1) break;
-          const int id = id0 + (g + b * 32 + lane) * VEC;
+    if (here) {
+      for (int i = 0; i < warp; ++i) before += s.wsum[i];
+      if (before <= target && before + mine > target) {  // one warp: batch by batch, then a granule
+        bool done = false;
+        scan<1>([&](const uint4 &v, int id) {
+          if (done) return;
           u64 own = 0;
-          by_four(v[b], id, [&](const float (&x)[4], int i) { own += amounts(x, i, ~0u); });
+          by_four(v, id, [&](const float (&x)[4], int i) { own += amounts(x, i); });
           u64 c = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -468,26 +463,23 @@ struct Row {
           if (past) {
             if (lane == __ffs(past) - 1) {
               u64 run = before + c - own;
-              int at = -1;
-              by_four(v[b], id, [&](const float (&x)[4], int i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  run += amounts(x, i, 1u << e);
-                  if (at < 0 && run > target) at = i + e;
-                }
-              });
-              if (at >= 0) s.id = at;
+              int at = id;
+              for (; at < id + VEC - 1; ++at) {
+                run += at >= 0 && at < a.V ? amount(get(x, at), at) : 0;
+                if (run > target) break;
+              }
+              s.id = at;
             }
             done = true;
           }
           before += __shfl_sync(~0u, c, 31);
-        }
+        });
       }
     }
     g0 = keep0;
     g1 = keep1;
     __syncthreads();
-    return s.id;
+    return here ? s.id : -1;
   }
 
   // A token's place on the histogram's scale: falling logits, rising bins.
@@ -554,14 +546,13 @@ struct Row {
     __syncthreads();
   }
 
-  // Puts tokens on the CTA's list; all lanes of the warp call it.
-  __device__ __forceinline__ void gather(bool take, float x, int v) {
-    const unsigned m = __ballot_sync(~0u, take);
-    if (m == 0) return;
-    unsigned at = 0;
-    if (lane == 0) at = atomicAdd(&s.listed, __popc(m));
-    at = __shfl_sync(~0u, at, 0) + __popc(m & ((1u << lane) - 1));
-    if (take && at < kList) s.own[at] = (u64)key_of(x) << 32 | (0xFFFFFFFFu - (unsigned)v);
+  // Puts those of the tokens v .. v + 3 whose bits are set on the CTA's list.
+  __device__ __forceinline__ void gather(unsigned bits, const float (&x)[4], int v) {
+    if (bits == 0) return;
+    unsigned at = atomicAdd(&s.listed, __popc(bits));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((bits >> e & 1) && at < kList) s.own[at++] = (u64)key_of(x[e]) << 32 | (0xFFFFFFFFu - (unsigned)(v + e));
   }
 
   // The cluster's lists, the largest entry first: every CTA makes its own copy.  The CTAs have told each other
@@ -703,14 +694,15 @@ struct Row {
     const u64 take = each_ ? (target - base + each_ - 1) / each_ : 0;
     u64 n;
     const float at = tr_unord(prefix);
+    auto one = [&](float x, int v) -> u64 { return x == at && old(x, v); };
     const int id = first_past(at,
-                              [&](const float (&x)[4], int v, unsigned which) -> u64 {
-                                unsigned t = 0;
+                              [&](const float (&x)[4], int v) {
+                                u64 t = 0;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) t += (which >> e & 1) && x[e] == at && old(x[e], v + e);
+                                for (int e = 0; e < 4; ++e) t += one(x[e], v + e);
                                 return t;
                               },
-                              [&](u64) -> u64 { return take - 1; }, &n);
+                              one, [&](u64) -> u64 { return take - 1; }, &n);
     tell(id >= 0, (u64)(unsigned)id);
     Edge e = {prefix, INT_MAX};
     for (int r = 0; r < CS; ++r)
@@ -757,8 +749,10 @@ struct Row {
     if (whole) {
       // often the list takes all tokens from `low` on
       each<kLight>(low, [&](const float (&x)[4], int v) {
+        unsigned bits = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) gather(x[e] >= low, x[e], v + e);
+        for (int e = 0; e < 4; ++e) bits |= x[e] >= low ? 1u << e : 0;
+        gather(bits, x, v);
       });
       ok = found();
     }
@@ -797,11 +791,13 @@ struct Row {
       if (!whole) need = k - (int)above;
       // (a logit of bin b lies at or above m - (b + 1) / scale, but for the roundings: half a bin covers them)
       each<kLight>(fmaxf(least, m - (b0 + 1.5f) / scale), [&](const float (&x)[4], int v) {
+        unsigned bits = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int b = x[e] >= least ? bin_of(m, x[e], scale) : kBins;
-          gather(whole ? b <= b0 : b == b0, x[e], v + e);
+          bits |= (whole ? b <= b0 : b == b0) ? 1u << e : 0;
         }
+        gather(bits, x, v);
       });
       ok = found();
     }
@@ -878,10 +874,7 @@ struct Row {
         above += t < first ? n : 0;
         in |= t >= first && t < behind && left ? 1u << e : 0;
       }
-      if (__any_sync(~0u, in != 0)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gather(in >> e & 1, x[e], v + e);
-      }
+      gather(in, x, v);
     });
     above = warp_sum(above);
     if (lane == 0) s.kept[warp] = above;
@@ -1048,13 +1041,14 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
   const float u = s.u;
   u64 all;
   const int id = r.first_past(left.at,
-                              [&](const float (&y)[4], int v, unsigned which) {
+                              [&](const float (&y)[4], int v) {
                                 u64 q[4], sum = 0;
                                 r.w.of(y, q);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) sum += (which >> e & 1) && left(y[e], v + e) ? q[e] : 0;
+                                for (int e = 0; e < 4; ++e) sum += left(y[e], v + e) ? q[e] : 0;
                                 return sum;
                               },
+                              [&](float y, int v) -> u64 { return left(y, v) ? r.w(y) : 0; },
                               [&](u64 sum) {
                                 bool exact;
                                 return part_of(u, sum, &exact);
