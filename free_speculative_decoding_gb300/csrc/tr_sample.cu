@@ -38,6 +38,7 @@ struct SampleArgs {
   int32_t *token;
   float *logprob;
   int granules;  // of a CTA's slice, kWarps * 32 or a multiple
+  int full;      // warps of a row's cluster whose ranges hold nothing but tokens, at least
   int drop;      // bits that top-p's histogram gives up
 };
 
@@ -79,6 +80,7 @@ struct Weight {
   float floor;          // logits up to this one have no weight
   int shift, S;         // shift: (K - (bits of 0 + 1.5 2^17) / 64) + 63 - S, see whole()
   bool infinite;        // the largest logit is +inf
+  bool far;
   const float2 *table;  // 2^(j / 64): 2^31 times it as a float, and as an integer (in its bits)
   __device__ __forceinline__ void set(float m_, float2 c, int S_, const float2 *t) {
     m = m_;
@@ -88,7 +90,7 @@ struct Weight {
     c_lo = c.y;
     infinite = m == INFINITY;
     const float mc = m * c_hi;
-    const bool far = !(fabsf(mc) < 32700.f);  // infinite too
+    far = !(fabsf(mc) < 32700.f);  // infinite too
     base = far ? m : 0.f;
     const int K = far ? 1 : (int)ceilf(mc + 0.01f);  // m c is off by 2^-9 at most
     shift = K + (0x48400000 >> 6) + 63 - S;
@@ -135,11 +137,11 @@ struct Weight {
     }
   }
 };
-// c of a temperature, in two numbers.
+// c of a temperature, in two numbers (2^-47 of it).
 __device__ __forceinline__ float2 log2e_over(float temp) {
-  const double c = 1.4426950408889634 / (double)temp;
-  const float hi = (float)c;
-  return make_float2(hi, (float)(c - (double)hi));
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e)
+  const float hi = kHi / temp;
+  return make_float2(hi, hi > 0.f ? (fmaf(-hi, temp, kHi) + kLo) / temp : 0.f);
 }
 
 // 2^(j / 64) 2^31, j = 0 .. 63, as a number and as an integer: worked out once on the host.
@@ -239,12 +241,12 @@ constexpr int kList = 1024;
 
 struct alignas(128) Smem {  // the slice lies behind it
   float2 table[64];
-  u64 box[2][kMaxCluster][3];     // what the cluster's CTAs have told this one, of two exchanges
+  u64 box[2][kMaxCluster][2 + kWarps / 2];  // what the cluster's CTAs have told this one, of two exchanges
   u64 wsum[kWarps];
   u64 kept[kWarps];               // the weights that are left in the warps' ranges, where they are known
   unsigned listed;                // tokens that were to go to this CTA's list
-  float temp, p, u;               // the row's rules
-  float2 c;
+  uint32_t listed_low;            // the key that at least k tokens lie at or above
+  float u;
   double below;
   unsigned found[3];
   int id;
@@ -305,8 +307,13 @@ struct Row {
   // alike.
   template <int N, typename F>
   __device__ __forceinline__ void scan(F f) const {
+    if constexpr (HELD) {
+#pragma unroll 1
+      for (int g = g0 + lane; g < g1; g += 32) f(data[g], id0 + g * VEC);
+      return;
+    }
     const int n = (g1 - g0) / 32;  // batches; those from i0 to i1 hold nothing but tokens
-    const int i0 = HELD || g0 >= whole0 ? 0 : 1, i1 = HELD ? n : min(n, (whole1 - g0) >> 5);
+    const int i0 = g0 >= whole0 ? 0 : 1, i1 = min(n, (whole1 - g0) >> 5);
     const uint4 *p = granules() + g0 + lane;
     int id = id0 + (g0 + lane) * VEC;
     for (int i = 0; i < n;) {
@@ -351,7 +358,7 @@ struct Row {
   }
   // Batches under way, of passes that do little or much.  From shared memory one: more copies of a pass's code, each of
   // which a short row runs through once, cost more in fetching instructions (gathering from 4096 logits a CTA took 9 us with four).
-  static constexpr int kLight = HELD ? 1 : 16 / VEC, kHeavy = HELD ? 1 : 8 / VEC;
+  static constexpr int kLight = HELD ? 1 : 32 / VEC, kHeavy = HELD ? 1 : 8 / VEC;
   // A granule's largest element.
   static __device__ __forceinline__ float most(const uint4 &v) {
     if constexpr (VEC == 4) {
@@ -389,6 +396,21 @@ struct Row {
     }
     sync();
     parity ^= 1;
+  }
+  // The same with 32 bits of every warp, which its lane 0 has in s.wsum.
+  __device__ __forceinline__ void tell_warps(u64 x) {
+    for (int i = threadIdx.x; i < CS * (1 + kWarps / 2); i += kThreads) {
+      const int r = i / (1 + kWarps / 2), w = i - r * (1 + kWarps / 2);
+      u64 *to = &s.box[parity][rank][w];
+      if (CS > 1) to = cg::this_cluster().map_shared_rank(to, r);
+      *to = w == 0 ? x : (s.wsum[2 * w - 2] & 0xFFFFFFFFu) | s.wsum[2 * w - 1] << 32;
+    }
+    sync();
+    parity ^= 1;
+  }
+  __device__ __forceinline__ uint32_t heard_warp(int i) const {  // i: of the cluster's
+    const int r = i / kWarps, w = i - r * kWarps;
+    return (uint32_t)(s.box[parity ^ 1][r][1 + w / 2] >> (w & 1) * 32);
   }
   __device__ __forceinline__ u64 heard(int r, int i) const { return s.box[parity ^ 1][r][i]; }
 
@@ -446,6 +468,11 @@ struct Row {
       g1 = min(hi, g0 + part);
     }
     if (here) {
+      if (known) {  // sums that were made otherwise may differ in their last places
+        u64 all_parts = 0;
+        for (int i = 0; i < kWarps; ++i) all_parts += s.wsum[i];
+        target = min(target, before + max(all_parts, 1ull) - 1);
+      }
       for (int i = 0; i < warp; ++i) before += s.wsum[i];
       if (before <= target && before + mine > target) {  // one warp: batch by batch, then a granule
         bool done = false;
@@ -574,41 +601,49 @@ struct Row {
     return (int)n;
   }
 
-  // Sorts the list's n <= kList entries, the largest first: short ones by counting the larger entries of each (no
-  // barrier between steps: 128 entries 0.4 us, by exchanges 1.0), longer ones by exchanges.
+  // Sorts the list's n <= kList entries (none is 0), the largest first: 32 of them by each warp in registers, then every
+  // entry's place is its place among these plus the numbers of larger ones in the other groups, found by bisection.
   __device__ __forceinline__ void sort_list(int n) {
-    if (n <= 2 * kThreads) {
-      const u64 e0 = (int)threadIdx.x < n ? s.list[threadIdx.x] : 0;
-      const u64 e1 = (int)threadIdx.x + kThreads < n ? s.list[threadIdx.x + kThreads] : 0;
-      int r0 = 0, r1 = 0;
-      if ((int)threadIdx.x - lane < n) {
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const u64 v = s.list[i];
-          r0 += v > e0;
-          r1 += v > e1;
+    constexpr int kMine = kList / 32 / kWarps;  // groups of a warp
+    u64 e[kMine];
+    int place[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int i = (warp + j * kWarps) * 32 + lane;
+      if (i - lane >= n) break;
+      u64 v = i < n ? s.list[i] : 0;
+#pragma unroll 1
+      for (int k = 2; k <= 32; k *= 2)
+#pragma unroll 1
+        for (int d = k / 2; d; d /= 2) {
+          const u64 o = __shfl_xor_sync(~0u, v, d);
+          v = (((lane & k) == 0 || k == 32) == ((lane & d) == 0)) == (v > o) ? v : o;
         }
-      }
-      __syncthreads();
-      if ((int)threadIdx.x < n) s.list[r0] = e0;
-      if ((int)threadIdx.x + kThreads < n) s.list[r1] = e1;
-      __syncthreads();
-      return;
+      s.list[i] = e[j] = v;
     }
-    for (int i = n + threadIdx.x; i < kList; i += kThreads) s.list[i] = 0;
     __syncthreads();
-    for (int k = 2; k <= kList; k *= 2)
-      for (int j = k / 2; j; j /= 2) {
-        for (int i = threadIdx.x; i < kList / 2; i += kThreads) {
-          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-          const u64 x = s.list[lo], y = s.list[hi];
-          if ((x < y) == ((lo & k) == 0)) {
-            s.list[lo] = y;
-            s.list[hi] = x;
-          }
-        }
-        __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int group = (warp + j * kWarps) * 32;
+      if (group >= n) break;
+      place[j] = lane;
+#pragma unroll 2
+      for (int g = 0; g < n; g += 32) {
+        if (g == group) continue;
+        const u64 *l = s.list + g;
+        int at = 0;
+#pragma unroll
+        for (int d = 16; d; d /= 2) at += l[at + d - 1] > e[j] ? d : 0;
+        place[j] += at + (l[at] > e[j]);
       }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      if ((warp + j * kWarps) * 32 >= n) break;
+      if (e[j]) s.list[place[j]] = e[j];
+    }
+    __syncthreads();
   }
 
   // The place in the sorted list of n entries at which the running sum of the weights,
@@ -949,59 +984,100 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
     const long long n = min((long long)a.granules * 16, (long long)((uintptr_t)(x + ahead * a.ld + a.V) - to)) & ~15ll;
     if (n > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(to), "r"((int)n) : "memory");
   }
+  const float temp = a.temperature ? a.temperature[row] : 1.f, p = a.top_p ? a.top_p[row] : 1.f,
+              min_p = a.min_p ? a.min_p[row] : 0.f;
   int k = a.top_k ? a.top_k[row] : 0;
   if (k >= a.V) k = 0;
+  const float2 c = log2e_over(temp);
   if (threadIdx.x == kThreads - 1) {  // the rules, while the slice is under way; 64-bit arithmetic once
-    const float temp = a.temperature ? a.temperature[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
-    s.temp = temp;
-    s.p = a.top_p ? a.top_p[row] : 1.f;
     s.u = uniform_of(a.U[row]);
-    s.c = log2e_over(temp);
-    s.below = min_p_below(mp, temp);
+    s.below = min_p_below(min_p, temp);
   }
   if (HELD) asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-  // The largest logit; and, for top-k, one that at least k lie at or above: with N warps in the cluster, at least
-  // ceil(k / N) lanes of each have a largest logit there.
+  // The largest logit; and, for top-k, one that at least k lie at or above: of each of the a.full warps whose ranges are
+  // full of tokens the j-th of the lanes' largest, of these the ceil(k / j)-th.
   float most = -INFINITY;
-  r.template scan<R::kLight>([&](const uint4 &v, int) { most = fmaxf(most, R::most(v)); });
-  const int lanes = k > 0 ? (int)(((long long)k + kWarps * CS - 1) / (kWarps * CS)) : 33;
-  float least = -INFINITY;
-  if (lanes <= 32) {
-    // the lanes' in falling order, the `lanes`-th of them
-    float v = most;
+  // Temperature alone, from global memory: the weights are summed in the same pass, relative to the largest logit that
+  // the warp has seen yet.
+  const bool once = !HELD && k == 0 && !(p < 1.f) && !(min_p > 0.f) && temp >= FLT_MIN;
+  bool known = false;  // the weights that are left, by warps
+  u64 sum = 0;
+  if (once) {
+    __syncthreads();  // the table
+    r.w.set(-INFINITY, c, a.S, s.table);
+    r.w.floor = FLT_MAX;
+    known = true;
+    r.template scan<R::kHeavy>([&](const uint4 &v, int id) {
+      const float top = R::most(v);
+      if (__any_sync(~0u, top > most)) {
+        most = fmaxf(most, top);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        const int shift = r.w.shift;
+        const bool first = r.w.m == -INFINITY;
+        r.w.set(most, c, a.S, s.table);
+        if (r.w.far) known = false;  // not a shift: the sums are found in a pass of their own
+        if (!first) sum >>= min(r.w.shift - shift, 63);
+      }
+      R::by_four(v, id, [&](const float (&x)[4], int) {
+        u64 q[4];
+        r.w.of(x, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += x[e] > r.w.floor ? q[e] : 0;
+      });
+    });
+    sum = warp_sum(sum);
+  } else {
+    r.template scan<R::kLight>([&](const uint4 &v, int) { most = fmaxf(most, R::most(v)); });
+  }
+  const int own_shift = r.w.shift;
+  const int j = k > 0 && a.full > 0 ? (int)(((long long)k + a.full - 1) / a.full) : 33;
+  float bound = -INFINITY;
+  if (j <= 32) {
+    float v = most;  // the lanes' in falling order
 #pragma unroll
     for (int n = 2; n <= 32; n *= 2)
 #pragma unroll
-      for (int j = n / 2; j; j /= 2) {
-        const float o = __shfl_xor_sync(~0u, v, j);
-        v = ((r.lane & n) == 0) == ((r.lane & j) == 0) ? fmaxf(v, o) : fminf(v, o);
+      for (int d = n / 2; d; d /= 2) {
+        const float o = __shfl_xor_sync(~0u, v, d);
+        v = ((r.lane & n) == 0 || n == 32) == ((r.lane & d) == 0) ? fmaxf(v, o) : fminf(v, o);
       }
-    least = __shfl_sync(~0u, v, lanes - 1);
+    bound = __shfl_sync(~0u, v, j - 1);
     most = __shfl_sync(~0u, v, 0);
   } else {
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
   }
-  if (r.lane == 0) s.wsum[r.warp] = (u64)key_of(most) << 32 | key_of(least);
+  if (r.lane == 0) s.wsum[r.warp] = (u64)key_of(most) << 32 | key_of(bound);
   __syncthreads();
-  uint32_t top = 0, low = ~0u;
-  for (int i = 0; i < kWarps; ++i) {
-    top = max(top, (uint32_t)(s.wsum[i] >> 32));
-    low = min(low, (uint32_t)s.wsum[i]);
-  }
+  uint32_t top = 0, low = 0;
+  for (int i = 0; i < kWarps; ++i) top = max(top, (uint32_t)(s.wsum[i] >> 32));
   const uint32_t own_top = top;
-  r.tell(top, low);
+  r.tell_warps(top);
   int owner = 0;  // the first CTA that has the largest
-  for (int k = CS - 1; k >= 0; --k) {
-    const uint32_t t = (uint32_t)r.heard(k, 0);
+  for (int i = CS - 1; i >= 0; --i) {
+    const uint32_t t = (uint32_t)r.heard(i, 0);
     if (t >= top) {
       top = t;
-      owner = k;
+      owner = i;
     }
-    low = min(low, (uint32_t)r.heard(k, 1));
   }
-  if (top <= kNever || !(s.temp >= FLT_MIN) || k == 1) {
+  if (j <= 32) {
+    const int rank = (k + j - 1) / j, n = a.full;
+    if ((int)threadIdx.x < n) {
+      const uint32_t mine = r.heard_warp(threadIdx.x);
+      int above = 0;
+      for (int i = 0; i < n; ++i) {
+        const uint32_t o = r.heard_warp(i);
+        above += o > mine || (o == mine && i < (int)threadIdx.x);
+      }
+      if (above == rank - 1) s.listed_low = mine;
+    }
+    __syncthreads();
+    low = s.listed_low;
+  }
+  if (top <= kNever || !(temp >= FLT_MIN) || k == 1) {
     if (top <= kNever) {
       if (r.rank == 0 && threadIdx.x == 0) {
         a.token[row] = -1;
@@ -1025,12 +1101,15 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
     }
     return;
   }
-  r.w.set(tr_unord(top), s.c, a.S, s.table);
+  r.w.set(tr_unord(top), c, a.S, s.table);
 
   Edge edge = {kNever, -1};
-  const float p = s.p;
   const uint32_t mp = min_p_key(s.below, r.w.m);
-  bool known = false;  // the weights that are left, by warps
+  if (once) {
+    known = !__syncthreads_or(!known || r.w.far);
+    if (known && r.lane == 0) s.kept[r.warp] = sum ? sum >> min(r.w.shift - own_shift, 63) : 0;
+    __syncwarp();
+  }
   int listed = -1;
   if (k > 0) {
     edge = r.top_k(k, p, mp, low > kNever ? tr_unord(low) : -INFINITY, &listed);
@@ -1108,6 +1187,7 @@ int launch(SampleArgs a, cudaStream_t s) {
   while (cs > 1 && held && granules(cs) * 16 <= 4096) cs /= 2;
   while (cs < kMaxCluster && granules(cs) * VEC > kMostTokens) cs *= 2;
   a.granules = (int)granules(cs);
+  a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / kWarps * VEC));
   a.drop = 0;
   while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
   const size_t slice = held ? (size_t)a.granules * 16 : 0;
