@@ -99,11 +99,11 @@ struct Weight {
   }
   // From p = q + 1.5 2^17, whose bits are 64 q more than those of 1.5 2^17, and e = 2^r - 1: the
   // mantissa, times 2^32 and shifted right by less than 64 (for what lies above `floor`).
-  __device__ __forceinline__ u64 whole(float p, float e) const {
+  __device__ __forceinline__ u64 whole(float p, float e, bool there = true) const {
     const int n = __float_as_int(p);
     const float2 f = table[n & 63];
     const unsigned mant = __float_as_uint(f.y) + (unsigned)__float2int_rn(e * f.x);
-    return ((u64)mant << 32) >> (shift - (n >> 6));
+    return ((u64)(there ? mant : 0) << 32) >> (shift - (n >> 6));
   }
   __device__ __forceinline__ u64 operator()(float x) const {
     if (infinite) return x == m ? 1ull << S : 0;
@@ -114,13 +114,13 @@ struct Weight {
     e = fmaf(r, e, kL1);
     return whole(p, e * r);
   }
-  // The weights of N logits, the same arithmetic, two to an instruction; what lies up to `floor`, or is NaN, gets any
-  // number.
+  // The weights of N logits, the same arithmetic, two to an instruction; 0 for those whose bit of `there` is not set: of
+  // all that lie up to `floor` or are NaN.
   template <int N>
-  __device__ __forceinline__ void of(const float (&x)[N], u64 (&w)[N]) const {
+  __device__ __forceinline__ void of(const float (&x)[N], const bool (&there)[N], u64 (&w)[N]) const {
     if (infinite) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = (*this)(x[i]);
+      for (int i = 0; i < N; ++i) w[i] = there[i] && x[i] == m ? 1ull << S : 0;
       return;
     }
 #pragma unroll
@@ -132,8 +132,8 @@ struct Weight {
       F2 e = fma(r, f2(kL3, kL3), f2(kL2, kL2));
       e = fma(r, e, f2(kL1, kL1)) * r;
       const float2 p1 = split(p), e1 = split(e);
-      w[i] = whole(p1.x, e1.x);
-      w[i + 1] = whole(p1.y, e1.y);
+      w[i] = whole(p1.x, e1.x, there[i]);
+      w[i + 1] = whole(p1.y, e1.y, there[i + 1]);
     }
   }
 };
@@ -601,49 +601,54 @@ struct Row {
     return (int)n;
   }
 
-  // Sorts the list's n <= kList entries (none is 0), the largest first: 32 of them by each warp in registers, then every
-  // entry's place is its place among these plus the numbers of larger ones in the other groups, found by bisection.
+  // Sorts the list's n <= kList entries (none is 0), the largest first.  Up to 256: 32 of them by each warp in registers,
+  // then every entry's place is its place among these plus the numbers of larger ones in the other warps', found by
+  // bisection.  More: by exchanges.
   __device__ __forceinline__ void sort_list(int n) {
-    constexpr int kMine = kList / 32 / kWarps;  // groups of a warp
-    u64 e[kMine];
-    int place[kMine];
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int i = (warp + j * kWarps) * 32 + lane;
-      if (i - lane >= n) break;
-      u64 v = i < n ? s.list[i] : 0;
+    if (n <= kThreads) {
+      const int i = threadIdx.x;
+      u64 e = i < n ? s.list[i] : 0;
 #pragma unroll 1
       for (int k = 2; k <= 32; k *= 2)
 #pragma unroll 1
         for (int d = k / 2; d; d /= 2) {
-          const u64 o = __shfl_xor_sync(~0u, v, d);
-          v = (((lane & k) == 0 || k == 32) == ((lane & d) == 0)) == (v > o) ? v : o;
+          const u64 o = __shfl_xor_sync(~0u, e, d);
+          e = (((lane & k) == 0 || k == 32) == ((lane & d) == 0)) == (e > o) ? e : o;
         }
-      s.list[i] = e[j] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int group = (warp + j * kWarps) * 32;
-      if (group >= n) break;
-      place[j] = lane;
+      s.list[i] = e;
+      __syncthreads();
+      int place = lane;
 #pragma unroll 2
       for (int g = 0; g < n; g += 32) {
-        if (g == group) continue;
+        if (g == i - lane) continue;
         const u64 *l = s.list + g;
         int at = 0;
 #pragma unroll
-        for (int d = 16; d; d /= 2) at += l[at + d - 1] > e[j] ? d : 0;
-        place[j] += at + (l[at] > e[j]);
+        for (int d = 16; d; d /= 2) at += l[at + d - 1] > e ? d : 0;
+        place += at + (l[at] > e);
       }
+      __syncthreads();
+      if (e) s.list[place] = e;
+      __syncthreads();
+      return;
     }
+    const int N = n <= kList / 2 ? kList / 2 : kList;
+    for (int i = n + threadIdx.x; i < N; i += kThreads) s.list[i] = 0;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      if ((warp + j * kWarps) * 32 >= n) break;
-      if (e[j]) s.list[place[j]] = e[j];
-    }
-    __syncthreads();
+#pragma unroll 1
+    for (int k = 2; k <= N; k *= 2)
+#pragma unroll 1
+      for (int j = k / 2; j; j /= 2) {
+        for (int i = threadIdx.x; i < N / 2; i += kThreads) {
+          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+          const u64 x = s.list[lo], y = s.list[hi];
+          if ((x < y) == ((lo & k) == 0)) {
+            s.list[lo] = y;
+            s.list[hi] = x;
+          }
+        }
+        __syncthreads();
+      }
   }
 
   // The place in the sorted list of n entries at which the running sum of the weights,
@@ -868,7 +873,7 @@ struct Row {
   // takes more).
   __device__ __forceinline__ Edge top_p(float p, Left old, uint32_t min_p_key, bool *known) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
-    // (2^16 of them: the sum of a slice of 65535 tokens stays below 2^32; of longer ones some bits are dropped).  A token beyond the last bin but one has a weight below
+    // (2^16 of them: the sum of a slice of 65000 tokens stays below 2^32; of longer ones some bits are dropped).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
     const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
     const Left weighted = old.above(w.floor);
@@ -876,13 +881,13 @@ struct Row {
     each<kHeavy>(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[4], int v) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float t = (m - x[e]) * scale;
-        if (!(t < (float)(kBins - 1)) || !old(x[e], v + e)) continue;
-        const int b = (int)t;
+        const float t = fmaf(m - x[e], scale, -0.5f);
+        const int b = __float_as_int(t + 0x1.8p23f) - 0x4B400000;  // the nearest whole number: that below t + 0.5
         float f;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(t * (-1.f / 64.f)));
-        // in (2^-(o + 1), 2^-o], o = b / 64: 16 bits of it from the float's own
-        atomicAdd(&s.hist[b], (32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8)) >> a.drop);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(fmaf(t, -1.f / 64.f, -0.5f / 64.f)));
+        // in [2^-(o + 1), 2^-o], o = b / 64: 16 bits of it from the float's own
+        const unsigned n = 32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8);
+        if (t < (float)(kBins - 1) && old(x[e], v + e)) atomicAdd(&s.hist[b], n >> a.drop);
       }
     });
     int b0, b1;
@@ -894,29 +899,28 @@ struct Row {
              [&](u64 all) -> u64 { return share_of(p, all - (all >> off)); },
              [&](u64 all) -> u64 { return share_of(p, all + (all >> off) + ((u64)a.V << max(a.S - 31, 0))); }, &b0, &b1, &base, &own);
     // the exact sums, of all and of what lies above the bins that hold the edge
-    u64 all = 0, above = 0;
-    const float first = (float)b0, behind = b1 < kBins ? (float)(b1 + 1) : INFINITY;  // of the bins with the edge
+    u64 rest = 0, above = 0;
+    const float first = (float)b0 - 0.5f, behind = b1 < kBins ? (float)b1 + 0.5f : INFINITY;  // of the bins with the edge
     each<kHeavy>(weighted.at, [&](const float (&x)[4], int v) {
       u64 q[4];
-      w.of(x, q);
+      w.of(x, {weighted(x[0], v), weighted(x[1], v + 1), weighted(x[2], v + 2), weighted(x[3], v + 3)}, q);
       unsigned in = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float t = (m - x[e]) * scale;
-        const bool left = weighted(x[e], v + e);
-        const u64 n = left ? q[e] : 0;
-        all += n;
-        above += t < first ? n : 0;
-        in |= t >= first && t < behind && left ? 1u << e : 0;
+        const float t = fmaf(m - x[e], scale, -0.5f);
+        if (t < first) above += q[e];
+        else rest += q[e];
+        in |= t >= first && t <= behind && q[e] ? 1u << e : 0;
       }
       gather(in, x, v);
     });
     above = warp_sum(above);
     if (lane == 0) s.kept[warp] = above;
-    all = block_sum(all);  // (its barrier makes s.kept known)
+    u64 all = block_sum(rest);  // (its barrier makes s.kept known)
     above = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) above += s.kept[i];
+    all += above;
     tell(s.listed, all, above);
     all = above = 0;
     for (int r = 0; r < CS; ++r) {
@@ -998,6 +1002,7 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
   // The largest logit; and, for top-k, one that at least k lie at or above: of each of the a.full warps whose ranges are
   // full of tokens the j-th of the lanes' largest, of these the ceil(k / j)-th.
   float most = -INFINITY;
+  int where = 0;  // the first ID of the granule that has the lane's largest
   // Temperature alone, from global memory: the weights are summed in the same pass, relative to the largest logit that
   // the warp has seen yet.
   const bool once = !HELD && k == 0 && !(p < 1.f) && !(min_p > 0.f) && temp >= FLT_MIN;
@@ -1008,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
     r.w.set(-INFINITY, c, a.S, s.table);
     r.w.floor = FLT_MAX;
     known = true;
-    r.template scan<R::kHeavy>([&](const uint4 &v, int id) {
+    r.template scan<16 / VEC>([&](const uint4 &v, int id) {
       const float top = R::most(v);
       if (__any_sync(~0u, top > most)) {
         most = fmaxf(most, top);
@@ -1022,15 +1027,20 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
       }
       R::by_four(v, id, [&](const float (&x)[4], int) {
         u64 q[4];
-        r.w.of(x, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += x[e] > r.w.floor ? q[e] : 0;
+        const float f = r.w.floor;
+        r.w.of(x, {x[0] > f, x[1] > f, x[2] > f, x[3] > f}, q);
+        sum += (q[0] + q[1]) + (q[2] + q[3]);
       });
     });
     sum = warp_sum(sum);
   } else {
-    r.template scan<R::kLight>([&](const uint4 &v, int) { most = fmaxf(most, R::most(v)); });
+    r.template scan<R::kLight>([&](const uint4 &v, int id) {
+      const float top = R::most(v);
+      where = top > most ? id : where;
+      most = fmaxf(most, top);
+    });
   }
+  const float lane_most = most;
   const int own_shift = r.w.shift;
   const int j = k > 0 && a.full > 0 ? (int)(((long long)k + a.full - 1) / a.full) : 33;
   float bound = -INFINITY;
@@ -1087,11 +1097,12 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
       if (threadIdx.x == 0) s.id = INT_MAX;
       __syncthreads();
       int first = INT_MAX;
-      const float m = tr_unord(top);
-      r.template each<R::kLight>(m, [&](const float (&y)[4], int v) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) first = min(first, y[e] == m ? v + e : INT_MAX);
-      });
+      if (key_of(lane_most) == top) {
+        for (int e = VEC - 1; e >= 0; --e) {
+          const int v = where + e;
+          if (v >= 0 && v < a.V && key_of(get(x, v)) == top) first = v;
+        }
+      }
       atomicMin(&s.id, first);
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -1121,11 +1132,9 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
   u64 all;
   const int id = r.first_past(left.at,
                               [&](const float (&y)[4], int v) {
-                                u64 q[4], sum = 0;
-                                r.w.of(y, q);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) sum += left(y[e], v + e) ? q[e] : 0;
-                                return sum;
+                                u64 q[4];
+                                r.w.of(y, {left(y[0], v), left(y[1], v + 1), left(y[2], v + 2), left(y[3], v + 3)}, q);
+                                return (q[0] + q[1]) + (q[2] + q[3]);
                               },
                               [&](float y, int v) -> u64 { return left(y, v) ? r.w(y) : 0; },
                               [&](u64 sum) {
@@ -1157,7 +1166,7 @@ const Table &table() {
 // Many rows: a CTA each (three on an SM), which reads it from L2 in every pass after the first.  Few: a cluster
 // each, in whose shared memory it lies, 64 KB to a CTA.
 constexpr long long kSlice = 64 * 1024;
-constexpr int kMostTokens = 65535;  // of a slice, see top_p
+constexpr int kMostTokens = 65000;  // of a slice, see top_p
 
 template <typename T, bool HELD>
 int launch(SampleArgs a, int cs, size_t smem, long long ahead, cudaStream_t s) {
