@@ -137,6 +137,9 @@ def lib():
     return _LIB
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
@@ -540,56 +543,69 @@ class Rope:
 _ROW_TYPES = {torch.bfloat16: TR_KV_BF16, torch.float16: TR_KV_F16}
 _QKV = struct.Struct("@PPPiiiii9q")  # tr_qkv
 assert _QKV.size == ctypes.sizeof(tr_qkv)
-_NO_STRIDE = (0, 0, 0)
+_NONE = (0, 0, (0, 0, 0))
 
 
-def _rows_of(Q, K, V, rope, index):
-    """A tr_qkv of the three (Q or K and V may be None), as bytes: a step is a few
-    microseconds on the device, so no ctypes fields are set here."""
-    x = K if Q is None else Q
+def _rows_of(x, name, B, T, d, dtype, index):
+    """Address, heads and strides of Q, K or V (None: not there)."""
     if x is None:
-        x = V
-    B, T, _, d = x.shape
-    if d != rope.d:
+        return _NONE
+    shape, st = x.shape, x.stride()
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d:
+        raise ValueError("%s must be [B, T, heads, d]" % name)
+    if x.dtype is not dtype:
+        raise ValueError("Q, K and V must have the same dtype")
+    if x.get_device() != index:
+        raise ValueError("%s must live on the current CUDA device" % name)
+    if st[3] != 1:
+        raise ValueError("%s must be contiguous along the last axis" % name)
+    return x.data_ptr(), shape[2], st[:3]
+
+
+def _qkv(Q, K, V, rope, index):
+    """A tr_qkv of the three (Q, or K and V, may be None), as bytes: a step is a few
+    microseconds on the device, so no ctypes fields are set here."""
+    x = Q if Q is not None else K if K is not None else V
+    if x is None:
+        raise ValueError("Q, K and V are all None")
+    if x.dim() != 4:
         raise ValueError("Q, K and V must be [B, T, heads, d]")
-    dtype, at, heads, strides = x.dtype, [], [], []
-    for t, name in ((Q, "Q"), (K, "K"), (V, "V")):
-        if t is None:
-            at.append(0)
-            heads.append(0)
-            strides += _NO_STRIDE
-            continue
-        shape, st = t.shape, t.stride()
-        if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d:
-            raise ValueError("Q, K and V must be [B, T, heads, d]")
-        if t.dtype != dtype:
-            raise ValueError("Q, K and V must have the same dtype")
-        if t.get_device() != index:
-            raise ValueError("%s must live on the current CUDA device" % name)
-        if st[3] != 1:
-            raise ValueError("%s must be contiguous along the last axis" % name)
-        at.append(t.data_ptr())
-        heads.append(shape[2])
-        strides += st[:3]
-    if heads[1] and heads[2] and heads[1] != heads[2]:
-        raise ValueError("K and V must have the same heads")
-    if dtype not in _ROW_TYPES:
+    B, T = x.shape[:2]
+    d, dtype = rope.d, x.dtype
+    kind = _ROW_TYPES.get(dtype)
+    if kind is None:
         raise ValueError("Q, K and V must be bfloat16 or float16")
     if rope._index != index and rope._index != -1:
         raise ValueError("the rope's tensors must live on the current CUDA device")
-    return _QKV.pack(at[0], at[1], at[2], _ROW_TYPES[dtype], B, T, heads[0], heads[1] or heads[2], *strides), B, T
+    q, Hq, qs = _rows_of(Q, "Q", B, T, d, dtype, index)
+    k, Hk, ks = _rows_of(K, "K", B, T, d, dtype, index)
+    v, Hv, vs = _rows_of(V, "V", B, T, d, dtype, index)
+    if Hk != Hv and K is not None and V is not None:
+        raise ValueError("K and V must have the same heads")
+    return _QKV.pack(q, k, v, kind, B, T, Hq, Hk or Hv, *qs, *ks, *vs)
 
 
-def _dense(t, name, dtype, index, shape=None):
-    if t.dtype != dtype:
+def _dense(t, name, dtype, index, shape):
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s" % (name, dtype))
     if t.get_device() != index:
         raise ValueError("%s must live on the current CUDA device" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s" % (name, list(shape)))
     return t.data_ptr()
+
+
+def _as(x, y, name, index):
+    """The address of the output y of the input x (both may be None)."""
+    if x is None:
+        if y is not None:
+            raise ValueError("%s belongs to its input" % name)
+        return None
+    if y is None:
+        raise ValueError("%s belongs to its input" % name)
+    return _dense(y, name, x.dtype, index, x.shape)
 
 
 def tr_qkv_rope(Q, K, V, rope, pos, Qo, Ko, Vo, tree=None):
@@ -597,20 +613,14 @@ def tr_qkv_rope(Q, K, V, rope, pos, Qo, Ko, Vo, tree=None):
     and copies V to Vo; the inputs may be strided views, None leaves one (and its
     output) out.  Row i of sequence b stands at position pos[b] + i, with ``tree``
     (T = its nodes) at pos[b] + depth of node i."""
-    index = torch._C._cuda_getDevice()
-    if Q is None and K is None and V is None:
-        raise ValueError("Q, K and V are all None")
-    rows, B, T = _rows_of(Q, K, V, rope, index)
-    if tree is not None and tree.N != T:
+    index = _current_device()
+    rows = _qkv(Q, K, V, rope, index)
+    x = Q if Q is not None else K if K is not None else V
+    if tree is not None and tree.N != x.shape[1]:
         raise ValueError("T must be the tree's nodes")
-    out = []
-    for x, y, name in ((Q, Qo, "Qo"), (K, Ko, "Ko"), (V, Vo, "Vo")):
-        if (x is None) != (y is None):
-            raise ValueError("%s belongs to its input" % name)
-        out.append(None if x is None else _dense(y, name, x.dtype, index, x.shape))
-    rc = lib().tr_qkv_rope(rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, (B,)),
-                           None if tree is None else tree.handle, out[0], out[1], out[2],
-                           torch._C._cuda_getCurrentRawStream(index))
+    rc = lib().tr_qkv_rope(rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, x.shape[:1]),
+                           None if tree is None else tree._h, _as(Q, Qo, "Qo", index), _as(K, Ko, "Ko", index),
+                           _as(V, Vo, "Vo", index), _current_stream(index))
     if rc:
         _check("tr_qkv_rope", rc)
 
@@ -621,18 +631,19 @@ def tr_kv_append_rope(Q, Kn, Vn, rope, cache, Qo, ws, pos=None, count=None):
     strided views.  Row i of sequence b stands at position pos[b] + i, without ``pos`` at
     its place in the cache, L[b] + i."""
     stream, index = cache._stream(), cache._index
-    if Kn is None or Vn is None or (Q is None) != (Qo is None):
-        raise ValueError("Kn and Vn are needed, Qo belongs to Q")
-    rows, B, T = _rows_of(Q, Kn, Vn, rope, index)
-    if B != cache.B or Kn.shape[2] != cache.Hkv or rope.d != cache.d:
+    if Kn is None or Vn is None:
+        raise ValueError("Kn and Vn are needed")
+    rows = _qkv(Q, Kn, Vn, rope, index)
+    shape = Kn.shape
+    if shape[0] != cache.B or shape[2] != cache.Hkv or rope.d != cache.d:
         raise ValueError("Kn and Vn must be [B, T, Hkv, d]")
-    if Kn.dtype != cache.row_dtype:
+    if Kn.dtype is not cache.row_dtype:
         raise ValueError("Kn must be %s" % cache.row_dtype)
+    n = shape[:1]
     rc = lib().tr_kv_append_rope(
-        rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, (B,)),
-        None if count is None else _dense(count, "count", torch.int32, index, (B,)), cache._ref,
-        None if Qo is None else _dense(Qo, "Qo", Q.dtype, index, Q.shape), cache._arg(ws, "ws", torch.uint8),
-        ws.numel(), stream)
+        rows, rope._ref, None if pos is None else _dense(pos, "pos", torch.int32, index, n),
+        None if count is None else _dense(count, "count", torch.int32, index, n), cache._ref,
+        _as(Q, Qo, "Qo", index), cache._arg(ws, "ws", torch.uint8), ws.numel(), stream)
     if rc:
         _check("tr_kv_append_rope", rc)
 
@@ -642,14 +653,17 @@ def tr_sample(logits, U, token, temperature=None, top_k=None, top_p=None, min_p=
     int32, by the uniforms U [rows]; temperature, top_p and min_p [rows] float32 and top_k [rows]
     int32 are each row's own rules (None: 1, and off).  logprob [rows] float32 gets the
     logarithm of the drawn token's probability among those that the rules left."""
-    index = torch._C._cuda_getDevice()
-    if logits.dim() != 2:
+    index = _current_device()
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [rows, ld]")
-    rows, ld = logits.shape
-    V = ld if V is None else V
-    _i31(V, "V")
-    at = _dense(logits, "logits", logits.dtype, index)
-    n = (rows,)
+    rows, ld = shape
+    if V is None:
+        V = ld
+    else:
+        _i31(V, "V")
+    at = _dense(logits, "logits", logits.dtype, index, shape)
+    n = shape[:1]
     rc = lib().tr_sample(
         at, _ftype(logits), rows, V, ld,
         None if temperature is None else _dense(temperature, "temperature", torch.float32, index, n),
@@ -658,7 +672,7 @@ def tr_sample(logits, U, token, temperature=None, top_k=None, top_p=None, min_p=
         None if min_p is None else _dense(min_p, "min_p", torch.float32, index, n),
         _dense(U, "U", torch.float32, index, n), _dense(token, "token", torch.int32, index, n),
         None if logprob is None else _dense(logprob, "logprob", torch.float32, index, n),
-        torch._C._cuda_getCurrentRawStream(index))
+        _current_stream(index))
     if rc:
         _check("tr_sample", rc)
 
