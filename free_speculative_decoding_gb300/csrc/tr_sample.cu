@@ -37,7 +37,7 @@ struct SampleArgs {
   const int32_t *top_k;
   int32_t *token;
   float *logprob;
-  int granules;  // of a CTA's slice, kWarps * 32 or a multiple
+  int granules;  // of a CTA's slice, its threads or a multiple
   int full;      // warps of a row's cluster whose ranges hold nothing but tokens, at least
   int drop;      // bits that top-p's histogram gives up
 };
@@ -233,17 +233,18 @@ __device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f
 // rows that a cluster's shared memory holds
 // ---------------------------------------------------------------------------
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: of rows in shared memory, where a CTA has an SM about to itself, and of rows that are read from L2.
+constexpr int kHeldThreads = 512, kReadThreads = 256;
+constexpr int kMaxWarps = kHeldThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;       // 64 to a power of two, where they are weighted
 constexpr int kList = 1024;
 
 struct alignas(128) Smem {  // the slice lies behind it
   float2 table[64];
-  u64 box[2][kMaxCluster][2 + kWarps / 2];  // what the cluster's CTAs have told this one, of two exchanges
-  u64 wsum[kWarps];
-  u64 kept[kWarps];               // the weights that are left in the warps' ranges, where they are known
+  u64 box[2][kMaxCluster][2 + kMaxWarps / 2];  // what the cluster's CTAs have told this one, of two exchanges
+  u64 wsum[kMaxWarps];
+  u64 kept[kMaxWarps];               // the weights that are left in the warps' ranges, where they are known
   unsigned listed;                // tokens that were to go to this CTA's list
   uint32_t listed_low;            // the key that at least k tokens lie at or above
   float u;
@@ -257,6 +258,7 @@ struct alignas(128) Smem {  // the slice lies behind it
     u64 list[kList];              // key << 32 | ~ID, of all the cluster's CTAs
   };
   u64 own[kList];                 // the same, gathered by this one
+  u64 groups[kMaxCluster][64];    // sums of the histograms' groups
 };
 
 static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, hist) % 16 == 0);
@@ -265,6 +267,7 @@ static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, hist) % 16 == 0);
 template <typename T, bool HELD>
 struct Row {
   static constexpr int VEC = 16 / sizeof(T);
+  static constexpr int NT = HELD ? kHeldThreads : kReadThreads, NW = NT / 32;
   const SampleArgs &a;
   Smem &s;
   const uint4 *data;   // held: the slice's 16-byte granules; what is no token is -inf
@@ -379,7 +382,7 @@ struct Row {
     __syncthreads();
     u64 r = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) r += s.wsum[i];
+    for (int i = 0; i < NW; ++i) r += s.wsum[i];
     __syncthreads();
     return r;
   }
@@ -399,8 +402,8 @@ struct Row {
   }
   // The same with 32 bits of every warp, which its lane 0 has in s.wsum.
   __device__ __forceinline__ void tell_warps(u64 x) {
-    for (int i = threadIdx.x; i < CS * (1 + kWarps / 2); i += kThreads) {
-      const int r = i / (1 + kWarps / 2), w = i - r * (1 + kWarps / 2);
+    for (int i = threadIdx.x; i < CS * (1 + NW / 2); i += NT) {
+      const int r = i / (1 + NW / 2), w = i - r * (1 + NW / 2);
       u64 *to = &s.box[parity][rank][w];
       if (CS > 1) to = cg::this_cluster().map_shared_rank(to, r);
       *to = w == 0 ? x : (s.wsum[2 * w - 2] & 0xFFFFFFFFu) | s.wsum[2 * w - 1] << 32;
@@ -409,7 +412,7 @@ struct Row {
     parity ^= 1;
   }
   __device__ __forceinline__ uint32_t heard_warp(int i) const {  // i: of the cluster's
-    const int r = i / kWarps, w = i - r * kWarps;
+    const int r = i / NW, w = i - r * NW;
     return (uint32_t)(s.box[parity ^ 1][r][1 + w / 2] >> (w & 1) * 32);
   }
   __device__ __forceinline__ u64 heard(int r, int i) const { return s.box[parity ^ 1][r][i]; }
@@ -434,7 +437,7 @@ struct Row {
   // amount(x, ID) one's.  known: the sums of the warps' ranges are in s.kept.
   template <typename F, typename A, typename G>
   __device__ __forceinline__ int first_past(float floor, F amounts, A amount, G target_of, u64 *all, bool known = false) {
-    const int keep0 = g0, keep1 = g1, seg = a.granules / kWarps;
+    const int keep0 = g0, keep1 = g1, seg = a.granules / NW;
     u64 before = 0, target = 0, mine;
     bool here = true;
     // the sums of the warps' ranges; then, in the CTA that holds the place, of an eighth of the range that does
@@ -451,7 +454,7 @@ struct Row {
       if (round) break;
       u64 cta = 0, sum = 0;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) cta += s.wsum[i];
+      for (int i = 0; i < NW; ++i) cta += s.wsum[i];
       tell(cta);
       for (int r = 0; r < CS; ++r) {
         if (r < rank) before += heard(r, 0);
@@ -462,15 +465,15 @@ struct Row {
       here = before <= target && before + cta > target;
       if (!here) break;
       int q = 0;
-      while (q < kWarps - 1 && before + s.wsum[q] <= target) before += s.wsum[q++];
-      const int part = ((seg + kWarps - 1) / kWarps + 31) & ~31, hi = (q + 1) * seg;
+      while (q < NW - 1 && before + s.wsum[q] <= target) before += s.wsum[q++];
+      const int part = ((seg + NW - 1) / NW + 31) & ~31, hi = (q + 1) * seg;
       g0 = min(hi, q * seg + warp * part);
       g1 = min(hi, g0 + part);
     }
     if (here) {
       if (known) {  // sums that were made otherwise may differ in their last places
         u64 all_parts = 0;
-        for (int i = 0; i < kWarps; ++i) all_parts += s.wsum[i];
+        for (int i = 0; i < NW; ++i) all_parts += s.wsum[i];
         target = min(target, before + max(all_parts, 1ull) - 1);
       }
       for (int i = 0; i < warp; ++i) before += s.wsum[i];
@@ -514,49 +517,68 @@ struct Row {
     return (int)fminf((m - x) * scale, (float)(kBins - 1));
   }
 
-  // Adds up the CTAs' histograms (each CTA all of them: one wait for the cluster instead of three); the first bins at
-  // which the running sum reaches lo_of(all) and hi_of(all) (kBins where it does not), the sum before the first of
-  // them, and its own entry in 32 bits.
+  // The sum of the cluster's histograms, found in two steps: each CTA tells the others the sums of its kGroups groups of
+  // bins; of the groups that matter the bins are read from all CTAs.  Found are the first bins at which the running sum
+  // reaches lo_of(all) and hi_of(all) (kBins where it does not), the sum before the first of them, and its own entry in
+  // 32 bits.
+  static constexpr int kGroups = 64, kGroup = kBins / kGroups;
   template <typename F, typename G, typename H>
   __device__ __forceinline__ void crossing(F value, G lo_of, H hi_of, int *b0, int *b1, u64 *base, unsigned *own) {
-    constexpr int kPer = kBins / kThreads;  // consecutive bins of a thread
     if (threadIdx.x < 3) s.found[threadIdx.x] = kBins;
-    sync();  // the histograms are whole
-    u64 v[kPer] = {}, sum = 0;
-#pragma unroll 4
+    __syncthreads();  // the histogram is whole
+    static_assert(kGroup == 32);
+#pragma unroll 1
+    for (int g = warp; g < kGroups; g += NW) {
+      const u64 v = warp_sum(value(g * 32 + lane, s.hist[g * 32 + lane]));
+      if (lane < CS) {
+        u64 *to = &s.groups[rank][g];
+        if (CS > 1) to = cg::this_cluster().map_shared_rank(to, lane);
+        *to = v;
+      }
+    }
+    sync();
+    // every warp: a lane has groups 2 lane and 2 lane + 1
+    u64 v0 = 0, v1 = 0;
     for (int r = 0; r < CS; ++r) {
-      const unsigned *h = s.hist + threadIdx.x * kPer;
-      if (CS > 1) h = cg::this_cluster().map_shared_rank(h, r);
-#pragma unroll
-      for (int j = 0; j < kPer; j += 4) {
-        const uint4 n = *reinterpret_cast<const uint4 *>(h + j);
-        v[j] += n.x;
-        v[j + 1] += n.y;
-        v[j + 2] += n.z;
-        v[j + 3] += n.w;
-      }
+      v0 += s.groups[r][2 * lane];
+      v1 += s.groups[r][2 * lane + 1];
     }
+    u64 incl = v0 + v1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      v[j] = value(threadIdx.x * kPer + j, v[j]);
-      sum += v[j];
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += y;
     }
-    const u64 incl = block_scan(sum);
-    if (threadIdx.x == kThreads - 1) s.cum = incl;
-    __syncthreads();
-    const u64 all = s.cum, lo = lo_of(all), hi = hi_of(all);
-    __syncthreads();
-    u64 run = incl - sum;
+    const u64 all = __shfl_sync(~0u, incl, 31), lo = lo_of(all), hi = hi_of(all);
+    if (warp < 2) {  // one for lo, one for hi
+      const u64 mark = warp ? hi : lo;
+      const unsigned past = __ballot_sync(~0u, incl >= mark);
+      if (past && mark > 0) {
+        const int l = __ffs(past) - 1;
+        const u64 e = __shfl_sync(~0u, incl, l), w0 = __shfl_sync(~0u, v0, l), w1 = __shfl_sync(~0u, v1, l);
+        u64 before = e - w0 - w1;
+        const int g = 2 * l + (before + w0 < mark);
+        if (before + w0 < mark) before += w0;
+        u64 n = 0;
+        for (int r = 0; r < CS; ++r) {
+          const unsigned *h = &s.hist[g * 32 + lane];
+          n += value(g * 32 + lane, CS > 1 ? *cg::this_cluster().map_shared_rank(h, r) : *h);
+        }
+        u64 c = n;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const unsigned b = threadIdx.x * kPer + j;
-      if (run < lo && run + v[j] >= lo) {
-        s.found[0] = b;
-        s.found[2] = (unsigned)v[j];
-        s.cum = run;
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 y = __shfl_up_sync(~0u, c, o);
+          if (lane >= o) c += y;
+        }
+        const unsigned in = __ballot_sync(~0u, before + c >= mark);
+        if (in && lane == __ffs(in) - 1) {
+          s.found[warp] = g * 32 + lane;
+          if (warp == 0) {
+            s.found[2] = (unsigned)n;
+            s.cum = before + c - n;
+          }
+        }
       }
-      if (run < hi && run + v[j] >= hi) s.found[1] = b;
-      run += v[j];
     }
     __syncthreads();
     *b0 = s.found[0];
@@ -568,7 +590,7 @@ struct Row {
   // Clears the histogram and the list before anybody adds to them.
   __device__ __forceinline__ void clear() {
     __syncthreads();  // the last list has been read
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += NT) s.hist[i] = 0;
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
   }
@@ -601,76 +623,76 @@ struct Row {
     return (int)n;
   }
 
-  // Sorts the list's n <= kList entries (none is 0), the largest first.  Up to 256: 32 of them by each warp in registers,
-  // then every entry's place is its place among these plus the numbers of larger ones in the other warps', found by
-  // bisection.  More: by exchanges.
+  // Sorts the list's n <= kList entries (none is 0), the largest first: 32 of them by each warp in registers, then every
+  // entry's place is its place among these plus the numbers of larger ones in the other groups, found by bisection,
+  // four groups at a time.
   __device__ __forceinline__ void sort_list(int n) {
-    if (n <= kThreads) {
-      const int i = threadIdx.x;
-      u64 e = i < n ? s.list[i] : 0;
+    constexpr int kMine = kList / NT;  // entries of a thread
+    for (int i = n + threadIdx.x; i < ((n + 127) & ~127); i += NT) s.list[i] = 0;
+    __syncthreads();
+    u64 e[kMine];
+    int at[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int i = threadIdx.x + j * NT;
+      if (i - lane >= n) break;
+      u64 v = s.list[i];
 #pragma unroll 1
       for (int k = 2; k <= 32; k *= 2)
 #pragma unroll 1
         for (int d = k / 2; d; d /= 2) {
-          const u64 o = __shfl_xor_sync(~0u, e, d);
-          e = (((lane & k) == 0 || k == 32) == ((lane & d) == 0)) == (e > o) ? e : o;
+          const u64 o = __shfl_xor_sync(~0u, v, d);
+          v = (((lane & k) == 0 || k == 32) == ((lane & d) == 0)) == (v > o) ? v : o;
         }
-      s.list[i] = e;
-      __syncthreads();
-      int place = lane;
-#pragma unroll 2
-      for (int g = 0; g < n; g += 32) {
-        if (g == i - lane) continue;
-        const u64 *l = s.list + g;
-        int at = 0;
-#pragma unroll
-        for (int d = 16; d; d /= 2) at += l[at + d - 1] > e ? d : 0;
-        place += at + (l[at] > e);
-      }
-      __syncthreads();
-      if (e) s.list[place] = e;
-      __syncthreads();
-      return;
+      s.list[i] = e[j] = v;
     }
-    const int N = n <= kList / 2 ? kList / 2 : kList;
-    for (int i = n + threadIdx.x; i < N; i += kThreads) s.list[i] = 0;
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int i = threadIdx.x + j * NT;
+      if (i - lane >= n) break;
+      at[j] = 0;  // its own group among them: the entries before it there
 #pragma unroll 1
-    for (int k = 2; k <= N; k *= 2)
-#pragma unroll 1
-      for (int j = k / 2; j; j /= 2) {
-        for (int i = threadIdx.x; i < N / 2; i += kThreads) {
-          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-          const u64 x = s.list[lo], y = s.list[hi];
-          if ((x < y) == ((lo & k) == 0)) {
-            s.list[lo] = y;
-            s.list[hi] = x;
-          }
-        }
-        __syncthreads();
+      for (int g = 0; g < n; g += 128) {
+        int c[4] = {};
+#pragma unroll
+        for (int d = 16; d; d /= 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) c[q] += s.list[g + q * 32 + c[q] + d - 1] > e[j] ? d : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at[j] += c[q] + (s.list[g + q * 32 + c[q]] > e[j]);
       }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      if ((int)threadIdx.x + j * NT - lane >= n) break;
+      if (e[j]) s.list[at[j]] = e[j];
+    }
+    __syncthreads();
   }
 
+  static constexpr int kPer = kList / NT;
   // The place in the sorted list of n entries at which the running sum of the weights,
   // from `base` on, reaches target_of(base + their sum); n where it does not.
   template <typename G>
   __device__ __forceinline__ int place(int n, u64 base, G target_of) {
-    u64 v[kList / kThreads], sum = 0;
+    u64 v[kPer], sum = 0;
 #pragma unroll
-    for (int j = 0; j < kList / kThreads; ++j) {
-      const int i = threadIdx.x * (kList / kThreads) + j;
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x * (kPer) + j;
       v[j] = i < n ? w(tr_unord((uint32_t)(s.list[i] >> 32))) : 0;
       sum += v[j];
     }
     const u64 incl = block_scan(sum);
-    if (threadIdx.x == kThreads - 1) s.cum = incl;
+    if (threadIdx.x == NT - 1) s.cum = incl;
     if (threadIdx.x == 0) s.id = n;
     __syncthreads();
     const u64 target = target_of(base + s.cum);
     u64 run = base + incl - sum;
 #pragma unroll
-    for (int j = 0; j < kList / kThreads; ++j) {
-      if (run < target && run + v[j] >= target) s.id = threadIdx.x * (kList / kThreads) + j;
+    for (int j = 0; j < kPer; ++j) {
+      if (run < target && run + v[j] >= target) s.id = threadIdx.x * (kPer) + j;
       run += v[j];
     }
     __syncthreads();
@@ -693,7 +715,7 @@ struct Row {
     u64 base = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       sync();  // the first CTA has read the last pass's sums
-      for (int i = threadIdx.x; i < 256; i += kThreads) s.wide[i] = 0;
+      for (int i = threadIdx.x; i < 256; i += NT) s.wide[i] = 0;
       __syncthreads();
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
       each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int v) {
@@ -718,7 +740,7 @@ struct Row {
         // thread t has the bin that is t-th from above
         const int b = 255 - (int)threadIdx.x;
         u64 n = 0;
-        for (int r = 0; r < CS; ++r) n += CS > 1 ? *cg::this_cluster().map_shared_rank(&s.wide[b], r) : s.wide[b];
+        for (int r = 0; b >= 0 && r < CS; ++r) n += CS > 1 ? *cg::this_cluster().map_shared_rank(&s.wide[b], r) : s.wide[b];
         const u64 incl = base + block_scan(n);
         if (incl >= target && incl - n < target) {
           s.found[0] = b;
@@ -752,11 +774,11 @@ struct Row {
 
   // Adds the weights of the sorted list's first n entries to s.kept of the warps in whose ranges they lie.
   __device__ __forceinline__ void add_listed(int n) {
-    const int seg = a.granules / kWarps * VEC;  // a warp's range
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int seg = a.granules / NW * VEC;  // a warp's range
+    for (int i = threadIdx.x; i < n; i += NT) {
       const u64 e = s.list[i];
       const unsigned at = (0xFFFFFFFFu - (uint32_t)e) - (unsigned)id0;
-      if (at < (unsigned)(kWarps * seg)) atomicAdd(&s.kept[at / seg], w(tr_unord((uint32_t)(e >> 32))));
+      if (at < (unsigned)(NW * seg)) atomicAdd(&s.kept[at / seg], w(tr_unord((uint32_t)(e >> 32))));
     }
     __syncthreads();
   }
@@ -808,7 +830,7 @@ struct Row {
         for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
         if (lane == 0) s.wsum[warp] = __float_as_uint(least);
         __syncthreads();
-        for (int i = 0; i < kWarps; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
+        for (int i = 0; i < NW; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
         tell(__float_as_uint(least));
         for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
       }
@@ -843,7 +865,7 @@ struct Row {
     }
     if (!ok) return narrow_down_k(k);
     if (whole) {
-      if (threadIdx.x < kWarps) s.kept[threadIdx.x] = 0;
+      if (threadIdx.x < NW) s.kept[threadIdx.x] = 0;
       __syncthreads();
       add_listed(*left);
     }
@@ -852,7 +874,7 @@ struct Row {
   // How many of the sorted list's first n entries have at least this key (the first one has).
   __device__ __forceinline__ int at_least(int n, uint32_t key) {
     int c = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) c += (uint32_t)(s.list[i] >> 32) >= key;
+    for (int i = threadIdx.x; i < n; i += NT) c += (uint32_t)(s.list[i] >> 32) >= key;
     return (int)block_sum(c);
   }
   __device__ __noinline__ Edge narrow_down_k(int k) {
@@ -919,7 +941,7 @@ struct Row {
     u64 all = block_sum(rest);  // (its barrier makes s.kept known)
     above = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) above += s.kept[i];
+    for (int i = 0; i < NW; ++i) above += s.kept[i];
     all += above;
     tell(s.listed, all, above);
     all = above = 0;
@@ -942,20 +964,20 @@ struct Row {
 };
 
 template <typename T, bool HELD>
-__global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const SampleArgs a, int CS, long long ahead,
+__global__ void __launch_bounds__(HELD ? kHeldThreads : kReadThreads, HELD ? 1 : 3) sample_kernel(const SampleArgs a, int CS,
                                                              const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
   using R = Row<T, HELD>;
   R r(a, s);
-  constexpr int VEC = R::VEC;
+  constexpr int VEC = R::VEC, NT = R::NT, NW = R::NW;
   const long long row = blockIdx.x / CS;
   r.CS = CS;
   r.rank = blockIdx.x - (int)row * CS;
   uint4 *const data = reinterpret_cast<uint4 *>(smem + sizeof(Smem));
   r.data = data;
-  r.g0 = r.warp * (a.granules / kWarps);
-  r.g1 = r.g0 + a.granules / kWarps;
+  r.g0 = r.warp * (a.granules / NW);
+  r.g1 = r.g0 + a.granules / NW;
   fill_table(s.table, table);
   if (threadIdx.x == 0) s.listed = 0;
   tr_let_next_start();
@@ -982,18 +1004,12 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  if (HELD && threadIdx.x == 0 && ahead > 0 && row + ahead < a.rows) {
-    // the slice that the CTA behind this one will want, into L2: memory works on while this one computes
-    const uintptr_t to = ((uintptr_t)(x + ahead * a.ld + r.id0 + off) + 15) & ~(uintptr_t)15;
-    const long long n = min((long long)a.granules * 16, (long long)((uintptr_t)(x + ahead * a.ld + a.V) - to)) & ~15ll;
-    if (n > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(to), "r"((int)n) : "memory");
-  }
   const float temp = a.temperature ? a.temperature[row] : 1.f, p = a.top_p ? a.top_p[row] : 1.f,
               min_p = a.min_p ? a.min_p[row] : 0.f;
   int k = a.top_k ? a.top_k[row] : 0;
   if (k >= a.V) k = 0;
   const float2 c = log2e_over(temp);
-  if (threadIdx.x == kThreads - 1) {  // the rules, while the slice is under way; 64-bit arithmetic once
+  if (threadIdx.x == NT - 1) {  // the rules, while the slice is under way; 64-bit arithmetic once
     s.u = uniform_of(a.U[row]);
     s.below = min_p_below(min_p, temp);
   }
@@ -1062,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 3) sample_kernel(const Sa
   if (r.lane == 0) s.wsum[r.warp] = (u64)key_of(most) << 32 | key_of(bound);
   __syncthreads();
   uint32_t top = 0, low = 0;
-  for (int i = 0; i < kWarps; ++i) top = max(top, (uint32_t)(s.wsum[i] >> 32));
+  for (int i = 0; i < NW; ++i) top = max(top, (uint32_t)(s.wsum[i] >> 32));
   const uint32_t own_top = top;
   r.tell_warps(top);
   int owner = 0;  // the first CTA that has the largest
@@ -1163,13 +1179,14 @@ const Table &table() {
   return t;
 }
 
-// Many rows: a CTA each (three on an SM), which reads it from L2 in every pass after the first.  Few: a cluster
-// each, in whose shared memory it lies, 64 KB to a CTA.
-constexpr long long kSlice = 64 * 1024;
+// Many rows: a CTA each (three on an SM), which reads it from L2 in every pass after the first.  Few: a cluster each, in
+// whose shared memory it lies, up to so many bytes to a CTA.
+constexpr long long kSlice = 192 * 1024;
+static_assert(sizeof(Smem) + kSlice <= 227 * 1024);
 constexpr int kMostTokens = 65000;  // of a slice, see top_p
 
 template <typename T, bool HELD>
-int launch(SampleArgs a, int cs, size_t smem, long long ahead, cudaStream_t s) {
+int launch(SampleArgs a, int cs, size_t smem, cudaStream_t s) {
   static std::atomic<bool> set[64];  // per device
   int dev = 0;
   TR_TRY_CUDA(cudaGetDevice(&dev));
@@ -1178,32 +1195,33 @@ int launch(SampleArgs a, int cs, size_t smem, long long ahead, cudaStream_t s) {
                                      (int)(sizeof(Smem) + kSlice)));
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  return tr_launch_next(sample_kernel<T, HELD>, {dim3((unsigned)(a.rows * cs)), kThreads, smem, cs}, s, a, cs, ahead, table());
+  return tr_launch_next(sample_kernel<T, HELD>, {dim3((unsigned)(a.rows * cs)), HELD ? kHeldThreads : kReadThreads, smem, cs}, s, a, cs, table());
 }
 
 template <typename T>
 int launch(SampleArgs a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
+  bool held = true;
   auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first one: a multiple of 32 for each warp
-    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs;
-    return (mine + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
+    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs, by = held ? kHeldThreads : kReadThreads;
+    return (mine + by - 1) / by * by;
   };
-  const long long slots = 2LL * tr_sm_count();
+  // held: as many CTAs for a row as there are SMs, if a slice then fits (down to 4 KB)
   int cs = 1;
-  while (cs < kMaxCluster && a.rows * cs * 2 <= slots) cs *= 2;
-  bool held = granules(cs) * 16 <= kSlice;
-  if (!held && cs == kMaxCluster / 2 && granules(kMaxCluster) * 16 <= kSlice && a.rows <= slots / 4) held = true, cs = kMaxCluster;
-  while (cs > 1 && held && granules(cs) * 16 <= 4096) cs /= 2;
+  while (cs < kMaxCluster && a.rows * cs * 2 <= tr_sm_count() && granules(cs) * 16 > 4096) cs *= 2;
+  held = a.rows * cs <= tr_sm_count() && granules(cs) * 16 <= kSlice;
+  if (!held) {
+    cs = 1;
+    while (cs < kMaxCluster && a.rows * cs * 2 <= 3LL * tr_sm_count()) cs *= 2;
+  }
   while (cs < kMaxCluster && granules(cs) * VEC > kMostTokens) cs *= 2;
   a.granules = (int)granules(cs);
-  a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / kWarps * VEC));
+  a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / ((held ? kHeldThreads : kReadThreads) / 32) * VEC));
   a.drop = 0;
   while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
   const size_t slice = held ? (size_t)a.granules * 16 : 0;
-  // rows that are in work at a time, about
-  const long long per_sm = std::min<long long>(3, (227 * 1024) / (long long)(sizeof(Smem) + slice + 1024));
-  return held ? launch<T, true>(a, cs, sizeof(Smem) + slice, per_sm * tr_sm_count() / cs, s)
-              : launch<T, false>(a, cs, sizeof(Smem), 0, s);
+  return held ? launch<T, true>(a, cs, sizeof(Smem) + slice, s)
+              : launch<T, false>(a, cs, sizeof(Smem), s);
 }
 
 }  // namespace
