@@ -233,9 +233,9 @@ __device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f
 // rows that a cluster's shared memory holds
 // ---------------------------------------------------------------------------
 
-// Threads of a CTA: of rows in shared memory, where a CTA has an SM about to itself, and of rows that are read from L2.
-constexpr int kHeldThreads = 512, kReadThreads = 256;
-constexpr int kMaxWarps = kHeldThreads / 32;
+// Threads of a CTA: where it has an SM to itself (rows in shared memory), and where it shares one.
+constexpr int kAlone = 512, kShared = 256;
+constexpr int kMaxWarps = kAlone / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;       // 64 to a power of two, where they are weighted
 constexpr int kList = 1024;
@@ -264,10 +264,10 @@ struct alignas(128) Smem {  // the slice lies behind it
 static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, hist) % 16 == 0);
 
 // HELD: the CTA's slice is in shared memory; else it is read from global memory (L2) in every pass.
-template <typename T, bool HELD>
+template <typename T, bool HELD, int NT>
 struct Row {
   static constexpr int VEC = 16 / sizeof(T);
-  static constexpr int NT = HELD ? kHeldThreads : kReadThreads, NW = NT / 32;
+  static constexpr int NW = NT / 32;
   const SampleArgs &a;
   Smem &s;
   const uint4 *data;   // held: the slice's 16-byte granules; what is no token is -inf
@@ -963,14 +963,14 @@ struct Row {
   __device__ __noinline__ Edge narrow_down_p(u64 target, Left old) { return narrow_down(target, old, w); }
 };
 
-template <typename T, bool HELD>
-__global__ void __launch_bounds__(HELD ? kHeldThreads : kReadThreads, HELD ? 1 : 3) sample_kernel(const SampleArgs a, int CS,
+template <typename T, bool HELD, int NT>
+__global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_kernel(const SampleArgs a, int CS,
                                                              const __grid_constant__ Table table) {
   extern __shared__ __align__(128) unsigned char smem[];
   Smem &s = *reinterpret_cast<Smem *>(smem);
-  using R = Row<T, HELD>;
+  using R = Row<T, HELD, NT>;
   R r(a, s);
-  constexpr int VEC = R::VEC, NT = R::NT, NW = R::NW;
+  constexpr int VEC = R::VEC, NW = R::NW;
   const long long row = blockIdx.x / CS;
   r.CS = CS;
   r.rank = blockIdx.x - (int)row * CS;
@@ -1179,49 +1179,50 @@ const Table &table() {
   return t;
 }
 
-// Many rows: a CTA each (three on an SM), which reads it from L2 in every pass after the first.  Few: a cluster each, in
-// whose shared memory it lies, up to so many bytes to a CTA.
-constexpr long long kSlice = 192 * 1024;
-static_assert(sizeof(Smem) + kSlice <= 227 * 1024);
-constexpr int kMostTokens = 65000;  // of a slice, see top_p
+// Slices that a CTA can hold in shared memory, alone on an SM and as one of two; tokens of any slice, see top_p.
+constexpr long long kAloneSlice = 192 * 1024, kSharedSlice = 88 * 1024;
+static_assert(sizeof(Smem) + kAloneSlice <= 227 * 1024 && 2 * (sizeof(Smem) + kSharedSlice + 1024) <= 228 * 1024);
+constexpr int kMostTokens = 65000;
 
-template <typename T, bool HELD>
-int launch(SampleArgs a, int cs, size_t smem, cudaStream_t s) {
+template <typename T, bool HELD, int NT>
+int launch(SampleArgs a, int cs, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
   static std::atomic<bool> set[64];  // per device
   int dev = 0;
   TR_TRY_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)(sizeof(Smem) + kSlice)));
+    TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T, HELD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(sizeof(Smem) + kAloneSlice)));
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  return tr_launch_next(sample_kernel<T, HELD>, {dim3((unsigned)(a.rows * cs)), HELD ? kHeldThreads : kReadThreads, smem, cs}, s, a, cs, table());
+  a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / (NT / 32) * VEC));
+  a.drop = 0;
+  while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
+  return tr_launch_next(sample_kernel<T, HELD, NT>,
+                        {dim3((unsigned)(a.rows * cs)), NT, sizeof(Smem) + (HELD ? (size_t)a.granules * 16 : 0), cs}, s, a, cs,
+                        table());
 }
 
 template <typename T>
 int launch(SampleArgs a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
-  bool held = true;
-  auto granules = [&](int cs) {  // of a slice, wherever the row starts in its first one: a multiple of 32 for each warp
-    const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, mine = (all + cs - 1) / cs, by = held ? kHeldThreads : kReadThreads;
-    return (mine + by - 1) / by * by;
+  const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, sms = tr_sm_count();  // granules, wherever the row starts in the first
+  // The CTAs of a row (a cluster), as many as leave every CTA a place on the SMs and 4 KB, and what a slice then has.
+  auto split = [&](long long places, int threads, int *cs) {
+    *cs = 1;
+    while (*cs < kMaxCluster && a.rows * *cs * 2 <= places && (all + *cs - 1) / *cs * 16 > 4096) *cs *= 2;
+    while (*cs < kMaxCluster && all / *cs * VEC > kMostTokens - 2 * kAlone * VEC) *cs *= 2;
+    return (int)((((all + *cs - 1) / *cs) + threads - 1) / threads * threads);
   };
-  // held: as many CTAs for a row as there are SMs, if a slice then fits (down to 4 KB)
-  int cs = 1;
-  while (cs < kMaxCluster && a.rows * cs * 2 <= tr_sm_count() && granules(cs) * 16 > 4096) cs *= 2;
-  held = a.rows * cs <= tr_sm_count() && granules(cs) * 16 <= kSlice;
-  if (!held) {
-    cs = 1;
-    while (cs < kMaxCluster && a.rows * cs * 2 <= 3LL * tr_sm_count()) cs *= 2;
+  int cs;
+  if (a.rows * kMaxCluster <= sms) {
+    a.granules = split(sms, kAlone, &cs);
+    if (a.granules * 16LL <= kAloneSlice) return launch<T, true, kAlone>(a, cs, s);
   }
-  while (cs < kMaxCluster && granules(cs) * VEC > kMostTokens) cs *= 2;
-  a.granules = (int)granules(cs);
-  a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / ((held ? kHeldThreads : kReadThreads) / 32) * VEC));
-  a.drop = 0;
-  while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
-  const size_t slice = held ? (size_t)a.granules * 16 : 0;
-  return held ? launch<T, true>(a, cs, sizeof(Smem) + slice, s)
-              : launch<T, false>(a, cs, sizeof(Smem), s);
+  a.granules = split(2 * sms, kShared, &cs);
+  if (a.rows * cs <= 2 * sms && a.granules * 16LL <= kSharedSlice) return launch<T, true, kShared>(a, cs, s);
+  a.granules = split(3 * sms, kShared, &cs);
+  return launch<T, false, kShared>(a, cs, s);
 }
 
 }  // namespace
