@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kMaxWarps = 8;
 constexpr int kCtas = 2;    // of rope_kernel on an SM
-constexpr int kStages = 8;  // groups in a warp's ring
+constexpr int kStages = 6;  // groups in a warp's ring
 constexpr int kShort = 2;   // groups of a task in append_rope_kernel
 
 struct RopeArgs {
@@ -553,8 +553,13 @@ int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   const long long rows = (long long)a.B * a.T, most = (long long)kCtas * tr_sm_count();
-  // shares of a token, where there are too few to go round
-  a.parts = (int)std::max<long long>(1, std::min<long long>(a.all_groups, most * 8 / rows));
+  // Shares of a token: as many as give every warp one, where tokens are few.  Where they are many, one, but two of tokens
+  // with 12 groups and more whose halves are paired behind a norm (its work is more than the angles that both halves
+  // then need).  One against two, 32 queries' and 8 keys' heads of 128, dense: 4 x 8192 tokens 146 / 133 us, 16 x 8192
+  // 548 / 518 us; without norms 141 / 147 us, pairs of neighbours 137 / 143 us, 8 x 700 tokens 27.9 / 28.6 us, heads of
+  // 64 (6 groups) 71 / 91 us; into a cache, ragged, 88 / 99 us.
+  const bool two = DST == kDense && !PAIRS && a.norm[0] && a.norm[1] && a.all_groups >= 12 && rows >= 8 * most * 8;
+  a.parts = (int)std::max<long long>(two ? 2 : 1, std::min<long long>(a.all_groups, most * 8 / rows));
   a.per = (a.all_groups + a.parts - 1) / a.parts;
   a.parts = (a.all_groups + a.per - 1) / a.per;
   const long long ctas = (rows * a.parts + 7) / 8;
