@@ -980,6 +980,8 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   r.g1 = r.g0 + a.granules / NW;
   fill_table(s.table, table);
   if (threadIdx.x == 0) s.listed = 0;
+  // a CTA's shared memory may be written from others only once it has started: waited for before the first number is told
+  if (CS > 1) asm volatile("barrier.cluster.arrive;" ::: "memory");
   tr_let_next_start();
   tr_wait_for_previous();
   // the slice, in granules that start on 16-byte boundaries; each lane copies what it reads
@@ -1080,6 +1082,7 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   uint32_t top = 0, low = 0;
   for (int i = 0; i < NW; ++i) top = max(top, (uint32_t)(s.wsum[i] >> 32));
   const uint32_t own_top = top;
+  if (CS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
   r.tell_warps(top);
   int owner = 0;  // the first CTA that has the largest
   for (int i = CS - 1; i >= 0; --i) {
