@@ -528,7 +528,8 @@ int fill(const tr_qkv *x, const tr_rope *r, const int32_t *pos, RopeArgs *out) {
     }
   }
   if ((r->d != 64 && r->d != 128) || r->rot % 16) return TR_E_UNSUPPORTED;
-  if ((long long)x->B * x->T >= (1LL << 31) || all > (1 << 20)) return TR_E_UNSUPPORTED;
+  // (two shares a token, and the warps' steps behind the last one, are counted in 32 bits)
+  if ((long long)x->B * x->T >= (1LL << 30) || all > (1 << 20)) return TR_E_UNSUPPORTED;
   a.B = x->B;
   a.T = x->T;
   a.rot = r->rot;

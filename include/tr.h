@@ -475,7 +475,7 @@ typedef struct tr_qkv {
  *   pos [B] int32 (device); NULL only where rot == 0
  * An output may be its (dense) input itself; no other overlap.  All pointers 16-byte
  * aligned but inv_freq, norms and pos (4).  TR_E_UNSUPPORTED for other d, rot no multiple
- * of 16, B * T past 2^31 - 1 or Hq + 2 Hkv past 2^20. */
+ * of 16, B * T from 2^30 on or Hq + 2 Hkv past 2^20. */
 int tr_qkv_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *pos, const struct tr_tree *tree, void *Qo,
                 void *Ko, void *Vo, tr_stream_t stream);
 

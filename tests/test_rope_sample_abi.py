@@ -47,7 +47,7 @@ BAD_ROWS = [
     (dict(type=2), "INVAL"), (dict(type=7), "INVAL"), (dict(Q=P + 8), "INVAL"), (dict(K=P + 2), "INVAL"),
     (dict(V=P + 4), "INVAL"), (dict(q_stride=(-8, 2048, 128)), "INVAL"), (dict(k_stride=(8192, 2044, 128)), "INVAL"),
     (dict(v_stride=(8192, 2048, 100)), "INVAL"), (dict(q_stride=(1 << 60, 2048, 128)), "INVAL"),
-    (dict(B=1 << 20, T=1 << 12), "UNSUPPORTED"), (dict(Hq=(1 << 20) + 1), "UNSUPPORTED"),
+    (dict(B=1 << 20, T=1 << 12), "UNSUPPORTED"), (dict(B=1 << 15, T=1 << 15), "UNSUPPORTED"), (dict(Hq=(1 << 20) + 1), "UNSUPPORTED"),
     (dict(Hkv=1 << 20), "UNSUPPORTED"),
 ]
 BAD_ROPES = [
