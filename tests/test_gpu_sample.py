@@ -5,8 +5,11 @@ A draw has to be the oracle's token wherever the uniform, and the sum at top-p's
 further from a border than the arithmetic can move it: the weights are off by 2^-29, relative,
 at most (the fraction's power of two: a table rounded to 2^-31, a polynomial whose value is below 2^-7
 in fp32 steps of 2^-31, one rounding to 2^-31; the exponent is good to 2^-33), so a sum's share of
-another by 2^-28, and each is cut to a multiple of 2^-S, V of them by V 2^-S <= V^2 2^-61 of a
-sum that is at least 1.  Rows nearer than that are counted and must be rare.  ln(w / W) is off by 2^-28 + that and
+another by 2^-28.  Weights are whole numbers of a unit of 2^-S, S = 62 - ceil(log2 V) > 61 - log2 V, and the largest
+is 2^(S - t), 0 <= t <= 1.02.  A cut to a whole number takes less than one unit from a token, and one whose weight is
+below 2^-(S - 2) of the largest, so of 2^(2 - t) units at most, counts as none.  The V tokens lose at most
+max(V, V 2^(2 - t)) units of a sum that is at least 2^(S - t): below V 2^(2 - S) < V^2 2^-59 of it (the one-unit
+cuts: V 2^(1.02 - S), less than that).  Rows nearer than that are counted and must be rare.  ln(w / W) is off by 2^-28 + that and
 fp32's half step of it (and of a double's log)."""
 import math
 
@@ -37,7 +40,7 @@ def status_stays_clean(tr):
 
 
 def near(V):
-    return 2.0 ** -28 + V * V * 2.0 ** -61
+    return 2.0 ** -28 + V * V * 2.0 ** -59
 
 
 def draw(tr, x, U, V=None, **rules):
