@@ -74,10 +74,20 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 
 // Turns a position as a fraction of 2^64: a multiplication by the position wraps around
-// with the whole turns, so far positions lose nothing.
+// with the whole turns, so far positions lose nothing.  Of f = man 2^e, man of 24 bits, in whole numbers:
+// off by 1 + f units at most.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  const double t = (double)f * 0.15915494309189535;  // 1 / (2 pi)
-  return __double2ull_rz((t - floor(t)) * 0x1p64);
+  constexpr unsigned long long kInv = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi), rounded down
+  const unsigned bits = __float_as_uint(f), power = bits >> 23 & 255;
+  const int right = 150 - (int)power;  // -e
+  if (right < 0) {                     // 2^24 and more, whose next number is more than a turn away
+    const double t = (double)f * 0.15915494309189535;
+    return __double2ull_rz((t - floor(t)) * 0x1p64);
+  }
+  const unsigned long long man = power ? (bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126: no turn
+  const unsigned long long lo = man * kInv, hi = __umul64hi(man, kInv);
+  const unsigned long long t = right == 0 ? lo : right < 64 ? hi << (64 - right) | lo >> right : right < 128 ? hi >> (right - 64) : 0;
+  return bits >> 31 ? 0 - t : t;
 }
 // cos and sin at position p: the nearest 2^-32 of a turn, as half turns in fp32.
 __device__ __forceinline__ float2 turn(long long p, unsigned long long f) {

@@ -443,7 +443,7 @@ size_t tr_kv_evict_workspace_bytes(const tr_kv_cache *cache, int budget);
  *   z_i = y_i cos(p f_i) - y_j sin(p f_i),  z_j = y_j cos(p f_i) + y_i sin(p f_i)
  * for 0 <= i < rot / 2, with j = i + rot / 2, or with pairs != 0 the elements 2 i and
  * 2 i + 1 in their place; the elements from rot on are those of y.  fp32 throughout
- * (the angle's turns are exact to 2^-54 of p f), rounded once to the output's type.
+ * (the angle's turns are known to p (1 + f) 2^-64), rounded once to the output's type.
  * The sum of a row's squares must stay in fp32's range. */
 typedef struct tr_rope {
   int d;                 /* 64 or 128 */

@@ -4,8 +4,8 @@ dense rows and into a KV cache (GB300 only).
 Tolerance, from the arithmetic: u = 2^-24 is half a step of fp32.  The sum of a row's d
 squares runs as chains of at most d adds and multiplications (each off by u), the square root halves
 that error, rsqrtf adds two steps, two more products follow: a normed element is off by at
-most (d / 2 + 8) u, relative: 72 u < 2^-17 at d = 128.  The angle is known to 2^-53 of its
-turns, rounded to fp32 as half turns (at most 1: off by u, pi u in radians); cos and sin add two steps
+most (d / 2 + 8) u, relative: 72 u < 2^-17 at d = 128.  The angle is known to p (1 + f) 2^-64 turns
+and to 2^-32 of one, rounded to fp32 as half turns (at most 1: off by u, pi u in radians); cos and sin add two steps
 of at most 2u each: under 8 u absolute.  A rotated element is a sum of two products, so it is off by at
 most (2^-17 + 10 u) (|y_i| + |y_j|) < 2^-16 (|y_i| + |y_j|), without a norm 10 u < 2^-20
 of it, and then by half a step of the output's type, relative, or of its smallest step."""
@@ -420,3 +420,66 @@ def test_rope_binding_refuses(tr):
     with pytest.raises(tr.TRError):
         rope(Q=off)                                                      # not 16-byte aligned
     assert p.L.tolist() == [4, 5]
+
+
+def test_rope_norms_of_one_kind_and_unaligned_arrays(tr):
+    """A norm of the queries or the keys alone, weights and frequencies at any 4 bytes, and no rotation without positions."""
+    for type, d, pairs in (("bf16", 128, False), ("f16", 64, True)):
+        for q, k in ((True, False), (False, True), (True, True)):
+            c = Case(tr, type, 3, 21, 8, 2, d, pairs=pairs)
+            off = lambda t: torch.cat([t.new_zeros(1), t]).cuda()[1:]
+            c.wq, c.wk = c.wq if q else None, c.wk if k else None
+            c.rope = tr.Rope(d, off(c.inv), pairs=pairs, q_norm=None if c.wq is None else off(c.wq),
+                             k_norm=None if c.wk is None else off(c.wk), eps=c.eps)
+            c.check_dense(c.run(tr, [0, 7, 4000]), [[p + i for i in range(21)] for p in (0, 7, 4000)])
+            check_append(tr, c, 16, [0, 3, 77], counts=[21, 0, 5])
+        c = Case(tr, type, 2, 5, 4, 4, d, rot=0)
+        out = c.outputs()
+        tr.tr_qkv_rope(c.Q, c.K, c.V, c.rope, None, *out)
+        c.check_dense(out, [[0] * 5] * 2)
+
+
+# 6 tasks a token (12 groups): up to 512 tasks a cluster takes a sequence, and tokens behind them a plan and all SMs.
+@pytest.mark.parametrize("T", [85, 86])
+@pytest.mark.parametrize("type", ["bf16", "f16", "e4m3"])
+def test_append_rope_on_both_sides_of_the_plan(tr, T, type):
+    c = Case(tr, type, 4, T, 32, 8, 128)
+    check_append(tr, c, 16, [0, 5, 130, 64])
+    check_append(tr, c, "dense", [0, 5, 130, 64], counts=[0, T, 1, T - 1], pos=[9, 1 << 20, 0, 3])
+
+
+# Shares of a token: few tokens, some, as many as warps, and many (two shares behind a norm).
+@pytest.mark.parametrize("T", [3, 30, 200, 607, 609, 5000])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 8), (9, 2)])
+def test_rope_shares(tr, T, Hq, Hkv):
+    c = Case(tr, "bf16", 4, T, Hq, Hkv, 128, seed=T)
+    pos = [0, 11, 1 << 16, 5]
+    c.check_dense(c.run(tr, pos), [[p + i for i in range(T)] for p in pos])
+
+
+def test_rope_on_two_streams_at_once(tr):
+    """Calls of both kinds under way at a time, each with its own workspace, give what they give alone."""
+    sizes = [("bf16", 2, 700, 8, 2), ("f16", 8, 3, 32, 8), ("bf16", 1, 1, 32, 32), ("e4m3", 3, 200, 12, 4)]
+    cases = [Case(tr, t, B, T, Hq, Hkv, 128, seed=i) for i, (t, B, T, Hq, Hkv) in enumerate(sizes)]
+    raw = lambda x: x.view(torch.uint8) if x.element_size() == 1 else x.view(torch.int16)
+
+    def run(c, pool, pos, out):
+        tr.tr_kv_append_rope(c.Q, c.K, c.V, c.rope, pool.cache, out[3], pool.ws)
+        tr.tr_qkv_rope(c.Q, c.K, c.V, c.rope, pos, *out[:3])
+    state = lambda c: (Pool(tr, c, 16, [5 * b for b in range(c.B)]),
+                       torch.arange(c.B, dtype=torch.int32, device="cuda"), c.outputs() + c.outputs()[:1])
+    alone = [state(c) for c in cases]
+    for c, s in zip(cases, alone):
+        run(c, *s)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for rep in range(3):
+        both = [state(c) for c in cases]
+        torch.cuda.synchronize()
+        for i, (c, s) in enumerate(zip(cases, both)):
+            with torch.cuda.stream(streams[(i + rep) % len(cases)]):
+                run(c, *s)
+        torch.cuda.synchronize()
+        for (p, _, out), (p2, _, out2) in zip(alone, both):
+            assert torch.equal(p.L, p2.L) and torch.equal(raw(p.K), raw(p2.K)) and torch.equal(raw(p.V), raw(p2.V))
+            assert all(torch.equal(raw(x), raw(y)) for x, y in zip(out, out2))

@@ -297,3 +297,90 @@ def test_binding_refuses(tr):
             tr.tr_sample(x, U, token, V=V)
     empty = torch.zeros(0, 10, device="cuda")
     tr.tr_sample(empty, U[:0], token[:0])
+
+
+# Where a launch changes its shape: a CTA's slice that fills shared memory (192 KB alone, 88 KB shared) in a
+# cluster of eight, and one granule more; rows from which CTAs share an SM, and from which there are more of them.
+@pytest.mark.parametrize("rows,V,dtype", [
+    (1, 8 * 48 * 1024, torch.float32), (1, 8 * 48 * 1024 + 5, torch.float32), (2, 8 * 96 * 1024 + 1, torch.bfloat16),
+    (19, 32003, torch.float32), (20, 32003, torch.float32), (38, 180223, torch.float32), (39, 180223, torch.float32),
+    (30, 180225, torch.float32), (30, 360447, torch.bfloat16), (30, 360451, torch.bfloat16), (76, 45000, torch.float32),
+    (152, 22529, torch.float32), (304, 22528, torch.float32), (305, 22528, torch.float32), (77, 90001, torch.float32)])
+def test_shapes_of_a_launch(tr, rows, V, dtype):
+    rng = np.random.default_rng(rows + V)
+    x = logits(rows, V + 3, 1.5, dtype, rows)
+    r = RULES["all"](rng, rows)
+    check(tr, x, uniforms(rng, rows), V, **r)
+    flat = x.view(-1)[1:1 + (rows - 1) * V].view(rows - 1, V) if rows > 1 else None  # rows that start anywhere
+    if flat is not None:
+        check(tr, flat, uniforms(rng, rows - 1), V, **{k: v[1:] for k, v in r.items()})
+
+
+@pytest.mark.parametrize("rows,V", [(1, 40000), (6, 32000), (200, 32000)])
+def test_more_tokens_at_the_edge_than_a_list_holds(tr, rows, V):
+    """k and p whose edges lie among thousands of equal logits, or of ones that share a histogram's bin."""
+    rng = np.random.default_rng(V + rows)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    steps = torch.randint(0, 4, (rows, V), device="cuda", generator=g).float()            # four values
+    close = 1e-4 * torch.empty(rows, V, device="cuda").normal_(generator=g)                # a narrow range ...
+    close[:, 17] = 60.0                                                                    # ... far below one token
+    for x in (steps, close):
+        for k in (2, 700, 1023, 1024, 1025, 5000, V - 1):
+            check(tr, x, uniforms(rng, rows), top_k=[k] * rows, temperature=[30.0] * rows)
+            check(tr, x, uniforms(rng, rows), top_k=[k] * rows, top_p=[0.6] * rows, temperature=[30.0] * rows)
+        for p in (0.01, 0.5, 0.999):
+            check(tr, x, uniforms(rng, rows), top_p=[p] * rows, temperature=[30.0] * rows)
+
+
+def test_calls_on_two_streams_at_once(tr):
+    """Nothing is shared between calls: eight of each kind under way at a time draw what they draw alone."""
+    rng = np.random.default_rng(12)
+    calls = []
+    for i, (rows, V, dtype) in enumerate([(1, 32000, torch.float32), (40, 50257, torch.float32), (700, 20000, torch.bfloat16),
+                                          (6, 128256, torch.bfloat16)] * 2):
+        x = logits(rows, V, 1.0, dtype, i)
+        r = RULES["all"](rng, rows)
+        cu = {k: torch.tensor(v, dtype=torch.int32 if k == "top_k" else torch.float32, device="cuda") for k, v in r.items()}
+        U = torch.tensor(uniforms(rng, rows), device="cuda")
+        calls.append((x, U, cu, [torch.full((rows,), -7, dtype=torch.int32, device="cuda") for _ in range(2)]))
+    for x, U, r, token in calls:
+        tr.tr_sample(x, U, token[0], **r)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for rep in range(5):
+        for i, (x, U, r, token) in enumerate(calls):
+            with torch.cuda.stream(streams[(i + rep) % 4]):
+                tr.tr_sample(x, U, token[1], **r)
+        torch.cuda.synchronize()
+        for _, _, _, token in calls:
+            assert torch.equal(token[0], token[1])
+            token[1].fill_(-7)
+
+
+def test_draws_one_behind_the_other(tr):
+    """A call's tokens feed the next call's logits without a wait in between, in a graph and without."""
+    n, V = 24, 32000
+    table = logits(512, V, 1.0, torch.float32, 21)
+    U = torch.rand(6, n, device="cuda")
+    p = torch.full((n,), 0.8, device="cuda")
+
+    def run(token, x):
+        for step in range(6):
+            torch.index_select(table, 0, (token % 512).long(), out=x)
+            tr.tr_sample(x, U[step], token, top_p=p)
+    token, x = torch.arange(n, dtype=torch.int32, device="cuda"), torch.empty(n, V, device="cuda")
+    want = token.clone()
+    for step in range(6):
+        y = table[(want % 512).long()]
+        torch.cuda.synchronize()
+        tr.tr_sample(y, U[step], want, top_p=p)
+        torch.cuda.synchronize()
+    run(token, x)
+    assert torch.equal(token, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(token, x)
+    for _ in range(3):
+        token.copy_(torch.arange(n))
+        g.replay()
+        assert torch.equal(token, want)
