@@ -135,10 +135,9 @@ struct Rows {
   static constexpr int LPH = D / 16, HPG = 32 / LPH;  // lanes of a head, heads of a group
   const RopeArgs &a;
   const KvDev &c;
-  float2 *table;      // the warp's, D / 2
+  float2 *table;      // the warp's, D / 2; behind it the frequencies' turns, of each lane its own
   int lane, sub, head, pa, pb;  // lane of its head, head of the group, the lane's pieces
   bool turned;
-  unsigned long long f[D / 64];
   Held k;
   int held;           // the kind that k is of
 
@@ -153,9 +152,11 @@ struct Rows {
     held = -1;
   }
 
+  __device__ __forceinline__ unsigned long long *turns() { return reinterpret_cast<unsigned long long *>(table + D / 2); }
   __device__ __forceinline__ void frequencies() {
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) f[e] = lane + 32 * e < a.rot / 2 ? turns_of(a.inv_freq[lane + 32 * e]) : 0;
+    for (int e = 0; e < D / 64; ++e)
+      if (lane + 32 * e < a.rot / 2) turns()[lane + 32 * e] = turns_of(a.inv_freq[lane + 32 * e]);
   }
 
   // Cosines and sines of the token at position p into the table.
@@ -165,7 +166,7 @@ struct Rows {
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < D / 64; ++e)
-      if (lane + 32 * e < a.rot / 2) table[lane + 32 * e] = turn(p, f[e]);
+      if (lane + 32 * e < a.rot / 2) table[lane + 32 * e] = turn(p, turns()[lane + 32 * e]);
     __syncwarp();
   }
 
@@ -344,8 +345,8 @@ __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, cons
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5;
   using R = Rows<BF, D, PAIRS, DST>;
-  R r(a, c, reinterpret_cast<float2 *>(smem) + warp * (D / 2));
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + 8 * (D / 2) * 8 + warp * (kStages * 1024);
+  R r(a, c, reinterpret_cast<float2 *>(smem) + warp * D);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + 8 * D * 8 + warp * (kStages * 1024);
   // a group's heads lie one behind the other in a stage: copied in order, read by pieces
   const uint32_t copy_at = ring + r.head * (D * 2) + r.sub * 16;
   const uint32_t read_a = ring + r.head * (D * 2) + r.pa * 16, read_b = ring + r.head * (D * 2) + r.pb * 16;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, cons
 template <bool BF, int D, bool PAIRS, int DST>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const RopeArgs a, const KvDev c) {
   constexpr int U = kShort;
-  __shared__ __align__(16) float2 tables[kMaxWarps][D / 2];
+  __shared__ __align__(16) float2 tables[kMaxWarps][D];
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   Rows<BF, D, PAIRS, DST> r(a, c, tables[warp]);
   tr_let_next_start();
@@ -555,7 +556,7 @@ int fill(const tr_qkv *x, const tr_rope *r, const int32_t *pos, RopeArgs *out) {
 
 template <bool BF, int D, bool PAIRS, int DST>
 int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
-  constexpr int kSmem = 8 * (kStages * 1024 + D / 2 * 8);
+  constexpr int kSmem = 8 * (kStages * 1024 + D * 8);
   static std::atomic<bool> set[64];  // per device
   int dev = 0;
   TR_TRY_CUDA(cudaGetDevice(&dev));
