@@ -893,23 +893,32 @@ struct Row {
 
   // top-p among the tokens that `old` leaves; *known: the weights that are left, by warps, are in s.kept (unless min_p
   // takes more).
+  template <bool PLAIN>
   __device__ __forceinline__ Edge top_p(float p, Left old, uint32_t min_p_key, bool *known) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
     // (2^16 of them: the sum of a slice of 65000 tokens stays below 2^32; of longer ones some bits are dropped).  A token beyond the last bin but one has a weight below
     // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
     const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
     const Left weighted = old.above(w.floor);
+    const uint32_t hist = (uint32_t)__cvta_generic_to_shared(s.hist) - 4 * 0x4B400000u;
     clear();
     each<kHeavy>(fmaxf(old.at, m - 32.f / w.c_hi), [&](const float (&x)[4], int v) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float t = fmaf(m - x[e], scale, -0.5f);
-        const int b = __float_as_int(t + 0x1.8p23f) - 0x4B400000;  // the nearest whole number: that below t + 0.5
-        float f;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(fmaf(t, -1.f / 64.f, -0.5f / 64.f)));
-        // in [2^-(o + 1), 2^-o], o = b / 64: 16 bits of it from the float's own
-        const unsigned n = 32768u + ((__float_as_int(f) - ((126 - (b >> 6)) << 23)) >> 8);
-        if (t < (float)(kBins - 1) && old(x[e], v + e)) atomicAdd(&s.hist[b], n >> a.drop);
+      for (int i = 0; i < 4; i += 2) {
+        const F2 y = fma(f2(x[i], x[i + 1]), f2(-1.f, -1.f), f2(m, m));
+        const F2 t2 = fma(y, f2(scale, scale), f2(-0.5f, -0.5f));
+        const float2 t = split(t2), b = split(fma(t2, f2(1.f, 1.f), f2(0x1.8p23f, 0x1.8p23f)));
+        const float2 at = split(fma(t2, f2(-1.f / 64, -1.f / 64), f2(-0.5f / 64, -0.5f / 64)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const unsigned bin = __float_as_uint(e ? b.y : b.x);  // + 0x4B400000: the whole number nearest to t, below t + 0.5
+          float f;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(e ? at.y : at.x));
+          // in [2^-(o + 1), 2^-o], o = bin / 64: 16 bits of it, from 2^15 on, out of the float's own
+          const unsigned n = (__float_as_uint(f) + ((bin & ~63u) << 17) + ((1u << 23) - (126u << 23))) >> (8 + a.drop);
+          if ((e ? t.y : t.x) < (float)(kBins - 1) && (PLAIN || old(x[i + e], v + i + e)))
+            asm volatile("red.shared.add.u32 [%0], %1;" ::"r"(hist + bin * 4), "r"(n) : "memory");
+        }
       }
     });
     int b0, b1;
@@ -920,21 +929,30 @@ struct Row {
     crossing([&](int b, u64 n) { return (n << (a.S - 16 + a.drop)) >> (b >> 6); },
              [&](u64 all) -> u64 { return share_of(p, all - (all >> off)); },
              [&](u64 all) -> u64 { return share_of(p, all + (all >> off) + ((u64)a.V << max(a.S - 31, 0))); }, &b0, &b1, &base, &own);
-    // the exact sums, of all and of what lies above the bins that hold the edge
+    // the exact sums, of all and of what lies above the bins that hold the edge (they end at logits `hi` and `lo`, with 2^-7
+    // of a bin for the roundings)
     u64 rest = 0, above = 0;
-    const float first = (float)b0 - 0.5f, behind = b1 < kBins ? (float)b1 + 0.5f : INFINITY;  // of the bins with the edge
+    const float hi = __fsub_ru(m, ((float)b0 - 0x1p-7f) / scale);
+    const float lo = b1 < kBins ? __fsub_rd(m, ((float)b1 + (1.f + 0x1p-7f)) / scale) : -INFINITY;
     each<kHeavy>(weighted.at, [&](const float (&x)[4], int v) {
       u64 q[4];
-      w.of(x, {weighted(x[0], v), weighted(x[1], v + 1), weighted(x[2], v + 2), weighted(x[3], v + 3)}, q);
-      unsigned in = 0;
+      bool there[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) there[e] = PLAIN ? x[e] > weighted.at : weighted(x[e], v + e);
+      w.of(x, there, q);
+      bool some = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float t = fmaf(m - x[e], scale, -0.5f);
-        if (t < first) above += q[e];
+        if (x[e] > hi) above += q[e];
         else rest += q[e];
-        in |= t >= first && t <= behind && q[e] ? 1u << e : 0;
+        some |= x[e] <= hi && x[e] >= lo;
       }
-      gather(in, x, v);
+      if (some) {
+        unsigned in = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in |= x[e] <= hi && x[e] >= lo && q[e] ? 1u << e : 0;
+        gather(in, x, v);
+      }
     });
     above = warp_sum(above);
     if (lane == 0) s.kept[warp] = above;
@@ -1145,7 +1163,10 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
     edge = r.top_k(k, p, mp, low > kNever ? tr_unord(low) : -INFINITY, &listed);
     known = listed >= 0;
   }
-  if (p < 1.f && listed < 0) edge = r.top_p(p, Left(edge), mp, &known);
+  if (p < 1.f && listed < 0) {
+    if (edge.key <= kNever) edge = r.template top_p<true>(p, Left(edge), mp, &known);
+    else edge = r.template top_p<false>(p, Left(edge), mp, &known);
+  }
   const Left left = Left(with_min_p(edge, mp)).above(r.w.floor);
   const float u = s.u;
   u64 all;
