@@ -785,11 +785,11 @@ struct Row {
 
   // top-k, and the other rules with it where the list takes all tokens at or above the edge: then *left is the number of
   // its entries that are left (else -1).
-  // low: at least k tokens lie at or above it, or -inf.
-  __device__ __forceinline__ Edge top_k(int k, float p, uint32_t min_p_key, float low, int *left) {
+  // low: at least k tokens lie at or above it where it is `sure`, else fewer, a known part of k; or -inf.
+  __device__ __forceinline__ Edge top_k(int k, float p, uint32_t min_p_key, float low, bool sure, int *left) {
     const Edge none = {kNever, -1};
     *left = -1;
-    bool whole = low > -INFINITY;
+    bool whole = sure;
     int need = k;
     Edge edge = none;
     auto found = [&] {  // from the gathered tokens
@@ -819,36 +819,44 @@ struct Row {
       ok = found();
     }
     if (!ok) {
-      float least = low;
-      if (!(low > -INFINITY)) {  // bins over all logits
-        least = INFINITY;
-        each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
-        });
-#pragma unroll
-        for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
-        if (lane == 0) s.wsum[warp] = __float_as_uint(least);
-        __syncthreads();
-        for (int i = 0; i < NW; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
-        tell(__float_as_uint(least));
-        for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
-      }
-      const float m = w.m, span = m - least;
-      if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
-      const float scale = fminf((float)(kBins - 1) / span, FLT_MAX);
-      clear();
-      each<kHeavy>(least, [&](const float (&x)[4], int) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (x[e] >= least) atomicAdd(&s.hist[bin_of(m, x[e], scale)], 1u);
-      });
+      // bins from `low` on; where it is not sure twice as far down, and over all logits if these are too few
+      const float m = w.m;
+      float least = sure ? low : low - (m - low), scale;
       int b0, b1;
       u64 above;
       unsigned at_edge;
-      crossing([](int, u64 n) { return n; }, [&](u64) -> u64 { return (u64)k; }, [&](u64) -> u64 { return (u64)k; }, &b0,
-               &b1, &above, &at_edge);
-      if (b0 >= kBins) return none;         // fewer than k tokens: all are left
+#pragma unroll 1
+      for (bool last = sure;;) {
+        if (!sure && !(least > -INFINITY && least < m)) {
+          last = true;
+          least = INFINITY;
+          each<kHeavy>(-FLT_MAX, [&](const float (&x)[4], int) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) least = x[e] > -INFINITY ? fminf(least, x[e]) : least;
+          });
+#pragma unroll
+          for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+          if (lane == 0) s.wsum[warp] = __float_as_uint(least);
+          __syncthreads();
+          for (int i = 0; i < NW; ++i) least = fminf(least, __uint_as_float((unsigned)s.wsum[i]));
+          tell(__float_as_uint(least));
+          for (int r = 0; r < CS; ++r) least = fminf(least, __uint_as_float((unsigned)heard(r, 0)));
+        }
+        const float span = m - least;
+        if (!(span > 0.f && span < INFINITY)) return narrow_down_k(k);
+        scale = fminf((float)(kBins - 1) / span, FLT_MAX);
+        clear();
+        each<kHeavy>(least, [&](const float (&x)[4], int) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (x[e] >= least) atomicAdd(&s.hist[bin_of(m, x[e], scale)], 1u);
+        });
+        crossing([](int, u64 n) { return n; }, [&](u64) -> u64 { return (u64)k; }, [&](u64) -> u64 { return (u64)k; }, &b0,
+                 &b1, &above, &at_edge);
+        if (b0 < kBins) break;
+        if (last) return none;  // fewer than k tokens: all are left
+        least = -INFINITY;
+      }
       whole = above + at_edge <= kList;  // the list takes them all, else those of the edge's bin
       if (!whole) need = k - (int)above;
       // (a logit of bin b lies at or above m - (b + 1) / scale, but for the roundings: half a bin covers them)
@@ -1078,7 +1086,9 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   }
   const float lane_most = most;
   const int own_shift = r.w.shift;
-  const int j = k > 0 && a.full > 0 ? (int)(((long long)k + a.full - 1) / a.full) : 33;
+  const int full_j = k > 0 && a.full > 0 ? (int)(((long long)k + a.full - 1) / a.full) : INT_MAX;
+  const bool sure = full_j <= 32;  // beyond, up to an eighth of k are known to lie at or above the least of the 32nd
+  const int j = sure ? full_j : full_j <= 8 * 32 ? 32 : 33;
   float bound = -INFINITY;
   if (j <= 32) {
     float v = most;  // the lanes' in falling order
@@ -1111,7 +1121,7 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
     }
   }
   if (j <= 32) {
-    const int rank = (k + j - 1) / j, n = a.full;
+    const int n = a.full, rank = sure ? (k + j - 1) / j : n;
     if ((int)threadIdx.x < n) {
       const uint32_t mine = r.heard_warp(threadIdx.x);
       int above = 0;
@@ -1160,7 +1170,7 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   }
   int listed = -1;
   if (k > 0) {
-    edge = r.top_k(k, p, mp, low > kNever ? tr_unord(low) : -INFINITY, &listed);
+    edge = r.top_k(k, p, mp, low > kNever ? tr_unord(low) : -INFINITY, sure && low > kNever, &listed);
     known = listed >= 0;
   }
   if (p < 1.f && listed < 0) {
