@@ -9,10 +9,15 @@
 // A head's row is held by d / 16 lanes of a warp, 16 elements each in two 16-byte
 // pieces that make whole pairs: pieces c and c + rot / 16 where halves are paired, else 2 c
 // and 2 c + 1.  A lane then turns its own pairs, and one set of eight cosines and sines
-// serves it for all heads of the token.  A task is a token's next U groups of heads (32 / (d / 16)
-// heads a group) of one kind (queries, keys or values), whose loads are all requested before
-// the first is used; a warp takes consecutive tasks, so that a token's angles and a
-// kind's weights are worked out once.
+// serves it for all heads of the token.  The weights of the norm are multiplied into these, the norm's factor comes
+// last: 16 elements take some 60 packed instructions.  A warp's step is a group of 32 / (d / 16) heads of one kind
+// (queries, keys or values), 1 KB.
+//
+// Measured in a graph (rows not in L2; of a copy's rate): 4 x 8192 tokens of 32/8 heads of 128, bf16, norms 135 us (88%),
+// 16 x 8192 520 (91%), without norms 141 (84%), pairs of neighbours 131 (91%), heads of 64 71 (84%), 64/8 heads 122 of
+// 2 x 8192 (81%), 8/2 heads 35 of 4 x 4096 (42%: groups of keys and values a quarter full); 8 x 700 29 (71%); a tree
+// of 80 nodes 4.4, 8 trees of 128 with 32/8 heads 8.7; into pages, 8 prompts up to 4096 long 85 (86%), one token for each
+// of 64 sequences, e4m3, 5.8.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -86,7 +91,9 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   }
   const unsigned long long man = power ? (bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126: no turn
   const unsigned long long lo = man * kInv, hi = __umul64hi(man, kInv);
-  const unsigned long long t = right == 0 ? lo : right < 64 ? hi << (64 - right) | lo >> right : right < 128 ? hi >> (right - 64) : 0;
+  const unsigned long long t = right == 0   ? lo
+                               : right < 64 ? hi << (64 - right) | lo >> right
+                                            : right < 128 ? hi >> (right - 64) : 0;
   return bits >> 31 ? 0 - t : t;
 }
 // cos and sin at position p: the nearest 2^-32 of a turn, as half turns in fp32.
@@ -337,8 +344,9 @@ struct Rows {
 
 // All tokens: an item is a token, or one of a.parts shares of its groups, and a warp takes every
 // gridDim * 8-th item.  Groups come through the warp's ring in shared memory (cp.async), kStages - 1
-// ahead of the one in work and across items, so that the bytes under way need no
-// registers.  With a cache the lengths are what the plan kernel has left in todo.
+// ahead of the one in work and across items, so that the bytes under way need no registers: loads into registers took
+// 4 x 8192 tokens 146 to 150 us when they were tried, 16 stages 160 (the L1 that they take is the stores'), three CTAs on an
+// SM with 80 registers 303 (they spill).  With a cache the lengths are what the plan kernel has left in todo.
 template <bool BF, int D, bool PAIRS, int DST>
 __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, const KvDev c,
                                                           const __grid_constant__ Depths tree) {
@@ -441,8 +449,9 @@ __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, cons
 }
 
 // Few rows: a cluster takes a sequence, checks it, copies its rows and advances its length,
-// so that no kernel is needed before this one.  A task is the next U groups of a token, a warp
-// takes every (gridDim * warps)-th.
+// so that no kernel is needed before this one.  A task is the next U groups of a token, whose loads are requested
+// before the sequence is checked; a warp takes every (gridDim * warps)-th.  Latency bounds it: one token 3 us, of which the
+// launch is most.
 template <bool BF, int D, bool PAIRS, int DST>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const RopeArgs a, const KvDev c) {
   constexpr int U = kShort;
@@ -578,8 +587,10 @@ int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
   return tr_launch_next(rope_kernel<BF, D, PAIRS, DST>, {dim3((unsigned)std::min(ctas, most)), 256, kSmem}, s, a, c, tree);
 }
 
-// One kernel for a sequence's rows up to this many tasks of a warp.
-constexpr int kRounds = 8, kMostCluster = 8;
+// One kernel for a sequence's rows up to this many tasks of a warp, else a plan and rope_kernel.  In a graph, one against
+// two, 32/8 heads of 128: 64 x 1 tokens 4.4 / 5.7 us, 1 x 10 4.9 / 5.4, 24 x 16 8.2 / 7.0, 24 x 33 12.0 / 8.2, 8 x 85
+// 16.7 / 8.1; the second launch takes the host 2.4 us.
+constexpr int kRounds = 2, kMostCluster = 8;
 
 template <bool BF, int D, bool PAIRS, int DST>
 int launch_append(RopeArgs a, const KvDev &c, const int32_t *count, void *ws, cudaStream_t s) {

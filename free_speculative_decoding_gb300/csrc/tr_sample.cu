@@ -6,13 +6,23 @@
 // from sums over any grouping, and equal calls give equal bits.  A token is left when its key
 // (the order of its logit) is above the row's edge, or at it with an ID up to the edge's.
 //
-// A cluster of up to eight CTAs holds a row in shared memory, which is read from DRAM once.
-// An edge is found in two steps.  A histogram over a linear scale of the logits
-// (counts for top-k; for top-p weights of 16 bits, whose error is bounded) gives the bins
-// that the edge must lie in; their tokens, few hundred at most, are gathered in the first
-// CTA, sorted, and the edge read off exact sums.  Where they are more than the list holds
-// (long runs of equal logits) the key is narrowed down by eight bits a pass instead.
-// A last pass sums the weights that are left over ascending IDs and finds the uniform's place.
+// A row is worked on by a cluster of one to eight CTAs.  Few rows lie in its shared memory, copied once; many
+// are read from global memory in every pass (the first from DRAM, the others mostly from L2).
+// The first pass finds the largest logit, and of each warp a logit that a known number of tokens reach.  top-k's
+// candidates are the tokens that reach enough of these, some k to 3 k of them; top-p's are found
+// from a histogram of the weights' first 16 bits over a linear scale of the logits, whose error is
+// bounded, as the tokens of the bins that the edge must lie in, a few hundred at most.  The candidates go to a
+// list, which is merged over the cluster and sorted, and the edge is read off exact sums.  Where they
+// are more than the list holds (long runs of equal logits) the key is narrowed down by eight
+// bits a pass instead.  The draw then goes from the warps' sums to one warp's range, an eighth of it, a batch and a
+// token.  With a temperature alone the weights are summed in the first pass already, relative to the warp's
+// largest logit so far.
+//
+// What bounds it: single rows a chain of latencies (some fifteen passes and barriers, those of a cluster about 1 us each,
+// instructions fetched for the first time); many rows the instructions of their passes.  Measured in a graph,
+// 1280 x 32000 fp32 (the bytes alone take 24 us): greedy 44 us, temperature 86, min_p 90, top-k 50 97, top-p 0.9 185 to
+// 200, top-k 900 248, rows of mixed rules 178.  One row of 32000: 4.2, 8.5, 9.6, 14, 19 and 29 us.  64 x 128256 bf16: 8.5, 24, 25, 20, 43 to 58 and
+// 67 us.
 #include <cfloat>
 #include <cmath>
 #include <cstddef>
@@ -203,7 +213,8 @@ struct Edge {
 struct Left {
   float at;
   int id;
-  __device__ __forceinline__ Left(Edge e) : at(e.key <= kNever ? -INFINITY : tr_unord(e.key)), id(e.key <= kNever ? -1 : e.id) {}
+  __device__ __forceinline__ Left(Edge e)
+      : at(e.key <= kNever ? -INFINITY : tr_unord(e.key)), id(e.key <= kNever ? -1 : e.id) {}
   __device__ __forceinline__ bool operator()(float x, int v) const { return x > at || (x == at && v <= id); }
   // Of these, the ones above `floor`.
   __device__ __forceinline__ Left above(float floor) const {
@@ -233,7 +244,8 @@ __device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f
 // rows that a cluster's shared memory holds
 // ---------------------------------------------------------------------------
 
-// Threads of a CTA: where it has an SM to itself (rows in shared memory), and where it shares one.
+// Threads of a CTA: where it has an SM to itself (rows in shared memory), and where it shares one.  With 256 threads alone
+// one row of 32000 takes 25 us instead of 20 (top-p), with 1024 29; 64 x 128256 in two CTAs of 512 to an SM 56 instead of 54.
 constexpr int kAlone = 512, kShared = 256;
 constexpr int kMaxWarps = kAlone / 32;
 constexpr int kMaxCluster = 8;
@@ -242,9 +254,9 @@ constexpr int kList = 1024;
 
 struct alignas(128) Smem {  // the slice lies behind it
   float2 table[64];
-  u64 box[2][kMaxCluster][2 + kMaxWarps / 2];  // what the cluster's CTAs have told this one, of two exchanges
+  u64 box[2][kMaxCluster][2 + kMaxWarps / 2];  // what the cluster's CTAs have told this one, in this exchange and the last
   u64 wsum[kMaxWarps];
-  u64 kept[kMaxWarps];               // the weights that are left in the warps' ranges, where they are known
+  u64 kept[kMaxWarps];            // the weights that are left in the warps' ranges, where they are known
   unsigned listed;                // tokens that were to go to this CTA's list
   uint32_t listed_low;            // the key that at least k tokens lie at or above
   float u;
@@ -255,9 +267,9 @@ struct alignas(128) Smem {  // the slice lies behind it
   union {
     alignas(16) unsigned hist[kBins];
     u64 wide[256];
-    u64 list[kList];              // key << 32 | ~ID, of all the cluster's CTAs
+    u64 list[kList];              // key << 32 | ~ID of the candidates, all of the cluster's CTAs
   };
-  u64 own[kList];                 // the same, gathered by this one
+  u64 own[kList];                 // the ones in this CTA's slice
   u64 groups[kMaxCluster][64];    // sums of the histograms' groups
 };
 
@@ -359,14 +371,18 @@ struct Row {
       }
     }
   }
-  // Batches under way, of passes that do little or much.  From shared memory one: more copies of a pass's code, each of
-  // which a short row runs through once, cost more in fetching instructions (gathering from 4096 logits a CTA took 9 us with four).
+  // Batches under way, of passes that do little or much (1280 x 32000 fp32: with four and 16 instead of eight in light passes
+  // greedy takes 46 and 58 us instead of 44; with four instead of two in heavy ones min_p 86 instead of 90, but rows of mixed
+  // rules 203 instead of 178, whose code the SM's CTAs fetch by turns).  From shared memory one: more copies of a pass's code, each of which a short row runs through once,
+  // cost more in fetching instructions (gathering from 4096 logits a CTA took 9 us with four).
   static constexpr int kLight = HELD ? 1 : 32 / VEC, kHeavy = HELD ? 1 : 8 / VEC;
   // A granule's largest element.
   static __device__ __forceinline__ float most(const uint4 &v) {
     if constexpr (VEC == 4) {
       float m;
-      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
+      asm("max.f32 %0, %1, %2, %3;"
+          : "=f"(m)
+          : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
       return fmaxf(m, __uint_as_float(v.w));
     } else {
       auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
@@ -904,8 +920,10 @@ struct Row {
   template <bool PLAIN>
   __device__ __forceinline__ Edge top_p(float p, Left old, uint32_t min_p_key, bool *known) {
     // 64 bins to a power of two; a token adds its weight's first 16 bits, in units of its bin's power of two
-    // (2^16 of them: the sum of a slice of 65000 tokens stays below 2^32; of longer ones some bits are dropped).  A token beyond the last bin but one has a weight below
-    // 2^-31.9 and is left out; a bin's sum is below the true one by less than 2^-15 of it (and fp32's errors).
+    // (2^16 of them: the sum of a slice of 65000 tokens stays below 2^32; of longer ones some bits are dropped).  A
+    // token beyond the last bin but one has a weight below 2^-31.9 and is left out; a bin's sum is below the true
+    // one by less than 2^-15 of it (and fp32's errors).  PLAIN: `old` leaves all (1280 x 32000, p = 0.9: its
+    // comparisons cost 12 of 209 us when the histogram was slower).
     const float m = w.m, scale = fminf(w.c_hi * 64.f, FLT_MAX);
     const Left weighted = old.above(w.floor);
     const uint32_t hist = (uint32_t)__cvta_generic_to_shared(s.hist) - 4 * 0x4B400000u;
@@ -936,7 +954,8 @@ struct Row {
     const int off = 14 - a.drop;  // sums are off by less than 2^-off
     crossing([&](int b, u64 n) { return (n << (a.S - 16 + a.drop)) >> (b >> 6); },
              [&](u64 all) -> u64 { return share_of(p, all - (all >> off)); },
-             [&](u64 all) -> u64 { return share_of(p, all + (all >> off) + ((u64)a.V << max(a.S - 31, 0))); }, &b0, &b1, &base, &own);
+             [&](u64 all) -> u64 { return share_of(p, all + (all >> off) + ((u64)a.V << max(a.S - 31, 0))); }, &b0, &b1,
+             &base, &own);
     // the exact sums, of all and of what lies above the bins that hold the edge (they end at logits `hi` and `lo`, with 2^-7
     // of a bin for the roundings)
     u64 rest = 0, above = 0;
@@ -1242,6 +1261,10 @@ int launch(SampleArgs a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
   const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, sms = tr_sm_count();  // granules, wherever the row starts in the first
   // The CTAs of a row (a cluster), as many as leave every CTA a place on the SMs and 4 KB, and what a slice then has.
+  // Rows are held in shared memory where all of them are at once: 64 x 128256 bf16 in four slices each take 43 to 57 us so
+  // (top-p) and 54 to 74 read from L2, 67 and 82 (top-k 900), 8.6 and 7.7 (greedy).  Many rows held by clusters, wave
+  // after wave, lose by it (1280 x 32000, when it was tried: temperature 156 instead of 108 us, top-k 50 185 instead
+  // of 99): fewer CTAs fit on an SM, and the barriers are clusters' instead of CTAs'.
   auto split = [&](long long places, int threads, int *cs) {
     *cs = 1;
     while (*cs < kMaxCluster && a.rows * *cs * 2 <= places && (all + *cs - 1) / *cs * 16 > 4096) *cs *= 2;

@@ -439,8 +439,8 @@ def test_rope_norms_of_one_kind_and_unaligned_arrays(tr):
         c.check_dense(out, [[0] * 5] * 2)
 
 
-# 6 tasks a token (12 groups): up to 512 tasks a cluster takes a sequence, and tokens behind them a plan and all SMs.
-@pytest.mark.parametrize("T", [85, 86])
+# 6 tasks a token (12 groups): up to 128 tasks a cluster takes a sequence, more go by a plan to all SMs.
+@pytest.mark.parametrize("T", [21, 22, 85, 86])
 @pytest.mark.parametrize("type", ["bf16", "f16", "e4m3"])
 def test_append_rope_on_both_sides_of_the_plan(tr, T, type):
     c = Case(tr, type, 4, T, 32, 8, 128)
