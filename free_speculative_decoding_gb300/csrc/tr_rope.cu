@@ -15,7 +15,8 @@
 //
 // Measured in a graph (rows not in L2; of a copy's rate): 4 x 8192 tokens of 32/8 heads of 128, bf16, norms 135 us (88%),
 // 16 x 8192 520 (91%), without norms 141 (84%), pairs of neighbours 131 (91%), heads of 64 71 (84%), 64/8 heads 122 of
-// 2 x 8192 (81%), 8/2 heads 35 of 4 x 4096 (42%: groups of keys and values a quarter full); 8 x 700 29 (71%); a tree
+// 2 x 8192 (81%), 8/2 heads 35 of 4 x 4096 (42%: keys and values are half a group each, and a
+// token's angles and factors serve four groups; 1377 instructions a token, issue slots 58% busy); 8 x 700 29 (71%); a tree
 // of 80 nodes 4.4, 8 trees of 128 with 32/8 heads 8.7; into pages, 8 prompts up to 4096 long 85 (86%), one token for each
 // of 64 sequences, e4m3, 5.8.
 #include <cuda_fp16.h>
