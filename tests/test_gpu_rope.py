@@ -483,3 +483,41 @@ def test_rope_on_two_streams_at_once(tr):
         for (p, _, out), (p2, _, out2) in zip(alone, both):
             assert torch.equal(p.L, p2.L) and torch.equal(raw(p.K), raw(p2.K)) and torch.equal(raw(p.V), raw(p2.V))
             assert all(torch.equal(raw(x), raw(y)) for x, y in zip(out, out2))
+
+
+@pytest.mark.parametrize("T", [1, 5, 60])
+@pytest.mark.parametrize("type", ["bf16", "e4m3"])
+def test_append_rope_into_strided_caches(tr, T, type):
+    """Pages of [position, K or V, head, d] in one tensor, and a slice of a larger dense cache: what lies between the rows
+    stays as it was, and the rows are those of a contiguous cache."""
+    c = Case(tr, type, 3, T, 6, 3, 64)
+    L, page = [4, 0, 33], 16
+    plain = Pool(tr, c, page, L)
+    Qo = c.outputs()[0]
+    tr.tr_kv_append_rope(c.Q, c.K, c.V, c.rope, plain.cache, Qo, plain.ws)
+    raw = lambda x: x.view(torch.uint8) if x.element_size() == 1 else x.view(torch.int16)
+    mark = 0x7F if type == "e4m3" else 0x7FFF
+    n, dt = plain.K.shape[0], plain.K.dtype
+    bits = raw(plain.K).dtype
+    both = torch.full((n, page, 2, 4, 64), mark, dtype=bits, device="cuda")
+    K, V = (both[:, :, i, :3].view(dt).transpose(1, 2) for i in range(2))
+    wide = torch.full((2, 5, 7, 4 * page * 2, 64), mark, dtype=bits, device="cuda")
+    Kd, Vd = (wide[i, 1:4, 2:5].view(dt) for i in range(2))
+    for K, V, pt in ((K, V, plain.pt), (Kd, Vd, None)):
+        L2 = torch.tensor(L, dtype=torch.int32, device="cuda")
+        cache = tr.KVCache(K, V, L2, page_table=pt, scores=torch.ones(3, 3, 200, device="cuda"), k_scale=plain.ks, v_scale=plain.vs)
+        Q2 = torch.full_like(Qo, 7.0)
+        tr.tr_kv_append_rope(c.Q, c.K, c.V, c.rope, cache, Q2, tr.workspace(tr.tr_kv_append_workspace_bytes(cache)))
+        assert torch.equal(Q2, Qo) and torch.equal(L2, plain.L)
+        assert all((cache.scores[b, :, L[b]:L[b] + T] == 0).all() and cache.scores[b].sum() == 3 * (200 - T) for b in range(3))
+        if pt is not None:
+            assert torch.equal(raw(K), raw(plain.K)) and torch.equal(raw(V), raw(plain.V))
+        else:
+            for b in range(3):
+                for own, want in ((K, plain.K), (V, plain.V)):
+                    assert torch.equal(raw(own[b, :, L[b]:L[b] + T].transpose(0, 1).contiguous()),
+                                       raw(plain.rows(want, b, L[b] + T)[L[b]:].contiguous()))
+    assert (both[:, :, :, 3] == mark).all()
+    assert (wide[:, 0] == mark).all() and (wide[:, 4] == mark).all() and (wide[:, :, :2] == mark).all() and (wide[:, :, 5:] == mark).all()
+    for b in range(3):
+        assert (wide[:, 1 + b, :, :L[b]] == mark).all() and (wide[:, 1 + b, :, L[b] + T:] == mark).all()

@@ -5,7 +5,7 @@ A draw has to be the oracle's token wherever the uniform, and the sum at top-p's
 further from a border than the arithmetic can move it: the weights are off by 2^-29, relative,
 at most (the fraction's power of two: a table rounded to 2^-31, a polynomial whose value is below 2^-7
 in fp32 steps of 2^-31, one rounding to 2^-31; the exponent is good to 2^-33), so a sum's share of
-another by 2^-28.  Weights are whole numbers of a unit of 2^-S, S = 62 - ceil(log2 V) > 61 - log2 V, and the largest
+another by 2^-28.  Weights are whole numbers of a unit of 2^-S, S = 62 - floor(log2 V) > 61 - log2 V, and the largest
 is 2^(S - t), 0 <= t <= 1.02.  A cut to a whole number takes less than one unit from a token, and one whose weight is
 below 2^-(S - 2) of the largest, so of 2^(2 - t) units at most, counts as none.  The V tokens lose at most
 max(V, V 2^(2 - t)) units of a sum that is at least 2^(S - t): below V 2^(2 - S) < V^2 2^-59 of it (the one-unit
@@ -384,3 +384,16 @@ def test_draws_one_behind_the_other(tr):
         token.copy_(torch.arange(n))
         g.replay()
         assert torch.equal(token, want)
+
+
+def test_longest_row(tr):
+    """2^30 equal logits, the most that a row may have: every draw is known exactly."""
+    V = 1 << 30
+    x = torch.zeros(1, V, dtype=torch.bfloat16, device="cuda")
+    for u in (0.0, 0.37, 1 - 2.0 ** -24):
+        for left, rules in ((V, {}), (V >> 1, dict(top_p=[0.5])), (12345, dict(top_k=[12345])), (50, dict(top_k=[50])),
+                            (V, dict(min_p=[0.5]))):
+            token, lp = draw(tr, x, [u], **rules)
+            want = int(float(np.float32(u)) * left)  # exact in 64 bits: 24 + 30 bits
+            assert token[0] == want, (u, rules, token[0], want)
+            assert abs(lp[0] + math.log(left)) <= 2.0 ** -23 * math.log(left)   # equal whole weights: fp32's half step of the log
