@@ -34,7 +34,7 @@ namespace {
 constexpr int kMaxWarps = 8;
 constexpr int kCtas = 2;    // of rope_kernel on an SM
 constexpr int kStages = 6;  // groups in a warp's ring
-constexpr int kShort = 2;   // groups of a task in append_rope_kernel
+constexpr int kShort = 2;   // groups of a task in append_rope_kernel, at most
 
 struct RopeArgs {
   const char *x[3];               // queries, keys, values
@@ -48,7 +48,7 @@ struct RopeArgs {
   const int2 *todo;               // cache: (old length, rows) of each sequence, or NULL: found here
   unsigned *status;
   int groups[3], all_groups;      // of heads: of a kind, of a token
-  int parts, per;                 // shares of a token, groups of a share
+  int parts, per;                 // shares of a token, groups of a share (append_rope_kernel: of a task)
 };
 
 // Depths of a tree's nodes; without nodes the positions follow the rows.
@@ -462,19 +462,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const Ro
   tr_let_next_start();
   tr_wait_for_previous();
   const int b = blockIdx.y, Lb = c.L[b], n0 = a.count ? a.count[b] : a.T;
-  const int step = gridDim.x * warps, tasks = (a.all_groups + U - 1) / U;
+  const int step = gridDim.x * warps, tasks = (a.all_groups + a.per - 1) / a.per;
   uint4 x[U][2];
   int i, g;
   auto load = [&](int t) {
     i = t / tasks;
-    g = (t - i * tasks) * U;
+    g = (t - i * tasks) * a.per;
     if (i >= a.T) return;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       int h0;
       const int kind = r.place(g + k, h0);
       x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
-      if (g + k >= a.all_groups || h0 + r.head >= a.heads[kind]) continue;
+      if (k >= a.per || g + k >= a.all_groups || h0 + r.head >= a.heads[kind]) continue;
       const uint4 *src = r.source(kind, b, i, h0 + r.head);
       x[k][0] = src[r.pa];
       x[k][1] = src[r.pb];
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const Ro
     for (int k = 0; k < U; ++k) {
       int h0;
       const int kind = r.place(g + k, h0);
-      if (g + k >= a.all_groups) break;
+      if (k >= a.per || g + k >= a.all_groups) break;
       if (kind < 2) {
         if (angle_of != i) r.angles(base + (angle_of = i));
         r.factors(kind);
@@ -595,7 +595,12 @@ constexpr int kRounds = 2, kMostCluster = 8;
 
 template <bool BF, int D, bool PAIRS, int DST>
 int launch_append(RopeArgs a, const KvDev &c, const int32_t *count, void *ws, cudaStream_t s) {
-  const long long tasks = (long long)a.T * ((a.all_groups + kShort - 1) / kShort);
+  // A task is a group where every warp of a cluster gets one at most and the clusters fill the SMs once, else two: one
+  // token of 32/32 heads 3.3 instead of 3.9 us, 1 x 4 of 32/8 3.8 / 4.6, 64 x 1 e4m3 4.5 to 5.0 / 5.8 (bf16 4.7 / 4.4); with
+  // one always 64 x 4 9.0 instead of 5.8, 24 x 21 10.1 / 8.4.
+  const long long alone = (long long)a.T * a.all_groups;
+  a.per = alone <= kMostCluster * kMaxWarps && a.B * ((alone + kMaxWarps - 1) / kMaxWarps) <= tr_sm_count() ? 1 : kShort;
+  const long long tasks = (long long)a.T * ((a.all_groups + a.per - 1) / a.per);
   if (tasks <= (long long)kMostCluster * kMaxWarps * kRounds) {
     int cs = 1;
     while (cs < kMostCluster && tasks > (long long)cs * kMaxWarps) cs *= 2;
