@@ -22,8 +22,8 @@
 // instructions fetched for the first time); many rows the latencies of their passes (1280 rows of mixed rules: issue slots
 // 36% busy, warps wait for L2, at barriers and for instructions).  Measured in a graph,
 // 1280 x 32000 fp32 (the bytes alone take 24 us): greedy 44 us, temperature 86, min_p 90, top-k 50 97, top-p 0.9 185 to
-// 200, top-k 900 248, rows of mixed rules 178.  One row of 32000: 4.2, 8.5, 9.6, 14, 19 and 29 us.  64 x 128256 bf16: 8.5, 24, 25, 20, 43 to 58 and
-// 67 us.
+// 200, top-k 900 248, rows of mixed rules 178.  One row of 32000: 4.0, 7.8, 8.4, 12, 18 and 32 us.  64 x 128256 bf16:
+// 8.5, 24, 25, 20, 43 to 58 and 67 us.
 #include <cfloat>
 #include <cmath>
 #include <cstddef>
@@ -245,8 +245,8 @@ __device__ __forceinline__ float uniform_of(float u) { return fminf(fmaxf(u, 0.f
 // rows that a cluster's shared memory holds
 // ---------------------------------------------------------------------------
 
-// Threads of a CTA: where it has an SM to itself (rows in shared memory), and where it shares one.  With 256 threads alone
-// one row of 32000 takes 25 us instead of 20 (top-p), with 1024 29; 64 x 128256 in two CTAs of 512 to an SM 56 instead of 54.
+// Threads of a CTA: where it has an SM to itself (long slices in shared memory), and where it shares one.  64 x 128256 in
+// two CTAs of 512 to an SM took 56 us instead of 54.
 constexpr int kAlone = 512, kShared = 256;
 constexpr int kMaxWarps = kAlone / 32;
 constexpr int kMaxCluster = 8;
@@ -372,10 +372,11 @@ struct Row {
       }
     }
   }
-  // Batches under way, of passes that do little or much (1280 x 32000 fp32: with four and 16 instead of eight in light passes
-  // greedy takes 46 and 58 us instead of 44; with four instead of two in heavy ones min_p 86 instead of 90, but rows of mixed
-  // rules 203 instead of 178, whose code the SM's CTAs fetch by turns).  From shared memory one: more copies of a pass's code, each of which a short row runs through once,
-  // cost more in fetching instructions (gathering from 4096 logits a CTA took 9 us with four).
+  // Batches under way, of passes that do little or much (1280 x 32000 fp32: with four and 16 instead of eight in light
+  // passes greedy takes 46 and 58 us instead of 44; with four instead of two in heavy ones min_p 86 instead of 90, but
+  // rows of mixed rules 203 instead of 178, whose code the SM's CTAs fetch by turns).  From shared memory one: more
+  // copies of a pass's code, each of which a short row runs through once, cost more in fetching instructions (gathering
+  // from 4096 logits a CTA took 9 us with four).
   static constexpr int kLight = HELD ? 1 : 32 / VEC, kHeavy = HELD ? 1 : 8 / VEC;
   // A granule's largest element.
   static __device__ __forceinline__ float most(const uint4 &v) {
@@ -1239,48 +1240,99 @@ static_assert(sizeof(Smem) + kAloneSlice <= 227 * 1024 && 2 * (sizeof(Smem) + kS
 constexpr int kMostTokens = 65000;
 
 template <typename T, bool HELD, int NT>
-int launch(SampleArgs a, int cs, cudaStream_t s) {
-  constexpr int VEC = 16 / sizeof(T);
-  static std::atomic<bool> set[64];  // per device
+constexpr size_t most_shared() {
+  return sizeof(Smem) + (HELD ? NT == kAlone ? kAloneSlice : kSharedSlice : 0);
+}
+
+// Clusters of 2^n CTAs that the device runs at once (those of eight do not fill its groups of SMs: 38 rows in clusters of
+// eight are 304 CTAs, two to an SM, and take two waves, 16 us instead of 10 for 33 rows).  Asked once for a device.
+template <typename T, bool HELD, int NT>
+int clusters_at_once(int n, long long *count) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];  // and one more
   int dev = 0;
   TR_TRY_CUDA(cudaGetDevice(&dev));
-  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+  int c = dev < kDevices ? known[dev][n].load(std::memory_order_relaxed) : 0;
+  if (c == 0) {
     TR_TRY_CUDA(cudaFuncSetAttribute(sample_kernel<T, HELD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)(sizeof(Smem) + kAloneSlice)));
-    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+                                     (int)most_shared<T, HELD, NT>()));
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1 << n;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 << n);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = most_shared<T, HELD, NT>();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    TR_TRY_CUDA(cudaOccupancyMaxActiveClusters(&c, sample_kernel<T, HELD, NT>, &cfg));
+    ++c;
+    if (dev < kDevices) known[dev][n].store(c, std::memory_order_relaxed);
   }
+  *count = c - 1;
+  return TR_OK;
+}
+
+// A row's share of the chip: 2^n CTAs, as many as leave all rows' a place at once and each CTA 4 KB.
+struct Shape {
+  int n, granules;
+  bool fits;  // all rows are under way at once
+};
+template <typename T, bool HELD, int NT>
+int shape_of(const SampleArgs &a, Shape *out) {
+  constexpr int VEC = 16 / sizeof(T), kMostN = 3;
+  static_assert(1 << kMostN == kMaxCluster);
+  const long long all = ((long long)a.V + 2 * VEC - 2) / VEC;  // granules, wherever the row starts in the first
+  int n = 0;
+  long long count = 0;
+  while (n < kMostN && (all >> n) * 16 > 4096) {
+    const int rc = clusters_at_once<T, HELD, NT>(n + 1, &count);
+    if (rc != TR_OK) return rc;
+    if (a.rows > count) break;
+    ++n;
+  }
+  while (n < kMostN && (all >> n) * VEC > kMostTokens - 2 * kAlone * VEC) ++n;
+  const int rc = clusters_at_once<T, HELD, NT>(n, &count);
+  if (rc != TR_OK) return rc;
+  const long long one = (all + (1 << n) - 1) >> n;
+  *out = {n, (int)((one + NT - 1) / NT * NT), a.rows <= count};
+  return TR_OK;
+}
+
+template <typename T, bool HELD, int NT>
+int launch(SampleArgs a, const Shape &shape, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
+  const int cs = 1 << shape.n;
+  a.granules = shape.granules;
   a.full = (int)(((long long)a.V - (VEC - 1)) / ((long long)a.granules / (NT / 32) * VEC));
   a.drop = 0;
   while (((long long)a.granules * VEC >> a.drop) > kMostTokens) ++a.drop;
   return tr_launch_next(sample_kernel<T, HELD, NT>,
-                        {dim3((unsigned)(a.rows * cs)), NT, sizeof(Smem) + (HELD ? (size_t)a.granules * 16 : 0), cs}, s, a, cs,
-                        table());
+                        {dim3((unsigned)(a.rows * cs)), NT, sizeof(Smem) + (HELD ? (size_t)a.granules * 16 : 0), cs}, s, a,
+                        cs, table());
 }
 
+// Rows are held in shared memory where all of them are at once: 64 x 128256 bf16 in four slices each take 43 to 57 us so
+// (top-p) and 54 to 74 read from L2, 67 and 82 (top-k 900), 8.6 and 7.7 (greedy).  Many rows held by clusters, wave
+// after wave, lose by it (1280 x 32000, when it was tried: temperature 156 instead of 108 us, top-k 50 185 instead
+// of 99): fewer CTAs fit on an SM, and the barriers are clusters' instead of CTAs'.  CTAs of 512 threads with an SM to
+// themselves pay from 8192 tokens a CTA on: 1 x 128256 bf16 22.0 instead of 23.8 us (top-p), 10.9 / 12.2 (temperature),
+// but 1 x 32000 18.7 / 17.9 and 8.6 / 7.9, 2 x 8000 17.9 / 15.9 and 8.3 / 6.7.
 template <typename T>
-int launch(SampleArgs a, cudaStream_t s) {
+int launch(const SampleArgs &a, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
-  const long long all = ((long long)a.V + 2 * VEC - 2) / VEC, sms = tr_sm_count();  // granules, wherever the row starts in the first
-  // The CTAs of a row (a cluster), as many as leave every CTA a place on the SMs and 4 KB, and what a slice then has.
-  // Rows are held in shared memory where all of them are at once: 64 x 128256 bf16 in four slices each take 43 to 57 us so
-  // (top-p) and 54 to 74 read from L2, 67 and 82 (top-k 900), 8.6 and 7.7 (greedy).  Many rows held by clusters, wave
-  // after wave, lose by it (1280 x 32000, when it was tried: temperature 156 instead of 108 us, top-k 50 185 instead
-  // of 99): fewer CTAs fit on an SM, and the barriers are clusters' instead of CTAs'.
-  auto split = [&](long long places, int threads, int *cs) {
-    *cs = 1;
-    while (*cs < kMaxCluster && a.rows * *cs * 2 <= places && (all + *cs - 1) / *cs * 16 > 4096) *cs *= 2;
-    while (*cs < kMaxCluster && all / *cs * VEC > kMostTokens - 2 * kAlone * VEC) *cs *= 2;
-    return (int)((((all + *cs - 1) / *cs) + threads - 1) / threads * threads);
-  };
-  int cs;
-  if (a.rows * kMaxCluster <= sms) {
-    a.granules = split(sms, kAlone, &cs);
-    if (a.granules * 16LL <= kAloneSlice) return launch<T, true, kAlone>(a, cs, s);
-  }
-  a.granules = split(2 * sms, kShared, &cs);
-  if (a.rows * cs <= 2 * sms && a.granules * 16LL <= kSharedSlice) return launch<T, true, kShared>(a, cs, s);
-  a.granules = split(3 * sms, kShared, &cs);
-  return launch<T, false, kShared>(a, cs, s);
+  Shape alone, shared;
+  int rc = shape_of<T, true, kAlone>(a, &alone);
+  if (rc != TR_OK) return rc;
+  if (alone.fits && alone.granules * VEC > 8192 && alone.n == 3 && alone.granules * 16LL <= kAloneSlice)
+    return launch<T, true, kAlone>(a, alone, s);
+  rc = shape_of<T, true, kShared>(a, &shared);
+  if (rc != TR_OK) return rc;
+  if (shared.fits && shared.granules * 16LL <= kSharedSlice) return launch<T, true, kShared>(a, shared, s);
+  rc = shape_of<T, false, kShared>(a, &shared);
+  if (rc != TR_OK) return rc;
+  return launch<T, false, kShared>(a, shared, s);
 }
 
 }  // namespace
