@@ -452,7 +452,8 @@ struct Row {
 
   // The lowest ID at which the running sum over ascending IDs passes target_of(whole sum), in the one CTA that
   // holds it; -1 in the others.  amounts(x[4], first ID) is the sum of four tokens, none of which lies below `floor`,
-  // amount(x, ID) one's.  known: the sums of the warps' ranges are in s.kept.
+  // amount(x, ID) one's.  known: the sums of the warps' ranges are in s.kept, and those that are not 0 hold a token whose
+  // amount is not.
   template <typename F, typename A, typename G>
   __device__ __forceinline__ int first_past(float floor, F amounts, A amount, G target_of, u64 *all, bool known = false) {
     const int keep0 = g0, keep1 = g1, seg = a.granules / NW;
@@ -467,7 +468,7 @@ struct Row {
       if (round == 0 && known) mine = s.kept[warp];
       __syncthreads();
       if (lane == 0) s.wsum[warp] = mine;
-      if (threadIdx.x == 0) s.id = max(id0, 0);
+      if (threadIdx.x == 0) s.id = -1;
       __syncthreads();
       if (round) break;
       u64 cta = 0, sum = 0;
@@ -489,10 +490,10 @@ struct Row {
       g1 = min(hi, g0 + part);
     }
     if (here) {
-      if (known) {  // sums that were made otherwise may differ in their last places
+      if (known) {  // sums that were made otherwise may differ in their last places (but 0 they are together)
         u64 all_parts = 0;
         for (int i = 0; i < NW; ++i) all_parts += s.wsum[i];
-        target = min(target, before + max(all_parts, 1ull) - 1);
+        target = min(target, before + all_parts - 1);
       }
       for (int i = 0; i < warp; ++i) before += s.wsum[i];
       if (before <= target && before + mine > target) {  // one warp: batch by batch, then a granule
@@ -1186,7 +1187,8 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   const uint32_t mp = min_p_key(s.below, r.w.m);
   if (once) {
     known = !__syncthreads_or(!known || r.w.far);
-    if (known && r.lane == 0) s.kept[r.warp] = sum ? sum >> min(r.w.shift - own_shift, 63) : 0;
+    // tokens that count beside the warp's largest may all lie too low beside the row's: then the range has none to draw
+    if (known && r.lane == 0) s.kept[r.warp] = most > r.w.floor ? sum >> min(r.w.shift - own_shift, 63) : 0;
     __syncwarp();
   }
   int listed = -1;

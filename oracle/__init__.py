@@ -40,7 +40,7 @@ from .tr import (
 )
 from .kv import decode_attention, e4m3_round, evict_keep
 from .rope import rope_rows
-from .sample import sample, sample_left
+from .sample import sample, sample_left, sample_may_draw
 from .loop import TRState, tr_loop, greedy_decode
 
 __all__ = [
@@ -48,5 +48,5 @@ __all__ = [
     "init_matrix", "retrieve", "tree_attention", "topk", "topk_rows", "accept", "update",
     "kv_commit", "lmhead_logits", "mix64_stream", "softmax_stats", "target_probs", "accept_sampled",
     "draw_is_valid", "decode_attention", "e4m3_round", "evict_keep", "rope_rows", "sample",
-    "sample_left", "TRState", "tr_loop", "greedy_decode",
+    "sample_left", "sample_may_draw", "TRState", "tr_loop", "greedy_decode",
 ]

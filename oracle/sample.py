@@ -40,6 +40,46 @@ def sample_left(x, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     return order[at], w[at], margin
 
 
+def sample_may_draw(x, token, u, tol, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """Whether arithmetic whose sums are off by up to ``tol`` of them may draw ``token`` by the uniform
+    u: the token has to be one that the rules leave, top-p's edge lying anywhere within tol of its
+    mark, and u times the sum within tol of its stretch of the running sum over ascending IDs.
+
+    Returns the least and the greatest logarithm of its probability as the edge moves, None where the
+    token may not be drawn.  A row in which nothing is left may only give -1."""
+    token, x = int(token), np.asarray(x, np.float64)
+    ids, w, _ = sample_left(x, temperature, top_k)           # ascending IDs
+    if len(ids) == 0:
+        return (-np.inf, -np.inf) if token == -1 else None
+    k = int(np.searchsorted(ids, token))
+    if k == len(ids) or ids[k] != token or w[k] == 0.0:      # out of range, masked, NaN, behind the k-th, no weight
+        return None
+    u = min(max(u, 0.0), 1.0 - 2.0 ** -24) if u == u else 0.0
+    order, whole = np.lexsort((ids, -x[ids])), math.fsum(w)
+    lo = hi = len(ids)                                       # how many of `order` top-p leaves
+    if top_p < 1.0:
+        p, mass = max(top_p, 0.0), np.cumsum(w[order])
+        lo, hi = (min(max(int(np.searchsorted(mass, mark * whole, side="left")) + 1, 1), len(ids))
+                  for mark in (p - tol, p + tol if p else 0.0))
+    stay = np.ones(len(ids), bool)
+    if min_p > 0.0 and temperature < np.inf and len(ids) > 1:
+        with np.errstate(invalid="ignore"):
+            stay = (x[ids] == x[ids].max()) | (x[ids] - x[ids].max() >= temperature * math.log(min(min_p, 1.0)))
+    rank = np.empty(len(ids), int)
+    rank[order] = np.arange(len(ids))
+    found = []
+    # the sums that edges from lo to hi - 1 leave differ by less than 2 tol of the whole: lo stands for them
+    for n, reach, slack in ((lo, max(lo, hi - 1), 2 * tol * whole if hi > lo else 0.0), (hi, hi, 0.0)):
+        left = stay & (rank < n)
+        sum_ = math.fsum(w[left])
+        before = math.fsum(w[:k][left[:k]])
+        after = before + (w[k] if left[k] else 0.0)
+        slack += tol * sum_
+        if stay[k] and rank[k] < reach and before - slack <= u * sum_ <= after + slack:
+            found.append(math.log(w[k] / sum_))
+    return (min(found), max(found)) if found else None
+
+
 def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """The token drawn by the uniform u, the logarithm of its probability among those left,
     and the distance of the nearest border (of the draw or of top-p's edge)."""

@@ -1,0 +1,120 @@
+"""Draws next to borders on the GPU (GB300 only): whatever the uniform, the token is one that the rules
+leave, and its stretch of the running sum is where the uniform points, within what the sums may be off.
+
+That is tol = 2^-28 + V^2 2^-59 of a sum, as tests/test_gpu_sample.py derives it for whole weights: every weight is off
+by 2^-29, relative, and V of them, each cut to a whole number of units or, below four units, left out, by V 2^(2 - S) of the
+largest.  Rows with a temperature alone that are read from global memory are summed in the first pass, in
+units of the warp's largest logit so far.  A token then loses one unit to its cut, two at most go with every lane's
+rescaled sum (each rescale that shifts by a bit or more loses less than one unit, and every later one
+halves that) and one with the warp's; a lane has four tokens and more, a warp 128, so that a token loses less than 1.6 units
+of a sum of at least 2^(S - 1.02): below V 2^(2 - S) again, and one that ends below four units is in a sum with as many or with none."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tr():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from free_speculative_decoding_gb300 import build as b
+    b.build()
+    import free_speculative_decoding_gb300 as m
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status_stays_clean(tr):
+    yield
+    assert tr.tr_get_status() == 0
+
+
+def near(V):
+    return 2.0 ** -28 + V * V * 2.0 ** -59
+
+
+def draw(tr, x, U, V=None, **rules):
+    cu = lambda v, t: None if v is None else torch.as_tensor(v, dtype=t).cuda()
+    token = torch.full((x.shape[0],), -7, dtype=torch.int32, device="cuda")
+    lp = torch.full((x.shape[0],), 7.0, device="cuda")
+    types = dict(top_k=torch.int32)
+    tr.tr_sample(x, cu(U, torch.float32), token, logprob=lp, V=V,
+                 **{k: cu(v, types.get(k, torch.float32)) for k, v in rules.items()})
+    return token.cpu().numpy(), lp.cpu().numpy()
+
+
+def check(tr, x, U, V=None, logprobs=False, rows=None, **rules):
+    """Every drawn token (of `rows`) is one that may be drawn."""
+    n = x.shape[1] if V is None else V
+    token, lp = draw(tr, x, U, V, **rules)
+    host = x[:, :n].float().cpu().numpy().astype(np.float64)
+    off = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
+    for r in range(x.shape[0]) if rows is None else rows:
+        kw = {k: float(np.float32(rules[k][r])) if k in rules else o for k, o in off.items()}
+        kw["top_k"] = int(kw["top_k"]) if "top_k" not in rules else int(rules["top_k"][r])
+        got = oracle.sample_may_draw(host[r], token[r], float(np.float32(U[r])), near(n), **kw)
+        assert got is not None, (r, kw, U[r], token[r], oracle.sample(host[r], float(np.float32(U[r])), **kw))
+        assert token[r] == -1 or host[r, token[r]] > -np.inf
+    return token, lp
+
+
+# Rows that are read from global memory (more of them than the chip holds at once, or longer ones), and held ones.
+@pytest.mark.parametrize("rows,V,dtype", [(200, 32000, torch.float32), (1, 32000, torch.float32), (400, 3001, torch.float32),
+                                          (160, 100003, torch.bfloat16), (2, 1000000, torch.float32)])
+def test_a_masked_token_is_not_drawn_where_the_first_weights_are_tiny(tr, rows, V, dtype):
+    """The first token is masked, and its range holds weights around the least that count: relative to that range's own
+    largest logit they are all large."""
+    S = 62 - int(math.log2(V))
+    x = torch.full((rows, V), -math.inf, device="cuda")
+    far = -(S - 2) * math.log(2.0)
+    levels = torch.linspace(-1.5, 1.5, rows, device="cuda") if rows > 1 else torch.full((1,), -0.3, device="cuda")
+    n = min(4096, V // 2)
+    x[:, 1:n] = (far + levels).unsqueeze(1)
+    x[:, 20000 % V] = 0.0
+    x = x.to(dtype)
+    for u in (0.0, 2.0 ** -149, -1.0, math.nan):
+        token, _ = check(tr, x, [u] * rows, rows=range(0, rows, 7))
+        assert (token > 0).all()
+        assert (x[torch.arange(rows), torch.from_numpy(token).long().cuda()] > -math.inf).all()
+
+
+def steps(kind, rows, V, rng):
+    """Logits in units of T."""
+    i = np.arange(V) / V
+    if kind == "rising":
+        x = np.stack([s * (i - 1) for s in rng.choice([0.5, 5.0, 50.0, 2000.0], rows)]) + 0.1 * rng.random((rows, V))
+    elif kind == "falling":
+        x = np.stack([-s * i for s in rng.choice([0.5, 5.0, 50.0, 2000.0], rows)]) + 0.1 * rng.random((rows, V))
+    elif kind == "jumps":   # of more than 63 powers of two, and of less
+        at = np.sort(rng.integers(0, V, (rows, 6)), axis=1)
+        x = sum((np.arange(V)[None] >= at[:, k:k + 1]) * rng.choice([0.0, 3.0, 30.0, 60.0, 200.0], (rows, 1)) for k in range(6))
+        x = x + rng.random((rows, V))
+    elif kind == "tails":   # all around the least weight that counts but a few tokens
+        x = -(60 - int(math.log2(V))) * math.log(2.0) + rng.normal(size=(rows, V))
+        x[np.arange(rows)[:, None], rng.integers(0, V, (rows, 3))] = 0.0
+    else:                   # masked
+        x = 4.0 * rng.normal(size=(rows, V))
+        x[rng.random((rows, V)) < 0.7] = -np.inf
+        x[:, 3::11] = np.nan
+    return x
+
+
+@pytest.mark.parametrize("kind", ["rising", "falling", "jumps", "tails", "masked"])
+@pytest.mark.parametrize("rows,V,dtype", [(170, 32000, torch.float32), (400, 3001, torch.float32), (310, 5003, torch.bfloat16),
+                                          (4, 500003, torch.float32)])
+def test_temperature_alone(tr, kind, rows, V, dtype):
+    """Sums that are rescaled as the largest logit rises: T from 0.2 to 2 over many rows, and the same rows a few at a time."""
+    rng = np.random.default_rng(V + rows)
+    T = np.float32(0.2 + 1.8 * rng.random(rows))
+    x = torch.from_numpy(steps(kind, rows, V, rng) * T[:, None]).to(dtype).cuda()
+    U = np.float32(rng.random(rows))
+    U[::5], U[1::5], U[2::10] = 0.0, np.float32(1 - 2.0 ** -24), np.float32(2.0 ** -149)
+    some = range(rows) if V < 10000 else range(0, rows, 4)
+    check(tr, x, U.tolist(), rows=some, temperature=T.tolist())
+    check(tr, x[:3].contiguous(), U[:3].tolist(), temperature=T[:3].tolist())
