@@ -629,7 +629,7 @@ def tr_kv_append_rope(Q, Kn, Vn, rope, cache, Qo, ws, pos=None, count=None):
     """tr_kv_append of Kn, Vn [B, T, Hkv, d] with the keys normed and rotated on the way,
     and Q [B, T, Hq, d] into the dense Qo (both may be None).  The inputs may be
     strided views.  Row i of sequence b stands at position pos[b] + i, without ``pos`` at
-    its place in the cache, L[b] + i."""
+    its place in the cache, L[b] + i.  ``pos`` and ``count`` may be the cache's L."""
     stream, index = cache._stream(), cache._index
     if Kn is None or Vn is None:
         raise ValueError("Kn and Vn are needed")

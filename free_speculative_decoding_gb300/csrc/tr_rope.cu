@@ -614,6 +614,13 @@ int launch_append(RopeArgs a, const KvDev &c, const int32_t *count, void *ws, cu
   return rc != TR_OK ? rc : launch<BF, D, PAIRS, DST>(a, c, Depths{}, s);
 }
 
+// Whether numbers of the sequences overlap the cache's lengths without being these: a sequence's could then be read
+// after another one's length was advanced.
+bool part_of_lengths(const int32_t *x, const tr_kv_cache &c) {
+  const uintptr_t a = (uintptr_t)x, l = (uintptr_t)c.L, bytes = (uintptr_t)c.B * sizeof(int32_t);
+  return x && a != l && (a < l ? l - a : a - l) < bytes;
+}
+
 // f(BF, D, PAIRS) as compile-time constants.
 template <typename F>
 int with(bool bf, int d, bool pairs, F f) {
@@ -666,6 +673,9 @@ extern "C" int tr_kv_append_rope(const tr_qkv *rows, const tr_rope *rope, const 
   if (rows->B != cache->B || rows->Hkv != cache->Hkv || rope->d != cache->d) return TR_E_INVAL;
   if (rows->type != (cache->type == TR_KV_F16 ? TR_KV_F16 : TR_KV_BF16)) return TR_E_INVAL;
   if (!ws || ((uintptr_t)ws & 15) || ws_bytes < tr_kv_append_workspace_bytes(cache)) return TR_E_INVAL;
+  if (part_of_lengths(pos, *cache) || part_of_lengths(count, *cache)) return TR_E_INVAL;
+  // the lengths before the call, which the plan kernel has advanced before rope_kernel would read them
+  if (pos == cache->L) a.pos = nullptr;
   rc = tr_check_device();
   if (rc != TR_OK) return rc;
   a.out[0] = (char *)Qo;

@@ -484,13 +484,15 @@ int tr_qkv_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *pos, con
  * pos[b] + i (pos NULL: L[b] + i, its place in the cache);
  *   K[b, h, L[b] + i] = the key normed and rotated, V[b, h, L[b] + i] = the value,
  *   Qo[b, i] = the query normed and rotated (Q and Qo NULL: no queries),
- * then L[b] += n (pos is left as it is).  The cache takes each number in one rounding from
+ * then L[b] += n (a pos of its own is left as it is).  The cache takes each number in one rounding from
  * fp32 (an e4m3 cache: e4m3(x / k_scale[h]) as tr_kv_append); scores, if present, are set to
  * 0 at the new rows.  Qo [B, T, Hq, d] dense, may be Q itself; its rows from n on are left as
  * they are.  Sequences that tr_kv_append would leave untouched are, in Qo too, and
  * set the same status bits.
  * rows->type is the type of the cache's new rows (TR_KV_F16 for an fp16 cache, else
  * TR_KV_BF16), rows->B, Hkv and rope->d are the cache's.
+ * pos and count may be the cache's L itself, its values before the call; neither may overlap it in part
+ * (TR_E_INVAL).
  * ws: tr_kv_append_workspace_bytes bytes, 16-byte aligned; its contents do not matter and
  * nothing is kept in it between calls. */
 int tr_kv_append_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *pos, const int32_t *count,
