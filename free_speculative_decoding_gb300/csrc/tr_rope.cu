@@ -81,23 +81,28 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 
 // Turns a position as a fraction of 2^64: a multiplication by the position wraps around
 // with the whole turns, so far positions lose nothing.  Of f = man 2^e, man of 24 bits, in whole numbers:
-// off by 1 + f units at most.
+// off by 1 + f units at most, from 2^24 on (whose next number is more than a turn away) by two: there
+// 1 / (2 pi) is taken from its e-th bit on, what is above being whole turns (Payne and Hanek 1983).
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  constexpr unsigned long long kInv = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi), rounded down
+  typedef unsigned long long u64;
+  constexpr u64 kInv = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi), rounded down, and its next 128 bits
+  constexpr u64 kInv1 = 0x7F09D5F47D4D3770ull, kInv2 = 0x36D8A5664F10E410ull;
   const unsigned bits = __float_as_uint(f), power = bits >> 23 & 255;
-  const int right = 150 - (int)power;  // -e
-  if (right < 0) {                     // 2^24 and more, whose next number is more than a turn away
-    const double t = (double)f * 0.15915494309189535;
-    return __double2ull_rz((t - floor(t)) * 0x1p64);
+  const int right = 150 - (int)power;                         // -e
+  const u64 man = power ? (bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126: no turn
+  u64 t;
+  if (right < 0) {
+    const int e = -right, by = e & 63;  // e is 104 at most
+    const u64 a = e < 64 ? kInv : kInv1, b = e < 64 ? kInv1 : kInv2, c = e < 64 ? kInv2 : 0;
+    const u64 hi = by ? a << by | b >> (64 - by) : a, lo = by ? b << by | c >> (64 - by) : b;
+    t = man * hi + __umul64hi(man, lo);
+  } else {
+    const u64 lo = man * kInv, hi = __umul64hi(man, kInv);
+    t = right == 0 ? lo : right < 64 ? hi << (64 - right) | lo >> right : right < 128 ? hi >> (right - 64) : 0;
   }
-  const unsigned long long man = power ? (bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126: no turn
-  const unsigned long long lo = man * kInv, hi = __umul64hi(man, kInv);
-  const unsigned long long t = right == 0   ? lo
-                               : right < 64 ? hi << (64 - right) | lo >> right
-                                            : right < 128 ? hi >> (right - 64) : 0;
   return bits >> 31 ? 0 - t : t;
 }
-// cos and sin at position p: the nearest 2^-32 of a turn, as half turns in fp32.
+// cos and sin at position p: its phase rounded down to 2^-32 of a turn, as half turns in fp32.
 __device__ __forceinline__ float2 turn(long long p, unsigned long long f) {
   const int phase = (int)(((unsigned long long)p * f) >> 32);
   float2 r;

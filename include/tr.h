@@ -443,13 +443,13 @@ size_t tr_kv_evict_workspace_bytes(const tr_kv_cache *cache, int budget);
  *   z_i = y_i cos(p f_i) - y_j sin(p f_i),  z_j = y_j cos(p f_i) + y_i sin(p f_i)
  * for 0 <= i < rot / 2, with j = i + rot / 2, or with pairs != 0 the elements 2 i and
  * 2 i + 1 in their place; the elements from rot on are those of y.  fp32 throughout
- * (the angle's turns are known to p (1 + f) 2^-64), rounded once to the output's type.
+ * (the angle's turns are known to 2^-32 + p (1 + f) 2^-64), rounded once to the output's type.
  * The sum of a row's squares must stay in fp32's range. */
 typedef struct tr_rope {
   int d;                 /* 64 or 128 */
   int rot;               /* elements that are rotated: a multiple of 16, 0 (none) .. d */
   int pairs;             /* which elements make a pair: 0 halves of the rotated part, else neighbours */
-  const float *inv_freq; /* [rot / 2] (device) f, in radians a position; ignored where rot == 0 */
+  const float *inv_freq; /* [rot / 2] (device) f, in radians a position, finite; ignored where rot == 0 */
   const float *q_norm;   /* [d] (device), or NULL: queries have no norm */
   const float *k_norm;
   float eps;             /* >= 0 and finite */
