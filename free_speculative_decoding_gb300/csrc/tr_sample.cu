@@ -125,6 +125,13 @@ struct Weight {
     e = fmaf(r, e, kL1);
     return whole(p, e * r);
   }
+  // ln(weight of x / all).  The whole number of a small weight has lost too much: its power of two itself then.
+  __device__ __forceinline__ double log_share(float x, u64 all) const {
+    const u64 n = (*this)(x);
+    const bool small = n < 1u << 30 && !infinite;
+    const double power = ((double)x - (double)base) * ((double)c_hi + (double)c_lo) + ((0x48400000 >> 6) + 63 - shift);
+    return log((small ? 1.0 : (double)n) / (double)all) + (small ? power * 0.6931471805599453 : 0.0);
+  }
   // The weights of N logits, the same arithmetic, two to an instruction; 0 for those whose bit of `there` is not set: of
   // all that lie up to `floor` or are NaN.
   template <int N>
@@ -1218,7 +1225,7 @@ __global__ void __launch_bounds__(NT, NT == kAlone ? 1 : HELD ? 2 : 3) sample_ke
   if (id >= 0 && threadIdx.x == 0) {
     a.token[row] = id;
     const float y = get(x, id);
-    if (a.logprob) a.logprob[row] = (float)log((double)r.w(y) / (double)all);
+    if (a.logprob) a.logprob[row] = (float)r.w.log_share(y, all);
   }
 }
 

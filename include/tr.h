@@ -525,8 +525,9 @@ int tr_kv_append_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *po
  *   token [rows] int32 out; logprob [rows] fp32 out, may be NULL
  * Weights are good to about 2^-29 (relative) and summed exactly as integers in units of less than
  * V / 2^61 of the largest (up to four units count as none), so a draw or an edge of the rules
- * differs from exact arithmetic only within about 4e-9 + V^2 / 2^59 of a border.  No workspace; equal calls give equal bits.  rows == 0 does nothing; TR_E_UNSUPPORTED for
- * rows past 2^24 or V past 2^30. */
+ * differs from exact arithmetic only within about 4e-9 + V^2 / 2^59 of a border, and logprob, whatever the token's
+ * weight, by twice that and fp32's rounding.  No workspace; equal calls give equal bits.
+ * rows == 0 does nothing; TR_E_UNSUPPORTED for rows past 2^24 or V past 2^30. */
 int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64_t V, int64_t ld, const float *temperature,
               const int32_t *top_k, const float *top_p, const float *min_p, const float *U, int32_t *token,
               float *logprob, tr_stream_t stream);

@@ -61,6 +61,9 @@ def check(tr, x, U, V=None, logprobs=False, rows=None, **rules):
         got = oracle.sample_may_draw(host[r], token[r], float(np.float32(U[r])), near(n), **kw)
         assert got is not None, (r, kw, U[r], token[r], oracle.sample(host[r], float(np.float32(U[r])), **kw))
         assert token[r] == -1 or host[r, token[r]] > -np.inf
+        if logprobs and token[r] >= 0:  # off by a weight's and the sum's error, and fp32's half step of it
+            e = 2 * near(n) + 2.0 ** -23 * max(abs(got[0]), abs(got[1])) + 2.0 ** -149
+            assert got[0] - e <= lp[r] <= got[1] + e, (r, kw, U[r], token[r], lp[r], got)
     return token, lp
 
 
@@ -118,3 +121,24 @@ def test_temperature_alone(tr, kind, rows, V, dtype):
     some = range(rows) if V < 10000 else range(0, rows, 4)
     check(tr, x, U.tolist(), rows=some, temperature=T.tolist())
     check(tr, x[:3].contiguous(), U[:3].tolist(), temperature=T[:3].tolist())
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(9, 3000, torch.float32), (400, 3001, torch.float32), (170, 32000, torch.bfloat16)])
+@pytest.mark.parametrize("rules", [dict(), dict(top_k=2000), dict(top_p=1 - 2.0 ** -24), dict(min_p=1e-30)])
+def test_log_probabilities_of_tiny_weights(tr, rows, V, dtype, rules):
+    """U = 0 draws the first token that has weight, down to four units of 2^-S: its logarithm keeps fp32's precision although
+    the whole number of units does not."""
+    rng = np.random.default_rng(rows)
+    S = 62 - int(math.log2(V))
+    T = np.float32(0.3 + rng.random(rows))
+    level = np.linspace(0.0, (S - 3.2) * math.log(2.0), rows)
+    x = np.full((rows, V), -np.inf)
+    x[:, 3] = -level
+    x[:, 50:1000] = -0.5 * rng.random((rows, 950))
+    x[:, 1700] = 0.0
+    x = (x * T[:, None] + rng.choice([0.0, -300.0, 2.0 ** 21], (rows, 1)) * (dtype is torch.float32))
+    x = torch.from_numpy(np.float32(x)).to(dtype).cuda()
+    x[rows // 2, 3:] = x[rows // 2, 3].clone()     # equal ones
+    token, _ = check(tr, x, [0.0] * rows, logprobs=True, temperature=T.tolist(), **{k: [v] * rows for k, v in rules.items()})
+    if not rules:
+        assert (token == 3).mean() > 0.9
