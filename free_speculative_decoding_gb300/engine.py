@@ -173,7 +173,9 @@ class TRState:
         """The end of a step without a draft, from the roots' logits [B, V]: the root's
         row of M becomes its top-K, its first token the next root (committed1).  With the
         uniforms U [B] the next root is drawn by tr_sample instead, with every
-        sequence's own rules [B]."""
+        sequence's own rules [B] (refused without U)."""
+        if U is None and not (temperature is None and top_k is None and top_p is None and min_p is None):
+            raise ValueError("temperature, top_k, top_p and min_p need the uniforms U")
         tr_topk(logits, self.K, self.ids1, None, self.ws_topk1, V=self.V)
         tok = self.root.unsqueeze(1)
         tr_update(self.M, self.tree1, tok, self.ids1)

@@ -28,3 +28,12 @@ def test_positions_and_counts_that_overlap_the_lengths_in_part(tr):
         return tr.lib().tr_kv_append_rope(ctypes.byref(x), ctypes.byref(r), pos, count, ctypes.byref(c), P, P, 1 << 40, None)
     for off in (4, 8, 12, -4, -8, -12):
         assert call(L + off, None) == call(None, L + off) == call(L, L + off) == tr.TR_E_INVAL, off
+
+
+@pytest.mark.parametrize("rule", ["temperature", "top_k", "top_p", "min_p"])
+def test_rules_without_uniforms(tr, rule):
+    """A step that would be greedy all the same; nothing of the state is touched before the refusal."""
+    from free_speculative_decoding_gb300.engine import TRState
+    state = object.__new__(TRState)
+    with pytest.raises(ValueError, match="uniforms"):
+        state.finish_decode(None, **{rule: [1]})
