@@ -15,6 +15,7 @@ import pytest
 import torch
 
 import oracle
+from test_gpu_sample import RULES, logits
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +143,38 @@ def test_log_probabilities_of_tiny_weights(tr, rows, V, dtype, rules):
     token, _ = check(tr, x, [0.0] * rows, logprobs=True, temperature=T.tolist(), **{k: [v] * rows for k, v in rules.items()})
     if not rules:
         assert (token == 3).mean() > 0.9
+
+
+# What tests/test_gpu_sample.py compares away from borders, next to them: there it asks only that a border is near.
+ENDS = [0.0, 1 - 2.0 ** -24, 1.0, -0.5, math.nan, 2.0 ** -149, 2.0 ** -30, 1e-9, 0.5]
+
+
+@pytest.mark.parametrize("rule", list(RULES))
+@pytest.mark.parametrize("rows,V,dtype,spread", [
+    (54, 33, torch.float32, 1.0), (54, 512, torch.bfloat16, 6.0), (54, 4099, torch.float32, 6.0), (9, 32000, torch.float32, 4.0),
+    (400, 601, torch.float32, 8.0), (180, 32003, torch.float32, 4.0), (45, 128256, torch.bfloat16, 4.0),
+    (3, 1000000, torch.float32, 4.0)])
+def test_uniforms_at_their_ends(tr, rule, rows, V, dtype, spread):
+    rng = np.random.default_rng(V)
+    x = logits(rows, V, spread, dtype, V)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x[torch.rand(rows, V, device="cuda", generator=g) < 0.3] = -math.inf
+    x[:, 2::9] = math.nan
+    x[:, :2] = -math.inf
+    U = [ENDS[i % 9] for i in rng.permutation(rows)]
+    some = range(rows) if rows * V < 10 ** 6 else range(0, rows, max(1, rows * V // 10 ** 6))
+    check(tr, x, U, logprobs=True, rows=some, **RULES[rule](rng, rows))
+
+
+@pytest.mark.parametrize("rows,V", [(40, 700), (320, 5001), (6, 40001)])
+def test_edges_among_equal_logits(tr, rows, V):
+    """top-p's mark on a sum of equal weights: the edge may lie on either side of it, no further."""
+    rng = np.random.default_rng(V)
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randint(-2, 3, (rows, V), generator=g) / 2).cuda()
+    x[::7, V // 3] = 9.0
+    left = [oracle.sample_left(r)[1] for r in x.double().cpu().numpy()]
+    p = [float(np.cumsum(np.sort(w)[::-1])[rng.integers(0, V)] / w.sum()) for w in left]
+    check(tr, x, rng.random(rows).tolist(), logprobs=True, top_p=p)
+    check(tr, x, [1 - 2.0 ** -24] * rows, logprobs=True, top_p=p)
+    check(tr, x, rng.random(rows).tolist(), logprobs=True, top_p=p, top_k=rng.integers(1, V, rows).tolist())
