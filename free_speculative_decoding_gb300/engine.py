@@ -173,7 +173,10 @@ class TRState:
         """The end of a step without a draft, from the roots' logits [B, V]: the root's
         row of M becomes its top-K, its first token the next root (committed1).  With the
         uniforms U [B] the next root is drawn by tr_sample instead, with every
-        sequence's own rules [B] (refused without U)."""
+        sequence's own rules [B] (refused without U); a row in which nothing can be drawn
+        makes the root -1 and sets TR_DEV_BAD_TOKEN.  Tree steps (finish) know one temperature for
+        all sequences and no other rule: a loop of both kinds of steps samples from one
+        distribution only with that temperature everywhere and no rules here."""
         if U is None and not (temperature is None and top_k is None and top_p is None and min_p is None):
             raise ValueError("temperature, top_k, top_p and min_p need the uniforms U")
         tr_topk(logits, self.K, self.ids1, None, self.ws_topk1, V=self.V)

@@ -178,3 +178,24 @@ def test_edges_among_equal_logits(tr, rows, V):
     check(tr, x, rng.random(rows).tolist(), logprobs=True, top_p=p)
     check(tr, x, [1 - 2.0 ** -24] * rows, logprobs=True, top_p=p)
     check(tr, x, rng.random(rows).tolist(), logprobs=True, top_p=p, top_k=rng.integers(1, V, rows).tolist())
+
+
+def test_a_step_whose_row_leaves_nothing(tr):
+    """The root is -1 and the status says so; the other sequence goes on, and so does this one from the next draw."""
+    from free_speculative_decoding_gb300.engine import TRState
+    V = 500
+    tree = tr.Tree((2, 1, 0, 0), 4)
+    st = TRState(tree, 2, V, Hq=2, Hkv=1, d=128, cap=64, single_token=True)
+    st.start([3, 4], [0, 0], mode=tr.TR_INIT_RANDOM)
+    x = torch.randn(2, V, device="cuda")
+    x[0] = -math.inf
+    U = torch.tensor([0.4, 0.4], device="cuda")
+    st.finish_decode(x, U)
+    assert tr.tr_get_status() == tr.TR_DEV_BAD_TOKEN
+    want = oracle.sample(x[1].double().cpu().numpy(), float(np.float32(0.4)))[0]
+    assert st.root.tolist() == [-1, want] and st.committed1.tolist() == [[-1], [want]] and st.tree_tok[1, 0].item() == want
+    x[0] = x[1]
+    st.finish_decode(x, U)                        # the row of M at the root -1 is not written
+    assert tr.tr_get_status() == tr.TR_DEV_BAD_TOKEN and st.root.tolist() == [want, want]
+    st.finish_decode(x, U)
+    assert tr.tr_get_status() == 0 and st.tree_tok[:, 0].tolist() == [want, want]
