@@ -582,10 +582,15 @@ int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
   const long long rows = (long long)a.B * a.T, most = (long long)kCtas * tr_sm_count();
   // Shares of a token: as many as give every warp one, where tokens are few.  Where they are many, one, but two of tokens
   // with 12 groups and more whose halves are paired behind a norm (its work is more than the angles that both halves
-  // then need).  One against two, 32 queries' and 8 keys' heads of 128, dense: 4 x 8192 tokens 146 / 133 us, 16 x 8192
-  // 548 / 518 us; without norms 141 / 147 us, pairs of neighbours 137 / 143 us, 8 x 700 tokens 27.9 / 28.6 us, heads of
-  // 64 (6 groups) 71 / 91 us; into a cache, ragged, 88 / 99 us.
-  const bool two = DST == kDense && !PAIRS && a.norm[0] && a.norm[1] && a.all_groups >= 12 && rows >= 8 * most * 8;
+  // then need), unless there are 16 groups and as many of them are keys' and values' as queries' (the cut then falls into
+  // the keys).  One against two, 32 queries' and 8 keys' heads of 128, dense: 4 x 8192 tokens 145 / 135 us, 3 x 8192
+  // 107 / 103, 4 x 5000 87 / 85; without norms 141 / 147 us, pairs of neighbours 137 / 143 us, 8 x 700 tokens 27.9 / 28.6
+  // us; into a cache, ragged, 88 / 99 us.  Other heads, 4 x 8192: of 128, 32/4 (10 groups) 107 / 127, 16/16 (12) 145 / 137,
+  // 24/12 (12) 146 / 132, 40/8 (14) 170 / 149, 48/8 (16) 194 / 172, 32/16 (16) 191 / 195, 24/24 (18) 211 / 224, 64/8 (20)
+  // 240 / 236, 48/16 (20) 238 / 237, 64/16 (24) 283 / 284, 32/32 (24) 274 / 295, 64/32 (32) 364 / 377; of 64, 32/8 (6)
+  // 71 / 90, 64/8 (10) 119 / 118, 64/16 (12) 146 / 128, 32/32 (12) 144 / 147, 128/8 (18) 217 / 215.
+  const bool two = DST == kDense && !PAIRS && a.norm[0] && a.norm[1] && a.all_groups >= 12 &&
+                   (a.all_groups < 16 || 2 * a.groups[0] > a.all_groups) && rows >= 8 * most * 8;
   a.parts = (int)std::max<long long>(two ? 2 : 1, std::min<long long>(a.all_groups, most * 8 / rows));
   a.per = (a.all_groups + a.parts - 1) / a.parts;
   a.parts = (a.all_groups + a.per - 1) / a.per;
