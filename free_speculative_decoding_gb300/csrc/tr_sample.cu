@@ -15,8 +15,10 @@
 // list, which is merged over the cluster and sorted, and the edge is read off exact sums.  Where they
 // are more than the list holds (long runs of equal logits) the key is narrowed down by eight
 // bits a pass instead.  The draw then goes from the warps' sums to one warp's range, an eighth of it, a batch and a
-// token.  With a temperature alone the weights are summed in the first pass already, relative to the warp's
-// largest logit so far.
+// token.  With a temperature alone, in rows that are read from global memory, the weights are summed in the first pass
+// already, relative to the warp's largest logit so far.  These sums are cut whenever that rises, so they are not the exact
+// ones: by two units for each lane and one for the warp, within the stated bound, but a row that lies in shared
+// memory in a call of fewer rows can differ in a last bit, or in its token next to a border.
 //
 // What bounds it: single rows a chain of latencies (some fifteen passes and barriers, those of a cluster about 1 us each,
 // instructions fetched for the first time); many rows the latencies of their passes (1280 rows of mixed rules: issue slots
@@ -129,8 +131,10 @@ struct Weight {
   __device__ __forceinline__ double log_share(float x, u64 all) const {
     const u64 n = (*this)(x);
     const bool small = n < 1u << 30 && !infinite;
-    const double power = ((double)x - (double)base) * ((double)c_hi + (double)c_lo) + ((0x48400000 >> 6) + 63 - shift);
-    return log((small ? 1.0 : (double)n) / (double)all) + (small ? power * 0.6931471805599453 : 0.0);
+    double r = log((double)(small ? 1 : n) / (double)all);
+    if (small)  // seldom, and a single row waits 0.2 us for it
+      r += 0.6931471805599453 * (((double)x - (double)base) * ((double)c_hi + (double)c_lo) + ((0x48400000 >> 6) + 63 - shift));
+    return r;
   }
   // The weights of N logits, the same arithmetic, two to an instruction; 0 for those whose bit of `there` is not set: of
   // all that lie up to `floor` or are NaN.
