@@ -14,11 +14,11 @@
 // (queries, keys or values), 1 KB.
 //
 // Measured in a graph (rows not in L2; of a copy's rate): 4 x 8192 tokens of 32/8 heads of 128, bf16, norms 135 us (88%),
-// 16 x 8192 520 (91%), without norms 141 (84%), pairs of neighbours 131 (91%), heads of 64 71 (84%), 64/8 heads 122 of
-// 2 x 8192 (81%), 8/2 heads 35 of 4 x 4096 (42%: keys and values are half a group each, and a
-// token's angles and factors serve four groups; 1377 instructions a token, issue slots 58% busy); 8 x 700 29 (71%); a tree
-// of 80 nodes 4.4, 8 trees of 128 with 32/8 heads 8.7; into pages, 8 prompts up to 4096 long 85 (86%), one token for each
-// of 64 sequences, e4m3, 5.8.
+// fp16 137, 16 x 8192 519 (91%), without norms 140 (85%), pairs of neighbours 132 (90%), 32/32 heads 274 (87%), heads of 64
+// 71 (84%), 64/8 heads 122 of 2 x 8192 (81%), 8/2 heads 35 of 4 x 4096 (43%: keys and values are half a group each, and a
+// token's angles and factors serve four groups; 1377 instructions a token, issue slots 58% busy); 8 x 700 28 (71%); a tree
+// of 80 nodes 3.7, 8 trees of 128 with 32/8 heads 8.5; into pages, 8 prompts up to 4096 long 84 (86%), e4m3 99 (68%: a
+// division by the scale, found anew for every group); one token for each of 64 sequences 3.8 to 4.1, e4m3, 4.4 to 4.8.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -352,7 +352,8 @@ struct Rows {
 // gridDim * 8-th item.  Groups come through the warp's ring in shared memory (cp.async), kStages - 1
 // ahead of the one in work and across items, so that the bytes under way need no registers: loads into registers took
 // 4 x 8192 tokens 146 to 150 us when they were tried, 16 stages 160 (the L1 that they take is the stores'), three CTAs on an
-// SM with 80 registers 303 (they spill).  With a cache the lengths are what the plan kernel has left in todo.
+// SM with 80 registers 303 (they spill; with two on an SM only the variants that write e4m3 do, 8 to 16 bytes).
+// With a cache the lengths are what the plan kernel has left in todo.
 template <bool BF, int D, bool PAIRS, int DST>
 __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, const KvDev c,
                                                           const __grid_constant__ Depths tree) {
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(256, kCtas) rope_kernel(const RopeArgs a, cons
 
 // Few rows: a cluster takes a sequence, checks it, copies its rows and advances its length,
 // so that no kernel is needed before this one.  A task is the next U groups of a token, whose loads are requested
-// before the sequence is checked; a warp takes every (gridDim * warps)-th.  Latency bounds it: one token 3 us, of which the
-// launch is most.
+// before the sequence is checked; a warp takes every (gridDim * warps)-th.  Latency bounds it: one token 3.4 to 3.6 us, of
+// which the launch is most.
 template <bool BF, int D, bool PAIRS, int DST>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2) append_rope_kernel(const RopeArgs a, const KvDev c) {
   constexpr int U = kShort;
@@ -599,15 +600,16 @@ int launch(RopeArgs a, const KvDev &c, const Depths &tree, cudaStream_t s) {
 }
 
 // One kernel for a sequence's rows up to this many tasks of a warp, else a plan and rope_kernel.  In a graph, one against
-// two, 32/8 heads of 128: 64 x 1 tokens 4.4 / 5.7 us, 1 x 10 4.9 / 5.4, 24 x 16 8.2 / 7.0, 24 x 33 12.0 / 8.2, 8 x 85
-// 16.7 / 8.1; the second launch takes the host 2.4 us.
+// two, 32/8 heads of 128: 64 x 1 tokens 3.8 / 5.0 us, 1 x 10 4.6 / 5.1, 24 x 16 7.5 / 6.4, 24 x 33 13.5 / 9.5, 8 x 85
+// 19.1 / 8.1; the second launch takes the host 2.4 us.
 constexpr int kRounds = 2, kMostCluster = 8;
 
 template <bool BF, int D, bool PAIRS, int DST>
 int launch_append(RopeArgs a, const KvDev &c, const int32_t *count, void *ws, cudaStream_t s) {
-  // A task is a group where every warp of a cluster gets one at most and the clusters fill the SMs once, else two: one
-  // token of 32/32 heads 3.3 instead of 3.9 us, 1 x 4 of 32/8 3.8 / 4.6, 64 x 1 e4m3 4.5 to 5.0 / 5.8 (bf16 4.7 / 4.4); with
-  // one always 64 x 4 9.0 instead of 5.8, 24 x 21 10.1 / 8.4.
+  // A task is a group where every warp of a cluster gets one at most and the clusters fill the SMs once, else two.  One
+  // against two, in us: one token of 32/32 heads 3.5 / 4.1 (e4m3 4.1 / 5.0), 1 x 4 of 32/8 3.5 / 4.1, 16 x 1 3.6 / 3.8,
+  // 32 x 1 3.8 / 3.8, 64 x 1 4.05 / 3.9 (e4m3 4.4 / 5.5), 72 x 1 3.9 / 4.0, 24 x 4 4.1 / 4.4, 64 x 1 of 8/2 3.3 / 3.6;
+  // with one always 64 x 4 9.0 / 5.8, 24 x 21 10.1 / 8.4.
   const long long alone = (long long)a.T * a.all_groups;
   a.per = alone <= kMostCluster * kMaxWarps && a.B * ((alone + kMaxWarps - 1) / kMaxWarps) <= tr_sm_count() ? 1 : kShort;
   const long long tasks = (long long)a.T * ((a.all_groups + a.per - 1) / a.per);

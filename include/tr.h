@@ -523,10 +523,12 @@ int tr_kv_append_rope(const tr_qkv *rows, const tr_rope *rope, const int32_t *po
  *   U [rows] fp32 uniforms in [0, 1) (the random numbers are inputs; others are
  *   moved to the nearest end, NaN to 0)
  *   token [rows] int32 out; logprob [rows] fp32 out, may be NULL
- * Weights are good to about 2^-29 (relative) and summed exactly as integers in units of less than
+ * Weights are good to about 2^-29 (relative) and summed as integers in units of less than
  * V / 2^61 of the largest (up to four units count as none), so a draw or an edge of the rules
  * differs from exact arithmetic only within about 4e-9 + V^2 / 2^59 of a border, and logprob, whatever the token's
- * weight, by twice that and fp32's rounding.  No workspace; equal calls give equal bits.
+ * weight, by twice that and fp32's rounding.  Sums are exact but those of rows with a temperature alone
+ * in calls of more or longer rows than the chip holds (cut again as the largest logit rises, within the same bound).
+ * No workspace; equal calls give equal bits, and a row alone or among others the same ones but for those sums.
  * rows == 0 does nothing; TR_E_UNSUPPORTED for rows past 2^24 or V past 2^30. */
 int tr_sample(const void *logits, tr_ftype ftype, int64_t rows, int64_t V, int64_t ld, const float *temperature,
               const int32_t *top_k, const float *top_p, const float *min_p, const float *U, int32_t *token,
