@@ -22,7 +22,7 @@ def sample_left(x, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         return order[:1], np.ones(1), np.inf
     with np.errstate(invalid="ignore", over="ignore"):
         d = np.where(x[order] == m, 0.0, x[order] - m)
-        w = np.where(d == 0.0, 1.0, np.exp(d / temperature))
+        w = np.where(d == 0.0, 1.0, np.where(d == -np.inf, 0.0, np.exp(d / temperature)))
     if top_k > 0:
         order, w, d = order[:top_k], w[:top_k], d[:top_k]
     margin = np.inf

@@ -199,3 +199,16 @@ def test_a_step_whose_row_leaves_nothing(tr):
     assert tr.tr_get_status() == tr.TR_DEV_BAD_TOKEN and st.root.tolist() == [want, want]
     st.finish_decode(x, U)
     assert tr.tr_get_status() == 0 and st.tree_tok[:, 0].tolist() == [want, want]
+
+
+@pytest.mark.parametrize("rows", [1, 60, 700])
+def test_infinite_logits_at_an_infinite_temperature(tr, rows):
+    """The infinite ones share the draw at every temperature."""
+    x = torch.randn(rows, 1001, device="cuda")
+    x[:, 900] = math.inf
+    x[rows // 2:, 17] = math.inf
+    U = [i / rows for i in range(rows)]
+    for T in (math.inf, 3e38, 1.0):
+        for rules in (dict(), dict(top_p=[0.9] * rows), dict(top_k=[5] * rows), dict(min_p=[0.1] * rows)):
+            token, lp = check(tr, x, U, logprobs=True, temperature=[T] * rows, **rules)
+            assert set(token) <= {17, 900}

@@ -22,6 +22,10 @@ def test_only_tokens_that_are_left():
     assert may(x, 1, 0.0, 1e-8, min_p=1e-3) is None and may(x, 1, 0.0, 1e-8, top_p=0.999) is None
     assert may(x, 4, NAN, 1e-8, temperature=0.0) and may(x, 3, 0.0, 1e-8, temperature=0.0) is None
     assert may([-INF, NAN], -1, 0.5, 1e-8) == (-INF, -INF) and may([-INF, NAN], 0, 0.5, 1e-8) is None
+    for T in (1.0, INF):                                       # all the draw is the infinite ones
+        assert list(oracle.sample_left([INF, 5.0, INF], temperature=T)[1]) == [1.0, 0.0, 1.0]
+        assert oracle.sample([5.0, INF, 5.0], 0.99, temperature=T)[:2] == (1, 0.0)
+        assert may([5.0, INF, 5.0], 1, 0.99, 1e-8, temperature=T) and not may([5.0, INF, 5.0], 2, 0.99, 1e-8, temperature=T)
     assert may([INF, 5.0, INF], 2, 0.5 - 1e-9, 1e-8) and may([INF, 5.0, INF], 1, 0.5, 1e-8) is None
 
 
